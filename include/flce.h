@@ -379,6 +379,118 @@ flce_status flce_shard_backward(const void* x, const void* W_shard, const void* 
                                 float* dx_partial, int accumulate_dx, void* dW_shard, void* db_shard,
                                 void* workspace, size_t workspace_bytes, hipStream_t stream);
 
+/*
+ * Feed-forward layers.  Two operators that a model has next to its head: the
+ * gated product of a feed-forward block and a linear layer (the block's output
+ * projection onto the residual stream, a plain feed-forward layer, the head's
+ * own transform), each with its gradients.  Conventions as above; also:
+ *  - x [N, H], weights [F, H], outputs and their gradients [N, F], biases [F];
+ *    every [.., ..] tensor 16-byte aligned, biases and their gradients
+ *    element-aligned; H a multiple of 8 (FLCE_ERR_UNSUPPORTED otherwise), F
+ *    and N any size, N = 0 included (weight gradients are then zero, and the
+ *    token tensors may be NULL).
+ *  - Products accumulate in fp32 whatever the dtype; results are rounded once.
+ *    The kept pre-activations (z; g and u) and the gradients of them (dz; dg
+ *    and du, in the workspace) are held in the tensors' dtype: each is an
+ *    operand of a 16-bit matrix product, or as large as all other outputs
+ *    together.  With float16 that bounds them by 65504 and rounds values under
+ *    2^-14 to multiples of 2^-24, as float16 autograd of the formulas does.
+ *  - Results do not depend on what else runs: sums are added in a fixed order.
+ */
+typedef FLCE_ENUM(flce_activation) {
+  FLCE_ACT_NONE = 0,      /* act(z) = z */
+  FLCE_ACT_RELU = 1,      /* max(z, 0); gradient 0 at 0 */
+  FLCE_ACT_GELU = 2,      /* z Phi(z), Phi the normal distribution function */
+  FLCE_ACT_GELU_TANH = 3, /* z (1 + tanh(sqrt(2/pi) (z + 0.044715 z^3))) / 2 */
+  FLCE_ACT_SILU = 4,      /* z sigmoid(z) */
+  FLCE_ACT_SIGMOID = 5
+} flce_activation;
+
+/*
+ * Linear layer:  z = x W^T + b,  y = act(z) + residual.
+ * b and residual may be NULL; y may be residual itself (any other overlap of
+ * an output with an input is not allowed).  z: if non-NULL, the forward writes
+ * the pre-activations there for the backward (not needed with FLCE_ACT_NONE).
+ *
+ * Backward, given dy [N, F]:  dz = dy act'(z),  dx = dz W,  dW = dz^T x,
+ * db = sum_n dz.  dx, dW, db may each be NULL.  (The residual's gradient is dy.)
+ * z is the forward's, ignored with FLCE_ACT_NONE.
+ *
+ * flce_linear_workspace_size: bytes for the forward (fp32 partial sums when a
+ * few output tiles are split along H; 0 otherwise, and the workspace may then
+ * be NULL) and the backward (dz unless it is dy itself, fp32 partials of db
+ * and of split products); pure host arithmetic, either output may be NULL.
+ */
+flce_status flce_linear_workspace_size(int64_t N, int64_t H, int64_t F, flce_dtype dtype, flce_activation activation,
+                                       size_t* fwd_bytes, size_t* bwd_bytes);
+
+flce_status flce_linear_forward(const void* x, const void* W, const void* b, const void* residual, int64_t N, int64_t H,
+                                int64_t F, flce_dtype dtype, flce_activation activation, void* y, void* z,
+                                void* workspace, size_t workspace_bytes, hipStream_t stream);
+
+flce_status flce_linear_backward(const void* x, const void* W, const void* z, const void* dy, int64_t N, int64_t H,
+                                 int64_t F, flce_dtype dtype, flce_activation activation, void* dx, void* dW, void* db,
+                                 void* workspace, size_t workspace_bytes, hipStream_t stream);
+
+/*
+ * Gated product:  g = x Wg^T + bg,  u = x Wu^T + bu,  h = act(g) * u.
+ * bg and bu may be NULL.  g, u: if non-NULL (both or neither), the forward
+ * writes the projections there for the backward.
+ *
+ * Backward, given dh [N, F] and the kept g and u:  dg = dh u act'(g),
+ * du = dh act(g),  dx = dg Wg + du Wu,  dWg = dg^T x,  dWu = du^T x,  dbg and
+ * dbu their column sums.  dx, dWg, dWu, dbg, dbu may each be NULL.
+ * flce_glu_workspace_size as flce_linear_workspace_size.
+ */
+flce_status flce_glu_workspace_size(int64_t N, int64_t H, int64_t F, flce_dtype dtype, size_t* fwd_bytes,
+                                    size_t* bwd_bytes);
+
+flce_status flce_glu_forward(const void* x, const void* Wg, const void* Wu, const void* bg, const void* bu, int64_t N,
+                             int64_t H, int64_t F, flce_dtype dtype, flce_activation activation, void* h, void* g,
+                             void* u, void* workspace, size_t workspace_bytes, hipStream_t stream);
+
+flce_status flce_glu_backward(const void* x, const void* Wg, const void* Wu, const void* g, const void* u,
+                              const void* dh, int64_t N, int64_t H, int64_t F, flce_dtype dtype,
+                              flce_activation activation, void* dx, void* dWg, void* dWu, void* dbg, void* dbu,
+                              void* workspace, size_t workspace_bytes, hipStream_t stream);
+
+/*
+ * Global gradient norm and clipping, over `count` tensors of any dtypes and
+ * sizes (numels[i] elements at grads[i], element-aligned; numels[i] = 0 is
+ * allowed and its pointer then ignored).  grads, outs, numels and dtypes are
+ * HOST arrays, read before the call returns; a captured graph holds their
+ * contents.
+ *
+ *   norm = sqrt(sum of g^2) (norm_type 2)  or  max |g| (norm_type INFINITY),
+ *          over every element of every tensor; 0 without any
+ *   out  = g * min(1, max_norm / (norm + 1e-6))
+ *
+ * The sum of squares is accumulated in fp64, in a fixed order.  A NaN among
+ * the gradients makes norm NaN, and then every output is NaN; an infinite one
+ * makes it infinite and the factor 0.
+ * flce_clip_grad_norm: outs NULL scales the gradients in place, else outs[i]
+ * receives grads[i] scaled (outs[i] may be grads[i]), and a factor of 1 leaves
+ * in-place gradients untouched.  No output may share memory with any other
+ * tensor of the call (FLCE_ERR_INVALID_ARGUMENT); max_norm >= 0.
+ * norm: float32 [1] on the device.
+ * flce_clip_grads_with_norm scales by a norm the caller has on the device (a
+ * norm over several ranks' gradients, say).
+ * flce_grad_norm_workspace_size: bytes for a call with `count` tensors (about
+ * 16 KB); pure host arithmetic.
+ */
+flce_status flce_grad_norm_workspace_size(int64_t count, size_t* bytes);
+
+flce_status flce_grad_norm(const void* const* grads, const int64_t* numels, const flce_dtype* dtypes, int64_t count,
+                           float norm_type, float* norm, void* workspace, size_t workspace_bytes, hipStream_t stream);
+
+flce_status flce_clip_grad_norm(const void* const* grads, void* const* outs, const int64_t* numels,
+                                const flce_dtype* dtypes, int64_t count, float max_norm, float norm_type, float* norm,
+                                void* workspace, size_t workspace_bytes, hipStream_t stream);
+
+flce_status flce_clip_grads_with_norm(const void* const* grads, void* const* outs, const int64_t* numels,
+                                      const flce_dtype* dtypes, int64_t count, float max_norm, const float* norm,
+                                      hipStream_t stream);
+
 /* A static, human-readable name for a status code. */
 const char* flce_status_string(flce_status status);
 

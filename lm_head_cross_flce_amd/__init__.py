@@ -16,7 +16,8 @@ def __getattr__(name):
         import importlib
         return importlib.import_module(f"{__name__}.{name}")
     if name in ("flce_forward", "flce_backward", "flce_workspace_size", "fused_linear_cross_entropy_loss",
-                "FusedLinearCrossEntropyLoss", "FusedLinearCrossEntropyFunction"):
+                "FusedLinearCrossEntropyLoss", "FusedLinearCrossEntropyFunction", "fused_linear", "fused_glu",
+                "GatedFeedForward", "clip_grad_norm_", "flce_grad_norm", "flce_clip_grad_norm"):
         from . import functional
         return getattr(functional, name)
     raise AttributeError(name)

@@ -28,6 +28,8 @@ FLCE_F16 = 2
 
 REDUCTIONS = {"none": 0, "sum": 1, "mean": 2}
 
+ACTIVATIONS = {"none": 0, "relu": 1, "gelu": 2, "gelu_tanh": 3, "silu": 4, "sigmoid": 5}
+
 # Every symbol the public header declares.
 EXPORTS = ("flce_workspace_size", "flce_forward", "flce_backward", "flce_forward_ex", "flce_backward_ex",
            "flce_forward_noalloc", "flce_fused_workspace_size", "flce_fused_forward_backward",
@@ -35,7 +37,10 @@ EXPORTS = ("flce_workspace_size", "flce_forward", "flce_backward", "flce_forward
            "flce_timing_start", "flce_timing_stop", "flce_timing_count", "flce_timing_read", "flce_timing_clear",
            "flce_status_string",
            "flce_backward_slab_cols", "flce_shard_workspace_size", "flce_shard_forward", "flce_shard_merge",
-           "flce_shard_backward")
+           "flce_shard_backward",
+           "flce_linear_workspace_size", "flce_linear_forward", "flce_linear_backward",
+           "flce_glu_workspace_size", "flce_glu_forward", "flce_glu_backward",
+           "flce_grad_norm_workspace_size", "flce_grad_norm", "flce_clip_grad_norm", "flce_clip_grads_with_norm")
 
 class FlceOptions(ctypes.Structure):
     """struct flce_options of flce.h."""
@@ -123,6 +128,28 @@ def load() -> ctypes.CDLL:
         lib.flce_shard_backward.argtypes = [vp, vp, vp, vp, i64, i64, i64, i64, i64, c_int, f32, f32, i64,
                                             c_int, vp, vp, vp, vp, c_int, vp, vp, vp, sz, vp]
         lib.flce_shard_backward.restype = c_int
+        psz = ctypes.POINTER(sz)
+        lib.flce_linear_workspace_size.argtypes = [i64, i64, i64, c_int, c_int, psz, psz]
+        lib.flce_linear_workspace_size.restype = c_int
+        lib.flce_linear_forward.argtypes = [vp, vp, vp, vp, i64, i64, i64, c_int, c_int, vp, vp, vp, sz, vp]
+        lib.flce_linear_forward.restype = c_int
+        lib.flce_linear_backward.argtypes = [vp, vp, vp, vp, i64, i64, i64, c_int, c_int, vp, vp, vp, vp, sz, vp]
+        lib.flce_linear_backward.restype = c_int
+        lib.flce_glu_workspace_size.argtypes = [i64, i64, i64, c_int, psz, psz]
+        lib.flce_glu_workspace_size.restype = c_int
+        lib.flce_glu_forward.argtypes = [vp, vp, vp, vp, vp, i64, i64, i64, c_int, c_int, vp, vp, vp, vp, sz, vp]
+        lib.flce_glu_forward.restype = c_int
+        lib.flce_glu_backward.argtypes = [vp, vp, vp, vp, vp, vp, i64, i64, i64, c_int, c_int, vp, vp, vp, vp, vp,
+                                          vp, sz, vp]
+        lib.flce_glu_backward.restype = c_int
+        lib.flce_grad_norm_workspace_size.argtypes = [i64, psz]
+        lib.flce_grad_norm_workspace_size.restype = c_int
+        lib.flce_grad_norm.argtypes = [vp, vp, vp, i64, f32, vp, vp, sz, vp]
+        lib.flce_grad_norm.restype = c_int
+        lib.flce_clip_grad_norm.argtypes = [vp, vp, vp, vp, i64, f32, f32, vp, vp, sz, vp]
+        lib.flce_clip_grad_norm.restype = c_int
+        lib.flce_clip_grads_with_norm.argtypes = [vp, vp, vp, vp, i64, f32, vp, vp]
+        lib.flce_clip_grads_with_norm.restype = c_int
         _lib = lib
         return lib
 
@@ -280,6 +307,93 @@ def flce_backward_kept(x, W, b, targets, N, H, V, dtype, label_smoothing, z_loss
                                      lse, n_valid, grad_loss, keep or None, keep_bytes, dx or None, dW or None,
                                      db or None, workspace, workspace_bytes, stream or None),
            "flce_backward_kept")
+
+
+def flce_linear_workspace_size(N: int, H: int, F: int, dtype: int, activation: int):
+    """(forward_bytes, backward_bytes) of the linear layer."""
+    f, b = ctypes.c_size_t(0), ctypes.c_size_t(0)
+    _check(load().flce_linear_workspace_size(N, H, F, dtype, activation, ctypes.byref(f), ctypes.byref(b)),
+           "flce_linear_workspace_size")
+    return f.value, b.value
+
+
+def flce_linear_forward(x, W, b, residual, N, H, F, dtype, activation, y, z, workspace, workspace_bytes,
+                        stream) -> None:
+    """Raw call: every tensor argument is an integer device address (or 0/None)."""
+    _check(load().flce_linear_forward(x or None, W, b or None, residual or None, N, H, F, dtype, activation, y or None,
+                                      z or None, workspace or None, workspace_bytes, stream or None),
+           "flce_linear_forward")
+
+
+def flce_linear_backward(x, W, z, dy, N, H, F, dtype, activation, dx, dW, db, workspace, workspace_bytes,
+                         stream) -> None:
+    """Raw call: every tensor argument is an integer device address (or 0/None)."""
+    _check(load().flce_linear_backward(x or None, W, z or None, dy or None, N, H, F, dtype, activation, dx or None,
+                                       dW or None, db or None, workspace or None, workspace_bytes, stream or None),
+           "flce_linear_backward")
+
+
+def flce_glu_workspace_size(N: int, H: int, F: int, dtype: int):
+    """(forward_bytes, backward_bytes) of the gated product."""
+    f, b = ctypes.c_size_t(0), ctypes.c_size_t(0)
+    _check(load().flce_glu_workspace_size(N, H, F, dtype, ctypes.byref(f), ctypes.byref(b)), "flce_glu_workspace_size")
+    return f.value, b.value
+
+
+def flce_glu_forward(x, Wg, Wu, bg, bu, N, H, F, dtype, activation, h, g, u, workspace, workspace_bytes,
+                     stream) -> None:
+    """Raw call: every tensor argument is an integer device address (or 0/None)."""
+    _check(load().flce_glu_forward(x or None, Wg, Wu, bg or None, bu or None, N, H, F, dtype, activation, h or None,
+                                   g or None, u or None, workspace or None, workspace_bytes, stream or None),
+           "flce_glu_forward")
+
+
+def flce_glu_backward(x, Wg, Wu, g, u, dh, N, H, F, dtype, activation, dx, dWg, dWu, dbg, dbu, workspace,
+                      workspace_bytes, stream) -> None:
+    """Raw call: every tensor argument is an integer device address (or 0/None)."""
+    _check(load().flce_glu_backward(x or None, Wg, Wu, g or None, u or None, dh or None, N, H, F, dtype, activation,
+                                    dx or None, dWg or None, dWu or None, dbg or None, dbu or None, workspace or None,
+                                    workspace_bytes, stream or None), "flce_glu_backward")
+
+
+def flce_grad_norm_workspace_size(count: int) -> int:
+    b = ctypes.c_size_t(0)
+    _check(load().flce_grad_norm_workspace_size(count, ctypes.byref(b)), "flce_grad_norm_workspace_size")
+    return b.value
+
+
+def pointer_array(addresses):
+    """A host void*[] (0 becomes NULL)."""
+    return (ctypes.c_void_p * max(len(addresses), 1))(*addresses)
+
+
+def size_array(sizes):
+    """A host int64_t[]."""
+    return (ctypes.c_int64 * max(len(sizes), 1))(*sizes)
+
+
+def dtype_array(codes):
+    """A host flce_dtype[]."""
+    return (ctypes.c_int * max(len(codes), 1))(*codes)
+
+
+def flce_grad_norm(grads, numels, dtypes, count, norm_type, norm, workspace, workspace_bytes, stream) -> None:
+    """Raw call: grads, numels, dtypes from pointer_array, size_array and dtype_array."""
+    _check(load().flce_grad_norm(grads, numels, dtypes, count, norm_type, norm, workspace, workspace_bytes,
+                                 stream or None), "flce_grad_norm")
+
+
+def flce_clip_grad_norm(grads, outs, numels, dtypes, count, max_norm, norm_type, norm, workspace, workspace_bytes,
+                        stream) -> None:
+    """Raw call: outs is a pointer_array or None (in place)."""
+    _check(load().flce_clip_grad_norm(grads, outs, numels, dtypes, count, max_norm, norm_type, norm, workspace,
+                                      workspace_bytes, stream or None), "flce_clip_grad_norm")
+
+
+def flce_clip_grads_with_norm(grads, outs, numels, dtypes, count, max_norm, norm, stream) -> None:
+    """Raw call: outs is a pointer_array or None (in place)."""
+    _check(load().flce_clip_grads_with_norm(grads, outs, numels, dtypes, count, max_norm, norm, stream or None),
+           "flce_clip_grads_with_norm")
 
 
 def flce_timing_start(capacity: int) -> None:

@@ -21,7 +21,8 @@ CSRC = os.path.join(PKG, "csrc")
 INCLUDE = os.path.join(ROOT, "include")
 LIB_NAME = "libflce.so"
 LIB_PATH = os.path.join(PKG, LIB_NAME)
-SOURCES = ["flce_kernels.hip", "flce_api.hip"]
+SOURCES = ["flce_kernels.hip", "flce_api.hip", "layer_bf16.hip", "layer_f16.hip", "layer_f32.hip",
+           "layer_kernels.hip", "grad_norm_kernels.hip"]
 ARCH = "gfx950"
 
 

@@ -1,6 +1,7 @@
 // C-ABI entry points of the FLCE library: argument validation, workspace
 // layout and the launch sequence.  No allocation and no host synchronisation:
 // everything is enqueued on the caller's stream.
+#include <algorithm>
 #include <cmath>
 #include <cstdlib>
 #include <cstring>
@@ -967,6 +968,399 @@ flce_status flce_shard_backward(const void* x, const void* W_shard, const void* 
   a.gscale = dtype == FLCE_F16 ? (float*)(ws + g.off_gscale) : nullptr;
   a.dx = dx_partial; a.dW = dW_shard; a.db = want_db ? db_shard : nullptr;
   return run_backward(a, g, V_shard, dtype, want_db, true, accumulate_dx != 0, (hipStream_t)stream);
+}
+
+}  // extern "C"
+
+// ---------------------------------------------------------------------------
+// Linear layer and gated product
+// ---------------------------------------------------------------------------
+
+namespace {
+
+// K parts of a product with `tiles` 256 x 256 output tiles.  Tiles that fill
+// over half the CUs are not split; fewer are, into as many parts as make one
+// workgroup per CU, each at least 512 deep and at most 16: every part costs a
+// pass over an fp32 copy of the output.
+int product_parts(int64_t tiles, int64_t K) {
+  if (2 * tiles > kCUs) return 1;
+  int64_t p = kCUs / tiles;
+  if (p > K / 512) p = K / 512;
+  if (p > 16) p = 16;
+  return p < 2 ? 1 : (int)p;
+}
+
+// Depth of a part: the 64-deep copy block divides it, so every part starts on
+// a block.
+int64_t part_depth(int64_t K, int parts) { return parts > 1 ? cdiv(cdiv(K, parts), 64) * 64 : K; }
+
+struct LayerGeometry {
+  int TM, TN, fwd_parts;
+  int64_t kc, ldp;
+  size_t fwd_total;
+  bool dz_is_dy;
+  int64_t ldz, segk;
+  int db_blocks, db_rows;
+  int64_t ldb;
+  int dx_parts, dw_parts;
+  int64_t dx_kc, dw_kc;
+  size_t off_dbp, off_part, bwd_total;
+};
+
+LayerGeometry layer_geometry(int64_t N, int64_t H, int64_t F, int dtype, int act, int nmat) {
+  LayerGeometry g{};
+  const int64_t es = dtype == FLCE_F32 ? 4 : 2;
+  g.TM = (int)cdiv(N, kTile);
+  g.TN = (int)cdiv(F, nmat == 2 ? kTile / 2 : kTile);
+  g.fwd_parts = N > flce::kSkinnyTokens ? product_parts((int64_t)g.TM * g.TN, H) : 1;
+  g.kc = part_depth(H, g.fwd_parts);
+  g.ldp = nmat * cdiv(F, 8) * 8;
+  g.fwd_total = g.fwd_parts > 1 ? align_up((size_t)g.fwd_parts * N * g.ldp * 4) : 0;
+
+  // dz: rows padded to 16-byte pieces; the gated product's two halves each to
+  // a whole 64-deep copy block, so that no block of the dx product straddles
+  // the weights.
+  g.dz_is_dy = nmat == 1 && act == FLCE_ACT_NONE && F % 8 == 0;
+  g.segk = nmat == 2 ? cdiv(F, 64) * 64 : int64_t(1) << 30;
+  g.ldz = nmat == 2 ? 2 * g.segk : cdiv(F, 8) * 8;
+  size_t off = g.dz_is_dy ? 0 : align_up((size_t)N * g.ldz * es);
+  // Column sums: 64 tokens a block, more when that makes over 128 blocks.
+  g.db_rows = (int)(cdiv(cdiv(N, 128), 64) * 64);
+  if (g.db_rows < 64) g.db_rows = 64;
+  g.db_blocks = (int)cdiv(N, g.db_rows);
+  g.ldb = nmat * F;
+  g.off_dbp = off;
+  off = align_up(off + (size_t)g.db_blocks * g.ldb * 4);
+  const int64_t th = cdiv(H, kTile), tf = cdiv(F, kTile);
+  g.dx_parts = N > 0 ? product_parts(th * g.TM, g.ldz) : 1;
+  g.dw_parts = product_parts(th * tf * nmat, N);
+  g.dx_kc = part_depth(g.ldz, g.dx_parts);
+  g.dw_kc = part_depth(N, g.dw_parts);
+  g.off_part = off;
+  const size_t dxp = g.dx_parts > 1 ? (size_t)g.dx_parts * N * H * 4 : 0;
+  const size_t dwp = g.dw_parts > 1 ? (size_t)g.dw_parts * nmat * F * H * 4 : 0;
+  g.bwd_total = align_up(off + (dxp > dwp ? dxp : dwp));
+  return g;
+}
+
+flce_status check_layer(int64_t N, int64_t H, int64_t F, int dtype, int act, int nmat) {
+  if (N < 0 || H < 1 || F < 1) return FLCE_ERR_INVALID_ARGUMENT;
+  if (act < FLCE_ACT_NONE || act > FLCE_ACT_SIGMOID) return FLCE_ERR_INVALID_ARGUMENT;
+  if (dtype != FLCE_F32 && dtype != FLCE_BF16 && dtype != FLCE_F16) return FLCE_ERR_UNSUPPORTED;
+  if (N > (int64_t(1) << 30) || H > (int64_t(1) << 20) || F > (int64_t(1) << (nmat == 2 ? 19 : 20)))
+    return FLCE_ERR_UNSUPPORTED;
+  if (H % 8 != 0) return FLCE_ERR_UNSUPPORTED;
+  const int64_t wide = H > F ? H : F;   // every plane of output tiles fits in an int
+  if (cdiv(N, kTile) * cdiv(wide, kTile / 2) > (int64_t(1) << 26)) return FLCE_ERR_UNSUPPORTED;
+  return FLCE_OK;
+}
+
+bool bad_tensor(const void* p, size_t align, bool required) { return p ? !aligned(p, align) : required; }
+
+// The entry points' shared parts: nmat = 1 is the linear layer, 2 the gated product.
+flce_status layer_forward(const void* x, const void* const (&W)[2], const void* const (&b)[2], const void* residual,
+                          int64_t N, int64_t H, int64_t F, int dtype, int act, int nmat, void* y, void* const (&z)[2],
+                          void* workspace, size_t workspace_bytes, hipStream_t stream) {
+  const flce_status st = check_layer(N, H, F, dtype, act, nmat);
+  if (st != FLCE_OK) return st;
+  const size_t es = dtype == FLCE_F32 ? 4 : 2;
+  const bool rows = N > 0;   // without rows the token tensors may be null
+  if (bad_tensor(x, 16, rows) || bad_tensor(y, 16, rows) || bad_tensor(residual, 16, false)) return FLCE_ERR_INVALID_ARGUMENT;
+  for (int m = 0; m < nmat; ++m)
+    if (bad_tensor(W[m], 16, true) || bad_tensor(b[m], es, false) || bad_tensor(z[m], 16, false))
+      return FLCE_ERR_INVALID_ARGUMENT;
+  if (nmat == 2 && (z[0] == nullptr) != (z[1] == nullptr)) return FLCE_ERR_INVALID_ARGUMENT;
+  const LayerGeometry g = layer_geometry(N, H, F, dtype, act, nmat);
+  if (workspace_bytes < g.fwd_total) return FLCE_ERR_WORKSPACE_TOO_SMALL;
+  if (bad_tensor(workspace, 16, g.fwd_total > 0)) return FLCE_ERR_INVALID_ARGUMENT;
+  if (!rows) return FLCE_OK;
+  flce::LayerFwd a{};
+  a.x = x;
+  for (int m = 0; m < nmat; ++m) {
+    a.W[m] = W[m];
+    a.b[m] = b[m];
+    a.z[m] = z[m];
+  }
+  a.residual = residual;
+  a.y = y;
+  a.N = (int)N; a.H = (int)H; a.F = (int)F;
+  a.act = act; a.nmat = nmat;
+  a.TM = g.TM; a.TN = g.TN;
+  a.parts = g.fwd_parts; a.kc = (int)g.kc;
+  a.part = (float*)workspace; a.ldp = g.ldp;
+  (void)hipGetLastError();
+  flce::mark_launch(stream, nullptr);
+  return flce::launch_layer_forward(a, dtype, stream) == hipSuccess ? FLCE_OK : FLCE_ERR_HIP;
+}
+
+flce_status layer_backward(const void* x, const void* const (&W)[2], const void* const (&z)[2], const void* dy,
+                           int64_t N, int64_t H, int64_t F, int dtype, int act, int nmat, void* dx,
+                           void* const (&dW)[2], void* const (&db)[2], void* workspace, size_t workspace_bytes,
+                           hipStream_t stream) {
+  const flce_status st = check_layer(N, H, F, dtype, act, nmat);
+  if (st != FLCE_OK) return st;
+  const size_t es = dtype == FLCE_F32 ? 4 : 2;
+  const bool rows = N > 0;
+  const bool need_z = rows && (nmat == 2 || act != FLCE_ACT_NONE);
+  if (bad_tensor(x, 16, rows) || bad_tensor(dy, 16, rows) || bad_tensor(dx, 16, false)) return FLCE_ERR_INVALID_ARGUMENT;
+  for (int m = 0; m < nmat; ++m)
+    if (bad_tensor(W[m], 16, true) || bad_tensor(z[m], 16, need_z) || bad_tensor(dW[m], 16, false) ||
+        bad_tensor(db[m], es, false))
+      return FLCE_ERR_INVALID_ARGUMENT;
+  const LayerGeometry g = layer_geometry(N, H, F, dtype, act, nmat);
+  if (workspace_bytes < g.bwd_total) return FLCE_ERR_WORKSPACE_TOO_SMALL;
+  if (bad_tensor(workspace, 16, g.bwd_total > 0)) return FLCE_ERR_INVALID_ARGUMENT;
+  const bool want_db = db[0] || db[1];
+  if (!dx && !dW[0] && !dW[1] && !want_db) return FLCE_OK;
+  char* ws = (char*)workspace;
+  flce::LayerBwd a{};
+  a.x = x; a.dy = dy;
+  for (int m = 0; m < nmat; ++m) {
+    a.W[m] = W[m];
+    a.z[m] = z[m];
+    a.dW[m] = dW[m];
+    a.db[m] = db[m];
+  }
+  a.N = (int)N; a.H = (int)H; a.F = (int)F;
+  a.act = act; a.nmat = nmat;
+  a.dz_is_dy = g.dz_is_dy;
+  a.dz = g.dz_is_dy ? const_cast<void*>(dy) : ws;
+  a.ldz = g.ldz; a.segk = (int)g.segk;
+  a.dbp = want_db ? (float*)(ws + g.off_dbp) : nullptr;
+  a.ldb = g.ldb; a.db_blocks = g.db_blocks; a.db_rows = g.db_rows;
+  a.dx = dx; a.dx_parts = g.dx_parts; a.dx_kc = (int)g.dx_kc;
+  a.dw_parts = g.dw_parts; a.dw_kc = (int)g.dw_kc;
+  a.part = (float*)(ws + g.off_part);
+  (void)hipGetLastError();
+  flce::mark_launch(stream, nullptr);
+  return flce::launch_layer_backward(a, dtype, stream) == hipSuccess ? FLCE_OK : FLCE_ERR_HIP;
+}
+
+// ---------------------------------------------------------------------------
+// Gradient norm and clipping
+// ---------------------------------------------------------------------------
+
+// Workgroups over all launches of one call (each launch has at least one): 8
+// per CU keep enough loads in flight, and the partials stay small enough for
+// every workgroup of the clipping pass to add them up.
+constexpr int64_t kNormBlocks = 8 * kCUs;
+
+// A tensor's chunks of work: whole chunks counted from its first 16-byte boundary.
+int64_t norm_chunks(const void* p, int64_t n, int64_t es) {
+  if (n == 0) return 0;
+  int64_t head = (int64_t)((16 - ((uintptr_t)p & 15)) & 15) / es;
+  if (head > n) head = n;
+  const int64_t c = cdiv(n - head, flce::kNormChunkBytes / es);
+  return c > 0 ? c : 1;
+}
+
+int64_t norm_launches(int64_t count) { return cdiv(count, flce::kNormTensors); }
+
+int64_t dtype_bytes(int dtype) { return dtype == FLCE_F32 ? 4 : 2; }
+
+flce_status check_norm(const void* const* grads, const int64_t* numels, const flce_dtype* dtypes, int64_t count) {
+  if (count < 0 || count > (int64_t(1) << 20)) return FLCE_ERR_INVALID_ARGUMENT;
+  if (count > 0 && (!grads || !numels || !dtypes)) return FLCE_ERR_INVALID_ARGUMENT;
+  for (int64_t i = 0; i < count; ++i) {
+    if (dtypes[i] != FLCE_F32 && dtypes[i] != FLCE_BF16 && dtypes[i] != FLCE_F16) return FLCE_ERR_UNSUPPORTED;
+    if (numels[i] < 0 || numels[i] > (int64_t(1) << 40)) return FLCE_ERR_INVALID_ARGUMENT;
+    if (numels[i] > 0 && (!grads[i] || !aligned(grads[i], dtype_bytes(dtypes[i])))) return FLCE_ERR_INVALID_ARGUMENT;
+  }
+  return FLCE_OK;
+}
+
+// No byte that clipping writes may belong to another tensor, read or written:
+// workgroups of both would race.  (A tensor's out may be its own gradient.)
+flce_status check_disjoint(const void* const* grads, void* const* outs, const int64_t* numels, const flce_dtype* dtypes,
+                           int64_t count) {
+  struct Range {
+    uintptr_t lo, hi;
+    bool written;
+  };
+  std::vector<Range> r;
+  r.reserve(outs ? 2 * count : count);
+  for (int64_t i = 0; i < count; ++i) {
+    if (numels[i] == 0) continue;
+    const uintptr_t bytes = (uintptr_t)(numels[i] * dtype_bytes(dtypes[i]));
+    const uintptr_t in = (uintptr_t)grads[i], out = outs ? (uintptr_t)outs[i] : in;
+    if (outs && (!outs[i] || !aligned(outs[i], dtype_bytes(dtypes[i])))) return FLCE_ERR_INVALID_ARGUMENT;
+    if (out != in) r.push_back({in, in + bytes, false});
+    r.push_back({out, out + bytes, true});
+  }
+  std::sort(r.begin(), r.end(), [](const Range& a, const Range& b) { return a.lo < b.lo; });
+  uintptr_t end = 0, wend = 0;   // furthest end of all ranges so far, and of the written ones
+  for (const Range& v : r) {
+    if (v.lo < (v.written ? end : wend)) return FLCE_ERR_INVALID_ARGUMENT;
+    end = std::max(end, v.hi);
+    if (v.written) wend = std::max(wend, v.hi);
+  }
+  return FLCE_OK;
+}
+
+// Launch table l of a call: tensors [l * kNormTensors, ...).  Returns its chunks.
+int64_t norm_table(flce::NormTable& t, const void* const* grads, void* const* outs, const int64_t* numels,
+                   const flce_dtype* dtypes, int64_t count, int64_t l) {
+  const int64_t i0 = l * flce::kNormTensors;
+  t.count = (int)std::min<int64_t>(flce::kNormTensors, count - i0);
+  t.in_place = 1;
+  int64_t end = 0;
+  for (int k = 0; k < t.count; ++k) {
+    const int64_t i = i0 + k;
+    t.in[k] = grads[i];
+    t.out[k] = outs ? outs[i] : const_cast<void*>(grads[i]);
+    if (t.out[k] != t.in[k] && numels[i] > 0) t.in_place = 0;
+    t.n[k] = numels[i];
+    t.dtype[k] = (uint8_t)dtypes[i];
+    end += norm_chunks(grads[i], numels[i], dtype_bytes(dtypes[i]));
+    t.end[k] = end;
+  }
+  return end;
+}
+
+// norm_out and the scaled gradients.  grads without out and clip = false: the norm alone.
+// given: the norm to scale by.
+flce_status run_grad_norm(const void* const* grads, void* const* outs, const int64_t* numels, const flce_dtype* dtypes,
+                          int64_t count, float max_norm, bool inf_norm, const float* given, bool clip, float* norm_out,
+                          double* part, hipStream_t stream) {
+  const int64_t launches = norm_launches(count);
+  int64_t total = 0;
+  for (int64_t i = 0; i < count; ++i) total += norm_chunks(grads[i], numels[i], dtype_bytes(dtypes[i]));
+  auto blocks_of = [&](int64_t chunks) -> int {   // this launch's share of the workgroups
+    if (total <= kNormBlocks) return (int)std::max<int64_t>(1, chunks);
+    return (int)std::max<int64_t>(1, (int64_t)((double)kNormBlocks * (double)chunks / (double)total));
+  };
+  (void)hipGetLastError();
+  flce::mark_launch(stream, nullptr);
+  flce::NormTable t;
+  int parts = 0;
+  if (!given) {
+    for (int64_t l = 0; l < launches; ++l) {
+      const int blocks = blocks_of(norm_table(t, grads, outs, numels, dtypes, count, l));
+      if (flce::launch_grad_norm(t, inf_norm, part + parts, blocks, stream) != hipSuccess) return FLCE_ERR_HIP;
+      parts += blocks;
+    }
+  }
+  if (!clip || launches == 0) {   // the norm alone
+    t.count = 0;
+    t.in_place = 1;
+    if (!norm_out) return FLCE_OK;
+    return flce::launch_grad_clip(t, inf_norm, part, parts, given, norm_out, max_norm, 1, stream) == hipSuccess
+               ? FLCE_OK : FLCE_ERR_HIP;
+  }
+  for (int64_t l = 0; l < launches; ++l) {
+    const int blocks = blocks_of(norm_table(t, grads, outs, numels, dtypes, count, l));
+    if (flce::launch_grad_clip(t, inf_norm, part, parts, given, l == 0 ? norm_out : nullptr, max_norm, blocks, stream) !=
+        hipSuccess)
+      return FLCE_ERR_HIP;
+  }
+  return FLCE_OK;
+}
+
+size_t norm_bytes(int64_t count) { return align_up((size_t)(kNormBlocks + norm_launches(count)) * sizeof(double)); }
+
+// Host memory for the overlap check is the one thing a call may fail to get.
+flce_status grad_norm_call(const void* const* grads, void* const* outs, const int64_t* numels, const flce_dtype* dtypes,
+                           int64_t count, float max_norm, float norm_type, const float* given, bool clip, float* norm_out,
+                           void* workspace, size_t workspace_bytes, hipStream_t stream) noexcept {
+  const flce_status st = check_norm(grads, numels, dtypes, count);
+  if (st != FLCE_OK) return st;
+  const bool inf_norm = std::isinf(norm_type) && norm_type > 0.f;
+  if (!inf_norm && norm_type != 2.f) return FLCE_ERR_UNSUPPORTED;
+  if (clip && !(max_norm >= 0.f)) return FLCE_ERR_INVALID_ARGUMENT;
+  if (bad_tensor(norm_out, 4, !given) || bad_tensor(given, 4, false)) return FLCE_ERR_INVALID_ARGUMENT;
+  if (!given) {
+    if (workspace_bytes < norm_bytes(count)) return FLCE_ERR_WORKSPACE_TOO_SMALL;
+    if (bad_tensor(workspace, 16, true)) return FLCE_ERR_INVALID_ARGUMENT;
+  }
+  if (clip) {
+    try {
+      const flce_status so = check_disjoint(grads, outs, numels, dtypes, count);
+      if (so != FLCE_OK) return so;
+    } catch (...) {
+      return FLCE_ERR_HIP;
+    }
+  }
+  return run_grad_norm(grads, outs, numels, dtypes, count, max_norm, inf_norm, given, clip, norm_out, (double*)workspace,
+                       stream);
+}
+
+}  // namespace
+
+extern "C" {
+
+flce_status flce_linear_workspace_size(int64_t N, int64_t H, int64_t F, flce_dtype dtype, flce_activation activation,
+                                       size_t* fwd_bytes, size_t* bwd_bytes) {
+  const flce_status st = check_layer(N, H, F, dtype, activation, 1);
+  if (st != FLCE_OK) return st;
+  const LayerGeometry g = layer_geometry(N, H, F, dtype, activation, 1);
+  if (fwd_bytes) *fwd_bytes = g.fwd_total;
+  if (bwd_bytes) *bwd_bytes = g.bwd_total;
+  return FLCE_OK;
+}
+
+flce_status flce_linear_forward(const void* x, const void* W, const void* b, const void* residual, int64_t N, int64_t H,
+                                int64_t F, flce_dtype dtype, flce_activation activation, void* y, void* z,
+                                void* workspace, size_t workspace_bytes, hipStream_t stream) {
+  return layer_forward(x, {W, nullptr}, {b, nullptr}, residual, N, H, F, dtype, activation, 1, y, {z, nullptr},
+                       workspace, workspace_bytes, stream);
+}
+
+flce_status flce_linear_backward(const void* x, const void* W, const void* z, const void* dy, int64_t N, int64_t H,
+                                 int64_t F, flce_dtype dtype, flce_activation activation, void* dx, void* dW, void* db,
+                                 void* workspace, size_t workspace_bytes, hipStream_t stream) {
+  return layer_backward(x, {W, nullptr}, {z, nullptr}, dy, N, H, F, dtype, activation, 1, dx, {dW, nullptr},
+                        {db, nullptr}, workspace, workspace_bytes, stream);
+}
+
+flce_status flce_glu_workspace_size(int64_t N, int64_t H, int64_t F, flce_dtype dtype, size_t* fwd_bytes,
+                                    size_t* bwd_bytes) {
+  const flce_status st = check_layer(N, H, F, dtype, FLCE_ACT_NONE, 2);
+  if (st != FLCE_OK) return st;
+  const LayerGeometry g = layer_geometry(N, H, F, dtype, FLCE_ACT_NONE, 2);
+  if (fwd_bytes) *fwd_bytes = g.fwd_total;
+  if (bwd_bytes) *bwd_bytes = g.bwd_total;
+  return FLCE_OK;
+}
+
+flce_status flce_glu_forward(const void* x, const void* Wg, const void* Wu, const void* bg, const void* bu, int64_t N,
+                             int64_t H, int64_t F, flce_dtype dtype, flce_activation activation, void* h, void* g,
+                             void* u, void* workspace, size_t workspace_bytes, hipStream_t stream) {
+  return layer_forward(x, {Wg, Wu}, {bg, bu}, nullptr, N, H, F, dtype, activation, 2, h, {g, u}, workspace,
+                       workspace_bytes, stream);
+}
+
+flce_status flce_glu_backward(const void* x, const void* Wg, const void* Wu, const void* g, const void* u,
+                              const void* dh, int64_t N, int64_t H, int64_t F, flce_dtype dtype,
+                              flce_activation activation, void* dx, void* dWg, void* dWu, void* dbg, void* dbu,
+                              void* workspace, size_t workspace_bytes, hipStream_t stream) {
+  return layer_backward(x, {Wg, Wu}, {g, u}, dh, N, H, F, dtype, activation, 2, dx, {dWg, dWu}, {dbg, dbu}, workspace,
+                        workspace_bytes, stream);
+}
+
+flce_status flce_grad_norm_workspace_size(int64_t count, size_t* bytes) {
+  if (count < 0 || count > (int64_t(1) << 20)) return FLCE_ERR_INVALID_ARGUMENT;
+  if (bytes) *bytes = norm_bytes(count);
+  return FLCE_OK;
+}
+
+flce_status flce_grad_norm(const void* const* grads, const int64_t* numels, const flce_dtype* dtypes, int64_t count,
+                           float norm_type, float* norm, void* workspace, size_t workspace_bytes, hipStream_t stream) {
+  return grad_norm_call(grads, nullptr, numels, dtypes, count, 0.f, norm_type, nullptr, false, norm, workspace,
+                        workspace_bytes, stream);
+}
+
+flce_status flce_clip_grad_norm(const void* const* grads, void* const* outs, const int64_t* numels,
+                                const flce_dtype* dtypes, int64_t count, float max_norm, float norm_type, float* norm,
+                                void* workspace, size_t workspace_bytes, hipStream_t stream) {
+  return grad_norm_call(grads, outs, numels, dtypes, count, max_norm, norm_type, nullptr, true, norm, workspace,
+                        workspace_bytes, stream);
+}
+
+flce_status flce_clip_grads_with_norm(const void* const* grads, void* const* outs, const int64_t* numels,
+                                      const flce_dtype* dtypes, int64_t count, float max_norm, const float* norm,
+                                      hipStream_t stream) {
+  if (!norm) return FLCE_ERR_INVALID_ARGUMENT;
+  return grad_norm_call(grads, outs, numels, dtypes, count, max_norm, 2.f, norm, true, nullptr, nullptr, 0, stream);
 }
 
 }  // extern "C"

@@ -237,6 +237,14 @@ __device__ __forceinline__ float acc_read1(const f32x4& blk) {
 // (correctness-oriented; no fine-grained interleave)
 // ---------------------------------------------------------------------------
 
+// Tile row t of an operand copied with permuted columns holds global row
+// m0 + tile_col_perm(t): within each half of 128 rows, row 16 j + c (the
+// MFMA output column c of block j) holds row 8 c + j, so a lane's values in
+// the eight blocks of one output row are eight consecutive global rows.
+__device__ __forceinline__ constexpr int tile_col_perm(int t) {
+  return (t & 0x80) | ((t & 0x0F) << 3) | ((t & 0x70) >> 4);
+}
+
 // One stage of one operand: 256 rows x 32 fp32, 8 x 16 bytes per thread,
 // stored to LDS rows of kRowBytes with K contiguous.
 template <class T, bool KCONTIG> struct Stager;
@@ -248,13 +256,14 @@ template <> struct Stager<float, true> {
   uint32_t off[8];
   const float* base;
   int kc_elem;
-  __device__ __forceinline__ void init(const Opnd<float>& o, int m0, int tid) {
+  // perm: tile rows hold permuted global rows (tile_col_perm).
+  __device__ __forceinline__ void init(const Opnd<float>& o, int m0, int tid, bool perm = false) {
     const int kc = tid & 7, rr = tid >> 3;
     kc_elem = kc * 4;
     base = o.p + (int64_t)m0 * o.ld;
 #pragma unroll
     for (int q = 0; q < 8; ++q) {
-      const int row = rr + 32 * q;
+      const int row = perm ? tile_col_perm(rr + 32 * q) : rr + 32 * q;
       off[q] = (m0 + row < o.mext) ? (uint32_t)(((int64_t)row * o.ld + kc_elem) * 4) : kOOB;
     }
   }
@@ -340,17 +349,14 @@ __device__ __forceinline__ void mma_stage_f32(Acc& acc, const lds_t* bA, const l
   }
 }
 
-// fp32 tile mainloop: two padded LDS buffers per operand, register staging.
-// Ends with a barrier; the accumulators need acc_drain() before they are read.
-template <bool AK, bool BK>
-__device__ __forceinline__ void gemm_tile_f32(Acc& acc, const Opnd<float>& A, int m0, const Opnd<float>& B, int n0,
-                                              int K, const Lds& L, int tid) {
+// fp32 tile mainloop: two padded LDS buffers per operand, register staging by
+// the operands' initialised stagers.  Ends with a barrier; the accumulators
+// need acc_drain() before they are read.
+template <class SA, class SB>
+__device__ __forceinline__ void gemm_tile_f32_run(Acc& acc, const Opnd<float>& A, SA& sa, const Opnd<float>& B, SB& sb,
+                                                  int K, const Lds& L, int tid) {
   constexpr int kBK = 32;
   const int lane = tid & 63, wave = tid >> 6, wm = wave >> 1, wn = wave & 1;
-  Stager<float, AK> sa;
-  Stager<float, BK> sb;
-  sa.init(A, m0, tid);
-  sb.init(B, n0, tid);
   const int KT = (K + kBK - 1) / kBK;
   sa.load(A, 0);
   sb.load(B, 0);
@@ -372,6 +378,16 @@ __device__ __forceinline__ void gemm_tile_f32(Acc& acc, const Opnd<float>& A, in
     }
     __syncthreads();
   }
+}
+
+template <bool AK, bool BK>
+__device__ __forceinline__ void gemm_tile_f32(Acc& acc, const Opnd<float>& A, int m0, const Opnd<float>& B, int n0,
+                                              int K, const Lds& L, int tid) {
+  Stager<float, AK> sa;
+  Stager<float, BK> sb;
+  sa.init(A, m0, tid);
+  sb.init(B, n0, tid);
+  gemm_tile_f32_run(acc, A, sa, B, sb, K, L, tid);
 }
 
 // ---------------------------------------------------------------------------
@@ -432,14 +448,6 @@ template <bool KCONTIG> struct Dma;
 // of four 16 rows apart), so it can store them as one 16-byte piece.
 __device__ __forceinline__ constexpr int tile_row_perm(int t) {
   return (t & 0xE3) | ((t & 0x0C) << 1) | ((t & 0x10) >> 2);
-}
-
-// Tile row t of an operand copied with permuted columns holds global row
-// m0 + tile_col_perm(t): within each half of 128 rows, row 16 j + c (the
-// MFMA output column c of block j) holds row 8 c + j, so a lane's values in
-// the eight blocks of one output row are eight consecutive global rows.
-__device__ __forceinline__ constexpr int tile_col_perm(int t) {
-  return (t & 0x80) | ((t & 0x0F) << 3) | ((t & 0x70) >> 4);
 }
 
 // K-contiguous: instruction idx fills rows 8 idx .. 8 idx + 7; lane l takes
@@ -609,17 +617,18 @@ template <int RA, int RB, int PAR> struct StagePlan {
 // (no previous MFMAs; blocks 0..3 start from zero); SECOND: blocks 4..7
 // start from zero.  Every instruction slot ends in a scheduling barrier,
 // which pins this order.
-template <int PAR, int BUF, bool FIRST, bool SECOND, bool AK, bool BK, int VMW, bool TAIL, bool BFIRST, class E>
+template <int PAR, int BUF, bool FIRST, bool SECOND, bool AK, bool BK, int VMW, bool TAIL, bool BFIRST, class E,
+          class DA, class DB>
 __device__ __forceinline__ void stage_bf16(Acc& acc, Frag& P, Frag& C, const FragAddr<AK>& fa,
                                            const FragAddr<BK>& fb, const Lds& L, int lane, const Opnd<E>& A,
-                                           const Opnd<E>& B, const Dma<AK>& da, const Dma<BK>& db,
+                                           const Opnd<E>& B, const DA& da, const DB& db,
                                            int k_copy) {
   constexpr bool F16 = IsF16<E>::value;
   typedef StagePlan<FragAddr<AK>::kReads, FragAddr<BK>::kReads, PAR> Plan;
   const lds_t* bA = L.a[BUF];
   const lds_t* bB = L.b[BUF];
-  const __amdgpu_buffer_rsrc_t rsa = da.rsrc(k_copy);
-  const __amdgpu_buffer_rsrc_t rsb = db.rsrc(k_copy);
+  const auto rsa = da.rsrc(k_copy);
+  const auto rsb = db.rsrc(k_copy);
   const int kla = A.kext - k_copy, klb = B.kext - k_copy;
   auto copy = [&](int q) {
     if (BFIRST ? q >= 8 : q < 8) da.template issue<TAIL>(rsa, kla, L.a[BUF ^ 1], lane, q & 7);
@@ -662,15 +671,20 @@ __device__ __forceinline__ void stage_last_half(Acc& acc, const Frag& P) {
 // last barrier follows its last fragment read and the completion of its
 // copies).  perm_a: A's tile rows hold permuted rows (tile_row_perm); perm_b:
 // B's hold permuted columns (tile_col_perm).  A permuted operand must be
-// K-contiguous.
-template <bool AK, bool BK> struct TileCopy {
-  Dma<AK> da;
-  Dma<BK> db;
+// K-contiguous.  DA, DB: the operands' copy classes; begin() is start() after
+// the caller has initialised da and db itself.
+template <bool AK, bool BK, class DA = Dma<AK>, class DB = Dma<BK>> struct TileCopy {
+  DA da;
+  DB db;
   template <class E>
   __device__ __forceinline__ void start(const Opnd<E>& A, int m0, const Opnd<E>& B, int n0,
                                         const Lds& L, int tid, bool perm_a = false, bool perm_b = false) {
     da.init(A, m0, tid, perm_a ? 1 : 0);
     db.init(B, n0, tid, perm_b ? 2 : 0);
+    begin(A, B, L, tid);
+  }
+  template <class E>
+  __device__ __forceinline__ void begin(const Opnd<E>& A, const Opnd<E>& B, const Lds& L, int tid) {
     const int lane = tid & 63;
     // Copies past K read zeros (out-of-range offsets), so the stage bodies
     // need no branches.
@@ -695,13 +709,13 @@ template <bool AK, bool BK> struct TileCopy {
 // depends on the kernel, from same-box A/Bs at the Llama-3-sized head: B first
 // makes the forward 3.8% faster and the recompute slower; dW and dx are
 // indifferent or slower.
-template <bool AK, bool BK, int EXTRA = 0, bool BFIRST = false, class E>
+template <bool AK, bool BK, int EXTRA = 0, bool BFIRST = false, class E, class DA = Dma<AK>, class DB = Dma<BK>>
 __device__ __forceinline__ void gemm_tile_bf16_run(Acc& acc, const Opnd<E>& A, const Opnd<E>& B, int K,
-                                                   const Lds& L, int tid, const TileCopy<AK, BK>& tc) {
+                                                   const Lds& L, int tid, const TileCopy<AK, BK, DA, DB>& tc) {
   static_assert(EXTRA >= 0 && EXTRA <= 63, "vmcnt holds at most 63");
   const int lane = tid & 63, wave = tid >> 6, wm = wave >> 1, wn = wave & 1;
-  const Dma<AK>& da = tc.da;
-  const Dma<BK>& db = tc.db;
+  const DA& da = tc.da;
+  const DB& db = tc.db;
   FragAddr<AK> fa;
   FragAddr<BK> fb;
   fa.init(wm * 128, lane);

@@ -121,4 +121,69 @@ hipError_t launch_finalize(const FwdLaunch& a, hipStream_t st);
 // phases whose partials follow head's; then the merge and the final loss.
 hipError_t launch_forward_keep(const FwdLaunch& head, const FwdLaunch& rest, int dtype, hipStream_t st);
 
+// ---------------------------------------------------------------------------
+// Feed-forward operators: the linear layer (nmat = 1) and the gated product
+// (nmat = 2, weights 0 = gate, 1 = up).
+// ---------------------------------------------------------------------------
+
+enum Activation { kActNone = 0, kActRelu = 1, kActGelu = 2, kActGeluTanh = 3, kActSilu = 4, kActSigmoid = 5 };
+
+// Forward by streaming the weights past few tokens: at most this many.
+constexpr int kSkinnyTokens = 64;
+
+struct LayerFwd {
+  const void* x; const void* W[2]; const void* b[2];
+  const void* residual;   // [N][F] added to the output, or null; may be y itself
+  void* y;                // [N][F]
+  void* z[2];             // [N][F] pre-activations kept for the backward (linear: z[0]), or null
+  int N, H, F, act, nmat;
+  int TM, TN;             // token tiles of 256, feature tiles of 256 (gated: 128 of each weight)
+  int parts, kc;          // K split: parts of kc columns of x each
+  float* part;            // parts > 1: [parts][N][ldp] fp32 sums; gated: u's at column ldp / 2
+  int64_t ldp;            // nmat * F rounded up to 8
+};
+
+struct LayerBwd {
+  const void* x; const void* W[2];
+  const void* z[2];       // kept pre-activations (linear with kActNone: null)
+  const void* dy;         // [N][F]
+  int N, H, F, act, nmat;
+  void* dz;               // [N][ldz]: dz, zero from column F on; gated: dg, then du from column segk
+  int64_t ldz;
+  int segk;               // K (columns of dz) where weight 1 starts; past every K when nmat == 1
+  bool dz_is_dy;          // dz is dy itself (no activation, F % 8 == 0): only its column sums are needed
+  float* dbp; int64_t ldb;   // [db_blocks][ldb] fp32 partial column sums; null if no db
+  int db_blocks, db_rows;    // token rows per block
+  void* db[2];
+  void* dx; int dx_parts, dx_kc;
+  void* dW[2]; int dw_parts, dw_kc;
+  float* part;            // split products: dx [parts][N][H], then dW [parts][mats written][F][H]
+};
+
+hipError_t launch_layer_forward(const LayerFwd& a, int dtype, hipStream_t st);
+hipError_t launch_layer_backward(const LayerBwd& a, int dtype, hipStream_t st);
+
+// ---------------------------------------------------------------------------
+// Gradient norm and clipping
+// ---------------------------------------------------------------------------
+
+constexpr int kNormTensors = 96;             // tensors of one launch: their table fits in the kernel arguments
+constexpr int64_t kNormChunkBytes = 32768;   // gradient bytes of one chunk of work
+
+struct NormTable {
+  const void* in[kNormTensors];
+  void* out[kNormTensors];          // clipping: where the scaled gradients go (in[] itself when in place)
+  int64_t n[kNormTensors];          // elements
+  int64_t end[kNormTensors];        // chunks of this tensor and the ones before it
+  uint8_t dtype[kNormTensors];
+  int count;
+  int in_place;                     // out is in for every tensor
+};
+
+// parts partial sums of squares (or maxima) of the table's tensors, one per workgroup.
+hipError_t launch_grad_norm(const NormTable& t, bool inf_norm, double* part, int parts, hipStream_t st);
+// The norm of `parts` partials, or *given, to norm_out (if set), and the table's tensors scaled by it.
+hipError_t launch_grad_clip(const NormTable& t, bool inf_norm, const double* part, int parts, const float* given,
+                            float* norm_out, float max_norm, int blocks, hipStream_t st);
+
 }  // namespace flce

@@ -14,6 +14,7 @@ from __future__ import annotations
 from typing import Optional, Tuple
 
 import torch
+from torch.autograd.function import once_differentiable
 
 from . import _lib
 
@@ -412,6 +413,278 @@ def flce_shard_backward(x: torch.Tensor, W_shard: torch.Tensor, b_shard: Optiona
     return dx_partial, dW, db
 
 
+def _activation_code(activation: str) -> int:
+    if activation not in _lib.ACTIVATIONS:
+        raise ValueError(f"activation must be one of {tuple(_lib.ACTIVATIONS)}")
+    return _lib.ACTIVATIONS[activation]
+
+
+def _dense(t: Optional[torch.Tensor]) -> Optional[torch.Tensor]:
+    """t as the library reads it: contiguous from a 16-byte boundary (a copy if it is not)."""
+    if t is None:
+        return None
+    t = t.contiguous()
+    return t if t.data_ptr() % 16 == 0 else t.clone()
+
+
+def _prep_layer(x, weights, rows, bias=()):
+    """The operands of a feed-forward call, checked and dense, with H padded to
+    a multiple of 8: x [N, H], weights [F, H], rows [N, F] (or None), bias [F] (or None)."""
+    if x.dim() != 2 or any(w.dim() != 2 for w in weights):
+        raise ValueError("x must be [N, H] and the weights [F, H]")
+    if not x.is_cuda:
+        raise ValueError("tensors must live on a GPU")
+    N, H = x.shape
+    F = weights[0].shape[0]
+    for w in weights:
+        if tuple(w.shape) != (F, H):
+            raise ValueError("x and the weights disagree on their sizes")
+    for t in rows:
+        if t is not None and tuple(t.shape) != (N, F):
+            raise ValueError(f"expected a tensor of shape {(N, F)}, not {tuple(t.shape)}")
+    for b in bias:
+        if b is not None and tuple(b.shape) != (F,):
+            raise ValueError("a bias must be [F]")
+    for t in (*weights, *rows, *bias):
+        if t is not None and t.dtype != x.dtype:
+            raise TypeError("all tensors must share one dtype")
+        if t is not None and t.device != x.device:
+            raise ValueError("all tensors must be on one device")
+    if H < 1 or F < 1:
+        raise ValueError("H and F must be at least 1")
+    _dtype_code(x)
+    return ([_pad_hidden(_dense(t)) for t in (x, *weights)], [_dense(t) for t in rows],
+            [b.contiguous() if b is not None else None for b in bias])
+
+
+def _workspace(workspace: Optional[torch.Tensor], nbytes: int, dev) -> Optional[torch.Tensor]:
+    if nbytes == 0:
+        return None
+    if workspace is None or workspace.numel() < nbytes:
+        return torch.empty(nbytes, dtype=torch.uint8, device=dev)
+    if workspace.dtype != torch.uint8 or workspace.device != dev or not workspace.is_contiguous():
+        raise ValueError(f"workspace must be a contiguous uint8 tensor on {dev}")
+    return workspace
+
+
+def _nbytes(t: Optional[torch.Tensor]) -> int:
+    return 0 if t is None else t.numel()
+
+
+def _layer_grads(x, H0, H, F, weights, need_dx, need_dW):
+    """(dx, [dW]) to fill, [.., H] wide."""
+    dx = torch.empty(x.shape[0], H, dtype=x.dtype, device=x.device) if need_dx else None
+    return dx, [torch.empty(F, H, dtype=x.dtype, device=x.device) if need else None for need in need_dW]
+
+
+def _narrow(t: Optional[torch.Tensor], H0: int) -> Optional[torch.Tensor]:
+    return t if t is None or t.shape[1] == H0 else t[:, :H0].contiguous()
+
+
+def flce_linear_workspace_size(N: int, H: int, F: int, dtype: torch.dtype,
+                               activation: str = "none") -> Tuple[int, int]:
+    """(forward bytes, backward bytes) of flce_linear_forward and flce_linear_backward."""
+    return _lib.flce_linear_workspace_size(N, H, F, _DTYPES[dtype], _activation_code(activation))
+
+
+def flce_linear_forward(x: torch.Tensor, W: torch.Tensor, b: Optional[torch.Tensor] = None,
+                        residual: Optional[torch.Tensor] = None, activation: str = "none", keep: bool = False,
+                        workspace: Optional[torch.Tensor] = None, out: Optional[torch.Tensor] = None):
+    """act(x W^T + b) + residual.  Returns (y, z): z the pre-activations that
+    flce_linear_backward takes, with keep and an activation, else None.
+    out: the tensor to write y to (it may be residual)."""
+    act = _activation_code(activation)
+    N, F = x.shape[0], W.shape[0]
+    (x, W), (residual_, out_), (b,) = _prep_layer(x, (W,), (residual, out), (b,))
+    if out is not None and (out_ is not out or (residual_ is not residual and residual is out)):
+        raise ValueError("out must be contiguous from a 16-byte boundary")
+    dt, dev, H = _dtype_code(x), x.device, x.shape[1]
+    y = out if out is not None else torch.empty(N, F, dtype=x.dtype, device=dev)
+    z = torch.empty(N, F, dtype=x.dtype, device=dev) if keep and activation != "none" else None
+    fwd_bytes, _ = _lib.flce_linear_workspace_size(N, H, F, dt, act)
+    workspace = _workspace(workspace, fwd_bytes, dev)
+    with torch.cuda.device(dev):
+        stream = torch.cuda.current_stream(dev).cuda_stream
+        _lib.flce_linear_forward(x.data_ptr(), W.data_ptr(), _ptr(b), _ptr(residual_), N, H, F, dt, act, y.data_ptr(),
+                                 _ptr(z), _ptr(workspace), _nbytes(workspace), stream)
+    return y, z
+
+
+def flce_linear_backward(x: torch.Tensor, W: torch.Tensor, dy: torch.Tensor, z: Optional[torch.Tensor] = None,
+                         activation: str = "none", need_dx: bool = True, need_dW: bool = True, need_db: bool = False,
+                         workspace: Optional[torch.Tensor] = None):
+    """Returns (dx, dW, db) in the input dtype (None where not requested); z as
+    flce_linear_forward kept it.  The residual's gradient is dy."""
+    act = _activation_code(activation)
+    if activation == "none":
+        z = None
+    elif z is None:
+        raise ValueError("z is what flce_linear_forward returned with keep=True")
+    H0, N, F = x.shape[-1], x.shape[0], W.shape[0]
+    (x, W), (dy, z), _ = _prep_layer(x, (W,), (dy, z))
+    dt, dev, H = _dtype_code(x), x.device, x.shape[1]
+    dx, (dW,) = _layer_grads(x, H0, H, F, (W,), need_dx, (need_dW,))
+    db = torch.empty(F, dtype=x.dtype, device=dev) if need_db else None
+    _, bwd_bytes = _lib.flce_linear_workspace_size(N, H, F, dt, act)
+    workspace = _workspace(workspace, bwd_bytes, dev)
+    with torch.cuda.device(dev):
+        stream = torch.cuda.current_stream(dev).cuda_stream
+        _lib.flce_linear_backward(x.data_ptr(), W.data_ptr(), _ptr(z), dy.data_ptr(), N, H, F, dt, act, _ptr(dx),
+                                  _ptr(dW), _ptr(db), _ptr(workspace), _nbytes(workspace), stream)
+    return _narrow(dx, H0), _narrow(dW, H0), db
+
+
+def flce_glu_workspace_size(N: int, H: int, F: int, dtype: torch.dtype) -> Tuple[int, int]:
+    """(forward bytes, backward bytes) of flce_glu_forward and flce_glu_backward."""
+    return _lib.flce_glu_workspace_size(N, H, F, _DTYPES[dtype])
+
+
+def flce_glu_forward(x: torch.Tensor, Wg: torch.Tensor, Wu: torch.Tensor, bg: Optional[torch.Tensor] = None,
+                     bu: Optional[torch.Tensor] = None, activation: str = "silu", keep: bool = False,
+                     workspace: Optional[torch.Tensor] = None):
+    """h = act(x Wg^T + bg) * (x Wu^T + bu).  Returns (h, g, u): the two
+    projections that flce_glu_backward takes, with keep, else None."""
+    act = _activation_code(activation)
+    N, F = x.shape[0], Wg.shape[0]
+    (x, Wg, Wu), _, (bg, bu) = _prep_layer(x, (Wg, Wu), (), (bg, bu))
+    dt, dev, H = _dtype_code(x), x.device, x.shape[1]
+    h = torch.empty(N, F, dtype=x.dtype, device=dev)
+    g, u = (torch.empty_like(h), torch.empty_like(h)) if keep else (None, None)
+    fwd_bytes, _ = _lib.flce_glu_workspace_size(N, H, F, dt)
+    workspace = _workspace(workspace, fwd_bytes, dev)
+    with torch.cuda.device(dev):
+        stream = torch.cuda.current_stream(dev).cuda_stream
+        _lib.flce_glu_forward(x.data_ptr(), Wg.data_ptr(), Wu.data_ptr(), _ptr(bg), _ptr(bu), N, H, F, dt, act,
+                              h.data_ptr(), _ptr(g), _ptr(u), _ptr(workspace), _nbytes(workspace), stream)
+    return h, g, u
+
+
+def flce_glu_backward(x: torch.Tensor, Wg: torch.Tensor, Wu: torch.Tensor, g: torch.Tensor, u: torch.Tensor,
+                      dh: torch.Tensor, activation: str = "silu", need_dx: bool = True, need_dWg: bool = True,
+                      need_dWu: bool = True, need_db: bool = False, workspace: Optional[torch.Tensor] = None):
+    """Returns (dx, dWg, dWu, dbg, dbu) in the input dtype (None where not
+    requested); g and u as flce_glu_forward kept them."""
+    act = _activation_code(activation)
+    if g is None or u is None:
+        raise ValueError("g and u are what flce_glu_forward returned with keep=True")
+    H0, N, F = x.shape[-1], x.shape[0], Wg.shape[0]
+    (x, Wg, Wu), (g, u, dh), _ = _prep_layer(x, (Wg, Wu), (g, u, dh))
+    dt, dev, H = _dtype_code(x), x.device, x.shape[1]
+    dx, (dWg, dWu) = _layer_grads(x, H0, H, F, (Wg, Wu), need_dx, (need_dWg, need_dWu))
+    dbg, dbu = ((torch.empty(F, dtype=x.dtype, device=dev), torch.empty(F, dtype=x.dtype, device=dev)) if need_db
+                else (None, None))
+    _, bwd_bytes = _lib.flce_glu_workspace_size(N, H, F, dt)
+    workspace = _workspace(workspace, bwd_bytes, dev)
+    with torch.cuda.device(dev):
+        stream = torch.cuda.current_stream(dev).cuda_stream
+        _lib.flce_glu_backward(x.data_ptr(), Wg.data_ptr(), Wu.data_ptr(), g.data_ptr(), u.data_ptr(), dh.data_ptr(),
+                               N, H, F, dt, act, _ptr(dx), _ptr(dWg), _ptr(dWu), _ptr(dbg), _ptr(dbu),
+                               _ptr(workspace), _nbytes(workspace), stream)
+    return _narrow(dx, H0), _narrow(dWg, H0), _narrow(dWu, H0), dbg, dbu
+
+
+def _is_dense(t: torch.Tensor) -> bool:
+    """Whether t's elements fill one stretch of memory, in any order of its dimensions."""
+    if t.is_contiguous():
+        return True
+    expected = 1
+    for stride, size in sorted((st, sz) for st, sz in zip(t.stride(), t.shape) if sz != 1):
+        if stride != expected:
+            return False
+        expected *= size
+    return True
+
+
+def _prep_grads(grads, out):
+    grads = list(grads)
+    if not grads:
+        raise ValueError("there are no gradients")
+    dev = grads[0].device
+    if not grads[0].is_cuda:
+        raise ValueError("tensors must live on a GPU")
+    for g in grads:
+        if g.device != dev:
+            raise ValueError("all gradients must be on one device")
+        _dtype_code(g)
+        if g.layout != torch.strided:
+            raise ValueError("gradients must be dense tensors")
+    if out is not None:
+        out = list(out)
+        if len(out) != len(grads):
+            raise ValueError("out must have one tensor per gradient")
+        for g, o in zip(grads, out):
+            if o.dtype != g.dtype or o.shape != g.shape or o.device != dev:
+                raise ValueError("each out tensor must have its gradient's shape, dtype and device")
+    return grads, out, dev
+
+
+def _grad_arrays(grads):
+    return (_lib.pointer_array([g.data_ptr() for g in grads]), _lib.size_array([g.numel() for g in grads]),
+            _lib.dtype_array([_DTYPES[g.dtype] for g in grads]), len(grads))
+
+
+def flce_grad_norm(grads, norm_type: float = 2.0) -> torch.Tensor:
+    """The norm (2 or inf) over every element of every tensor, float32 [1]."""
+    grads, _, dev = _prep_grads(grads, None)
+    grads = [g if _is_dense(g) else g.contiguous() for g in grads]
+    norm = torch.empty(1, dtype=torch.float32, device=dev)
+    nbytes = _lib.flce_grad_norm_workspace_size(len(grads))
+    workspace = torch.empty(nbytes, dtype=torch.uint8, device=dev)
+    with torch.cuda.device(dev):
+        stream = torch.cuda.current_stream(dev).cuda_stream
+        _lib.flce_grad_norm(*_grad_arrays(grads), float(norm_type), norm.data_ptr(), workspace.data_ptr(), nbytes,
+                            stream)
+    return norm
+
+
+def flce_clip_grad_norm(grads, max_norm: float, norm_type: float = 2.0, out=None) -> torch.Tensor:
+    """Scales the gradients by min(1, max_norm / (norm + 1e-6)), in place or
+    into the out tensors; returns the norm before, float32 [1]."""
+    return _clip(grads, max_norm, norm_type, None, out)
+
+
+def flce_clip_grads_with_norm(grads, max_norm: float, norm: torch.Tensor, out=None) -> None:
+    """flce_clip_grad_norm by a norm the caller has (float32, one element)."""
+    if norm.dtype != torch.float32 or norm.numel() != 1:
+        raise ValueError("norm must be one float32 value")
+    _clip(grads, max_norm, 2.0, norm, out)
+
+
+def _clip(grads, max_norm, norm_type, given, out):
+    grads, out, dev = _prep_grads(grads, out)
+    if given is not None and given.device != dev:
+        raise ValueError("norm and the gradients must be on one device")
+    # A gradient whose elements do not fill one stretch of memory goes through
+    # a dense copy, as does one whose out tensor orders its elements otherwise.
+    dst = grads if out is None else out
+    for d in dst:
+        if any(st == 0 and sz > 1 for st, sz in zip(d.stride(), d.shape)):
+            raise ValueError("a tensor that repeats its elements cannot be scaled")
+    src, tmp = [], []
+    for g, d in zip(grads, dst):
+        plain = _is_dense(g) and _is_dense(d) and (g.stride() == d.stride() or (g.is_contiguous() and d.is_contiguous()))
+        src.append(g if plain else g.contiguous())
+        tmp.append(d if plain else torch.empty(g.shape, dtype=g.dtype, device=dev))
+    arrays = _grad_arrays(src)
+    outs = None if out is None and all(a is b for a, b in zip(tmp, dst)) else _lib.pointer_array(
+        [t.data_ptr() for t in tmp])
+    with torch.cuda.device(dev):
+        stream = torch.cuda.current_stream(dev).cuda_stream
+        if given is not None:
+            _lib.flce_clip_grads_with_norm(arrays[0], outs, *arrays[1:], float(max_norm), given.data_ptr(), stream)
+            norm = None
+        else:
+            norm = torch.empty(1, dtype=torch.float32, device=dev)
+            nbytes = _lib.flce_grad_norm_workspace_size(len(grads))
+            workspace = torch.empty(nbytes, dtype=torch.uint8, device=dev)
+            _lib.flce_clip_grad_norm(arrays[0], outs, *arrays[1:], float(max_norm), float(norm_type),
+                                     norm.data_ptr(), workspace.data_ptr(), nbytes, stream)
+    for t, d in zip(tmp, dst):
+        if t is not d:
+            d.copy_(t)
+    return norm
+
+
 class FusedLinearCrossEntropyFunction(torch.autograd.Function):
     """loss = FLCE(x, target, weight, bias); saves only lse and the count."""
 
@@ -473,3 +746,90 @@ class FusedLinearCrossEntropyLoss(torch.nn.Module):
         return fused_linear_cross_entropy_loss(x.reshape(-1, x.shape[-1]), target.reshape(-1), weight, bias,
                                                self.ignore_index, self.label_smoothing, self.z_loss_scale,
                                                self.reduction, self.logit_scale, self.keep_first_slab)
+
+
+class FusedLinearFunction(torch.autograd.Function):
+    """y = act(x weight^T + bias) + residual; keeps the pre-activations if there is an activation."""
+
+    @staticmethod
+    def forward(ctx, x, weight, bias=None, residual=None, activation="none"):
+        y, z = flce_linear_forward(x, weight, bias, residual, activation, keep=any(ctx.needs_input_grad[:3]))
+        ctx.save_for_backward(x, weight, z)
+        ctx.activation = activation
+        return y
+
+    @staticmethod
+    @once_differentiable
+    def backward(ctx, dy):
+        x, weight, z = ctx.saved_tensors
+        need = ctx.needs_input_grad
+        dx = dW = db = None
+        if any(need[:3]):
+            dx, dW, db = flce_linear_backward(x, weight, dy, z, ctx.activation, need[0], need[1], need[2])
+        return dx, dW, db, dy if need[3] else None, None
+
+
+class FusedGLUFunction(torch.autograd.Function):
+    """h = act(x w_gate^T + b_gate) * (x w_up^T + b_up); keeps both projections."""
+
+    @staticmethod
+    def forward(ctx, x, w_gate, w_up, b_gate=None, b_up=None, activation="silu"):
+        h, g, u = flce_glu_forward(x, w_gate, w_up, b_gate, b_up, activation, keep=any(ctx.needs_input_grad[:5]))
+        ctx.save_for_backward(x, w_gate, w_up, g, u)
+        ctx.activation = activation
+        return h
+
+    @staticmethod
+    @once_differentiable
+    def backward(ctx, dh):
+        x, w_gate, w_up, g, u = ctx.saved_tensors
+        need = ctx.needs_input_grad
+        dx, dWg, dWu, dbg, dbu = flce_glu_backward(x, w_gate, w_up, g, u, dh, ctx.activation, need[0], need[1], need[2],
+                                                   need[3] or need[4])
+        return dx, dWg, dWu, dbg if need[3] else None, dbu if need[4] else None, None
+
+
+def fused_linear(x, weight, bias=None, residual=None, activation="none"):
+    """act(x weight^T + bias) + residual for x [..., H], residual [..., F]; differentiable."""
+    lead, F = x.shape[:-1], weight.shape[0]
+    if residual is not None:
+        if residual.shape != (*lead, F):
+            raise ValueError(f"residual must be {(*lead, F)}")
+        residual = residual.reshape(-1, F)
+    return FusedLinearFunction.apply(x.reshape(-1, x.shape[-1]), weight, bias, residual, activation).reshape(*lead, F)
+
+
+def fused_glu(x, w_gate, w_up, b_gate=None, b_up=None, activation="silu"):
+    """act(x w_gate^T + b_gate) * (x w_up^T + b_up) for x [..., H]; differentiable."""
+    return FusedGLUFunction.apply(x.reshape(-1, x.shape[-1]), w_gate, w_up, b_gate, b_up,
+                                  activation).reshape(*x.shape[:-1], w_gate.shape[0])
+
+
+class GatedFeedForward(torch.nn.Module):
+    """A gated feed-forward block: down(act(gate(x)) * up(x)) + residual, two fused calls."""
+
+    def __init__(self, hidden: int, intermediate: int, activation: str = "silu", bias: bool = False, device=None,
+                 dtype=None):
+        super().__init__()
+        _activation_code(activation)
+        kw = dict(bias=bias, device=device, dtype=dtype)
+        self.activation = activation
+        self.gate_proj = torch.nn.Linear(hidden, intermediate, **kw)
+        self.up_proj = torch.nn.Linear(hidden, intermediate, **kw)
+        self.down_proj = torch.nn.Linear(intermediate, hidden, **kw)
+
+    def forward(self, x, residual=None):
+        h = fused_glu(x, self.gate_proj.weight, self.up_proj.weight, self.gate_proj.bias, self.up_proj.bias,
+                      self.activation)
+        return fused_linear(h, self.down_proj.weight, self.down_proj.bias, residual)
+
+
+def clip_grad_norm_(parameters, max_norm: float, norm_type: float = 2.0) -> torch.Tensor:
+    """Clips the parameters' gradients in place by their global norm, as
+    torch.nn.utils.clip_grad_norm_ does; returns the norm before (a scalar tensor)."""
+    if isinstance(parameters, torch.Tensor):
+        parameters = [parameters]
+    grads = [p.grad for p in parameters if p.grad is not None]
+    if not grads:
+        return torch.zeros((), dtype=torch.float32)
+    return flce_clip_grad_norm(grads, max_norm, norm_type).reshape(())
