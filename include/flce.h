@@ -390,11 +390,13 @@ flce_status flce_shard_backward(const void* x, const void* W_shard, const void* 
  *    and N any size, N = 0 included (weight gradients are then zero, and the
  *    token tensors may be NULL).
  *  - Products accumulate in fp32 whatever the dtype; results are rounded once.
- *    The kept pre-activations (z; g and u) and the gradients of them (dz; dg
- *    and du, in the workspace) are held in the tensors' dtype: each is an
- *    operand of a 16-bit matrix product, or as large as all other outputs
- *    together.  With float16 that bounds them by 65504 and rounds values under
- *    2^-14 to multiples of 2^-24, as float16 autograd of the formulas does.
+ *    The kept pre-activations (z; g and u) are float32 [N, F] whatever the
+ *    dtype: rounded to 16 bits they would add as much error to the gradients
+ *    as the gradients' own rounding does.  The gradients with respect to them
+ *    (dz; dg and du, in the workspace) are rounded to the dtype, as operands of
+ *    the matrix products: with float16 that bounds them by 65504 and rounds
+ *    values under 2^-14 to multiples of 2^-24, as float16 autograd of the
+ *    formulas does.
  *  - Results do not depend on what else runs: sums are added in a fixed order.
  */
 typedef FLCE_ENUM(flce_activation) {
@@ -425,10 +427,10 @@ flce_status flce_linear_workspace_size(int64_t N, int64_t H, int64_t F, flce_dty
                                        size_t* fwd_bytes, size_t* bwd_bytes);
 
 flce_status flce_linear_forward(const void* x, const void* W, const void* b, const void* residual, int64_t N, int64_t H,
-                                int64_t F, flce_dtype dtype, flce_activation activation, void* y, void* z,
+                                int64_t F, flce_dtype dtype, flce_activation activation, void* y, float* z,
                                 void* workspace, size_t workspace_bytes, hipStream_t stream);
 
-flce_status flce_linear_backward(const void* x, const void* W, const void* z, const void* dy, int64_t N, int64_t H,
+flce_status flce_linear_backward(const void* x, const void* W, const float* z, const void* dy, int64_t N, int64_t H,
                                  int64_t F, flce_dtype dtype, flce_activation activation, void* dx, void* dW, void* db,
                                  void* workspace, size_t workspace_bytes, hipStream_t stream);
 
@@ -446,10 +448,10 @@ flce_status flce_glu_workspace_size(int64_t N, int64_t H, int64_t F, flce_dtype 
                                     size_t* bwd_bytes);
 
 flce_status flce_glu_forward(const void* x, const void* Wg, const void* Wu, const void* bg, const void* bu, int64_t N,
-                             int64_t H, int64_t F, flce_dtype dtype, flce_activation activation, void* h, void* g,
-                             void* u, void* workspace, size_t workspace_bytes, hipStream_t stream);
+                             int64_t H, int64_t F, flce_dtype dtype, flce_activation activation, void* h, float* g,
+                             float* u, void* workspace, size_t workspace_bytes, hipStream_t stream);
 
-flce_status flce_glu_backward(const void* x, const void* Wg, const void* Wu, const void* g, const void* u,
+flce_status flce_glu_backward(const void* x, const void* Wg, const void* Wu, const float* g, const float* u,
                               const void* dh, int64_t N, int64_t H, int64_t F, flce_dtype dtype,
                               flce_activation activation, void* dx, void* dWg, void* dWu, void* dbg, void* dbu,
                               void* workspace, size_t workspace_bytes, hipStream_t stream);

@@ -978,13 +978,14 @@ flce_status flce_shard_backward(const void* x, const void* W_shard, const void* 
 
 namespace {
 
-// K parts of a product with `tiles` 256 x 256 output tiles.  Tiles that fill
-// over half the CUs are not split; fewer are, into as many parts as make one
-// workgroup per CU, each at least 512 deep and at most 16: every part costs a
-// pass over an fp32 copy of the output.
-int product_parts(int64_t tiles, int64_t K) {
-  if (2 * tiles > kCUs) return 1;
-  int64_t p = kCUs / tiles;
+// K parts of a product with `tiles` output tiles.  Tiles that fill over half
+// the places for workgroups (one per CU; two for fp32's smaller tiles) are not
+// split; fewer are, into as many parts as fill them, each at least 512 deep and
+// at most 16: every part costs a pass over an fp32 copy of the output.
+int product_parts(int64_t tiles, int64_t K, int dtype) {
+  const int64_t places = dtype == FLCE_F32 ? 2 * kCUs : kCUs;
+  if (2 * tiles > places) return 1;
+  int64_t p = places / tiles;
   if (p > K / 512) p = K / 512;
   if (p > 16) p = 16;
   return p < 2 ? 1 : (int)p;
@@ -1010,9 +1011,10 @@ struct LayerGeometry {
 LayerGeometry layer_geometry(int64_t N, int64_t H, int64_t F, int dtype, int act, int nmat) {
   LayerGeometry g{};
   const int64_t es = dtype == FLCE_F32 ? 4 : 2;
-  g.TM = (int)cdiv(N, kTile);
-  g.TN = (int)cdiv(F, nmat == 2 ? kTile / 2 : kTile);
-  g.fwd_parts = N > flce::kSkinnyTokens ? product_parts((int64_t)g.TM * g.TN, H) : 1;
+  const int64_t tile = flce::layer_tile(dtype);
+  g.TM = (int)cdiv(N, tile);
+  g.TN = (int)cdiv(F, tile / nmat);
+  g.fwd_parts = N > flce::kSkinnyTokens ? product_parts((int64_t)g.TM * g.TN, H, dtype) : 1;
   g.kc = part_depth(H, g.fwd_parts);
   g.ldp = nmat * cdiv(F, 8) * 8;
   g.fwd_total = g.fwd_parts > 1 ? align_up((size_t)g.fwd_parts * N * g.ldp * 4) : 0;
@@ -1024,16 +1026,16 @@ LayerGeometry layer_geometry(int64_t N, int64_t H, int64_t F, int dtype, int act
   g.segk = nmat == 2 ? cdiv(F, 64) * 64 : int64_t(1) << 30;
   g.ldz = nmat == 2 ? 2 * g.segk : cdiv(F, 8) * 8;
   size_t off = g.dz_is_dy ? 0 : align_up((size_t)N * g.ldz * es);
-  // Column sums: 64 tokens a block, more when that makes over 128 blocks.
-  g.db_rows = (int)(cdiv(cdiv(N, 128), 64) * 64);
+  // Column sums: 64 tokens a block, more when that makes over 64 blocks.
+  g.db_rows = (int)(cdiv(cdiv(N, 64), 64) * 64);
   if (g.db_rows < 64) g.db_rows = 64;
   g.db_blocks = (int)cdiv(N, g.db_rows);
   g.ldb = nmat * F;
   g.off_dbp = off;
   off = align_up(off + (size_t)g.db_blocks * g.ldb * 4);
-  const int64_t th = cdiv(H, kTile), tf = cdiv(F, kTile);
-  g.dx_parts = N > 0 ? product_parts(th * g.TM, g.ldz) : 1;
-  g.dw_parts = product_parts(th * tf * nmat, N);
+  const int64_t th = cdiv(H, tile), tf = cdiv(F, tile);
+  g.dx_parts = N > 0 ? product_parts(th * g.TM, g.ldz, dtype) : 1;
+  g.dw_parts = product_parts(th * tf * nmat, N, dtype);
   g.dx_kc = part_depth(g.ldz, g.dx_parts);
   g.dw_kc = part_depth(N, g.dw_parts);
   g.off_part = off;
@@ -1051,7 +1053,7 @@ flce_status check_layer(int64_t N, int64_t H, int64_t F, int dtype, int act, int
     return FLCE_ERR_UNSUPPORTED;
   if (H % 8 != 0) return FLCE_ERR_UNSUPPORTED;
   const int64_t wide = H > F ? H : F;   // every plane of output tiles fits in an int
-  if (cdiv(N, kTile) * cdiv(wide, kTile / 2) > (int64_t(1) << 26)) return FLCE_ERR_UNSUPPORTED;
+  if (cdiv(N, 128) * cdiv(wide, 64) > (int64_t(1) << 27)) return FLCE_ERR_UNSUPPORTED;
   return FLCE_OK;
 }
 
@@ -1059,7 +1061,7 @@ bool bad_tensor(const void* p, size_t align, bool required) { return p ? !aligne
 
 // The entry points' shared parts: nmat = 1 is the linear layer, 2 the gated product.
 flce_status layer_forward(const void* x, const void* const (&W)[2], const void* const (&b)[2], const void* residual,
-                          int64_t N, int64_t H, int64_t F, int dtype, int act, int nmat, void* y, void* const (&z)[2],
+                          int64_t N, int64_t H, int64_t F, int dtype, int act, int nmat, void* y, float* const (&z)[2],
                           void* workspace, size_t workspace_bytes, hipStream_t stream) {
   const flce_status st = check_layer(N, H, F, dtype, act, nmat);
   if (st != FLCE_OK) return st;
@@ -1093,7 +1095,7 @@ flce_status layer_forward(const void* x, const void* const (&W)[2], const void* 
   return flce::launch_layer_forward(a, dtype, stream) == hipSuccess ? FLCE_OK : FLCE_ERR_HIP;
 }
 
-flce_status layer_backward(const void* x, const void* const (&W)[2], const void* const (&z)[2], const void* dy,
+flce_status layer_backward(const void* x, const void* const (&W)[2], const float* const (&z)[2], const void* dy,
                            int64_t N, int64_t H, int64_t F, int dtype, int act, int nmat, void* dx,
                            void* const (&dW)[2], void* const (&db)[2], void* workspace, size_t workspace_bytes,
                            hipStream_t stream) {
@@ -1299,13 +1301,13 @@ flce_status flce_linear_workspace_size(int64_t N, int64_t H, int64_t F, flce_dty
 }
 
 flce_status flce_linear_forward(const void* x, const void* W, const void* b, const void* residual, int64_t N, int64_t H,
-                                int64_t F, flce_dtype dtype, flce_activation activation, void* y, void* z,
+                                int64_t F, flce_dtype dtype, flce_activation activation, void* y, float* z,
                                 void* workspace, size_t workspace_bytes, hipStream_t stream) {
   return layer_forward(x, {W, nullptr}, {b, nullptr}, residual, N, H, F, dtype, activation, 1, y, {z, nullptr},
                        workspace, workspace_bytes, stream);
 }
 
-flce_status flce_linear_backward(const void* x, const void* W, const void* z, const void* dy, int64_t N, int64_t H,
+flce_status flce_linear_backward(const void* x, const void* W, const float* z, const void* dy, int64_t N, int64_t H,
                                  int64_t F, flce_dtype dtype, flce_activation activation, void* dx, void* dW, void* db,
                                  void* workspace, size_t workspace_bytes, hipStream_t stream) {
   return layer_backward(x, {W, nullptr}, {z, nullptr}, dy, N, H, F, dtype, activation, 1, dx, {dW, nullptr},
@@ -1323,13 +1325,13 @@ flce_status flce_glu_workspace_size(int64_t N, int64_t H, int64_t F, flce_dtype 
 }
 
 flce_status flce_glu_forward(const void* x, const void* Wg, const void* Wu, const void* bg, const void* bu, int64_t N,
-                             int64_t H, int64_t F, flce_dtype dtype, flce_activation activation, void* h, void* g,
-                             void* u, void* workspace, size_t workspace_bytes, hipStream_t stream) {
+                             int64_t H, int64_t F, flce_dtype dtype, flce_activation activation, void* h, float* g,
+                             float* u, void* workspace, size_t workspace_bytes, hipStream_t stream) {
   return layer_forward(x, {Wg, Wu}, {bg, bu}, nullptr, N, H, F, dtype, activation, 2, h, {g, u}, workspace,
                        workspace_bytes, stream);
 }
 
-flce_status flce_glu_backward(const void* x, const void* Wg, const void* Wu, const void* g, const void* u,
+flce_status flce_glu_backward(const void* x, const void* Wg, const void* Wu, const float* g, const float* u,
                               const void* dh, int64_t N, int64_t H, int64_t F, flce_dtype dtype,
                               flce_activation activation, void* dx, void* dWg, void* dWu, void* dbg, void* dbu,
                               void* workspace, size_t workspace_bytes, hipStream_t stream) {

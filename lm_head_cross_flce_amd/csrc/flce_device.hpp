@@ -237,14 +237,6 @@ __device__ __forceinline__ float acc_read1(const f32x4& blk) {
 // (correctness-oriented; no fine-grained interleave)
 // ---------------------------------------------------------------------------
 
-// Tile row t of an operand copied with permuted columns holds global row
-// m0 + tile_col_perm(t): within each half of 128 rows, row 16 j + c (the
-// MFMA output column c of block j) holds row 8 c + j, so a lane's values in
-// the eight blocks of one output row are eight consecutive global rows.
-__device__ __forceinline__ constexpr int tile_col_perm(int t) {
-  return (t & 0x80) | ((t & 0x0F) << 3) | ((t & 0x70) >> 4);
-}
-
 // One stage of one operand: 256 rows x 32 fp32, 8 x 16 bytes per thread,
 // stored to LDS rows of kRowBytes with K contiguous.
 template <class T, bool KCONTIG> struct Stager;
@@ -256,14 +248,13 @@ template <> struct Stager<float, true> {
   uint32_t off[8];
   const float* base;
   int kc_elem;
-  // perm: tile rows hold permuted global rows (tile_col_perm).
-  __device__ __forceinline__ void init(const Opnd<float>& o, int m0, int tid, bool perm = false) {
+  __device__ __forceinline__ void init(const Opnd<float>& o, int m0, int tid) {
     const int kc = tid & 7, rr = tid >> 3;
     kc_elem = kc * 4;
     base = o.p + (int64_t)m0 * o.ld;
 #pragma unroll
     for (int q = 0; q < 8; ++q) {
-      const int row = perm ? tile_col_perm(rr + 32 * q) : rr + 32 * q;
+      const int row = rr + 32 * q;
       off[q] = (m0 + row < o.mext) ? (uint32_t)(((int64_t)row * o.ld + kc_elem) * 4) : kOOB;
     }
   }
@@ -349,14 +340,17 @@ __device__ __forceinline__ void mma_stage_f32(Acc& acc, const lds_t* bA, const l
   }
 }
 
-// fp32 tile mainloop: two padded LDS buffers per operand, register staging by
-// the operands' initialised stagers.  Ends with a barrier; the accumulators
-// need acc_drain() before they are read.
-template <class SA, class SB>
-__device__ __forceinline__ void gemm_tile_f32_run(Acc& acc, const Opnd<float>& A, SA& sa, const Opnd<float>& B, SB& sb,
-                                                  int K, const Lds& L, int tid) {
+// fp32 tile mainloop: two padded LDS buffers per operand, register staging.
+// Ends with a barrier; the accumulators need acc_drain() before they are read.
+template <bool AK, bool BK>
+__device__ __forceinline__ void gemm_tile_f32(Acc& acc, const Opnd<float>& A, int m0, const Opnd<float>& B, int n0,
+                                              int K, const Lds& L, int tid) {
   constexpr int kBK = 32;
   const int lane = tid & 63, wave = tid >> 6, wm = wave >> 1, wn = wave & 1;
+  Stager<float, AK> sa;
+  Stager<float, BK> sb;
+  sa.init(A, m0, tid);
+  sb.init(B, n0, tid);
   const int KT = (K + kBK - 1) / kBK;
   sa.load(A, 0);
   sb.load(B, 0);
@@ -378,16 +372,6 @@ __device__ __forceinline__ void gemm_tile_f32_run(Acc& acc, const Opnd<float>& A
     }
     __syncthreads();
   }
-}
-
-template <bool AK, bool BK>
-__device__ __forceinline__ void gemm_tile_f32(Acc& acc, const Opnd<float>& A, int m0, const Opnd<float>& B, int n0,
-                                              int K, const Lds& L, int tid) {
-  Stager<float, AK> sa;
-  Stager<float, BK> sb;
-  sa.init(A, m0, tid);
-  sb.init(B, n0, tid);
-  gemm_tile_f32_run(acc, A, sa, B, sb, K, L, tid);
 }
 
 // ---------------------------------------------------------------------------
@@ -448,6 +432,14 @@ template <bool KCONTIG> struct Dma;
 // of four 16 rows apart), so it can store them as one 16-byte piece.
 __device__ __forceinline__ constexpr int tile_row_perm(int t) {
   return (t & 0xE3) | ((t & 0x0C) << 1) | ((t & 0x10) >> 2);
+}
+
+// Tile row t of an operand copied with permuted columns holds global row
+// m0 + tile_col_perm(t): within each half of 128 rows, row 16 j + c (the
+// MFMA output column c of block j) holds row 8 c + j, so a lane's values in
+// the eight blocks of one output row are eight consecutive global rows.
+__device__ __forceinline__ constexpr int tile_col_perm(int t) {
+  return (t & 0x80) | ((t & 0x0F) << 3) | ((t & 0x70) >> 4);
 }
 
 // K-contiguous: instruction idx fills rows 8 idx .. 8 idx + 7; lane l takes

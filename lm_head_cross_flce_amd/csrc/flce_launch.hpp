@@ -128,6 +128,9 @@ hipError_t launch_forward_keep(const FwdLaunch& head, const FwdLaunch& rest, int
 
 enum Activation { kActNone = 0, kActRelu = 1, kActGelu = 2, kActGeluTanh = 3, kActSilu = 4, kActSigmoid = 5 };
 
+// Side of an output tile.
+constexpr int layer_tile(int dtype) { return dtype == 0 ? 128 : 256; }
+
 // Forward by streaming the weights past few tokens: at most this many.
 constexpr int kSkinnyTokens = 64;
 
@@ -135,9 +138,9 @@ struct LayerFwd {
   const void* x; const void* W[2]; const void* b[2];
   const void* residual;   // [N][F] added to the output, or null; may be y itself
   void* y;                // [N][F]
-  void* z[2];             // [N][F] pre-activations kept for the backward (linear: z[0]), or null
+  float* z[2];            // [N][F] pre-activations kept for the backward (linear: z[0]), or null
   int N, H, F, act, nmat;
-  int TM, TN;             // token tiles of 256, feature tiles of 256 (gated: 128 of each weight)
+  int TM, TN;             // token tiles, feature tiles (layer_tile; gated: half as many of each weight)
   int parts, kc;          // K split: parts of kc columns of x each
   float* part;            // parts > 1: [parts][N][ldp] fp32 sums; gated: u's at column ldp / 2
   int64_t ldp;            // nmat * F rounded up to 8
@@ -145,7 +148,7 @@ struct LayerFwd {
 
 struct LayerBwd {
   const void* x; const void* W[2];
-  const void* z[2];       // kept pre-activations (linear with kActNone: null)
+  const float* z[2];      // kept pre-activations (linear with kActNone: null)
   const void* dy;         // [N][F]
   int N, H, F, act, nmat;
   void* dz;               // [N][ldz]: dz, zero from column F on; gated: dg, then du from column segk

@@ -3,6 +3,8 @@
 // the tile routine of flce_device.hpp that take rows from two weights.
 #pragma once
 
+#include <type_traits>
+
 #include "flce_device.hpp"
 #include "flce_launch.hpp"
 
@@ -124,24 +126,35 @@ template <class T> __device__ __forceinline__ void store1(T* p, float v) {
   else *(uint16_t*)p = (uint16_t)(pack2<T>(v, 0.f) & 0xffffu);
 }
 
-// C consecutive elements (C = 4 or 8) of a 16-byte (C = 4, 16-bit: 8-byte)
-// aligned address.
+// C consecutive elements (16-bit: 4 or 8; fp32: 2, 4 or 8) as whole 4- to
+// 16-byte accesses from any element's address: rows of odd sizes start on no
+// boundary, and global memory takes wide accesses there.
+typedef u32x2 u32x2_any __attribute__((aligned(2)));
+typedef u32x4 u32x4_any __attribute__((aligned(2)));
+typedef float f32x2 __attribute__((ext_vector_type(2)));
+typedef f32x2 f32x2_any __attribute__((aligned(4)));
+typedef f32x4 f32x4_any __attribute__((aligned(4)));
+
 template <class T, int C> __device__ __forceinline__ void load_vec(const T* p, float (&v)[C]) {
-  if constexpr (sizeof(T) == 4) {
+  if constexpr (sizeof(T) == 4 && C == 2) {
+    const f32x2 t = *(const f32x2_any*)p;
+    v[0] = t[0];
+    v[1] = t[1];
+  } else if constexpr (sizeof(T) == 4) {
 #pragma unroll
     for (int e = 0; e < C; e += 4) {
-      const f32x4 t = *(const f32x4*)((const float*)p + e);
+      const f32x4 t = *(const f32x4_any*)((const float*)p + e);
 #pragma unroll
       for (int k = 0; k < 4; ++k) v[e + k] = t[k];
     }
   } else {
     uint32_t w[C / 2];
     if constexpr (C == 8) {
-      const u32x4 t = *(const u32x4*)p;
+      const u32x4 t = *(const u32x4_any*)p;
 #pragma unroll
       for (int k = 0; k < 4; ++k) w[k] = t[k];
     } else {
-      const u32x2 t = *(const u32x2*)p;
+      const u32x2 t = *(const u32x2_any*)p;
       w[0] = t[0];
       w[1] = t[1];
     }
@@ -153,74 +166,72 @@ template <class T, int C> __device__ __forceinline__ void load_vec(const T* p, f
   }
 }
 template <class T, int C> __device__ __forceinline__ void store_vec(T* p, const float (&v)[C]) {
-  if constexpr (sizeof(T) == 4) {
+  if constexpr (sizeof(T) == 4 && C == 2) {
+    *(f32x2_any*)p = f32x2{v[0], v[1]};
+  } else if constexpr (sizeof(T) == 4) {
 #pragma unroll
-    for (int e = 0; e < C; e += 4) *(f32x4*)((float*)p + e) = f32x4{v[e], v[e + 1], v[e + 2], v[e + 3]};
+    for (int e = 0; e < C; e += 4) *(f32x4_any*)((float*)p + e) = f32x4{v[e], v[e + 1], v[e + 2], v[e + 3]};
   } else if constexpr (C == 8) {
-    *(u32x4*)p = u32x4{pack2<T>(v[0], v[1]), pack2<T>(v[2], v[3]), pack2<T>(v[4], v[5]), pack2<T>(v[6], v[7])};
+    *(u32x4_any*)p = u32x4{pack2<T>(v[0], v[1]), pack2<T>(v[2], v[3]), pack2<T>(v[4], v[5]), pack2<T>(v[6], v[7])};
   } else {
-    *(u32x2*)p = u32x2{pack2<T>(v[0], v[1]), pack2<T>(v[2], v[3])};
+    *(u32x2_any*)p = u32x2{pack2<T>(v[0], v[1]), pack2<T>(v[2], v[3])};
   }
 }
 
-// The same through a buffer descriptor: byte offset off, kOOB reads zeros and
-// stores nothing.  vec: the C elements are aligned as above and all in the
-// row or all past it; else element e moves alone, `left` of them in the row.
-template <class T, int C>
-__device__ __forceinline__ void buf_store_vec(__amdgpu_buffer_rsrc_t r, uint32_t off, const float (&v)[C], bool vec,
-                                              int left) {
-  if (vec) {
-    if constexpr (sizeof(T) == 4) {
-#pragma unroll
-      for (int e = 0; e < C; e += 4)
-        __builtin_amdgcn_raw_buffer_store_b128(__builtin_bit_cast(u32x4, f32x4{v[e], v[e + 1], v[e + 2], v[e + 3]}), r,
-                                               off + 4 * e, 0, 0);
-    } else if constexpr (C == 8) {
-      __builtin_amdgcn_raw_buffer_store_b128(
-          u32x4{pack2<T>(v[0], v[1]), pack2<T>(v[2], v[3]), pack2<T>(v[4], v[5]), pack2<T>(v[6], v[7])}, r, off, 0, 0);
-    } else {
-      __builtin_amdgcn_raw_buffer_store_b64(u32x2{pack2<T>(v[0], v[1]), pack2<T>(v[2], v[3])}, r, off, 0, 0);
-    }
+// The first `left` of them (any left; none when it is not positive), zeros for the rest.
+template <class T, int C> __device__ __forceinline__ void load_some(const T* p, int left, float (&v)[C]) {
+  if (left >= C) {
+    load_vec<T, C>(p, v);
   } else {
 #pragma unroll
-    for (int e = 0; e < C; ++e) {
-      const uint32_t o = e < left ? off + (uint32_t)(sizeof(T) * e) : kOOB;
-      if constexpr (sizeof(T) == 4) __builtin_amdgcn_raw_buffer_store_b32(__float_as_uint(v[e]), r, o, 0, 0);
-      else __builtin_amdgcn_raw_buffer_store_b16((uint16_t)(pack2<T>(v[e], 0.f) & 0xffffu), r, o, 0, 0);
-    }
+    for (int e = 0; e < C; ++e) v[e] = e < left ? load1<T>(p + e) : 0.f;
+  }
+}
+template <class T, int C> __device__ __forceinline__ void store_some(T* p, int left, const float (&v)[C]) {
+  if (left >= C) {
+    store_vec<T, C>(p, v);
+  } else {
+#pragma unroll
+    for (int e = 0; e < C; ++e)
+      if (e < left) store1<T>(p + e, v[e]);
+  }
+}
+
+// Whole aligned runs through a buffer descriptor: byte offset off (a lane's,
+// kOOB reads zeros and stores nothing) plus so (the wave's).
+template <class T, int C>
+__device__ __forceinline__ void buf_store_vec(__amdgpu_buffer_rsrc_t r, uint32_t off, int so, const float (&v)[C]) {
+  if constexpr (sizeof(T) == 4 && C == 2) {
+    __builtin_amdgcn_raw_buffer_store_b64(__builtin_bit_cast(u32x2, f32x2{v[0], v[1]}), r, off, so, 0);
+  } else if constexpr (sizeof(T) == 4) {
+#pragma unroll
+    for (int e = 0; e < C; e += 4)
+      __builtin_amdgcn_raw_buffer_store_b128(__builtin_bit_cast(u32x4, f32x4{v[e], v[e + 1], v[e + 2], v[e + 3]}), r,
+                                             off + 4 * e, so, 0);
+  } else if constexpr (C == 8) {
+    __builtin_amdgcn_raw_buffer_store_b128(
+        u32x4{pack2<T>(v[0], v[1]), pack2<T>(v[2], v[3]), pack2<T>(v[4], v[5]), pack2<T>(v[6], v[7])}, r, off, so, 0);
+  } else {
+    __builtin_amdgcn_raw_buffer_store_b64(u32x2{pack2<T>(v[0], v[1]), pack2<T>(v[2], v[3])}, r, off, so, 0);
   }
 }
 template <class T, int C>
-__device__ __forceinline__ void buf_load_vec(__amdgpu_buffer_rsrc_t r, uint32_t off, float (&v)[C], bool vec, int left) {
-  if (vec) {
-    if constexpr (sizeof(T) == 4) {
+__device__ __forceinline__ void buf_load_vec(__amdgpu_buffer_rsrc_t r, uint32_t off, int so, float (&v)[C]) {
+  if constexpr (sizeof(T) == 4) {
+    static_assert(C == 4 || C == 8, "whole 16-byte pieces");
 #pragma unroll
-      for (int e = 0; e < C; e += 4) {
-        const f32x4 t = __builtin_bit_cast(f32x4, buf_load16(r, off + 4 * e));
+    for (int e = 0; e < C; e += 4) {
+      const f32x4 t = __builtin_bit_cast(f32x4, __builtin_amdgcn_raw_buffer_load_b128(r, off + 4 * e, so, 0));
 #pragma unroll
-        for (int k = 0; k < 4; ++k) v[e + k] = t[k];
-      }
-    } else if constexpr (C == 8) {
-      const u32x4 t = buf_load16(r, off);
-#pragma unroll
-      for (int k = 0; k < 4; ++k) {
-        v[2 * k] = h16_to_f32<T>(t[k]);
-        v[2 * k + 1] = h16_to_f32<T>(t[k] >> 16);
-      }
-    } else {
-      const u32x2 t = __builtin_bit_cast(u32x2, __builtin_amdgcn_raw_buffer_load_b64(r, off, 0, 0));
-#pragma unroll
-      for (int k = 0; k < 2; ++k) {
-        v[2 * k] = h16_to_f32<T>(t[k]);
-        v[2 * k + 1] = h16_to_f32<T>(t[k] >> 16);
-      }
+      for (int k = 0; k < 4; ++k) v[e + k] = t[k];
     }
   } else {
+    static_assert(C == 8, "whole 16-byte pieces");
+    const u32x4 t = __builtin_bit_cast(u32x4, __builtin_amdgcn_raw_buffer_load_b128(r, off, so, 0));
 #pragma unroll
-    for (int e = 0; e < C; ++e) {
-      const uint32_t o = e < left ? off + (uint32_t)(sizeof(T) * e) : kOOB;
-      if constexpr (sizeof(T) == 4) v[e] = __uint_as_float(__builtin_amdgcn_raw_buffer_load_b32(r, o, 0, 0));
-      else v[e] = h16_to_f32<T>(__builtin_amdgcn_raw_buffer_load_b16(r, o, 0, 0));
+    for (int k = 0; k < 4; ++k) {
+      v[2 * k] = h16_to_f32<T>(t[k]);
+      v[2 * k + 1] = h16_to_f32<T>(t[k] >> 16);
     }
   }
 }
@@ -229,14 +240,25 @@ __device__ __forceinline__ void buf_load_vec(__amdgpu_buffer_rsrc_t r, uint32_t 
 // Operands over two weights
 // ---------------------------------------------------------------------------
 
-// The gated product's weight tile: 128 rows of Wg and the same 128 of Wu as
-// one 256-row K-contiguous operand.  In each half of 128 tile rows, row
-// 16 j + c (output column c of block j) holds row 64 half + 4 c + j % 4 of Wg
-// (j < 4) or of Wu (j >= 4): a lane's eight blocks of one output row are four
-// consecutive columns of g and the same four of u, so the product act(g) u
-// needs no other lane.
-__device__ __forceinline__ constexpr int glu_row(int t) {
-  return ((t & 0x80) >> 1) | ((t & 0x0F) << 2) | ((t & 0x30) >> 4);
+// Output tiles, four waves in a 2 x 2 grid of MI x NJ blocks of 16 x 16 each:
+// 256 x 256 for 16-bit operands; 128 x 128 for fp32, whose matrix instruction
+// is 16 times slower per byte, so that small tiles starve on nothing and two
+// workgroups share a CU (one's epilogue runs under the other's products).
+template <class T> struct Tile {
+  static constexpr int MI = sizeof(T) == 2 ? 8 : 4, NJ = MI;
+  static constexpr int M = 32 * MI, N = 32 * NJ;
+  static constexpr int kPerCu = sizeof(T) == 2 ? 1 : 2;   // workgroups that fit on a CU
+};
+
+// Column order of a tile: in each wave's half (16 NJ rows of the weight
+// operand), row 16 j + c (output column c of block j) holds weight row
+// NJ c + j, so a lane's NJ blocks of one output row are NJ consecutive columns.
+// Gated: the half holds 8 NJ rows of Wg (blocks j < NJ / 2) and the same of Wu:
+// row NJ / 2 c + j % (NJ / 2), so a lane has NJ / 2 consecutive columns of g and
+// the same of u, and the product act(g) u needs no other lane.
+template <int NJ, bool GLU> __device__ __forceinline__ constexpr int weight_row(int t) {
+  const int half = t / (16 * NJ), j = t / 16 % NJ, c = t % 16;
+  return GLU ? half * 8 * NJ + NJ / 2 * c + j % (NJ / 2) : half * 16 * NJ + NJ * c + j;
 }
 
 // 16-bit copies.  Tile row t = 32 q + 8 wave + lane / 8 lies in block
@@ -257,7 +279,7 @@ struct DmaGlu {
     const int c = (lane & 7) ^ (lane >> 3);
 #pragma unroll
     for (int q = 0; q < 8; ++q) {
-      const int row = glu_row(8 * (4 * q + wave) + (lane >> 3));
+      const int row = weight_row<8, true>(8 * (4 * q + wave) + (lane >> 3));
       off[q] = (f0 + row < F) ? (uint32_t)(((int64_t)row * ld + 8 * c) * 2) : kOOB;
     }
   }
@@ -266,36 +288,6 @@ struct DmaGlu {
   __device__ __forceinline__ void issue(const Pair& rs, int kleft, lds_t* buf, int lane, int q) const {
     const int c = (lane & 7) ^ (lane >> 3);
     dma16((q & 2) ? rs.u : rs.g, buf + (4 * q + wave) * 1024, (!TAIL || 8 * c < kleft) ? off[q] : kOOB);
-  }
-};
-
-// fp32 form: tile row t = tid / 8 + 32 q, again bit 1 of q names the weight.
-struct StagerGlu {
-  u32x4 r[8];
-  uint32_t off[8];
-  const float* base[2];
-  int kc_elem;
-  __device__ __forceinline__ void init(const float* Wg, const float* Wu, int64_t ld, int F, int f0, int tid) {
-    const int kc = tid & 7, rr = tid >> 3;
-    kc_elem = kc * 4;
-    base[0] = Wg + (int64_t)f0 * ld;
-    base[1] = Wu + (int64_t)f0 * ld;
-#pragma unroll
-    for (int q = 0; q < 8; ++q) {
-      const int row = glu_row(rr + 32 * q);
-      off[q] = (f0 + row < F) ? (uint32_t)(((int64_t)row * ld + kc_elem) * 4) : kOOB;
-    }
-  }
-  __device__ __forceinline__ void load(const Opnd<float>& o, int k0) {
-    const __amdgpu_buffer_rsrc_t rg = make_rsrc(base[0] + k0), ru = make_rsrc(base[1] + k0);
-    const bool kok = k0 + kc_elem < o.kext;
-#pragma unroll
-    for (int q = 0; q < 8; ++q) r[q] = buf_load16((q & 2) ? ru : rg, kok ? off[q] : kOOB);
-  }
-  __device__ __forceinline__ void store(lds_t* buf, int tid) const {
-    const int kc = tid & 7, rr = tid >> 3;
-#pragma unroll
-    for (int q = 0; q < 8; ++q) lds_store16(buf + (rr + 32 * q) * kRowBytes + kc * 16, r[q]);
   }
 };
 
@@ -331,17 +323,141 @@ struct DmaSeg {
   }
 };
 
-struct StagerSeg {
-  Stager<float, false> st;
-  SegRows s;
-  int m0;
-  __device__ __forceinline__ void load(const Opnd<float>& o, int k0) {
-    const __amdgpu_buffer_rsrc_t rs = s.rsrc<4>(k0, m0);
-    const int kleft = o.kext - k0 - st.krow;
+// ---------------------------------------------------------------------------
+// fp32 tile: 128 x 128, 32-deep stages through registers into two padded LDS
+// buffers per operand, v_mfma_f32_16x16x4_f32.  MFMA bounds it (32 cycles an
+// instruction against one 16-byte LDS read per 8 of them).
+// ---------------------------------------------------------------------------
+
+constexpr int kF32Rows = 128, kF32K = 32;
+
+// K-contiguous operand of up to two weights: thread (kc, rr) = (tid % 8,
+// tid / 8) loads 16 bytes of K of tile rows rr + 32 q.  A gated tile's rows
+// 32 q .. 32 q + 31 lie in blocks j = 2 q and 2 q + 1 (mod 4): bit 0 of q tells
+// the weight.
+template <bool PERM, bool GLU> struct RowStager {
+  u32x4 r[4];
+  uint32_t off[4];
+  const float* base[2];
+  int kc4;
+  __device__ __forceinline__ void init(const float* p0, const float* p1, int64_t ld, int rows, int m0, int tid) {
+    const int rr = tid >> 3;
+    kc4 = (tid & 7) * 4;
+    base[0] = p0 + (int64_t)m0 * ld;
+    base[1] = GLU ? p1 + (int64_t)m0 * ld : base[0];
 #pragma unroll
-    for (int i = 0; i < 8; ++i) st.r[i] = buf_load16(rs, (i & 3) < kleft ? st.off[i] : kOOB);
+    for (int q = 0; q < 4; ++q) {
+      const int t = rr + 32 * q, row = PERM ? weight_row<4, GLU>(t) : t;
+      off[q] = m0 + row < rows ? (uint32_t)(((int64_t)row * ld + kc4) * 4) : kOOB;
+    }
   }
-  __device__ __forceinline__ void store(lds_t* buf, int tid) const { st.store(buf, tid); }
+  __device__ __forceinline__ void load(int k0, int kext) {
+    const __amdgpu_buffer_rsrc_t r0 = make_rsrc(base[0] + k0), r1 = make_rsrc(base[1] + k0);
+    const bool in = k0 + kc4 < kext;
+#pragma unroll
+    for (int q = 0; q < 4; ++q) r[q] = buf_load16(GLU && (q & 1) ? r1 : r0, in ? off[q] : kOOB);
+  }
+  __device__ __forceinline__ void store(lds_t* buf, int tid) const {
+#pragma unroll
+    for (int q = 0; q < 4; ++q) lds_store16(buf + ((tid >> 3) + 32 * q) * kRowBytes + (tid & 7) * 16, r[q]);
+  }
 };
+
+// M-contiguous operand: 4 x 4 blocks transposed in registers, thread (kc, mc)
+// = (tid % 8, tid / 8).  SegRows gives the rows (K).
+struct ColStager {
+  u32x4 r[4];
+  uint32_t off[4];
+  SegRows s;
+  int m0, krow;
+  __device__ __forceinline__ void init(const SegRows& rows, int cols, int m0_, int tid) {
+    s = rows;
+    m0 = m0_;
+    krow = (tid & 7) * 4;
+    const int m = (tid >> 3) * 4;
+#pragma unroll
+    for (int e = 0; e < 4; ++e) off[e] = m0 + m < cols ? (uint32_t)(((int64_t)(krow + e) * s.ld + m) * 4) : kOOB;
+  }
+  __device__ __forceinline__ void load(int k0, int kext) {
+    const __amdgpu_buffer_rsrc_t rs = s.rsrc<4>(k0, m0);
+    const int left = kext - k0 - krow;
+#pragma unroll
+    for (int e = 0; e < 4; ++e) r[e] = buf_load16(rs, e < left ? off[e] : kOOB);
+  }
+  __device__ __forceinline__ void store(lds_t* buf, int tid) const {
+#pragma unroll
+    for (int i = 0; i < 4; ++i)
+      lds_store16(buf + ((tid >> 3) * 4 + i) * kRowBytes + (tid & 7) * 16, u32x4{r[0][i], r[1][i], r[2][i], r[3][i]});
+  }
+};
+
+typedef f32x4 AccF32[4][4];
+
+// acc = the tile's sums over K.  Lane l's 16 bytes of a row are four
+// consecutive k; instruction e takes element e, so K runs permuted, the same
+// for both operands.
+template <class SA, class SB>
+__device__ __forceinline__ void gemm_f32(AccF32& acc, SA& sa, int ka, SB& sb, int kb, int K, int tid) {
+  __shared__ __attribute__((aligned(16))) char lds[2][2][kF32Rows * kRowBytes];
+  const int lane = tid & 63, wave = tid >> 6;
+#pragma unroll
+  for (int i = 0; i < 4; ++i)
+#pragma unroll
+    for (int j = 0; j < 4; ++j) acc[i][j] = f32x4{0.f, 0.f, 0.f, 0.f};
+  const int frag = (lane & 15) * kRowBytes + (lane >> 4) * 16;
+  const int pa = (wave >> 1) * 64 * kRowBytes + frag, pb = (wave & 1) * 64 * kRowBytes + frag;
+  const int KT = (K + kF32K - 1) / kF32K;
+  sa.load(0, ka);
+  sb.load(0, kb);
+  sa.store((lds_t*)lds[0][0], tid);
+  sb.store((lds_t*)lds[0][1], tid);
+  __syncthreads();
+  for (int kt = 0; kt < KT; ++kt) {
+    const int cur = kt & 1;
+    if (kt + 1 < KT) {
+      sa.load((kt + 1) * kF32K, ka);
+      sb.load((kt + 1) * kF32K, kb);
+    }
+    const lds_t* A = (const lds_t*)lds[cur][0];
+    const lds_t* B = (const lds_t*)lds[cur][1];
+#pragma unroll
+    for (int h = 0; h < 2; ++h) {
+      f32x4 a[4], b[4];
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        a[i] = __builtin_bit_cast(f32x4, lds_load16(A + pa + 16 * i * kRowBytes + 64 * h));
+        b[i] = __builtin_bit_cast(f32x4, lds_load16(B + pb + 16 * i * kRowBytes + 64 * h));
+      }
+#pragma unroll
+      for (int e = 0; e < 4; ++e)
+#pragma unroll
+        for (int i = 0; i < 4; ++i)
+#pragma unroll
+          for (int j = 0; j < 4; ++j)
+            acc[i][j] = __builtin_amdgcn_mfma_f32_16x16x4f32(a[i][e], b[j][e], acc[i][j], 0, 0, 0);
+    }
+    if (kt + 1 < KT) {
+      sa.store((lds_t*)lds[cur ^ 1][0], tid);
+      sb.store((lds_t*)lds[cur ^ 1][1], tid);
+    }
+    __syncthreads();
+  }
+}
+
+// f(integral_constant<int, 0>) .. f(integral_constant<int, N - 1>): an unrolled
+// loop whatever its length (the compiler gives up on long ones, and then keeps
+// the accumulators they index in memory).
+template <int N, class F> __device__ __forceinline__ void unrolled(F&& f) {
+  if constexpr (N > 0) {
+    unrolled<N - 1>(f);
+    f(std::integral_constant<int, N - 1>{});
+  }
+}
+
+// One block's sums in vector registers.
+template <class T> __device__ __forceinline__ f32x4 block_sums(const f32x4& blk) {
+  if constexpr (sizeof(T) == 2) return acc_read4(blk);
+  else return blk;
+}
 
 }  // namespace flce

@@ -2,14 +2,12 @@
 // product, h = act(x Wg^T + bg) * (x Wu^T + bu), with their gradients, for one
 // element type T (each type is its own translation unit).
 //
-// Many tokens: the products run on the 256 x 256 MFMA tile routine of
-// flce_device.hpp, with the activation, product and residual in the epilogue,
+// Many tokens: the products run on MFMA tiles (16-bit: the 256 x 256 tile
+// routine of flce_device.hpp; fp32: 128 x 128), with the activation, product and residual in the epilogue,
 // while the accumulators are still in registers.  MFMA bounds them.
 // Few tokens: every weight is read once for at most 64 rows of x, so HBM
 // bounds the call and a kernel that streams weights runs instead.
 #pragma once
-
-#include <type_traits>
 
 #include "layer_device.hpp"
 
@@ -21,21 +19,20 @@ namespace flce {
 
 // Workgroup w computes tiles w, w + grid, ... of the tokens x features plane
 // (times the K parts).  Tokens are the MFMA rows and features its columns, in
-// permuted order (tile_col_perm, glu_row): a lane holds 8 consecutive
-// features of a token (gated: 4 of g and the same 4 of u), so a token's 128
-// features of a wave are written as 16 adjacent 16-byte pieces (gated: 64
-// features, 8-byte pieces).  16-bit: the next tile's first copies run under
-// the epilogue.
-//
-// fp32: one tile a workgroup (a loop costs its register-staged copies 100
-// spilled registers).
+// weight_row's order: a lane holds 8 consecutive features of a token (gated: 4
+// of g and the same 4 of u; fp32: half as many), so a token's features of a
+// wave are written as 16 adjacent 16-byte pieces (gated: 8 bytes).  16-bit: the
+// next tile's first copies run under the epilogue.  fp32: one tile a workgroup,
+// two workgroups a CU.
 //
 // SPLIT: the sums go to a.part in fp32 and layer_join_fwd_kernel does the rest.
 template <class T, int ACT, bool GLU, bool SPLIT>
-__global__ void __launch_bounds__(kThreads, 1) layer_fwd_kernel(LayerFwd a) {
-  FLCE_LDS(L, T);
-  constexpr int FT = GLU ? kTile / 2 : kTile;   // features of a tile
-  constexpr int C = GLU ? 4 : 8;                // consecutive features of a lane
+__global__ void __launch_bounds__(kThreads, Tile<T>::kPerCu) layer_fwd_kernel(LayerFwd a) {
+  typedef Tile<T> TS;
+  constexpr bool k16 = sizeof(T) == 2;
+  constexpr int MI = TS::MI, NJ = TS::NJ;
+  constexpr int FT = GLU ? TS::N / 2 : TS::N;   // features of a tile
+  constexpr int C = GLU ? NJ / 2 : NJ;          // consecutive features of a lane
   typedef typename std::conditional<GLU, DmaGlu, Dma<true>>::type DB;
   const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6, wm = wave >> 1, wn = wave & 1;
   const int g = lane >> 4, c = lane & 15;
@@ -45,138 +42,162 @@ __global__ void __launch_bounds__(kThreads, 1) layer_fwd_kernel(LayerFwd a) {
     const int part = SPLIT ? t / tiles : 0;
     int tm, tn;
     tile_coords(t - part * tiles, tiles, a.TM, a.TN, tm, tn);
-    n0 = tm * kTile;
+    n0 = tm * TS::M;
     f0 = tn * FT;
     k0 = part * a.kc;
   };
   auto opa = [&]() { return Opnd<T>{(const T*)a.x + k0, a.H, a.N, min(a.kc, a.H - k0)}; };
   auto opb = [&]() { return Opnd<T>{(const T*)a.W[0] + k0, a.H, a.F, min(a.kc, a.H - k0)}; };
-  TileCopy<true, true, Dma<true>, DB> tc;
-  auto begin = [&]() {
-    const Opnd<T> A = opa(), B = opb();
-    tc.da.init(A, n0, tid);
-    if constexpr (GLU) tc.db.init(B.p, (const T*)a.W[1] + k0, B.ld, a.F, f0, tid);
-    else tc.db.init(B, f0, tid, 2);
-    tc.begin(A, B, L, tid);
-  };
   int t = blockIdx.x;
   place(t);
-  if constexpr (sizeof(T) == 2) {
-    begin();
-    __builtin_amdgcn_s_waitcnt(waitcnt_vm_lgkm0<0>());   // the mainloop's first wait allows the epilogue's stores
-  }
-  const bool vec = a.F % C == 0;   // whole 16-byte (gated: 8-byte) pieces of a row, all aligned
-  Acc acc;
-  while (true) {
-    const Opnd<T> A = opa(), B = opb();
-    const int fl = GLU ? wn * 64 + 4 * c : wn * kWaveTile + 8 * c;
-    const int n0w = n0 + wm * kWaveTile, f = f0 + fl, part = SPLIT ? t / tiles : 0;
+  const bool vec = a.F % C == 0;   // every lane's run is whole and aligned to its size
+  auto tile = [&](auto& acc, int n0, int f0, int part, const float (&b0)[C], const float (&b1)[C]) {
+    // Value (i, r) of a lane is token n0w + 4 g + 16 i + r.  Its byte offset is
+    // the lane's (token 4 g, or kOOB for a token past N) plus the wave's (16 i + r
+    // tokens), from a descriptor at the wave's first token: at most 128 * ld * 4.
+    const int n0w = n0 + wm * 16 * MI, f = f0 + (wn * 16 + c) * C;
     const int left = a.F - f;   // features of this lane's run inside the row
-    float b0[C], b1[C];
-    if constexpr (!SPLIT) {
+    const int lim = left > 0 ? a.N - n0w - 4 * g : 0;
+    const int64_t ld = SPLIT ? a.ldp : a.F;
+    const uint32_t lane0 = (uint32_t)(4 * g * (int)ld + f);
+    auto offset = [&](int i, int r, uint32_t es) -> uint32_t { return 16 * i + r < lim ? lane0 * es : kOOB; };
+    auto wave_offset = [&](int i, int r, int es) -> int { return (16 * i + r) * (int)ld * es; };
+    const int64_t base = ((int64_t)part * a.N + n0w) * ld;
+    if constexpr (SPLIT) {
+      // Rows are padded to 8 columns, so every run that starts in one is whole.
+      const __amdgpu_buffer_rsrc_t r0 = make_rsrc(a.part + base);
+      const __amdgpu_buffer_rsrc_t r1 = make_rsrc(a.part + base + (GLU ? a.ldp / 2 : 0));
 #pragma unroll
-      for (int e = 0; e < C; ++e) {
-        b0[e] = (a.b[0] && e < left) ? load1<T>((const T*)a.b[0] + f + e) : 0.f;
-        b1[e] = (GLU && a.b[1] && e < left) ? load1<T>((const T*)a.b[1] + f + e) : 0.f;
+      for (int i = 0; i < MI; ++i) {
+        f32x4 z[NJ];
+#pragma unroll
+        for (int j = 0; j < NJ; ++j) z[j] = block_sums<T>(acc[i][j]);
+#pragma unroll
+        for (int r = 0; r < 4; ++r) {
+          float s0[C], s1[C];
+#pragma unroll
+          for (int e = 0; e < C; ++e) {
+            s0[e] = z[e][r];
+            s1[e] = z[NJ - C + e][r];
+          }
+          buf_store_vec<float, C>(r0, offset(i, r, 4), wave_offset(i, r, 4), s0);
+          if constexpr (GLU) buf_store_vec<float, C>(r1, offset(i, r, 4), wave_offset(i, r, 4), s1);
+        }
+        __builtin_amdgcn_sched_barrier(0);
       }
+    } else {
+      constexpr int ES = sizeof(T);
+      const __amdgpu_buffer_rsrc_t ry = make_rsrc((const T*)a.y + base);
+      const __amdgpu_buffer_rsrc_t rr = make_rsrc((const T*)a.residual + base);
+      const __amdgpu_buffer_rsrc_t rz0 = make_rsrc(a.z[0] + base);
+      const __amdgpu_buffer_rsrc_t rz1 = make_rsrc(a.z[1] + base);
+      const bool res = !GLU && a.residual != nullptr, keep = a.z[0] != nullptr;
+      auto rows = [&](auto whole) {   // whole: vec, as a constant
+        unrolled<MI>([&](auto block) {
+          constexpr int i = block.value;
+          constexpr bool kVec = whole.value;
+          float rs[4][C];
+          if constexpr (!GLU) {
+            if (res) {
+#pragma unroll
+              for (int r = 0; r < 4; ++r) {
+                if constexpr (kVec) buf_load_vec<T, C>(rr, offset(i, r, ES), wave_offset(i, r, ES), rs[r]);
+                else if (16 * i + r < lim)
+                  load_some<T, C>((const T*)a.residual + base + lane0 + (16 * i + r) * ld, left, rs[r]);
+              }
+            }
+          }
+          f32x4 z[NJ];
+#pragma unroll
+          for (int j = 0; j < NJ; ++j) z[j] = block_sums<T>(acc[i][j]);
+#pragma unroll
+          for (int r = 0; r < 4; ++r) {
+            float z0[C], z1[C], v[C];
+#pragma unroll
+            for (int e = 0; e < C; ++e) {
+              z0[e] = z[e][r] + b0[e];
+              if constexpr (GLU) z1[e] = z[C + e][r] + b1[e];
+              v[e] = act_fwd<T, ACT>(z0[e]);
+              if constexpr (GLU) v[e] *= z1[e];
+              else if (res) v[e] += rs[r][e];
+            }
+            if constexpr (kVec) {
+              if (keep) {
+                buf_store_vec<float, C>(rz0, offset(i, r, 4), wave_offset(i, r, 4), z0);
+                if constexpr (GLU) buf_store_vec<float, C>(rz1, offset(i, r, 4), wave_offset(i, r, 4), z1);
+              }
+              buf_store_vec<T, C>(ry, offset(i, r, ES), wave_offset(i, r, ES), v);
+            } else if (16 * i + r < lim) {
+              const int64_t o = base + lane0 + (16 * i + r) * ld;
+              if (keep) {
+                store_some<float, C>(a.z[0] + o, left, z0);
+                if constexpr (GLU) store_some<float, C>(a.z[1] + o, left, z1);
+              }
+              store_some<T, C>((T*)a.y + o, left, v);
+            }
+          }
+          __builtin_amdgcn_sched_barrier(0);
+        });
+      };
+      if (vec) rows(std::true_type{});
+      else rows(std::false_type{});
     }
-    t += gridDim.x;
-    const bool more = sizeof(T) == 2 && t < total;
-    if constexpr (sizeof(T) == 2) {
-      // Each tile's epilogue stores at least 32 times per wave, after the next tile's first copies.
+  };
+  auto biases = [&](float (&b0)[C], float (&b1)[C]) {
+    const int f = f0 + (wn * 16 + c) * C;
+#pragma unroll
+    for (int e = 0; e < C; ++e) {
+      b0[e] = (!SPLIT && a.b[0] && f + e < a.F) ? load1<T>((const T*)a.b[0] + f + e) : 0.f;
+      b1[e] = (!SPLIT && GLU && a.b[1] && f + e < a.F) ? load1<T>((const T*)a.b[1] + f + e) : 0.f;
+    }
+  };
+  float b0[C], b1[C];
+  if constexpr (k16) {
+    FLCE_LDS(L, T);
+    TileCopy<true, true, Dma<true>, DB> tc;
+    auto begin = [&]() {
+      const Opnd<T> A = opa(), B = opb();
+      tc.da.init(A, n0, tid);
+      if constexpr (GLU) tc.db.init(B.p, (const T*)a.W[1] + k0, B.ld, a.F, f0, tid);
+      else tc.db.init(B, f0, tid, 2);
+      tc.begin(A, B, L, tid);
+    };
+    begin();
+    __builtin_amdgcn_s_waitcnt(waitcnt_vm_lgkm0<0>());   // the mainloop's first wait allows for an epilogue's stores
+    Acc acc;
+    while (true) {
+      const Opnd<T> A = opa(), B = opb();
+      const int n0c = n0, f0c = f0, part = SPLIT ? t / tiles : 0;
+      biases(b0, b1);
+      // Each tile's epilogue stores at least 32 times per wave after the next tile's first copies.
       gemm_tile_bf16_run<true, true, 32>(acc, A, B, A.kext, L, tid, tc);
+      t += gridDim.x;
+      const bool more = t < total;
       if (more) {
         place(t);
         begin();
       }
-    } else {
-      Stager<float, true> sa;
-      sa.init(A, n0, tid);
-      if constexpr (GLU) {
-        StagerGlu sb;
-        sb.init(B.p, (const T*)a.W[1] + k0, B.ld, a.F, f0, tid);
-        gemm_tile_f32_run(acc, A, sa, B, sb, A.kext, L, tid);
-      } else {
-        Stager<float, true> sb;
-        sb.init(B, f0, tid, true);
-        gemm_tile_f32_run(acc, A, sa, B, sb, A.kext, L, tid);
-      }
+      acc_drain();
+      tile(acc, n0c, f0c, part, b0, b1);
+      if (!more) break;
+      if (!SPLIT && !vec) __builtin_amdgcn_s_waitcnt(waitcnt_vm_lgkm0<0>());   // lanes past the row stored nothing
     }
-    acc_drain();
-    if constexpr (SPLIT) {
-      // 8 consecutive sums (gated: 4 and 4); rows are padded to 8 columns.
-      const int64_t row0 = (int64_t)part * a.N + n0w;
-      const __amdgpu_buffer_rsrc_t r0 = make_rsrc(a.part + row0 * a.ldp);
-      const __amdgpu_buffer_rsrc_t r1 = GLU ? make_rsrc(a.part + row0 * a.ldp + a.ldp / 2) : r0;
-#pragma unroll
-      for (int i = 0; i < 8; ++i) {
-        f32x4 z[8];
-#pragma unroll
-        for (int j = 0; j < 8; ++j) z[j] = acc_read4(acc[i][j]);
-#pragma unroll
-        for (int r = 0; r < 4; ++r) {
-          const int nl = 16 * i + 4 * g + r;
-          const uint32_t off = (n0w + nl < a.N && left > 0) ? (uint32_t)(nl * a.ldp + f) * 4u : kOOB;
-          const float lo[4] = {z[0][r], z[1][r], z[2][r], z[3][r]}, hi[4] = {z[4][r], z[5][r], z[6][r], z[7][r]};
-          buf_store_vec<float, 4>(r0, off, lo, true, 4);
-          buf_store_vec<float, 4>(r1, GLU ? off : off + 16, hi, true, 4);
-        }
-        __builtin_amdgcn_sched_barrier(0);
-      }
-    } else {
-      // Descriptors start at the wave's first token, so offsets stay below 128 * F * 4 bytes.
-      const int64_t base = (int64_t)n0w * a.F;
-      const __amdgpu_buffer_rsrc_t ry = make_rsrc((const T*)a.y + base);
-      const __amdgpu_buffer_rsrc_t rr = make_rsrc((const T*)a.residual + base);
-      const __amdgpu_buffer_rsrc_t rz0 = make_rsrc((const T*)a.z[0] + base);
-      const __amdgpu_buffer_rsrc_t rz1 = make_rsrc((const T*)a.z[1] + base);
-      const bool res = !GLU && a.residual != nullptr, keep = a.z[0] != nullptr;
-      auto offset = [&](int i, int r) -> uint32_t {
-        const int nl = 16 * i + 4 * g + r;
-        return (n0w + nl < a.N && left > 0) ? (uint32_t)(nl * a.F + f) * (uint32_t)sizeof(T) : kOOB;
-      };
-#pragma unroll
-      for (int i = 0; i < 8; ++i) {
-        float rs[4][C];
-        if (res) {
-#pragma unroll
-          for (int r = 0; r < 4; ++r) buf_load_vec<T, C>(rr, offset(i, r), rs[r], vec, left);
-        }
-        f32x4 z[8];
-#pragma unroll
-        for (int j = 0; j < 8; ++j) z[j] = acc_read4(acc[i][j]);
-#pragma unroll
-        for (int r = 0; r < 4; ++r) {
-          const uint32_t off = offset(i, r);
-          float z0[C], z1[C], v[C];
-#pragma unroll
-          for (int e = 0; e < C; ++e) {
-            z0[e] = z[e][r] + b0[e];
-            if constexpr (GLU) z1[e] = z[4 + e][r] + b1[e];
-          }
-          if (keep) {
-            buf_store_vec<T, C>(rz0, off, z0, vec, left);
-            if constexpr (GLU) buf_store_vec<T, C>(rz1, off, z1, vec, left);
-          }
-#pragma unroll
-          for (int e = 0; e < C; ++e) {
-            v[e] = act_fwd<T, ACT>(z0[e]);
-            if constexpr (GLU) v[e] *= z1[e];
-            if (res) v[e] += rs[r][e];
-          }
-          buf_store_vec<T, C>(ry, off, v, vec, left);
-        }
-        __builtin_amdgcn_sched_barrier(0);
-      }
-    }
-    if (!more) break;
+  } else {
+    biases(b0, b1);
+    AccF32 acc;
+    const Opnd<T> A = opa(), B = opb();
+    RowStager<false, false> sa;
+    RowStager<true, GLU> sb;
+    sa.init(A.p, nullptr, A.ld, a.N, n0, tid);
+    sb.init(B.p, (const float*)a.W[1] + k0, B.ld, a.F, f0, tid);
+    gemm_f32(acc, sa, A.kext, sb, B.kext, A.kext, tid);
+    tile(acc, n0, f0, SPLIT ? t / tiles : 0, b0, b1);
   }
 }
 
 // The epilogue of a split forward: thread i takes 8 features of one token.
-template <class T, bool GLU> __global__ void __launch_bounds__(256) layer_join_fwd_kernel(LayerFwd a) {
+template <class T, int ACT, bool GLU> __global__ void __launch_bounds__(256) layer_join_fwd_kernel(LayerFwd a) {
   const int F8 = (a.F + 7) / 8;
-  const bool vec = a.F % 8 == 0;
   for (int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x; i < (int64_t)a.N * F8; i += (int64_t)gridDim.x * 256) {
     const int n = (int)(i / F8), f = (int)(i - (int64_t)n * F8) * 8;
     const int left = min(8, a.F - f);
@@ -193,33 +214,26 @@ template <class T, bool GLU> __global__ void __launch_bounds__(256) layer_join_f
       }
     }
     const int64_t o = (int64_t)n * a.F + f;
-    float rs[8] = {};
-    if (!GLU && a.residual) {
-      if (vec) load_vec<T, 8>((const T*)a.residual + o, rs);
-      else for (int e = 0; e < left; ++e) rs[e] = load1<T>((const T*)a.residual + o + e);
+    float rs[8] = {}, t[8];
+    if (!GLU && a.residual) load_some<T, 8>((const T*)a.residual + o, left, rs);
+    if (a.b[0]) {
+      load_some<T, 8>((const T*)a.b[0] + f, left, t);
+#pragma unroll
+      for (int e = 0; e < 8; ++e) z0[e] += t[e];
+    }
+    if (GLU && a.b[1]) {
+      load_some<T, 8>((const T*)a.b[1] + f, left, t);
+#pragma unroll
+      for (int e = 0; e < 8; ++e) z1[e] += t[e];
     }
 #pragma unroll
     for (int e = 0; e < 8; ++e) {
-      if (e < left) {
-        if (a.b[0]) z0[e] += load1<T>((const T*)a.b[0] + f + e);
-        if (GLU && a.b[1]) z1[e] += load1<T>((const T*)a.b[1] + f + e);
-      }
-      v[e] = act_fwd_rt<T>(a.act, z0[e]);
+      v[e] = act_fwd<T, ACT>(z0[e]);
       v[e] = GLU ? v[e] * z1[e] : v[e] + rs[e];
     }
-    if (vec) {
-      if (a.z[0]) store_vec<T, 8>((T*)a.z[0] + o, z0);
-      if (GLU && a.z[1]) store_vec<T, 8>((T*)a.z[1] + o, z1);
-      store_vec<T, 8>((T*)a.y + o, v);
-    } else {
-#pragma unroll
-      for (int e = 0; e < 8; ++e) {
-        if (e >= left) continue;
-        if (a.z[0]) store1<T>((T*)a.z[0] + o + e, z0[e]);
-        if (GLU && a.z[1]) store1<T>((T*)a.z[1] + o + e, z1[e]);
-        store1<T>((T*)a.y + o + e, v[e]);
-      }
-    }
+    if (a.z[0]) store_some<float, 8>(a.z[0] + o, left, z0);
+    if (GLU && a.z[1]) store_some<float, 8>(a.z[1] + o, left, z1);
+    store_some<T, 8>((T*)a.y + o, left, v);
   }
 }
 
@@ -325,8 +339,8 @@ __global__ void __launch_bounds__(64 * kSkinnyWaves) layer_fwd_skinny_kernel(Lay
     if constexpr (GLU) v *= z[R - 1];
     else if (a.residual) v += load1<T>((const T*)a.residual + o);
     if (a.z[0]) {
-      store1<T>((T*)a.z[0] + o, z[0]);
-      if constexpr (GLU) store1<T>((T*)a.z[1] + o, z[R - 1]);
+      a.z[0][o] = z[0];
+      if constexpr (GLU) a.z[1][o] = z[R - 1];
     }
     store1<T>((T*)a.y + o, v);
   }
@@ -339,28 +353,30 @@ template <class T, bool GLU> static void launch_skinny(const LayerFwd& a, hipStr
   else FLCE_LAUNCH((layer_fwd_skinny_kernel<T, GLU, 4>), grid, blk, 0, st, a);
 }
 
-template <class T, bool GLU, int ACT> static void launch_fwd_act(const LayerFwd& a, dim3 grid, hipStream_t st) {
-  FLCE_LAUNCH((layer_fwd_kernel<T, ACT, GLU, false>), grid, dim3(kThreads), 0, st, a);
+// f.operator()<ACT>() for the activation.
+template <class F> static void with_act(int act, F&& f) {
+  switch (act) {
+    case kActRelu: return f(std::integral_constant<int, kActRelu>{});
+    case kActGelu: return f(std::integral_constant<int, kActGelu>{});
+    case kActGeluTanh: return f(std::integral_constant<int, kActGeluTanh>{});
+    case kActSilu: return f(std::integral_constant<int, kActSilu>{});
+    case kActSigmoid: return f(std::integral_constant<int, kActSigmoid>{});
+    default: return f(std::integral_constant<int, kActNone>{});
+  }
 }
 
 template <class T, bool GLU> static void launch_fwd(const LayerFwd& a, hipStream_t st) {
   if (a.N <= kSkinnyTokens) return launch_skinny<T, GLU>(a, st);
   const int total = a.TM * a.TN * a.parts;
-  const dim3 grid(sizeof(T) == 4 || total < kPersistGrid ? total : kPersistGrid);
+  const dim3 grid(sizeof(T) == 4 || total < kPersistGrid ? total : kPersistGrid), blk(kThreads);
   if (a.parts > 1) {
-    FLCE_LAUNCH((layer_fwd_kernel<T, kActNone, GLU, true>), grid, dim3(kThreads), 0, st, a);
+    FLCE_LAUNCH((layer_fwd_kernel<T, kActNone, GLU, true>), grid, blk, 0, st, a);
     const int64_t blocks = ((int64_t)a.N * ((a.F + 7) / 8) + 255) / 256;
-    FLCE_LAUNCH((layer_join_fwd_kernel<T, GLU>), dim3((unsigned)(blocks < 4096 ? blocks : 4096)), dim3(256), 0, st, a);
+    const dim3 gj((unsigned)(blocks < 4096 ? blocks : 4096));
+    with_act(a.act, [&](auto act) { FLCE_LAUNCH((layer_join_fwd_kernel<T, act.value, GLU>), gj, dim3(256), 0, st, a); });
     return;
   }
-  switch (a.act) {
-    case kActRelu: return launch_fwd_act<T, GLU, kActRelu>(a, grid, st);
-    case kActGelu: return launch_fwd_act<T, GLU, kActGelu>(a, grid, st);
-    case kActGeluTanh: return launch_fwd_act<T, GLU, kActGeluTanh>(a, grid, st);
-    case kActSilu: return launch_fwd_act<T, GLU, kActSilu>(a, grid, st);
-    case kActSigmoid: return launch_fwd_act<T, GLU, kActSigmoid>(a, grid, st);
-    default: return launch_fwd_act<T, GLU, kActNone>(a, grid, st);
-  }
+  with_act(a.act, [&](auto act) { FLCE_LAUNCH((layer_fwd_kernel<T, act.value, GLU, false>), grid, blk, 0, st, a); });
 }
 
 // ---------------------------------------------------------------------------
@@ -375,7 +391,6 @@ template <class T, int ACT, bool GLU> __global__ void __launch_bounds__(256) lay
   constexpr int R = GLU ? 2 : 1;
   const int tid = threadIdx.x, f = (blockIdx.x * 32 + (tid & 31)) * 8;
   const int n1 = min(a.N, (int)(blockIdx.y + 1) * a.db_rows);
-  const bool vec = a.F % 8 == 0;
   const int left = a.F - f;
   const int width = GLU ? a.segk : (int)a.ldz;   // columns of one weight in dz
   float sum[R][8] = {};
@@ -383,20 +398,10 @@ template <class T, int ACT, bool GLU> __global__ void __launch_bounds__(256) lay
 #pragma unroll 2
     for (int n = blockIdx.y * a.db_rows + (tid >> 5); n < n1; n += 8) {
       const int64_t o = (int64_t)n * a.F + f;
-      float dy[8] = {}, z0[8] = {}, z1[8] = {}, d[R][8];
-      if (vec && left > 0) {
-        load_vec<T, 8>((const T*)a.dy + o, dy);
-        if (ACT != kActNone || GLU) load_vec<T, 8>((const T*)a.z[0] + o, z0);
-        if (GLU) load_vec<T, 8>((const T*)a.z[1] + o, z1);
-      } else {
-#pragma unroll
-        for (int e = 0; e < 8; ++e) {
-          if (e >= left) continue;
-          dy[e] = load1<T>((const T*)a.dy + o + e);
-          if (ACT != kActNone || GLU) z0[e] = load1<T>((const T*)a.z[0] + o + e);
-          if (GLU) z1[e] = load1<T>((const T*)a.z[1] + o + e);
-        }
-      }
+      float dy[8], z0[8] = {}, z1[8] = {}, d[R][8];
+      load_some<T, 8>((const T*)a.dy + o, left, dy);
+      if (ACT != kActNone || GLU) load_some<float, 8>(a.z[0] + o, left, z0);
+      if (GLU) load_some<float, 8>(a.z[1] + o, left, z1);
 #pragma unroll
       for (int e = 0; e < 8; ++e) {
         float v;
@@ -429,38 +434,54 @@ template <class T, int ACT, bool GLU> __global__ void __launch_bounds__(256) lay
   }
 }
 
-// db[m][f] = the partial sums added in block order: 64 columns a workgroup, a
-// quarter of the blocks per thread.
-template <class T> __global__ void __launch_bounds__(256) layer_db_kernel(LayerBwd a) {
-  __shared__ float red[4][64];
-  const int cl = threadIdx.x & 63, q = threadIdx.x >> 6, f = blockIdx.x * 64 + cl, m = blockIdx.y;
+// db[m][f] = the blocks' sums added in block order.
+template <class T> __device__ __forceinline__ void column_sum(const LayerBwd& a, int m, int f) {
   const float* p = a.dbp + m * (a.ldb / a.nmat) + f;
   float s = 0.f;
-  if (f < a.F) {
-#pragma unroll 4
-    for (int b = q; b < a.db_blocks; b += 4) s += p[b * a.ldb];
-  }
-  red[q][cl] = s;
-  __syncthreads();
-  if (q == 0 && f < a.F && a.db[m]) store1<T>((T*)a.db[m] + f, (red[0][cl] + red[1][cl]) + (red[2][cl] + red[3][cl]));
+#pragma unroll 8
+  for (int b = 0; b < a.db_blocks; ++b) s += p[b * a.ldb];
+  store1<T>((T*)a.db[m] + f, s);
+}
+
+// db of the weights whose gradient no launch of layer_dw_kernel forms.
+template <class T> __global__ void __launch_bounds__(256) layer_db_kernel(LayerBwd a) {
+  const int f = blockIdx.x * 256 + threadIdx.x, m = blockIdx.y;
+  if (f < a.F && a.db[m] && !a.dW[m]) column_sum<T>(a, m, f);
 }
 
 // dx[n][h] = sum over the rows f of W (gated: of Wg, then of Wu) of
 // dz[n][f] W[f][h]: C[h][n], so a lane holds four consecutive h of a token.
 // Workgroup b computes tile b % G over part b / G of K.
-template <class T, bool SPLIT> __global__ void __launch_bounds__(kThreads, 1) layer_dx_kernel(LayerBwd a, int TH, int TM) {
-  FLCE_LDS(L, T);
+template <class T, bool SPLIT>
+__global__ void __launch_bounds__(kThreads, Tile<T>::kPerCu) layer_dx_kernel(LayerBwd a, int TH, int TM) {
+  typedef Tile<T> TS;
   const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6, wm = wave >> 1, wn = wave & 1;
   const int G = TH * TM, part = SPLIT ? blockIdx.x / G : 0;
   int tm, tn;
   tile_coords(blockIdx.x - part * G, G, TH, TM, tm, tn);
-  const int h0 = tm * kTile, n0 = tn * kTile, k0 = part * a.dx_kc;
+  const int h0 = tm * TS::M, n0 = tn * TS::N, k0 = part * a.dx_kc;
   const int K = max(1, min(a.dx_kc, (int)a.ldz - k0));
   const SegRows rows{{a.W[0], a.W[1]}, a.H, a.F, a.segk, k0};
-  const Opnd<T> A{(const T*)a.W[0], a.H, a.H, K};   // K only: rows past F read zeros
-  const Opnd<T> B{(const T*)a.dz + k0, a.ldz, a.N, (int)a.ldz - k0};
-  Acc acc;
+  auto epilogue = [&](auto& acc) {
+#pragma unroll
+    for (int j = 0; j < TS::NJ; ++j) {
+      const int n = n0 + wn * 16 * TS::NJ + 16 * j + (lane & 15);
+#pragma unroll
+      for (int i = 0; i < TS::MI; ++i) {
+        const f32x4 z = block_sums<T>(acc[i][j]);
+        const int h = h0 + wm * 16 * TS::MI + 16 * i + 4 * (lane >> 4);
+        if (n < a.N && h < a.H) {
+          if constexpr (SPLIT) *(f32x4*)(a.part + ((int64_t)part * a.N + n) * a.H + h) = z;
+          else store4<T>((T*)a.dx + (int64_t)n * a.H + h, z[0], z[1], z[2], z[3]);
+        }
+      }
+    }
+  };
   if constexpr (sizeof(T) == 2) {
+    FLCE_LDS(L, T);
+    const Opnd<T> A{(const T*)a.W[0], a.H, a.H, K};   // K only: rows past F read zeros
+    const Opnd<T> B{(const T*)a.dz + k0, a.ldz, a.N, (int)a.ldz - k0};
+    Acc acc;
     TileCopy<false, true, DmaSeg, Dma<true>> tc;
     tc.da.d.init(A, h0, tid);
     tc.da.s = rows;
@@ -468,63 +489,70 @@ template <class T, bool SPLIT> __global__ void __launch_bounds__(kThreads, 1) la
     tc.db.init(B, n0, tid);
     tc.begin(A, B, L, tid);
     gemm_tile_bf16_run<false, true>(acc, A, B, K, L, tid, tc);
+    acc_drain();
+    epilogue(acc);
   } else {
-    StagerSeg sa;
-    sa.st.init(A, h0, tid);
-    sa.s = rows;
-    sa.m0 = h0;
-    Stager<float, true> sb;
-    sb.init(B, n0, tid);
-    gemm_tile_f32_run(acc, A, sa, B, sb, K, L, tid);
-  }
-  acc_drain();
-  const int g = lane >> 4;
-#pragma unroll
-  for (int j = 0; j < 8; ++j) {
-    const int n = n0 + wn * kWaveTile + 16 * j + (lane & 15);
-#pragma unroll
-    for (int i = 0; i < 8; ++i) {
-      const f32x4 z = acc_read4(acc[i][j]);
-      const int h = h0 + wm * kWaveTile + 16 * i + 4 * g;
-      if (n < a.N && h < a.H) {
-        if constexpr (SPLIT) *(f32x4*)(a.part + ((int64_t)part * a.N + n) * a.H + h) = z;
-        else store4<T>((T*)a.dx + (int64_t)n * a.H + h, z[0], z[1], z[2], z[3]);
-      }
-    }
+    AccF32 acc;
+    ColStager sa;
+    RowStager<false, false> sb;
+    sa.init(rows, a.H, h0, tid);
+    sb.init((const float*)a.dz + k0, nullptr, a.ldz, a.N, n0, tid);
+    gemm_f32(acc, sa, K, sb, (int)a.ldz - k0, K, tid);
+    epilogue(acc);
   }
 }
 
 // dW[f][h] = sum_n dz[n][f] x[n][h]: C[h][f].  Column tile tn belongs to
-// weight m0 + tn / TF.  SPLIT: part b / G of the tokens.
+// weight m0 (tn < TF) or the next.  SPLIT: part b / G of the tokens.
+// The weight is told by a compare: a division put the descriptors' addresses
+// into vector registers, which costs a loop over the lanes at every copy (the
+// product at N=8192, H=4096, 24576 rows took 1463 us so).  The first H tile's
+// workgroups also finish db for their columns.
 template <class T, bool SPLIT>
-__global__ void __launch_bounds__(kThreads, 1) layer_dw_kernel(LayerBwd a, int TH, int TF, int m0, int mats) {
-  FLCE_LDS(L, T);
+__global__ void __launch_bounds__(kThreads, Tile<T>::kPerCu) layer_dw_kernel(LayerBwd a, int TH, int TF, int m0,
+                                                                            int mats) {
+  typedef Tile<T> TS;
   const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6, wm = wave >> 1, wn = wave & 1;
   const int G = TH * TF * mats, part = SPLIT ? blockIdx.x / G : 0;
   int tm, tn;
   tile_coords(blockIdx.x - part * G, G, TH, TF * mats, tm, tn);
-  const int m = m0 + tn / TF;
-  const int h0 = tm * kTile, f0 = (tn - (m - m0) * TF) * kTile, k0 = part * a.dw_kc;
+  const int second = tn >= TF ? 1 : 0, m = m0 + second;
+  const int h0 = tm * TS::M, f0 = (tn - second * TF) * TS::N, k0 = part * a.dw_kc;
   const int K = min(a.dw_kc, a.N - k0);
   const int width = a.nmat == 2 ? a.segk : (int)a.ldz;
-  const Opnd<T> A{(const T*)a.x + (int64_t)k0 * a.H, a.H, a.H, max(K, 0)};
-  const Opnd<T> B{(const T*)a.dz + (int64_t)k0 * a.ldz + (m ? a.segk : 0), a.ldz, width, max(K, 0)};
-  Acc acc;
-  gemm_tile<T, false, false>(acc, A, h0, B, f0, max(K, 1), L, tid);   // K >= 1: no token sums zeros
-  acc_drain();
-  const int g = lane >> 4;
+  const T* x = (const T*)a.x + (int64_t)k0 * a.H;
+  const T* dz = (const T*)a.dz + (int64_t)k0 * a.ldz + (int64_t)m * a.segk;
+  if (tm == 0 && part == 0 && a.db[m] && tid < TS::N && f0 + tid < a.F) column_sum<T>(a, m, f0 + tid);
+  auto epilogue = [&](auto& acc) {
 #pragma unroll
-  for (int j = 0; j < 8; ++j) {
-    const int f = f0 + wn * kWaveTile + 16 * j + (lane & 15);
+    for (int j = 0; j < TS::NJ; ++j) {
+      const int f = f0 + wn * 16 * TS::NJ + 16 * j + (lane & 15);
 #pragma unroll
-    for (int i = 0; i < 8; ++i) {
-      const f32x4 z = acc_read4(acc[i][j]);
-      const int h = h0 + wm * kWaveTile + 16 * i + 4 * g;
-      if (f < a.F && h < a.H) {
-        if constexpr (SPLIT) *(f32x4*)(a.part + (((int64_t)part * mats + (m - m0)) * a.F + f) * a.H + h) = z;
-        else store4<T>((T*)a.dW[m] + (int64_t)f * a.H + h, z[0], z[1], z[2], z[3]);
+      for (int i = 0; i < TS::MI; ++i) {
+        const f32x4 z = block_sums<T>(acc[i][j]);
+        const int h = h0 + wm * 16 * TS::MI + 16 * i + 4 * (lane >> 4);
+        if (f < a.F && h < a.H) {
+          if constexpr (SPLIT) *(f32x4*)(a.part + (((int64_t)part * mats + second) * a.F + f) * a.H + h) = z;
+          else store4<T>((T*)a.dW[m] + (int64_t)f * a.H + h, z[0], z[1], z[2], z[3]);
+        }
       }
     }
+  };
+  if constexpr (sizeof(T) == 2) {
+    FLCE_LDS(L, T);
+    const Opnd<T> A{x, a.H, a.H, max(K, 0)};
+    const Opnd<T> B{dz, a.ldz, width, max(K, 0)};
+    Acc acc;
+    gemm_tile<T, false, false>(acc, A, h0, B, f0, max(K, 1), L, tid);   // K >= 1: no token sums zeros
+    acc_drain();
+    epilogue(acc);
+  } else {
+    AccF32 acc;
+    ColStager sa, sb;
+    sa.init(SegRows{{x, x}, a.H, max(K, 0), 1 << 30, 0}, a.H, h0, tid);
+    sb.init(SegRows{{dz, dz}, a.ldz, max(K, 0), 1 << 30, 0}, width, f0, tid);
+    gemm_f32(acc, sa, K, sb, K, max(K, 1), tid);
+    epilogue(acc);
   }
 }
 
@@ -546,31 +574,22 @@ template <class T> static void launch_join(const float* part, int parts, int64_t
               (T*)d0, (T*)d1);
 }
 
-template <class T, bool GLU, int ACT> static void launch_dz_act(const LayerBwd& a, hipStream_t st) {
-  const int width = GLU ? a.segk : (int)a.ldz;
-  FLCE_LAUNCH((layer_dz_kernel<T, ACT, GLU>), dim3((width + 255) / 256, a.db_blocks), dim3(256), 0, st, a);
-}
-
 template <class T, bool GLU> static void launch_dz(const LayerBwd& a, hipStream_t st) {
-  switch (a.act) {
-    case kActRelu: return launch_dz_act<T, GLU, kActRelu>(a, st);
-    case kActGelu: return launch_dz_act<T, GLU, kActGelu>(a, st);
-    case kActGeluTanh: return launch_dz_act<T, GLU, kActGeluTanh>(a, st);
-    case kActSilu: return launch_dz_act<T, GLU, kActSilu>(a, st);
-    case kActSigmoid: return launch_dz_act<T, GLU, kActSigmoid>(a, st);
-    default: return launch_dz_act<T, GLU, kActNone>(a, st);
-  }
+  const int width = GLU ? a.segk : (int)a.ldz;
+  const dim3 grid((width + 255) / 256, a.db_blocks);
+  with_act(a.act, [&](auto act) { FLCE_LAUNCH((layer_dz_kernel<T, act.value, GLU>), grid, dim3(256), 0, st, a); });
 }
 
 template <class T> static void launch_bwd(const LayerBwd& a, hipStream_t st) {
-  const int TH = (a.H + kTile - 1) / kTile, TM = (a.N + kTile - 1) / kTile, TF = (a.F + kTile - 1) / kTile;
+  typedef Tile<T> TS;
+  const int TH = (a.H + TS::M - 1) / TS::M, TM = (a.N + TS::N - 1) / TS::N, TF = (a.F + TS::N - 1) / TS::N;
   const dim3 blk(kThreads);
-  const bool want_db = a.db[0] || a.db[1];
-  if (a.N > 0 && (!a.dz_is_dy || want_db)) {
+  if (a.N > 0 && (!a.dz_is_dy || a.db[0] || a.db[1])) {
     if (a.nmat == 2) launch_dz<T, true>(a, st);
     else launch_dz<T, false>(a, st);
   }
-  if (want_db) FLCE_LAUNCH((layer_db_kernel<T>), dim3((a.F + 63) / 64, a.nmat), dim3(256), 0, st, a);
+  if ((a.db[0] && !a.dW[0]) || (a.db[1] && !a.dW[1]))
+    FLCE_LAUNCH((layer_db_kernel<T>), dim3((a.F + 255) / 256, a.nmat), dim3(256), 0, st, a);
   if (a.dx && a.N > 0) {
     if (a.dx_parts > 1) {
       FLCE_LAUNCH((layer_dx_kernel<T, true>), dim3(TH * TM * a.dx_parts), blk, 0, st, a, TH, TM);

@@ -427,9 +427,10 @@ def _dense(t: Optional[torch.Tensor]) -> Optional[torch.Tensor]:
     return t if t.data_ptr() % 16 == 0 else t.clone()
 
 
-def _prep_layer(x, weights, rows, bias=()):
+def _prep_layer(x, weights, rows, bias=(), kept=()):
     """The operands of a feed-forward call, checked and dense, with H padded to
-    a multiple of 8: x [N, H], weights [F, H], rows [N, F] (or None), bias [F] (or None)."""
+    a multiple of 8: x [N, H], weights [F, H], rows [N, F] (or None), bias [F]
+    (or None); kept: float32 pre-activations [N, F] (or None)."""
     if x.dim() != 2 or any(w.dim() != 2 for w in weights):
         raise ValueError("x must be [N, H] and the weights [F, H]")
     if not x.is_cuda:
@@ -439,7 +440,7 @@ def _prep_layer(x, weights, rows, bias=()):
     for w in weights:
         if tuple(w.shape) != (F, H):
             raise ValueError("x and the weights disagree on their sizes")
-    for t in rows:
+    for t in (*rows, *kept):
         if t is not None and tuple(t.shape) != (N, F):
             raise ValueError(f"expected a tensor of shape {(N, F)}, not {tuple(t.shape)}")
     for b in bias:
@@ -448,13 +449,17 @@ def _prep_layer(x, weights, rows, bias=()):
     for t in (*weights, *rows, *bias):
         if t is not None and t.dtype != x.dtype:
             raise TypeError("all tensors must share one dtype")
+    for t in kept:
+        if t is not None and t.dtype != torch.float32:
+            raise TypeError("the kept pre-activations are float32")
+    for t in (*weights, *rows, *bias, *kept):
         if t is not None and t.device != x.device:
             raise ValueError("all tensors must be on one device")
     if H < 1 or F < 1:
         raise ValueError("H and F must be at least 1")
     _dtype_code(x)
     return ([_pad_hidden(_dense(t)) for t in (x, *weights)], [_dense(t) for t in rows],
-            [b.contiguous() if b is not None else None for b in bias])
+            [b.contiguous() if b is not None else None for b in bias], [_dense(t) for t in kept])
 
 
 def _workspace(workspace: Optional[torch.Tensor], nbytes: int, dev) -> Optional[torch.Tensor]:
@@ -490,17 +495,17 @@ def flce_linear_workspace_size(N: int, H: int, F: int, dtype: torch.dtype,
 def flce_linear_forward(x: torch.Tensor, W: torch.Tensor, b: Optional[torch.Tensor] = None,
                         residual: Optional[torch.Tensor] = None, activation: str = "none", keep: bool = False,
                         workspace: Optional[torch.Tensor] = None, out: Optional[torch.Tensor] = None):
-    """act(x W^T + b) + residual.  Returns (y, z): z the pre-activations that
-    flce_linear_backward takes, with keep and an activation, else None.
+    """act(x W^T + b) + residual.  Returns (y, z): z the float32 pre-activations
+    that flce_linear_backward takes, with keep and an activation, else None.
     out: the tensor to write y to (it may be residual)."""
     act = _activation_code(activation)
     N, F = x.shape[0], W.shape[0]
-    (x, W), (residual_, out_), (b,) = _prep_layer(x, (W,), (residual, out), (b,))
+    (x, W), (residual_, out_), (b,), _ = _prep_layer(x, (W,), (residual, out), (b,))
     if out is not None and (out_ is not out or (residual_ is not residual and residual is out)):
         raise ValueError("out must be contiguous from a 16-byte boundary")
     dt, dev, H = _dtype_code(x), x.device, x.shape[1]
     y = out if out is not None else torch.empty(N, F, dtype=x.dtype, device=dev)
-    z = torch.empty(N, F, dtype=x.dtype, device=dev) if keep and activation != "none" else None
+    z = torch.empty(N, F, dtype=torch.float32, device=dev) if keep and activation != "none" else None
     fwd_bytes, _ = _lib.flce_linear_workspace_size(N, H, F, dt, act)
     workspace = _workspace(workspace, fwd_bytes, dev)
     with torch.cuda.device(dev):
@@ -521,7 +526,7 @@ def flce_linear_backward(x: torch.Tensor, W: torch.Tensor, dy: torch.Tensor, z: 
     elif z is None:
         raise ValueError("z is what flce_linear_forward returned with keep=True")
     H0, N, F = x.shape[-1], x.shape[0], W.shape[0]
-    (x, W), (dy, z), _ = _prep_layer(x, (W,), (dy, z))
+    (x, W), (dy,), _, (z,) = _prep_layer(x, (W,), (dy,), kept=(z,))
     dt, dev, H = _dtype_code(x), x.device, x.shape[1]
     dx, (dW,) = _layer_grads(x, H0, H, F, (W,), need_dx, (need_dW,))
     db = torch.empty(F, dtype=x.dtype, device=dev) if need_db else None
@@ -543,13 +548,13 @@ def flce_glu_forward(x: torch.Tensor, Wg: torch.Tensor, Wu: torch.Tensor, bg: Op
                      bu: Optional[torch.Tensor] = None, activation: str = "silu", keep: bool = False,
                      workspace: Optional[torch.Tensor] = None):
     """h = act(x Wg^T + bg) * (x Wu^T + bu).  Returns (h, g, u): the two
-    projections that flce_glu_backward takes, with keep, else None."""
+    projections, float32, that flce_glu_backward takes, with keep, else None."""
     act = _activation_code(activation)
     N, F = x.shape[0], Wg.shape[0]
-    (x, Wg, Wu), _, (bg, bu) = _prep_layer(x, (Wg, Wu), (), (bg, bu))
+    (x, Wg, Wu), _, (bg, bu), _ = _prep_layer(x, (Wg, Wu), (), (bg, bu))
     dt, dev, H = _dtype_code(x), x.device, x.shape[1]
     h = torch.empty(N, F, dtype=x.dtype, device=dev)
-    g, u = (torch.empty_like(h), torch.empty_like(h)) if keep else (None, None)
+    g, u = (torch.empty(N, F, dtype=torch.float32, device=dev) for _ in range(2)) if keep else (None, None)
     fwd_bytes, _ = _lib.flce_glu_workspace_size(N, H, F, dt)
     workspace = _workspace(workspace, fwd_bytes, dev)
     with torch.cuda.device(dev):
@@ -568,7 +573,7 @@ def flce_glu_backward(x: torch.Tensor, Wg: torch.Tensor, Wu: torch.Tensor, g: to
     if g is None or u is None:
         raise ValueError("g and u are what flce_glu_forward returned with keep=True")
     H0, N, F = x.shape[-1], x.shape[0], Wg.shape[0]
-    (x, Wg, Wu), (g, u, dh), _ = _prep_layer(x, (Wg, Wu), (g, u, dh))
+    (x, Wg, Wu), (dh,), _, (g, u) = _prep_layer(x, (Wg, Wu), (dh,), kept=(g, u))
     dt, dev, H = _dtype_code(x), x.device, x.shape[1]
     dx, (dWg, dWu) = _layer_grads(x, H0, H, F, (Wg, Wu), need_dx, (need_dWg, need_dWu))
     dbg, dbu = ((torch.empty(F, dtype=x.dtype, device=dev), torch.empty(F, dtype=x.dtype, device=dev)) if need_db
