@@ -978,32 +978,80 @@ flce_status flce_shard_backward(const void* x, const void* W_shard, const void* 
 
 namespace {
 
-// K parts of a product with `tiles` output tiles.  Tiles that fill over half
-// the places for workgroups (one per CU; two for fp32's smaller tiles) are not
-// split; fewer are, into as many parts as fill them, each at least 512 deep and
-// at most 16: every part costs a pass over an fp32 copy of the output.
-int product_parts(int64_t tiles, int64_t K, int dtype) {
-  const int64_t places = dtype == FLCE_F32 ? 2 * kCUs : kCUs;
-  if (2 * tiles > places) return 1;
-  int64_t p = places / tiles;
-  if (p > K / 512) p = K / 512;
-  if (p > 16) p = 16;
-  return p < 2 ? 1 : (int)p;
-}
+// How a product of M x N outputs over K is cut: output tiles of 32 S x 32 S
+// (S = 8, 16-bit only; 4; 2) and parts of K.
+struct Cut {
+  int S, parts;
+};
 
 // Depth of a part: the 64-deep copy block divides it, so every part starts on
 // a block.
-int64_t part_depth(int64_t K, int parts) { return parts > 1 ? cdiv(cdiv(K, parts), 64) * 64 : K; }
+int64_t part_depth(int64_t K, int64_t parts) { return parts > 1 ? cdiv(cdiv(K, parts), 64) * 64 : K; }
+
+// The cut with the least estimated time, in ns, of the busiest CU's q tiles:
+//   q * per_tile + K * max(alone, q * shared) + fixed,
+// `alone` a tile's time per K when nothing else is on its CU (the latency of
+// its loop) and `shared` what a tile costs a full CU.  A split adds a launch and
+// the fp32 partial sums' way out and back.  Fitted to bf16 and fp32 runs of 16
+// shapes from 100 x 64 x 64 to 517 x 20480 x 4096 at each S (no bias, no
+// activation): within a fifth of most, and it picks the fastest or one within
+// 15% of it.  Some of them, us at S = 8 / 4 / 2: 300 x 700 x 500 20.4 / 8.4 / 5.0,
+// 1024 x 4096 x 1024 23.5 / 16.3 / 10.8, 2048 x 4096 x 1024 35.6 / 17.4 / 24.1,
+// 4096 x 4096 x 4096 90 / 120 / 175; fp32 300 x 700 x 500 - / 37 / 12,
+// 4096 x 4096 x 1024 - / 275 / 294.
+struct TileCost {
+  int S;
+  double alone, shared, per_tile, fixed;
+};
+constexpr TileCost kCost16[] = {{8, 20.0, 20.0, 7000.0, 0.0}, {4, 10.5, 7.3, 500.0, 1000.0}, {2, 8.0, 2.7, 200.0, 800.0}};
+constexpr TileCost kCost32[] = {{4, 72.0, 67.0, 500.0, 1500.0}, {2, 23.0, 18.0, 200.0, 1000.0}};
+constexpr double kJoinNs = 1500.0, kJoinNsPerByte = 0.235e-3;
+
+// FLCE_DEBUG_LAYER_TILE: the tests run every S (2, 4, 8) on every shape with it,
+// and 1 the few-token kernel wherever it fits.
+int forced_tile() {
+  const char* env = std::getenv("FLCE_DEBUG_LAYER_TILE");
+  return env ? std::atoi(env) : 0;
+}
+
+Cut product_cut(int64_t M, int64_t N, int64_t K, int dtype) {
+  Cut best{2, 1};
+  if (M < 1 || N < 1) return best;
+  const int forced = forced_tile();
+  double least = 0.0;
+  auto consider = [&](const TileCost& t) {
+    if ((forced == 2 || forced == 4 || (forced == 8 && dtype != FLCE_F32)) && t.S != forced) return;
+    const int64_t tiles = cdiv(M, 32 * t.S) * cdiv(N, 32 * t.S);
+    for (int64_t parts : {1, 2, 3, 4, 6, 8, 12, 16}) {
+      const int64_t kc = part_depth(K, parts);
+      if (parts > 1 && (kc < 256 || cdiv(K, kc) != parts)) continue;
+      const double q = (double)cdiv(tiles * parts, kCUs);
+      const double loop = (double)kc * (t.S == 8 ? q * t.shared : std::max(t.alone, q * t.shared));
+      double ns = t.fixed + q * t.per_tile + loop;
+      if (parts > 1) ns += kJoinNs + kJoinNsPerByte * 4.0 * (double)parts * (double)M * (double)N;
+      if (least == 0.0 || ns < least) {
+        least = ns;
+        best = {t.S, (int)parts};
+      }
+    }
+  };
+  if (dtype == FLCE_F32) {
+    for (const TileCost& t : kCost32) consider(t);
+  } else {
+    for (const TileCost& t : kCost16) consider(t);
+  }
+  return best;
+}
 
 struct LayerGeometry {
-  int TM, TN, fwd_parts;
+  int fwd_tile, TM, TN, fwd_parts;
   int64_t kc, ldp;
   size_t fwd_total;
   bool dz_is_dy;
   int64_t ldz, segk;
   int db_blocks, db_rows;
   int64_t ldb;
-  int dx_parts, dw_parts;
+  int dx_tile, dx_parts, dw_tile, dw_parts;
   int64_t dx_kc, dw_kc;
   size_t off_dbp, off_part, bwd_total;
 };
@@ -1011,10 +1059,13 @@ struct LayerGeometry {
 LayerGeometry layer_geometry(int64_t N, int64_t H, int64_t F, int dtype, int act, int nmat) {
   LayerGeometry g{};
   const int64_t es = dtype == FLCE_F32 ? 4 : 2;
-  const int64_t tile = flce::layer_tile(dtype);
-  g.TM = (int)cdiv(N, tile);
-  g.TN = (int)cdiv(F, tile / nmat);
-  g.fwd_parts = N > flce::kSkinnyTokens ? product_parts((int64_t)g.TM * g.TN, H, dtype) : 1;
+  Cut fwd = product_cut(N, nmat * F, H, dtype);
+  const int forced = forced_tile();
+  if (forced == 1 ? N <= flce::kSkinnyMost : forced == 0 && N <= flce::skinny_tokens(dtype)) fwd = {0, 1};
+  g.fwd_tile = fwd.S;
+  g.TM = fwd.S ? (int)cdiv(N, 32 * fwd.S) : 0;
+  g.TN = fwd.S ? (int)cdiv(F, 32 * fwd.S / nmat) : 0;
+  g.fwd_parts = fwd.parts;
   g.kc = part_depth(H, g.fwd_parts);
   g.ldp = nmat * cdiv(F, 8) * 8;
   g.fwd_total = g.fwd_parts > 1 ? align_up((size_t)g.fwd_parts * N * g.ldp * 4) : 0;
@@ -1033,9 +1084,11 @@ LayerGeometry layer_geometry(int64_t N, int64_t H, int64_t F, int dtype, int act
   g.ldb = nmat * F;
   g.off_dbp = off;
   off = align_up(off + (size_t)g.db_blocks * g.ldb * 4);
-  const int64_t th = cdiv(H, tile), tf = cdiv(F, tile);
-  g.dx_parts = N > 0 ? product_parts(th * g.TM, g.ldz, dtype) : 1;
-  g.dw_parts = product_parts(th * tf * nmat, N, dtype);
+  const Cut cx = product_cut(H, N, g.ldz, dtype), cw = product_cut(H, nmat * F, N, dtype);
+  g.dx_tile = cx.S;
+  g.dx_parts = cx.parts;
+  g.dw_tile = cw.S;
+  g.dw_parts = cw.parts;
   g.dx_kc = part_depth(g.ldz, g.dx_parts);
   g.dw_kc = part_depth(N, g.dw_parts);
   g.off_part = off;
@@ -1053,7 +1106,8 @@ flce_status check_layer(int64_t N, int64_t H, int64_t F, int dtype, int act, int
     return FLCE_ERR_UNSUPPORTED;
   if (H % 8 != 0) return FLCE_ERR_UNSUPPORTED;
   const int64_t wide = H > F ? H : F;   // every plane of output tiles fits in an int
-  if (cdiv(N, 128) * cdiv(wide, 64) > (int64_t(1) << 27)) return FLCE_ERR_UNSUPPORTED;
+  if (cdiv(N, 64) * cdiv(wide, 32) > (int64_t(1) << 27) || cdiv(F, 32) * cdiv(H, 64) > (int64_t(1) << 27))
+    return FLCE_ERR_UNSUPPORTED;
   return FLCE_OK;
 }
 
@@ -1087,7 +1141,7 @@ flce_status layer_forward(const void* x, const void* const (&W)[2], const void* 
   a.y = y;
   a.N = (int)N; a.H = (int)H; a.F = (int)F;
   a.act = act; a.nmat = nmat;
-  a.TM = g.TM; a.TN = g.TN;
+  a.tile = g.fwd_tile; a.TM = g.TM; a.TN = g.TN;
   a.parts = g.fwd_parts; a.kc = (int)g.kc;
   a.part = (float*)workspace; a.ldp = g.ldp;
   (void)hipGetLastError();
@@ -1130,8 +1184,8 @@ flce_status layer_backward(const void* x, const void* const (&W)[2], const float
   a.ldz = g.ldz; a.segk = (int)g.segk;
   a.dbp = want_db ? (float*)(ws + g.off_dbp) : nullptr;
   a.ldb = g.ldb; a.db_blocks = g.db_blocks; a.db_rows = g.db_rows;
-  a.dx = dx; a.dx_parts = g.dx_parts; a.dx_kc = (int)g.dx_kc;
-  a.dw_parts = g.dw_parts; a.dw_kc = (int)g.dw_kc;
+  a.dx = dx; a.dx_tile = g.dx_tile; a.dx_parts = g.dx_parts; a.dx_kc = (int)g.dx_kc;
+  a.dw_tile = g.dw_tile; a.dw_parts = g.dw_parts; a.dw_kc = (int)g.dw_kc;
   a.part = (float*)(ws + g.off_part);
   (void)hipGetLastError();
   flce::mark_launch(stream, nullptr);

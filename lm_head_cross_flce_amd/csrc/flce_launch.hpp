@@ -128,11 +128,13 @@ hipError_t launch_forward_keep(const FwdLaunch& head, const FwdLaunch& rest, int
 
 enum Activation { kActNone = 0, kActRelu = 1, kActGelu = 2, kActGeluTanh = 3, kActSilu = 4, kActSigmoid = 5 };
 
-// Side of an output tile.
-constexpr int layer_tile(int dtype) { return dtype == 0 ? 128 : 256; }
-
-// Forward by streaming the weights past few tokens: at most this many.
-constexpr int kSkinnyTokens = 64;
+// Most tokens that the few-token kernel takes.  16-bit: above 4 the 64 x 64
+// tiles are as fast or faster (F=12288, H=4096 gated: 4 tokens 37.5 us against
+// 35.2, 16 tokens 45 against 36); below, a small product spares the join's
+// launch (F=1024, H=4096: 5.3 us against 8.3).  fp32: its MFMA is slow enough for
+// the tiles to lose up to 16 tokens (gated 83 us against 117).
+constexpr int skinny_tokens(int dtype) { return dtype == 0 ? 16 : 4; }
+constexpr int kSkinnyMost = 16;
 
 struct LayerFwd {
   const void* x; const void* W[2]; const void* b[2];
@@ -140,7 +142,8 @@ struct LayerFwd {
   void* y;                // [N][F]
   float* z[2];            // [N][F] pre-activations kept for the backward (linear: z[0]), or null
   int N, H, F, act, nmat;
-  int TM, TN;             // token tiles, feature tiles (layer_tile; gated: half as many of each weight)
+  int tile;               // S of the 32 S x 32 S output tiles: 8 (16-bit only), 4 or 2; 0: the few-token kernel
+  int TM, TN;             // token tiles, feature tiles (gated: 16 S features each)
   int parts, kc;          // K split: parts of kc columns of x each
   float* part;            // parts > 1: [parts][N][ldp] fp32 sums; gated: u's at column ldp / 2
   int64_t ldp;            // nmat * F rounded up to 8
@@ -158,8 +161,8 @@ struct LayerBwd {
   float* dbp; int64_t ldb;   // [db_blocks][ldb] fp32 partial column sums; null if no db
   int db_blocks, db_rows;    // token rows per block
   void* db[2];
-  void* dx; int dx_parts, dx_kc;
-  void* dW[2]; int dw_parts, dw_kc;
+  void* dx; int dx_tile, dx_parts, dx_kc;
+  void* dW[2]; int dw_tile, dw_parts, dw_kc;
   float* part;            // split products: dx [parts][N][H], then dW [parts][mats written][F][H]
 };
 

@@ -126,9 +126,9 @@ template <class T> __device__ __forceinline__ void store1(T* p, float v) {
   else *(uint16_t*)p = (uint16_t)(pack2<T>(v, 0.f) & 0xffffu);
 }
 
-// C consecutive elements (16-bit: 4 or 8; fp32: 2, 4 or 8) as whole 4- to
-// 16-byte accesses from any element's address: rows of odd sizes start on no
+// C consecutive elements (1, 2, 4 or 8) as whole accesses of up to 16 bytes from any element's address: rows of odd sizes start on no
 // boundary, and global memory takes wide accesses there.
+typedef uint32_t u32_any __attribute__((aligned(2)));
 typedef u32x2 u32x2_any __attribute__((aligned(2)));
 typedef u32x4 u32x4_any __attribute__((aligned(2)));
 typedef float f32x2 __attribute__((ext_vector_type(2)));
@@ -136,7 +136,9 @@ typedef f32x2 f32x2_any __attribute__((aligned(4)));
 typedef f32x4 f32x4_any __attribute__((aligned(4)));
 
 template <class T, int C> __device__ __forceinline__ void load_vec(const T* p, float (&v)[C]) {
-  if constexpr (sizeof(T) == 4 && C == 2) {
+  if constexpr (C == 1) {
+    v[0] = load1<T>(p);
+  } else if constexpr (sizeof(T) == 4 && C == 2) {
     const f32x2 t = *(const f32x2_any*)p;
     v[0] = t[0];
     v[1] = t[1];
@@ -153,10 +155,12 @@ template <class T, int C> __device__ __forceinline__ void load_vec(const T* p, f
       const u32x4 t = *(const u32x4_any*)p;
 #pragma unroll
       for (int k = 0; k < 4; ++k) w[k] = t[k];
-    } else {
+    } else if constexpr (C == 4) {
       const u32x2 t = *(const u32x2_any*)p;
       w[0] = t[0];
       w[1] = t[1];
+    } else {
+      w[0] = *(const u32_any*)p;
     }
 #pragma unroll
     for (int k = 0; k < C / 2; ++k) {
@@ -166,15 +170,19 @@ template <class T, int C> __device__ __forceinline__ void load_vec(const T* p, f
   }
 }
 template <class T, int C> __device__ __forceinline__ void store_vec(T* p, const float (&v)[C]) {
-  if constexpr (sizeof(T) == 4 && C == 2) {
+  if constexpr (C == 1) {
+    store1<T>(p, v[0]);
+  } else if constexpr (sizeof(T) == 4 && C == 2) {
     *(f32x2_any*)p = f32x2{v[0], v[1]};
   } else if constexpr (sizeof(T) == 4) {
 #pragma unroll
     for (int e = 0; e < C; e += 4) *(f32x4_any*)((float*)p + e) = f32x4{v[e], v[e + 1], v[e + 2], v[e + 3]};
   } else if constexpr (C == 8) {
     *(u32x4_any*)p = u32x4{pack2<T>(v[0], v[1]), pack2<T>(v[2], v[3]), pack2<T>(v[4], v[5]), pack2<T>(v[6], v[7])};
-  } else {
+  } else if constexpr (C == 4) {
     *(u32x2_any*)p = u32x2{pack2<T>(v[0], v[1]), pack2<T>(v[2], v[3])};
+  } else {
+    *(u32_any*)p = pack2<T>(v[0], v[1]);
   }
 }
 
@@ -197,12 +205,13 @@ template <class T, int C> __device__ __forceinline__ void store_some(T* p, int l
   }
 }
 
-// Whole aligned runs through a buffer descriptor: byte offset off (a lane's,
-// kOOB reads zeros and stores nothing) plus so (the wave's).
+// Whole aligned runs of 4 or 8 elements through a buffer descriptor: byte
+// offset off (a lane's, kOOB reads zeros and stores nothing) plus so (the
+// wave's).
 template <class T, int C>
 __device__ __forceinline__ void buf_store_vec(__amdgpu_buffer_rsrc_t r, uint32_t off, int so, const float (&v)[C]) {
-  if constexpr (sizeof(T) == 4 && C == 2) {
-    __builtin_amdgcn_raw_buffer_store_b64(__builtin_bit_cast(u32x2, f32x2{v[0], v[1]}), r, off, so, 0);
+  if constexpr (C < 4) {
+    // not taken: small tiles store through store_some
   } else if constexpr (sizeof(T) == 4) {
 #pragma unroll
     for (int e = 0; e < C; e += 4)
@@ -215,18 +224,10 @@ __device__ __forceinline__ void buf_store_vec(__amdgpu_buffer_rsrc_t r, uint32_t
     __builtin_amdgcn_raw_buffer_store_b64(u32x2{pack2<T>(v[0], v[1]), pack2<T>(v[2], v[3])}, r, off, so, 0);
   }
 }
+// Eight 16-bit elements (other C are never taken; the type is for code that is not reached).
 template <class T, int C>
 __device__ __forceinline__ void buf_load_vec(__amdgpu_buffer_rsrc_t r, uint32_t off, int so, float (&v)[C]) {
-  if constexpr (sizeof(T) == 4) {
-    static_assert(C == 4 || C == 8, "whole 16-byte pieces");
-#pragma unroll
-    for (int e = 0; e < C; e += 4) {
-      const f32x4 t = __builtin_bit_cast(f32x4, __builtin_amdgcn_raw_buffer_load_b128(r, off + 4 * e, so, 0));
-#pragma unroll
-      for (int k = 0; k < 4; ++k) v[e + k] = t[k];
-    }
-  } else {
-    static_assert(C == 8, "whole 16-byte pieces");
+  if constexpr (C == 8) {
     const u32x4 t = __builtin_bit_cast(u32x4, __builtin_amdgcn_raw_buffer_load_b128(r, off, so, 0));
 #pragma unroll
     for (int k = 0; k < 4; ++k) {
@@ -240,14 +241,15 @@ __device__ __forceinline__ void buf_load_vec(__amdgpu_buffer_rsrc_t r, uint32_t 
 // Operands over two weights
 // ---------------------------------------------------------------------------
 
-// Output tiles, four waves in a 2 x 2 grid of MI x NJ blocks of 16 x 16 each:
-// 256 x 256 for 16-bit operands; 128 x 128 for fp32, whose matrix instruction
-// is 16 times slower per byte, so that small tiles starve on nothing and two
-// workgroups share a CU (one's epilogue runs under the other's products).
-template <class T> struct Tile {
-  static constexpr int MI = sizeof(T) == 2 ? 8 : 4, NJ = MI;
-  static constexpr int M = 32 * MI, N = 32 * NJ;
-  static constexpr int kPerCu = sizeof(T) == 2 ? 1 : 2;   // workgroups that fit on a CU
+// Output tiles of 32 S x 32 S, four waves in a 2 x 2 grid of S x S blocks of
+// 16 x 16 each.  S = 8 (16-bit only) is the tile routine of flce_device.hpp:
+// one workgroup a CU, the best rate on large products.  S = 4 and 2 run two and
+// four workgroups a CU, so that one's epilogue and first loads run under the
+// others' products, and cut small products finely enough to fill the CUs.
+template <class T, int S_> struct Tile {
+  static_assert(S_ == 2 || S_ == 4 || (S_ == 8 && sizeof(T) == 2), "tile sizes");
+  static constexpr int S = S_, M = 32 * S;
+  static constexpr int kPerCu = S == 8 ? 1 : S == 4 ? 2 : 4;
 };
 
 // Column order of a tile: in each wave's half (16 NJ rows of the weight
@@ -324,30 +326,196 @@ struct DmaSeg {
 };
 
 // ---------------------------------------------------------------------------
-// fp32 tile: 128 x 128, 32-deep stages through registers into two padded LDS
-// buffers per operand, v_mfma_f32_16x16x4_f32.  MFMA bounds it (32 cycles an
-// instruction against one 16-byte LDS read per 8 of them).
+// Small tiles (S = 4, 2): operands of 32 S rows, two LDS buffers each, plain
+// loops; the other workgroups of the CU cover the waits.
 // ---------------------------------------------------------------------------
 
-constexpr int kF32Rows = 128, kF32K = 32;
+// One 16 x 16 block from 16 bytes of K per lane of either operand.  fp32: the
+// lane's four consecutive k go to four instructions, so K runs permuted, the
+// same for both operands.
+template <class T> __device__ __forceinline__ void mma_frag(f32x4& c, const u32x4& a, const u32x4& b) {
+  if constexpr (sizeof(T) == 4) {
+    const f32x4 fa = __builtin_bit_cast(f32x4, a), fb = __builtin_bit_cast(f32x4, b);
+#pragma unroll
+    for (int e = 0; e < 4; ++e) c = __builtin_amdgcn_mfma_f32_16x16x4f32(fa[e], fb[e], c, 0, 0, 0);
+  } else if constexpr (IsF16<T>::value) {
+    typedef _Float16 f16x8 __attribute__((ext_vector_type(8)));
+    c = __builtin_amdgcn_mfma_f32_16x16x32_f16(__builtin_bit_cast(f16x8, a), __builtin_bit_cast(f16x8, b), c, 0, 0, 0);
+  } else {
+    c = __builtin_amdgcn_mfma_f32_16x16x32_bf16(__builtin_bit_cast(bf16x8, a), __builtin_bit_cast(bf16x8, b), c, 0, 0,
+                                                0);
+  }
+}
 
-// K-contiguous operand of up to two weights: thread (kc, rr) = (tid % 8,
-// tid / 8) loads 16 bytes of K of tile rows rr + 32 q.  A gated tile's rows
-// 32 q .. 32 q + 31 lie in blocks j = 2 q and 2 q + 1 (mod 4): bit 0 of q tells
-// the weight.
-template <bool PERM, bool GLU> struct RowStager {
-  u32x4 r[4];
-  uint32_t off[4];
+// Whether pass q of a gated weight tile's copies (32 tile rows; the caller's
+// wave / 2 takes rows 16 (wave / 2) .. + 15 of them, block 2 q + wave / 2) reads
+// Wu.  S = 2: the wave alone decides, so its base is chosen once.
+template <int S> __device__ __forceinline__ constexpr bool pass_is_up(int q) { return S > 2 && (2 * q) % S >= S / 2; }
+
+// 16-bit K-contiguous operand, LDS rows of 128 bytes (64 k) with 16-byte chunk
+// p of row r holding chunk p ^ (r & 7).
+template <class T, int S, bool PERM, bool GLU> struct RowCopy {
+  static constexpr int kBytes = 32 * S * 128;
+  uint32_t off[S];
+  const uint16_t* base[2];
+  int wave, c8;
+  __device__ __forceinline__ void init(const T* p0, const T* p1, int64_t ld, int rows, int m0, int tid) {
+    wave = __builtin_amdgcn_readfirstlane(tid >> 6);
+    const int lane = tid & 63;
+    c8 = 8 * ((lane & 7) ^ (lane >> 3));
+    base[0] = (const uint16_t*)p0 + (int64_t)m0 * ld;
+    base[1] = GLU ? (const uint16_t*)p1 + (int64_t)m0 * ld : base[0];
+    if (S == 2 && (wave >> 1)) base[0] = base[1];
+#pragma unroll
+    for (int q = 0; q < S; ++q) {
+      const int t = 8 * (4 * q + wave) + (lane >> 3), row = PERM ? weight_row<S, GLU>(t) : t;
+      off[q] = m0 + row < rows ? (uint32_t)(((int64_t)row * ld + c8) * 2) : kOOB;
+    }
+  }
+  __device__ __forceinline__ void issue(int k0, int kext, lds_t* buf) const {
+    const __amdgpu_buffer_rsrc_t r0 = make_rsrc(base[0] + k0), r1 = make_rsrc(base[1] + k0);
+    const bool in = k0 + c8 < kext;
+#pragma unroll
+    for (int q = 0; q < S; ++q) dma16(GLU && pass_is_up<S>(q) ? r1 : r0, buf + (4 * q + wave) * 1024, in ? off[q] : kOOB);
+  }
+};
+template <int S> struct RowFrag {
+  int base[2];
+  __device__ __forceinline__ void init(int wbase, int lane) {
+    const int rl = lane & 15, c = lane >> 4;
+#pragma unroll
+    for (int h = 0; h < 2; ++h) base[h] = (wbase + rl) * 128 + 16 * ((4 * h + c) ^ (rl & 7));
+  }
+  __device__ __forceinline__ u32x4 read(const lds_t* buf, int half, int i) const {
+    return lds_load16(buf + base[half] + 2048 * i);
+  }
+};
+
+// 16-bit M-contiguous operand: LDS rows (one per k) of 64 S bytes, chunk p of
+// row k holding chunk p ^ col_swz(k); read with the transposing loads (see
+// flce_device.hpp).  The swizzle spreads the eight 32-byte runs that the LDS
+// serves in a cycle (four rows of two groups 8 rows apart) over its 256 bytes:
+// rows of 128 bytes already alternate halves.
+template <int S> __device__ __forceinline__ constexpr int col_swz(int k) {
+  return S == 2 ? (2 * ((k >> 1) & 1)) | (4 * ((k >> 3) & 1)) : mswz(k);
+}
+template <class T, int S> struct ColCopy {
+  static constexpr int kBytes = 32 * S * 128;
+  uint32_t off[S];
+  SegRows s;
+  int m0, wave;
+  __device__ __forceinline__ void init(const SegRows& rows, int cols, int m0_, int tid) {
+    s = rows;
+    m0 = m0_;
+    wave = __builtin_amdgcn_readfirstlane(tid >> 6);
+    const int lane = tid & 63;
+#pragma unroll
+    for (int q = 0; q < S; ++q) {
+      const int k = (4 * q + wave) * (16 / S) + lane / (4 * S), c = (lane % (4 * S)) ^ col_swz<S>(k);
+      off[q] = m0 + 8 * c < cols ? (uint32_t)(((int64_t)k * s.ld + 8 * c) * 2) : kOOB;
+    }
+  }
+  __device__ __forceinline__ void issue(int k0, int, lds_t* buf) const {
+    const __amdgpu_buffer_rsrc_t rs = s.rsrc<2>(k0, m0);
+#pragma unroll
+    for (int q = 0; q < S; ++q) dma16(rs, buf + (4 * q + wave) * 1024, off[q]);
+  }
+};
+template <int S> struct ColFrag {
+  int a[2][S];
+  __device__ __forceinline__ void init(int wbase, int lane) {
+    const int j = lane & 15, G = lane >> 4;
+#pragma unroll
+    for (int h = 0; h < 2; ++h)
+#pragma unroll
+      for (int i = 0; i < S; ++i) {
+        const int k = 8 * G + 4 * h + (j >> 2), m = wbase + 16 * i + 4 * (j & 3);
+        a[h][i] = k * 64 * S + 16 * ((m >> 3) ^ col_swz<S>(k)) + 2 * (m & 7);
+      }
+  }
+  __device__ __forceinline__ u32x4 read(const lds_t* buf, int half, int i) const {
+    typedef __attribute__((address_space(3))) bf16x4_t lds_bf16x4;
+    u32x4 f;
+#pragma unroll
+    for (int h = 0; h < 2; ++h) {
+      const u32x2 v = __builtin_bit_cast(
+          u32x2, __builtin_amdgcn_ds_read_tr16_b64_v4bf16((lds_bf16x4*)(buf + 2048 * S * half + a[h][i])));
+      f[2 * h] = v[0];
+      f[2 * h + 1] = v[1];
+    }
+    return f;
+  }
+};
+
+// acc = the tile's sums over K, 16-bit.  Block b + 1 is copied while block b is
+// computed; the barrier at the head of a block publishes it and frees the other
+// buffer.  Each buffer is its own object, so that the compiler need not wait
+// for copies into one before reads of the other.
+template <class T, int S, class FA, class FB, class CA, class CB>
+__device__ __forceinline__ void gemm_small(f32x4 (&acc)[S][S], const CA& ca, int ka, const CB& cb, int kb, int K,
+                                           int tid) {
+  __shared__ __attribute__((aligned(16))) char a0[CA::kBytes];
+  __shared__ __attribute__((aligned(16))) char a1[CA::kBytes];
+  __shared__ __attribute__((aligned(16))) char b0[CB::kBytes];
+  __shared__ __attribute__((aligned(16))) char b1[CB::kBytes];
+  const int lane = tid & 63, wave = tid >> 6;
+  FA fa;
+  FB fb;
+  fa.init((wave >> 1) * 16 * S, lane);
+  fb.init((wave & 1) * 16 * S, lane);
+#pragma unroll
+  for (int i = 0; i < S; ++i)
+#pragma unroll
+    for (int j = 0; j < S; ++j) acc[i][j] = f32x4{0.f, 0.f, 0.f, 0.f};
+  const int KB = (K + kBlockK - 1) / kBlockK;
+  ca.issue(0, ka, (lds_t*)a0);
+  cb.issue(0, kb, (lds_t*)b0);
+  auto step = [&](int b, const lds_t* A, const lds_t* B, lds_t* nA, lds_t* nB) {
+    __builtin_amdgcn_s_waitcnt(waitcnt_vm_lgkm0<0>());
+    __builtin_amdgcn_s_barrier();
+    __builtin_amdgcn_sched_barrier(0);
+    if (b + 1 < KB) {
+      ca.issue((b + 1) * kBlockK, ka, nA);
+      cb.issue((b + 1) * kBlockK, kb, nB);
+    }
+#pragma unroll
+    for (int h = 0; h < 2; ++h) {
+      u32x4 x[S], y[S];
+#pragma unroll
+      for (int i = 0; i < S; ++i) x[i] = fa.read(A, h, i);
+#pragma unroll
+      for (int j = 0; j < S; ++j) y[j] = fb.read(B, h, j);
+#pragma unroll
+      for (int i = 0; i < S; ++i)
+#pragma unroll
+        for (int j = 0; j < S; ++j) mma_frag<T>(acc[i][j], x[i], y[j]);
+    }
+  };
+  for (int b = 0; b < KB; b += 2) {
+    step(b, (const lds_t*)a0, (const lds_t*)b0, (lds_t*)a1, (lds_t*)b1);
+    if (b + 1 < KB) step(b + 1, (const lds_t*)a1, (const lds_t*)b1, (lds_t*)a0, (lds_t*)b0);
+  }
+}
+
+// fp32: 32-deep stages through registers into padded LDS rows.  MFMA bounds it
+// (v_mfma_f32_16x16x4_f32 takes 32 cycles, against one 16-byte LDS read per S
+// of them).
+constexpr int kF32K = 32;
+
+template <int S, bool PERM, bool GLU> struct RowCopy<float, S, PERM, GLU> {
+  static constexpr int kBytes = 32 * S * kRowBytes;
+  u32x4 r[S];
+  uint32_t off[S];
   const float* base[2];
   int kc4;
   __device__ __forceinline__ void init(const float* p0, const float* p1, int64_t ld, int rows, int m0, int tid) {
-    const int rr = tid >> 3;
     kc4 = (tid & 7) * 4;
     base[0] = p0 + (int64_t)m0 * ld;
     base[1] = GLU ? p1 + (int64_t)m0 * ld : base[0];
+    if (S == 2 && __builtin_amdgcn_readfirstlane(tid >> 7)) base[0] = base[1];
 #pragma unroll
-    for (int q = 0; q < 4; ++q) {
-      const int t = rr + 32 * q, row = PERM ? weight_row<4, GLU>(t) : t;
+    for (int q = 0; q < S; ++q) {
+      const int t = (tid >> 3) + 32 * q, row = PERM ? weight_row<S, GLU>(t) : t;
       off[q] = m0 + row < rows ? (uint32_t)(((int64_t)row * ld + kc4) * 4) : kOOB;
     }
   }
@@ -355,90 +523,88 @@ template <bool PERM, bool GLU> struct RowStager {
     const __amdgpu_buffer_rsrc_t r0 = make_rsrc(base[0] + k0), r1 = make_rsrc(base[1] + k0);
     const bool in = k0 + kc4 < kext;
 #pragma unroll
-    for (int q = 0; q < 4; ++q) r[q] = buf_load16(GLU && (q & 1) ? r1 : r0, in ? off[q] : kOOB);
+    for (int q = 0; q < S; ++q) r[q] = buf_load16(GLU && pass_is_up<S>(q) ? r1 : r0, in ? off[q] : kOOB);
   }
   __device__ __forceinline__ void store(lds_t* buf, int tid) const {
 #pragma unroll
-    for (int q = 0; q < 4; ++q) lds_store16(buf + ((tid >> 3) + 32 * q) * kRowBytes + (tid & 7) * 16, r[q]);
+    for (int q = 0; q < S; ++q) lds_store16(buf + ((tid >> 3) + 32 * q) * kRowBytes + (tid & 7) * 16, r[q]);
   }
 };
 
 // M-contiguous operand: 4 x 4 blocks transposed in registers, thread (kc, mc)
-// = (tid % 8, tid / 8).  SegRows gives the rows (K).
-struct ColStager {
+// = (tid % 8, tid / 8); S = 2 needs half the threads.
+template <int S> struct ColCopy<float, S> {
+  static constexpr int kBytes = 32 * S * kRowBytes;
   u32x4 r[4];
   uint32_t off[4];
   SegRows s;
-  int m0, krow;
+  int m0;
   __device__ __forceinline__ void init(const SegRows& rows, int cols, int m0_, int tid) {
     s = rows;
     m0 = m0_;
-    krow = (tid & 7) * 4;
-    const int m = (tid >> 3) * 4;
+    const int k = (tid & 7) * 4, m = (tid >> 3) * 4;
 #pragma unroll
-    for (int e = 0; e < 4; ++e) off[e] = m0 + m < cols ? (uint32_t)(((int64_t)(krow + e) * s.ld + m) * 4) : kOOB;
+    for (int e = 0; e < 4; ++e)
+      off[e] = m < 32 * S && m0 + m < cols ? (uint32_t)(((int64_t)(k + e) * s.ld + m) * 4) : kOOB;
   }
-  __device__ __forceinline__ void load(int k0, int kext) {
+  __device__ __forceinline__ void load(int k0, int) {
     const __amdgpu_buffer_rsrc_t rs = s.rsrc<4>(k0, m0);
-    const int left = kext - k0 - krow;
 #pragma unroll
-    for (int e = 0; e < 4; ++e) r[e] = buf_load16(rs, e < left ? off[e] : kOOB);
+    for (int e = 0; e < 4; ++e) r[e] = buf_load16(rs, off[e]);
   }
   __device__ __forceinline__ void store(lds_t* buf, int tid) const {
+    const int m = (tid >> 3) * 4;
+    if (m >= 32 * S) return;
 #pragma unroll
     for (int i = 0; i < 4; ++i)
-      lds_store16(buf + ((tid >> 3) * 4 + i) * kRowBytes + (tid & 7) * 16, u32x4{r[0][i], r[1][i], r[2][i], r[3][i]});
+      lds_store16(buf + (m + i) * kRowBytes + (tid & 7) * 16, u32x4{r[0][i], r[1][i], r[2][i], r[3][i]});
   }
 };
 
-typedef f32x4 AccF32[4][4];
-
-// acc = the tile's sums over K.  Lane l's 16 bytes of a row are four
-// consecutive k; instruction e takes element e, so K runs permuted, the same
-// for both operands.
-template <class SA, class SB>
-__device__ __forceinline__ void gemm_f32(AccF32& acc, SA& sa, int ka, SB& sb, int kb, int K, int tid) {
-  __shared__ __attribute__((aligned(16))) char lds[2][2][kF32Rows * kRowBytes];
+template <int S, class CA, class CB>
+__device__ __forceinline__ void gemm_small_f32(f32x4 (&acc)[S][S], CA& ca, int ka, CB& cb, int kb, int K, int tid) {
+  __shared__ __attribute__((aligned(16))) char lds[2][2][CA::kBytes];
+  static_assert(CA::kBytes == CB::kBytes, "square tiles");
   const int lane = tid & 63, wave = tid >> 6;
 #pragma unroll
-  for (int i = 0; i < 4; ++i)
+  for (int i = 0; i < S; ++i)
 #pragma unroll
-    for (int j = 0; j < 4; ++j) acc[i][j] = f32x4{0.f, 0.f, 0.f, 0.f};
+    for (int j = 0; j < S; ++j) acc[i][j] = f32x4{0.f, 0.f, 0.f, 0.f};
   const int frag = (lane & 15) * kRowBytes + (lane >> 4) * 16;
-  const int pa = (wave >> 1) * 64 * kRowBytes + frag, pb = (wave & 1) * 64 * kRowBytes + frag;
+  const int pa = (wave >> 1) * 16 * S * kRowBytes + frag, pb = (wave & 1) * 16 * S * kRowBytes + frag;
   const int KT = (K + kF32K - 1) / kF32K;
-  sa.load(0, ka);
-  sb.load(0, kb);
-  sa.store((lds_t*)lds[0][0], tid);
-  sb.store((lds_t*)lds[0][1], tid);
+  ca.load(0, ka);
+  cb.load(0, kb);
+  ca.store((lds_t*)lds[0][0], tid);
+  cb.store((lds_t*)lds[0][1], tid);
   __syncthreads();
   for (int kt = 0; kt < KT; ++kt) {
     const int cur = kt & 1;
     if (kt + 1 < KT) {
-      sa.load((kt + 1) * kF32K, ka);
-      sb.load((kt + 1) * kF32K, kb);
+      ca.load((kt + 1) * kF32K, ka);
+      cb.load((kt + 1) * kF32K, kb);
     }
     const lds_t* A = (const lds_t*)lds[cur][0];
     const lds_t* B = (const lds_t*)lds[cur][1];
 #pragma unroll
     for (int h = 0; h < 2; ++h) {
-      f32x4 a[4], b[4];
+      f32x4 a[S], b[S];
 #pragma unroll
-      for (int i = 0; i < 4; ++i) {
+      for (int i = 0; i < S; ++i) {
         a[i] = __builtin_bit_cast(f32x4, lds_load16(A + pa + 16 * i * kRowBytes + 64 * h));
         b[i] = __builtin_bit_cast(f32x4, lds_load16(B + pb + 16 * i * kRowBytes + 64 * h));
       }
 #pragma unroll
       for (int e = 0; e < 4; ++e)
 #pragma unroll
-        for (int i = 0; i < 4; ++i)
+        for (int i = 0; i < S; ++i)
 #pragma unroll
-          for (int j = 0; j < 4; ++j)
+          for (int j = 0; j < S; ++j)
             acc[i][j] = __builtin_amdgcn_mfma_f32_16x16x4f32(a[i][e], b[j][e], acc[i][j], 0, 0, 0);
     }
     if (kt + 1 < KT) {
-      sa.store((lds_t*)lds[cur ^ 1][0], tid);
-      sb.store((lds_t*)lds[cur ^ 1][1], tid);
+      ca.store((lds_t*)lds[cur ^ 1][0], tid);
+      cb.store((lds_t*)lds[cur ^ 1][1], tid);
     }
     __syncthreads();
   }
@@ -455,8 +621,8 @@ template <int N, class F> __device__ __forceinline__ void unrolled(F&& f) {
 }
 
 // One block's sums in vector registers.
-template <class T> __device__ __forceinline__ f32x4 block_sums(const f32x4& blk) {
-  if constexpr (sizeof(T) == 2) return acc_read4(blk);
+template <int S> __device__ __forceinline__ f32x4 block_sums(const f32x4& blk) {
+  if constexpr (S == 8) return acc_read4(blk);
   else return blk;
 }
 

@@ -2,11 +2,10 @@
 // product, h = act(x Wg^T + bg) * (x Wu^T + bu), with their gradients, for one
 // element type T (each type is its own translation unit).
 //
-// Many tokens: the products run on MFMA tiles (16-bit: the 256 x 256 tile
-// routine of flce_device.hpp; fp32: 128 x 128), with the activation, product and residual in the epilogue,
+// Many tokens: the products run on MFMA tiles of one of three sizes, with the activation, product and residual in the epilogue,
 // while the accumulators are still in registers.  MFMA bounds them.
-// Few tokens: every weight is read once for at most 64 rows of x, so HBM
-// bounds the call and a kernel that streams weights runs instead.
+// Few tokens: every weight is read once for a few rows of x, so HBM bounds the
+// call and a kernel that streams weights past them runs instead.
 #pragma once
 
 #include "layer_device.hpp"
@@ -19,21 +18,17 @@ namespace flce {
 
 // Workgroup w computes tiles w, w + grid, ... of the tokens x features plane
 // (times the K parts).  Tokens are the MFMA rows and features its columns, in
-// weight_row's order: a lane holds 8 consecutive features of a token (gated: 4
-// of g and the same 4 of u; fp32: half as many), so a token's features of a
-// wave are written as 16 adjacent 16-byte pieces (gated: 8 bytes).  16-bit: the
-// next tile's first copies run under the epilogue.  fp32: one tile a workgroup,
-// two workgroups a CU.
+// weight_row's order: a lane holds S consecutive features of a token (gated:
+// S / 2 of g and the same of u), so a token's features of a wave are written as
+// 16 adjacent pieces.  S = 8: 16-byte pieces (gated: 8), and the next tile's
+// first copies run under the epilogue.  S = 4, 2: one tile a workgroup.
 //
 // SPLIT: the sums go to a.part in fp32 and layer_join_fwd_kernel does the rest.
-template <class T, int ACT, bool GLU, bool SPLIT>
-__global__ void __launch_bounds__(kThreads, Tile<T>::kPerCu) layer_fwd_kernel(LayerFwd a) {
-  typedef Tile<T> TS;
-  constexpr bool k16 = sizeof(T) == 2;
-  constexpr int MI = TS::MI, NJ = TS::NJ;
-  constexpr int FT = GLU ? TS::N / 2 : TS::N;   // features of a tile
-  constexpr int C = GLU ? NJ / 2 : NJ;          // consecutive features of a lane
-  typedef typename std::conditional<GLU, DmaGlu, Dma<true>>::type DB;
+template <class T, int S, int ACT, bool GLU, bool SPLIT>
+__global__ void __launch_bounds__(kThreads, (Tile<T, S>::kPerCu)) layer_fwd_kernel(LayerFwd a) {
+  constexpr int M = Tile<T, S>::M;
+  constexpr int FT = GLU ? M / 2 : M;   // features of a tile
+  constexpr int C = GLU ? S / 2 : S;    // consecutive features of a lane
   const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6, wm = wave >> 1, wn = wave & 1;
   const int g = lane >> 4, c = lane & 15;
   const int tiles = a.TM * a.TN, total = tiles * a.parts;
@@ -42,7 +37,7 @@ __global__ void __launch_bounds__(kThreads, Tile<T>::kPerCu) layer_fwd_kernel(La
     const int part = SPLIT ? t / tiles : 0;
     int tm, tn;
     tile_coords(t - part * tiles, tiles, a.TM, a.TN, tm, tn);
-    n0 = tm * TS::M;
+    n0 = tm * M;
     f0 = tn * FT;
     k0 = part * a.kc;
   };
@@ -50,97 +45,85 @@ __global__ void __launch_bounds__(kThreads, Tile<T>::kPerCu) layer_fwd_kernel(La
   auto opb = [&]() { return Opnd<T>{(const T*)a.W[0] + k0, a.H, a.F, min(a.kc, a.H - k0)}; };
   int t = blockIdx.x;
   place(t);
-  const bool vec = a.F % C == 0;   // every lane's run is whole and aligned to its size
+  const bool vec = S == 8 && a.F % C == 0;   // every lane's run is whole and aligned to its size
   auto tile = [&](auto& acc, int n0, int f0, int part, const float (&b0)[C], const float (&b1)[C]) {
-    // Value (i, r) of a lane is token n0w + 4 g + 16 i + r.  Its byte offset is
-    // the lane's (token 4 g, or kOOB for a token past N) plus the wave's (16 i + r
-    // tokens), from a descriptor at the wave's first token: at most 128 * ld * 4.
-    const int n0w = n0 + wm * 16 * MI, f = f0 + (wn * 16 + c) * C;
-    const int left = a.F - f;   // features of this lane's run inside the row
-    const int lim = left > 0 ? a.N - n0w - 4 * g : 0;
+    // Value (i, r) of a lane is token n0w + 4 g + 16 i + r.  In an aligned tile
+    // its byte offset is the lane's (token 4 g, or kOOB for a token past N) plus
+    // the wave's (16 i + r tokens), from a descriptor at the wave's first token: at
+    // most 128 * ld * 4.
+    const int n0w = n0 + wm * 16 * S, f = f0 + (wn * 16 + c) * C;
     const int64_t ld = SPLIT ? a.ldp : a.F;
+    const int left = (SPLIT ? (int)(GLU ? a.ldp / 2 : a.ldp) : a.F) - f;   // features of this lane's run inside the row
+    const int lim = left > 0 ? a.N - n0w - 4 * g : 0;
     const uint32_t lane0 = (uint32_t)(4 * g * (int)ld + f);
     auto offset = [&](int i, int r, uint32_t es) -> uint32_t { return 16 * i + r < lim ? lane0 * es : kOOB; };
     auto wave_offset = [&](int i, int r, int es) -> int { return (16 * i + r) * (int)ld * es; };
     const int64_t base = ((int64_t)part * a.N + n0w) * ld;
-    if constexpr (SPLIT) {
-      // Rows are padded to 8 columns, so every run that starts in one is whole.
-      const __amdgpu_buffer_rsrc_t r0 = make_rsrc(a.part + base);
-      const __amdgpu_buffer_rsrc_t r1 = make_rsrc(a.part + base + (GLU ? a.ldp / 2 : 0));
-#pragma unroll
-      for (int i = 0; i < MI; ++i) {
-        f32x4 z[NJ];
-#pragma unroll
-        for (int j = 0; j < NJ; ++j) z[j] = block_sums<T>(acc[i][j]);
-#pragma unroll
-        for (int r = 0; r < 4; ++r) {
-          float s0[C], s1[C];
-#pragma unroll
-          for (int e = 0; e < C; ++e) {
-            s0[e] = z[e][r];
-            s1[e] = z[NJ - C + e][r];
-          }
-          buf_store_vec<float, C>(r0, offset(i, r, 4), wave_offset(i, r, 4), s0);
-          if constexpr (GLU) buf_store_vec<float, C>(r1, offset(i, r, 4), wave_offset(i, r, 4), s1);
-        }
-        __builtin_amdgcn_sched_barrier(0);
-      }
-    } else {
+    auto rows = [&](auto whole) {   // whole: vec, as a constant
+      constexpr bool kVec = whole.value;
       constexpr int ES = sizeof(T);
-      const __amdgpu_buffer_rsrc_t ry = make_rsrc((const T*)a.y + base);
-      const __amdgpu_buffer_rsrc_t rr = make_rsrc((const T*)a.residual + base);
-      const __amdgpu_buffer_rsrc_t rz0 = make_rsrc(a.z[0] + base);
-      const __amdgpu_buffer_rsrc_t rz1 = make_rsrc(a.z[1] + base);
-      const bool res = !GLU && a.residual != nullptr, keep = a.z[0] != nullptr;
-      auto rows = [&](auto whole) {   // whole: vec, as a constant
-        unrolled<MI>([&](auto block) {
-          constexpr int i = block.value;
-          constexpr bool kVec = whole.value;
-          float rs[4][C];
-          if constexpr (!GLU) {
-            if (res) {
+      const bool res = !GLU && !SPLIT && a.residual != nullptr, keep = !SPLIT && a.z[0] != nullptr;
+      __amdgpu_buffer_rsrc_t ry, rr, rz0, rz1;
+      if constexpr (kVec) {
+        ry = make_rsrc((const T*)a.y + base);
+        rr = make_rsrc((const T*)a.residual + base);
+        rz0 = make_rsrc((SPLIT ? a.part : a.z[0]) + base);
+        rz1 = make_rsrc((SPLIT ? a.part + a.ldp / 2 : a.z[1]) + base);
+      }
+      unrolled<S>([&](auto block) {
+        constexpr int i = block.value;
+        float rs[4][C];
+        if constexpr (!GLU && !SPLIT) {
+          if (res) {
 #pragma unroll
-              for (int r = 0; r < 4; ++r) {
-                if constexpr (kVec) buf_load_vec<T, C>(rr, offset(i, r, ES), wave_offset(i, r, ES), rs[r]);
-                else if (16 * i + r < lim)
-                  load_some<T, C>((const T*)a.residual + base + lane0 + (16 * i + r) * ld, left, rs[r]);
-              }
+            for (int r = 0; r < 4; ++r) {
+              if constexpr (kVec) buf_load_vec<T, C>(rr, offset(i, r, ES), wave_offset(i, r, ES), rs[r]);
+              else if (16 * i + r < lim)
+                load_some<T, C>((const T*)a.residual + base + lane0 + (16 * i + r) * ld, left, rs[r]);
             }
           }
-          f32x4 z[NJ];
+        }
+        f32x4 z[S];
 #pragma unroll
-          for (int j = 0; j < NJ; ++j) z[j] = block_sums<T>(acc[i][j]);
+        for (int j = 0; j < S; ++j) z[j] = block_sums<S>(acc[i][j]);
 #pragma unroll
-          for (int r = 0; r < 4; ++r) {
-            float z0[C], z1[C], v[C];
+        for (int r = 0; r < 4; ++r) {
+          float z0[C], z1[C], v[C];
 #pragma unroll
-            for (int e = 0; e < C; ++e) {
-              z0[e] = z[e][r] + b0[e];
-              if constexpr (GLU) z1[e] = z[C + e][r] + b1[e];
+          for (int e = 0; e < C; ++e) {
+            z0[e] = z[e][r] + (SPLIT ? 0.f : b0[e]);
+            z1[e] = z[S - C + e][r] + (SPLIT ? 0.f : b1[e]);
+            if constexpr (!SPLIT) {
               v[e] = act_fwd<T, ACT>(z0[e]);
               if constexpr (GLU) v[e] *= z1[e];
               else if (res) v[e] += rs[r][e];
             }
-            if constexpr (kVec) {
-              if (keep) {
-                buf_store_vec<float, C>(rz0, offset(i, r, 4), wave_offset(i, r, 4), z0);
-                if constexpr (GLU) buf_store_vec<float, C>(rz1, offset(i, r, 4), wave_offset(i, r, 4), z1);
-              }
-              buf_store_vec<T, C>(ry, offset(i, r, ES), wave_offset(i, r, ES), v);
-            } else if (16 * i + r < lim) {
-              const int64_t o = base + lane0 + (16 * i + r) * ld;
-              if (keep) {
-                store_some<float, C>(a.z[0] + o, left, z0);
-                if constexpr (GLU) store_some<float, C>(a.z[1] + o, left, z1);
-              }
-              store_some<T, C>((T*)a.y + o, left, v);
-            }
           }
-          __builtin_amdgcn_sched_barrier(0);
-        });
-      };
+          if constexpr (kVec) {
+            if (SPLIT || keep) {
+              buf_store_vec<float, C>(rz0, offset(i, r, 4), wave_offset(i, r, 4), z0);
+              if constexpr (GLU) buf_store_vec<float, C>(rz1, offset(i, r, 4), wave_offset(i, r, 4), z1);
+            }
+            if constexpr (!SPLIT) buf_store_vec<T, C>(ry, offset(i, r, ES), wave_offset(i, r, ES), v);
+          } else if (16 * i + r < lim) {
+            const int64_t o = base + lane0 + (16 * i + r) * ld;
+            if (SPLIT || keep) {
+              store_some<float, C>((SPLIT ? a.part : a.z[0]) + o, left, z0);
+              if constexpr (GLU) store_some<float, C>((SPLIT ? a.part + a.ldp / 2 : a.z[1]) + o, left, z1);
+            }
+            if constexpr (!SPLIT) store_some<T, C>((T*)a.y + o, left, v);
+          }
+        }
+        __builtin_amdgcn_sched_barrier(0);
+      });
+    };
+    if constexpr (S == 8 && SPLIT) {
+      rows(std::true_type{});   // rows of the partial sums are padded to 8 columns
+    } else if constexpr (S == 8) {
       if (vec) rows(std::true_type{});
       else rows(std::false_type{});
+    } else {
+      rows(std::false_type{});
     }
   };
   auto biases = [&](float (&b0)[C], float (&b1)[C]) {
@@ -152,7 +135,8 @@ __global__ void __launch_bounds__(kThreads, Tile<T>::kPerCu) layer_fwd_kernel(La
     }
   };
   float b0[C], b1[C];
-  if constexpr (k16) {
+  if constexpr (S == 8) {
+    typedef typename std::conditional<GLU, DmaGlu, Dma<true>>::type DB;
     FLCE_LDS(L, T);
     TileCopy<true, true, Dma<true>, DB> tc;
     auto begin = [&]() {
@@ -184,13 +168,14 @@ __global__ void __launch_bounds__(kThreads, Tile<T>::kPerCu) layer_fwd_kernel(La
     }
   } else {
     biases(b0, b1);
-    AccF32 acc;
+    f32x4 acc[S][S];
     const Opnd<T> A = opa(), B = opb();
-    RowStager<false, false> sa;
-    RowStager<true, GLU> sb;
-    sa.init(A.p, nullptr, A.ld, a.N, n0, tid);
-    sb.init(B.p, (const float*)a.W[1] + k0, B.ld, a.F, f0, tid);
-    gemm_f32(acc, sa, A.kext, sb, B.kext, A.kext, tid);
+    RowCopy<T, S, false, false> ca;
+    RowCopy<T, S, true, GLU> cb;
+    ca.init(A.p, nullptr, A.ld, a.N, n0, tid);
+    cb.init(B.p, (const T*)a.W[1] + k0, B.ld, a.F, f0, tid);
+    if constexpr (sizeof(T) == 2) gemm_small<T, S, RowFrag<S>, RowFrag<S>>(acc, ca, A.kext, cb, B.kext, A.kext, tid);
+    else gemm_small_f32<S>(acc, ca, A.kext, cb, B.kext, A.kext, tid);
     tile(acc, n0, f0, SPLIT ? t / tiles : 0, b0, b1);
   }
 }
@@ -241,43 +226,25 @@ template <class T, int ACT, bool GLU> __global__ void __launch_bounds__(256) lay
 // Forward, few tokens
 // ---------------------------------------------------------------------------
 
-// One 16 x 16 block from 16 bytes of K per lane of either operand.  fp32: the
-// lane's four consecutive k go to four instructions, so K runs permuted, the
-// same for both operands.
-template <class T> __device__ __forceinline__ void mma_frag(f32x4& c, const u32x4& a, const u32x4& b) {
-  if constexpr (sizeof(T) == 4) {
-    const f32x4 fa = __builtin_bit_cast(f32x4, a), fb = __builtin_bit_cast(f32x4, b);
-#pragma unroll
-    for (int e = 0; e < 4; ++e) c = __builtin_amdgcn_mfma_f32_16x16x4f32(fa[e], fb[e], c, 0, 0, 0);
-  } else if constexpr (IsF16<T>::value) {
-    typedef _Float16 f16x8 __attribute__((ext_vector_type(8)));
-    c = __builtin_amdgcn_mfma_f32_16x16x32_f16(__builtin_bit_cast(f16x8, a), __builtin_bit_cast(f16x8, b), c, 0, 0, 0);
-  } else {
-    c = __builtin_amdgcn_mfma_f32_16x16x32_bf16(__builtin_bit_cast(bf16x8, a), __builtin_bit_cast(bf16x8, b), c, 0, 0,
-                                                0);
-  }
-}
-
 constexpr int kSkinnyWaves = 8;
 
-// Workgroup b computes features 16 b .. 16 b + 15 of at most 16 TB tokens.
-// Its 8 waves split K; each loads its weight rows straight into registers (no
-// two waves share a weight, so LDS would only add a hop) with two groups of
-// kU loads in flight, and x's rows through the caches.  The waves' sums meet
-// in LDS and are added in wave order.
-template <class T, bool GLU, int TB>
+// Workgroup b computes features 16 b .. 16 b + 15 of at most 16 tokens.  Its 8
+// waves split K; each loads its weight rows straight into registers (no two
+// waves share a weight, so LDS would only add a hop) with two groups of 4 loads
+// of each weight in flight, and x's rows through the caches.  The waves' sums
+// meet in LDS and are added in wave order.  HBM bounds it: one token, H=4096,
+// F=12288 bf16, gated: 35 us, 5.75 TB/s of weights.
+template <class T, bool GLU>
 __global__ void __launch_bounds__(64 * kSkinnyWaves) layer_fwd_skinny_kernel(LayerFwd a) {
   constexpr int R = GLU ? 2 : 1, ES = sizeof(T);
   constexpr int kStep = 64 / ES;   // K of one step: 16 bytes in each of the 4 lane groups
   constexpr int kU = 4;
-  __shared__ f32x4 red[kSkinnyWaves][R * TB][64];
+  __shared__ f32x4 red[kSkinnyWaves][R][64];
   const int tid = threadIdx.x, lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6);
   const int g = lane >> 4, rl = lane & 15, f0 = blockIdx.x * 16;
   // Rows past F or N repeat the last one: their sums are not stored.
   const uint32_t offw = (uint32_t)min(rl, a.F - 1 - f0) * (uint32_t)(a.H * ES) + 16u * g;
-  uint32_t offx[TB];
-#pragma unroll
-  for (int t = 0; t < TB; ++t) offx[t] = (uint32_t)min(16 * t + rl, a.N - 1) * (uint32_t)(a.H * ES) + 16u * g;
+  const uint32_t offx = (uint32_t)min(rl, a.N - 1) * (uint32_t)(a.H * ES) + 16u * g;
   __amdgpu_buffer_rsrc_t rw[R];
 #pragma unroll
   for (int r = 0; r < R; ++r) rw[r] = make_rsrc((const T*)a.W[r] + (int64_t)f0 * a.H);
@@ -286,8 +253,8 @@ __global__ void __launch_bounds__(64 * kSkinnyWaves) layer_fwd_skinny_kernel(Lay
   const int steps = (a.H + kStep - 1) / kStep, per = (steps + kSkinnyWaves - 1) / kSkinnyWaves;
   const int s0 = wave * per, s1 = min(steps, s0 + per);
   const int klim = min(s1 * kStep, a.H) - g * (16 / ES);   // step s of this lane is inside K when s * kStep < klim
-  f32x4 acc[R][TB] = {};
-  u32x4 w[2][kU][R], x[2][kU][TB];
+  f32x4 acc[R] = {};
+  u32x4 w[2][kU][R], x[2][kU];
   auto load = [&](int h, int s) {
 #pragma unroll
     for (int u = 0; u < kU; ++u) {
@@ -296,18 +263,14 @@ __global__ void __launch_bounds__(64 * kSkinnyWaves) layer_fwd_skinny_kernel(Lay
 #pragma unroll
       for (int r = 0; r < R; ++r)
         w[h][u][r] = __builtin_bit_cast(u32x4, __builtin_amdgcn_raw_buffer_load_b128(rw[r], in ? offw : kOOB, so, 0));
-#pragma unroll
-      for (int t = 0; t < TB; ++t)
-        x[h][u][t] = __builtin_bit_cast(u32x4, __builtin_amdgcn_raw_buffer_load_b128(rx, in ? offx[t] : kOOB, so, 0));
+      x[h][u] = __builtin_bit_cast(u32x4, __builtin_amdgcn_raw_buffer_load_b128(rx, in ? offx : kOOB, so, 0));
     }
   };
   auto mma = [&](int h) {
 #pragma unroll
     for (int u = 0; u < kU; ++u)
 #pragma unroll
-      for (int r = 0; r < R; ++r)
-#pragma unroll
-        for (int t = 0; t < TB; ++t) mma_frag<T>(acc[r][t], w[h][u][r], x[h][u][t]);
+      for (int r = 0; r < R; ++r) mma_frag<T>(acc[r], w[h][u][r], x[h][u]);
   };
   load(0, s0);
   for (int s = s0; s < s1; s += 2 * kU) {
@@ -317,40 +280,28 @@ __global__ void __launch_bounds__(64 * kSkinnyWaves) layer_fwd_skinny_kernel(Lay
     mma(1);
   }
 #pragma unroll
-  for (int r = 0; r < R; ++r)
-#pragma unroll
-    for (int t = 0; t < TB; ++t) red[wave][r * TB + t][lane] = acc[r][t];
+  for (int r = 0; r < R; ++r) red[wave][r][lane] = acc[r];
   __syncthreads();
-  // Element (token n, feature f) sits in lane 16 (f / 4) + n % 16, value f % 4, of block n / 16.
-  for (int i = tid; i < 256 * TB; i += 64 * kSkinnyWaves) {
-    const int f = i & 15, n = i >> 4;
-    if (n >= a.N || f0 + f >= a.F) continue;
-    float z[R];
+  // Element (token n, feature f) sits in lane 16 (f / 4) + n, value f % 4.
+  const int f = tid & 15, n = tid >> 4;
+  if (n >= a.N || f0 + f >= a.F) return;
+  float z[R];
 #pragma unroll
-    for (int r = 0; r < R; ++r) {
-      z[r] = 0.f;
+  for (int r = 0; r < R; ++r) {
+    z[r] = 0.f;
 #pragma unroll
-      for (int q = 0; q < kSkinnyWaves; ++q)
-        z[r] += ((const float*)&red[q][r * TB + (n >> 4)][16 * (f >> 2) + (n & 15)])[f & 3];
-      if (a.b[r]) z[r] += load1<T>((const T*)a.b[r] + f0 + f);
-    }
-    const int64_t o = (int64_t)n * a.F + f0 + f;
-    float v = act_fwd_rt<T>(a.act, z[0]);
-    if constexpr (GLU) v *= z[R - 1];
-    else if (a.residual) v += load1<T>((const T*)a.residual + o);
-    if (a.z[0]) {
-      a.z[0][o] = z[0];
-      if constexpr (GLU) a.z[1][o] = z[R - 1];
-    }
-    store1<T>((T*)a.y + o, v);
+    for (int q = 0; q < kSkinnyWaves; ++q) z[r] += ((const float*)&red[q][r][16 * (f >> 2) + n])[f & 3];
+    if (a.b[r]) z[r] += load1<T>((const T*)a.b[r] + f0 + f);
   }
-}
-
-template <class T, bool GLU> static void launch_skinny(const LayerFwd& a, hipStream_t st) {
-  const dim3 grid((a.F + 15) / 16), blk(64 * kSkinnyWaves);
-  if (a.N <= 16) FLCE_LAUNCH((layer_fwd_skinny_kernel<T, GLU, 1>), grid, blk, 0, st, a);
-  else if (a.N <= 32) FLCE_LAUNCH((layer_fwd_skinny_kernel<T, GLU, 2>), grid, blk, 0, st, a);
-  else FLCE_LAUNCH((layer_fwd_skinny_kernel<T, GLU, 4>), grid, blk, 0, st, a);
+  const int64_t o = (int64_t)n * a.F + f0 + f;
+  float v = act_fwd_rt<T>(a.act, z[0]);
+  if constexpr (GLU) v *= z[R - 1];
+  else if (a.residual) v += load1<T>((const T*)a.residual + o);
+  if (a.z[0]) {
+    a.z[0][o] = z[0];
+    if constexpr (GLU) a.z[1][o] = z[R - 1];
+  }
+  store1<T>((T*)a.y + o, v);
 }
 
 // f.operator()<ACT>() for the activation.
@@ -365,18 +316,37 @@ template <class F> static void with_act(int act, F&& f) {
   }
 }
 
+// f(integral_constant<int, S>) for the tile.
+template <class T, class F> static void with_tile(int s, F&& f) {
+  if constexpr (sizeof(T) == 2) {
+    if (s == 8) return f(std::integral_constant<int, 8>{});
+  }
+  if (s == 4) return f(std::integral_constant<int, 4>{});
+  return f(std::integral_constant<int, 2>{});
+}
+
 template <class T, bool GLU> static void launch_fwd(const LayerFwd& a, hipStream_t st) {
-  if (a.N <= kSkinnyTokens) return launch_skinny<T, GLU>(a, st);
+  if (a.tile == 0) {
+    FLCE_LAUNCH((layer_fwd_skinny_kernel<T, GLU>), dim3((a.F + 15) / 16), dim3(64 * kSkinnyWaves), 0, st, a);
+    return;
+  }
   const int total = a.TM * a.TN * a.parts;
-  const dim3 grid(sizeof(T) == 4 || total < kPersistGrid ? total : kPersistGrid), blk(kThreads);
+  const dim3 grid(a.tile < 8 || total < kPersistGrid ? total : kPersistGrid), blk(kThreads);
+  with_tile<T>(a.tile, [&](auto tile) {
+    constexpr int S = tile.value;
+    if (a.parts > 1) {
+      FLCE_LAUNCH((layer_fwd_kernel<T, S, kActNone, GLU, true>), grid, blk, 0, st, a);
+    } else {
+      with_act(a.act, [&](auto act) {
+        FLCE_LAUNCH((layer_fwd_kernel<T, S, act.value, GLU, false>), grid, blk, 0, st, a);
+      });
+    }
+  });
   if (a.parts > 1) {
-    FLCE_LAUNCH((layer_fwd_kernel<T, kActNone, GLU, true>), grid, blk, 0, st, a);
     const int64_t blocks = ((int64_t)a.N * ((a.F + 7) / 8) + 255) / 256;
     const dim3 gj((unsigned)(blocks < 4096 ? blocks : 4096));
     with_act(a.act, [&](auto act) { FLCE_LAUNCH((layer_join_fwd_kernel<T, act.value, GLU>), gj, dim3(256), 0, st, a); });
-    return;
   }
-  with_act(a.act, [&](auto act) { FLCE_LAUNCH((layer_fwd_kernel<T, act.value, GLU, false>), grid, blk, 0, st, a); });
 }
 
 // ---------------------------------------------------------------------------
@@ -452,24 +422,24 @@ template <class T> __global__ void __launch_bounds__(256) layer_db_kernel(LayerB
 // dx[n][h] = sum over the rows f of W (gated: of Wg, then of Wu) of
 // dz[n][f] W[f][h]: C[h][n], so a lane holds four consecutive h of a token.
 // Workgroup b computes tile b % G over part b / G of K.
-template <class T, bool SPLIT>
-__global__ void __launch_bounds__(kThreads, Tile<T>::kPerCu) layer_dx_kernel(LayerBwd a, int TH, int TM) {
-  typedef Tile<T> TS;
+template <class T, int S, bool SPLIT>
+__global__ void __launch_bounds__(kThreads, (Tile<T, S>::kPerCu)) layer_dx_kernel(LayerBwd a, int TH, int TM) {
+  constexpr int M = Tile<T, S>::M;
   const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6, wm = wave >> 1, wn = wave & 1;
   const int G = TH * TM, part = SPLIT ? blockIdx.x / G : 0;
   int tm, tn;
   tile_coords(blockIdx.x - part * G, G, TH, TM, tm, tn);
-  const int h0 = tm * TS::M, n0 = tn * TS::N, k0 = part * a.dx_kc;
+  const int h0 = tm * M, n0 = tn * M, k0 = part * a.dx_kc;
   const int K = max(1, min(a.dx_kc, (int)a.ldz - k0));
   const SegRows rows{{a.W[0], a.W[1]}, a.H, a.F, a.segk, k0};
   auto epilogue = [&](auto& acc) {
 #pragma unroll
-    for (int j = 0; j < TS::NJ; ++j) {
-      const int n = n0 + wn * 16 * TS::NJ + 16 * j + (lane & 15);
+    for (int j = 0; j < S; ++j) {
+      const int n = n0 + wn * 16 * S + 16 * j + (lane & 15);
 #pragma unroll
-      for (int i = 0; i < TS::MI; ++i) {
-        const f32x4 z = block_sums<T>(acc[i][j]);
-        const int h = h0 + wm * 16 * TS::MI + 16 * i + 4 * (lane >> 4);
+      for (int i = 0; i < S; ++i) {
+        const f32x4 z = block_sums<S>(acc[i][j]);
+        const int h = h0 + wm * 16 * S + 16 * i + 4 * (lane >> 4);
         if (n < a.N && h < a.H) {
           if constexpr (SPLIT) *(f32x4*)(a.part + ((int64_t)part * a.N + n) * a.H + h) = z;
           else store4<T>((T*)a.dx + (int64_t)n * a.H + h, z[0], z[1], z[2], z[3]);
@@ -477,7 +447,7 @@ __global__ void __launch_bounds__(kThreads, Tile<T>::kPerCu) layer_dx_kernel(Lay
       }
     }
   };
-  if constexpr (sizeof(T) == 2) {
+  if constexpr (S == 8) {
     FLCE_LDS(L, T);
     const Opnd<T> A{(const T*)a.W[0], a.H, a.H, K};   // K only: rows past F read zeros
     const Opnd<T> B{(const T*)a.dz + k0, a.ldz, a.N, (int)a.ldz - k0};
@@ -492,12 +462,13 @@ __global__ void __launch_bounds__(kThreads, Tile<T>::kPerCu) layer_dx_kernel(Lay
     acc_drain();
     epilogue(acc);
   } else {
-    AccF32 acc;
-    ColStager sa;
-    RowStager<false, false> sb;
-    sa.init(rows, a.H, h0, tid);
-    sb.init((const float*)a.dz + k0, nullptr, a.ldz, a.N, n0, tid);
-    gemm_f32(acc, sa, K, sb, (int)a.ldz - k0, K, tid);
+    f32x4 acc[S][S];
+    ColCopy<T, S> ca;
+    RowCopy<T, S, false, false> cb;
+    ca.init(rows, a.H, h0, tid);
+    cb.init((const T*)a.dz + k0, nullptr, a.ldz, a.N, n0, tid);
+    if constexpr (sizeof(T) == 2) gemm_small<T, S, ColFrag<S>, RowFrag<S>>(acc, ca, K, cb, (int)a.ldz - k0, K, tid);
+    else gemm_small_f32<S>(acc, ca, K, cb, (int)a.ldz - k0, K, tid);
     epilogue(acc);
   }
 }
@@ -508,29 +479,29 @@ __global__ void __launch_bounds__(kThreads, Tile<T>::kPerCu) layer_dx_kernel(Lay
 // into vector registers, which costs a loop over the lanes at every copy (the
 // product at N=8192, H=4096, 24576 rows took 1463 us so).  The first H tile's
 // workgroups also finish db for their columns.
-template <class T, bool SPLIT>
-__global__ void __launch_bounds__(kThreads, Tile<T>::kPerCu) layer_dw_kernel(LayerBwd a, int TH, int TF, int m0,
-                                                                            int mats) {
-  typedef Tile<T> TS;
+template <class T, int S, bool SPLIT>
+__global__ void __launch_bounds__(kThreads, (Tile<T, S>::kPerCu)) layer_dw_kernel(LayerBwd a, int TH, int TF, int m0,
+                                                                                int mats) {
+  constexpr int M = Tile<T, S>::M;
   const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6, wm = wave >> 1, wn = wave & 1;
   const int G = TH * TF * mats, part = SPLIT ? blockIdx.x / G : 0;
   int tm, tn;
   tile_coords(blockIdx.x - part * G, G, TH, TF * mats, tm, tn);
   const int second = tn >= TF ? 1 : 0, m = m0 + second;
-  const int h0 = tm * TS::M, f0 = (tn - second * TF) * TS::N, k0 = part * a.dw_kc;
+  const int h0 = tm * M, f0 = (tn - second * TF) * M, k0 = part * a.dw_kc;
   const int K = min(a.dw_kc, a.N - k0);
   const int width = a.nmat == 2 ? a.segk : (int)a.ldz;
   const T* x = (const T*)a.x + (int64_t)k0 * a.H;
   const T* dz = (const T*)a.dz + (int64_t)k0 * a.ldz + (int64_t)m * a.segk;
-  if (tm == 0 && part == 0 && a.db[m] && tid < TS::N && f0 + tid < a.F) column_sum<T>(a, m, f0 + tid);
+  if (tm == 0 && part == 0 && a.db[m] && tid < M && f0 + tid < a.F) column_sum<T>(a, m, f0 + tid);
   auto epilogue = [&](auto& acc) {
 #pragma unroll
-    for (int j = 0; j < TS::NJ; ++j) {
-      const int f = f0 + wn * 16 * TS::NJ + 16 * j + (lane & 15);
+    for (int j = 0; j < S; ++j) {
+      const int f = f0 + wn * 16 * S + 16 * j + (lane & 15);
 #pragma unroll
-      for (int i = 0; i < TS::MI; ++i) {
-        const f32x4 z = block_sums<T>(acc[i][j]);
-        const int h = h0 + wm * 16 * TS::MI + 16 * i + 4 * (lane >> 4);
+      for (int i = 0; i < S; ++i) {
+        const f32x4 z = block_sums<S>(acc[i][j]);
+        const int h = h0 + wm * 16 * S + 16 * i + 4 * (lane >> 4);
         if (f < a.F && h < a.H) {
           if constexpr (SPLIT) *(f32x4*)(a.part + (((int64_t)part * mats + second) * a.F + f) * a.H + h) = z;
           else store4<T>((T*)a.dW[m] + (int64_t)f * a.H + h, z[0], z[1], z[2], z[3]);
@@ -538,7 +509,7 @@ __global__ void __launch_bounds__(kThreads, Tile<T>::kPerCu) layer_dw_kernel(Lay
       }
     }
   };
-  if constexpr (sizeof(T) == 2) {
+  if constexpr (S == 8) {
     FLCE_LDS(L, T);
     const Opnd<T> A{x, a.H, a.H, max(K, 0)};
     const Opnd<T> B{dz, a.ldz, width, max(K, 0)};
@@ -547,11 +518,12 @@ __global__ void __launch_bounds__(kThreads, Tile<T>::kPerCu) layer_dw_kernel(Lay
     acc_drain();
     epilogue(acc);
   } else {
-    AccF32 acc;
-    ColStager sa, sb;
-    sa.init(SegRows{{x, x}, a.H, max(K, 0), 1 << 30, 0}, a.H, h0, tid);
-    sb.init(SegRows{{dz, dz}, a.ldz, max(K, 0), 1 << 30, 0}, width, f0, tid);
-    gemm_f32(acc, sa, K, sb, K, max(K, 1), tid);
+    f32x4 acc[S][S];
+    ColCopy<T, S> ca, cb;
+    ca.init(SegRows{{x, x}, a.H, max(K, 0), 1 << 30, 0}, a.H, h0, tid);
+    cb.init(SegRows{{dz, dz}, a.ldz, max(K, 0), 1 << 30, 0}, width, f0, tid);
+    if constexpr (sizeof(T) == 2) gemm_small<T, S, ColFrag<S>, ColFrag<S>>(acc, ca, K, cb, K, K, tid);
+    else gemm_small_f32<S>(acc, ca, K, cb, K, K, tid);
     epilogue(acc);
   }
 }
@@ -581,8 +553,6 @@ template <class T, bool GLU> static void launch_dz(const LayerBwd& a, hipStream_
 }
 
 template <class T> static void launch_bwd(const LayerBwd& a, hipStream_t st) {
-  typedef Tile<T> TS;
-  const int TH = (a.H + TS::M - 1) / TS::M, TM = (a.N + TS::N - 1) / TS::N, TF = (a.F + TS::N - 1) / TS::N;
   const dim3 blk(kThreads);
   if (a.N > 0 && (!a.dz_is_dy || a.db[0] || a.db[1])) {
     if (a.nmat == 2) launch_dz<T, true>(a, st);
@@ -590,23 +560,32 @@ template <class T> static void launch_bwd(const LayerBwd& a, hipStream_t st) {
   }
   if ((a.db[0] && !a.dW[0]) || (a.db[1] && !a.dW[1]))
     FLCE_LAUNCH((layer_db_kernel<T>), dim3((a.F + 255) / 256, a.nmat), dim3(256), 0, st, a);
+  auto tiles = [](int n, int s) { return (n + 32 * s - 1) / (32 * s); };
   if (a.dx && a.N > 0) {
-    if (a.dx_parts > 1) {
-      FLCE_LAUNCH((layer_dx_kernel<T, true>), dim3(TH * TM * a.dx_parts), blk, 0, st, a, TH, TM);
-      launch_join<T>(a.part, a.dx_parts, (int64_t)a.N * a.H, a.dx, nullptr, st);
-    } else {
-      FLCE_LAUNCH((layer_dx_kernel<T, false>), dim3(TH * TM), blk, 0, st, a, TH, TM);
-    }
+    with_tile<T>(a.dx_tile, [&](auto tile) {
+      constexpr int S = tile.value;
+      const int TH = tiles(a.H, S), TM = tiles(a.N, S);
+      if (a.dx_parts > 1) {
+        FLCE_LAUNCH((layer_dx_kernel<T, S, true>), dim3(TH * TM * a.dx_parts), blk, 0, st, a, TH, TM);
+      } else {
+        FLCE_LAUNCH((layer_dx_kernel<T, S, false>), dim3(TH * TM), blk, 0, st, a, TH, TM);
+      }
+    });
+    if (a.dx_parts > 1) launch_join<T>(a.part, a.dx_parts, (int64_t)a.N * a.H, a.dx, nullptr, st);
   }
   if (a.dW[0] || a.dW[1]) {
     const int m0 = a.dW[0] ? 0 : 1, mats = (a.dW[0] && a.dW[1]) ? 2 : 1;
-    const int G = TH * TF * mats;
-    if (a.dw_parts > 1) {
-      FLCE_LAUNCH((layer_dw_kernel<T, true>), dim3(G * a.dw_parts), blk, 0, st, a, TH, TF, m0, mats);
+    with_tile<T>(a.dw_tile, [&](auto tile) {
+      constexpr int S = tile.value;
+      const int TH = tiles(a.H, S), TF = tiles(a.F, S);
+      if (a.dw_parts > 1) {
+        FLCE_LAUNCH((layer_dw_kernel<T, S, true>), dim3(TH * TF * mats * a.dw_parts), blk, 0, st, a, TH, TF, m0, mats);
+      } else {
+        FLCE_LAUNCH((layer_dw_kernel<T, S, false>), dim3(TH * TF * mats), blk, 0, st, a, TH, TF, m0, mats);
+      }
+    });
+    if (a.dw_parts > 1)
       launch_join<T>(a.part, a.dw_parts, (int64_t)a.F * a.H, a.dW[m0], mats == 2 ? a.dW[1] : nullptr, st);
-    } else {
-      FLCE_LAUNCH((layer_dw_kernel<T, false>), dim3(G), blk, 0, st, a, TH, TF, m0, mats);
-    }
   }
 }
 

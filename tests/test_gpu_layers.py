@@ -199,6 +199,30 @@ def test_whole_grid_of_tiles(dtype):
     check_glu(2100, 64, 4200, DT[dtype], "silu", False, seed=10)
 
 
+TILED = [(65, 72, 40), (70, 4096, 256), (257, 264, 300), (300, 1032, 515), (700, 72, 1000), (100, 64, 4104),
+         (5000, 64, 72), (1030, 512, 640)]
+
+
+@pytest.mark.parametrize("tile", [8, 4, 2])
+@pytest.mark.parametrize("dtype", ["bf16", "f16", "f32"])
+@pytest.mark.parametrize("shape", TILED, ids=str)
+def test_every_tile(monkeypatch, shape, dtype, tile):
+    # each size of output tile on shapes that the library may give another
+    monkeypatch.setenv("FLCE_DEBUG_LAYER_TILE", str(tile))
+    i = TILED.index(shape)
+    check_linear(*shape, DT[dtype], ACTS[(i + 2) % 6], bias=i % 2 == 0, residual=i % 3 == 0, seed=i)
+    check_glu(*shape, DT[dtype], ACTS[(i + 3) % 6], bias=i % 2 == 1, seed=i)
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f16", "f32"])
+@pytest.mark.parametrize("shape", [(1, 8, 1), (3, 4096, 37), (9, 1032, 100), (16, 72, 515), (5, 12288, 16)], ids=str)
+def test_few_tokens(monkeypatch, shape, dtype):
+    monkeypatch.setenv("FLCE_DEBUG_LAYER_TILE", "1")
+    i = shape[0]
+    check_linear(*shape, DT[dtype], ACTS[i % 6], bias=i % 2 == 0, residual=True, seed=i)
+    check_glu(*shape, DT[dtype], ACTS[(i + 3) % 6], bias=i % 2 == 1, seed=i)
+
+
 def extreme(dt):
     big = float(torch.finfo(dt).max)
     return [0.0, -0.0, 1e-6, -1e-6, 1.0, -1.0, 20.0, -20.0, 21.0, -21.0, 90.0, -90.0, 3e4, -3e4, big, -big, math.inf,
