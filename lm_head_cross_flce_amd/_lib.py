@@ -6,6 +6,7 @@ library; if the library is missing or fails to load, every call raises.
 
 from __future__ import annotations
 
+import array
 import ctypes
 import os
 import threading
@@ -362,37 +363,43 @@ def flce_grad_norm_workspace_size(count: int) -> int:
     return b.value
 
 
-def pointer_array(addresses):
-    """A host void*[] (0 becomes NULL)."""
-    return (ctypes.c_void_p * max(len(addresses), 1))(*addresses)
+def pointer_array(addresses) -> array.array:
+    """A host void*[] (0 is NULL)."""
+    return array.array("Q", addresses)
 
 
-def size_array(sizes):
+def size_array(sizes) -> array.array:
     """A host int64_t[]."""
-    return (ctypes.c_int64 * max(len(sizes), 1))(*sizes)
+    return array.array("q", sizes)
 
 
-def dtype_array(codes):
+def dtype_array(codes) -> array.array:
     """A host flce_dtype[]."""
-    return (ctypes.c_int * max(len(codes), 1))(*codes)
+    return array.array("i", codes)
+
+
+def _host(a):
+    """The address of a host array (None: NULL)."""
+    return None if a is None else a.buffer_info()[0]
 
 
 def flce_grad_norm(grads, numels, dtypes, count, norm_type, norm, workspace, workspace_bytes, stream) -> None:
     """Raw call: grads, numels, dtypes from pointer_array, size_array and dtype_array."""
-    _check(load().flce_grad_norm(grads, numels, dtypes, count, norm_type, norm, workspace, workspace_bytes,
+    _check(load().flce_grad_norm(_host(grads), _host(numels), _host(dtypes), count, norm_type, norm, workspace, workspace_bytes,
                                  stream or None), "flce_grad_norm")
 
 
 def flce_clip_grad_norm(grads, outs, numels, dtypes, count, max_norm, norm_type, norm, workspace, workspace_bytes,
                         stream) -> None:
     """Raw call: outs is a pointer_array or None (in place)."""
-    _check(load().flce_clip_grad_norm(grads, outs, numels, dtypes, count, max_norm, norm_type, norm, workspace,
-                                      workspace_bytes, stream or None), "flce_clip_grad_norm")
+    _check(load().flce_clip_grad_norm(_host(grads), _host(outs), _host(numels), _host(dtypes), count, max_norm, norm_type,
+                                      norm, workspace, workspace_bytes, stream or None), "flce_clip_grad_norm")
 
 
 def flce_clip_grads_with_norm(grads, outs, numels, dtypes, count, max_norm, norm, stream) -> None:
     """Raw call: outs is a pointer_array or None (in place)."""
-    _check(load().flce_clip_grads_with_norm(grads, outs, numels, dtypes, count, max_norm, norm, stream or None),
+    _check(load().flce_clip_grads_with_norm(_host(grads), _host(outs), _host(numels), _host(dtypes), count, max_norm, norm,
+                                            stream or None),
            "flce_clip_grads_with_norm")
 
 

@@ -1196,17 +1196,41 @@ flce_status layer_backward(const void* x, const void* const (&W)[2], const float
 // Gradient norm and clipping
 // ---------------------------------------------------------------------------
 
-// Workgroups over all launches of one call (each launch has at least one): 8
-// per CU keep enough loads in flight, and the partials stay small enough for
-// every workgroup of the clipping pass to add them up.
-constexpr int64_t kNormBlocks = 8 * kCUs;
+// Workgroups over all launches of one call (each launch has at least one): 4
+// per CU, all resident at once, keep enough loads in flight, and the partials
+// stay few enough for every workgroup of the clipping pass to add them up.
+constexpr int64_t kNormBlocks = 4 * kCUs;
+
+// Past this many gradient bytes the norm's loads leave nothing in the 256 MB
+// memory-side cache.  Below, the clipping pass finds there what the norm has read;
+// above, little of it is left by then, and making room for it costs more.  bf16,
+// norm + clipping pass, us, keeping / not: 128 MB 52 + 41 / 24 + 79, 192 MB 74 + 70
+// / 32 + 104, 1 GB 232 + 382 / 156 + 435.
+constexpr double kNormStreamBytes = 160.0 * (1 << 20);
+
+double norm_bytes_read(const int64_t* numels, const flce_dtype* dtypes, int64_t count) {
+  double bytes = 0.0;
+  for (int64_t i = 0; i < count; ++i) bytes += (double)numels[i] * (dtypes[i] == FLCE_F32 ? 4.0 : 2.0);
+  return bytes;
+}
+
+// Bytes of a chunk: about 8 chunks a workgroup balance them, but 16 KB where
+// that still makes one each (four 16-byte loads of each thread in flight); 4 KB
+// at least, 256 KB at most.
+int64_t norm_chunk_bytes(double bytes) {
+  int64_t chunk = 4096;
+  while (chunk < (int64_t(1) << 18) &&
+         bytes > (double)chunk * (chunk < 16384 ? 1.0 : 8.0) * (double)kNormBlocks)
+    chunk *= 2;
+  return chunk;
+}
 
 // A tensor's chunks of work: whole chunks counted from its first 16-byte boundary.
-int64_t norm_chunks(const void* p, int64_t n, int64_t es) {
+int64_t norm_chunks(const void* p, int64_t n, int64_t es, int64_t chunk) {
   if (n == 0) return 0;
   int64_t head = (int64_t)((16 - ((uintptr_t)p & 15)) & 15) / es;
   if (head > n) head = n;
-  const int64_t c = cdiv(n - head, flce::kNormChunkBytes / es);
+  const int64_t c = cdiv(n - head, chunk / es);
   return c > 0 ? c : 1;
 }
 
@@ -1255,7 +1279,8 @@ flce_status check_disjoint(const void* const* grads, void* const* outs, const in
 
 // Launch table l of a call: tensors [l * kNormTensors, ...).  Returns its chunks.
 int64_t norm_table(flce::NormTable& t, const void* const* grads, void* const* outs, const int64_t* numels,
-                   const flce_dtype* dtypes, int64_t count, int64_t l) {
+                   const flce_dtype* dtypes, int64_t count, int64_t l, int64_t chunk) {
+  t.chunk_bytes = (int)chunk;
   const int64_t i0 = l * flce::kNormTensors;
   t.count = (int)std::min<int64_t>(flce::kNormTensors, count - i0);
   t.in_place = 1;
@@ -1267,7 +1292,7 @@ int64_t norm_table(flce::NormTable& t, const void* const* grads, void* const* ou
     if (t.out[k] != t.in[k] && numels[i] > 0) t.in_place = 0;
     t.n[k] = numels[i];
     t.dtype[k] = (uint8_t)dtypes[i];
-    end += norm_chunks(grads[i], numels[i], dtype_bytes(dtypes[i]));
+    end += norm_chunks(grads[i], numels[i], dtype_bytes(dtypes[i]), chunk);
     t.end[k] = end;
   }
   return end;
@@ -1279,8 +1304,10 @@ flce_status run_grad_norm(const void* const* grads, void* const* outs, const int
                           int64_t count, float max_norm, bool inf_norm, const float* given, bool clip, float* norm_out,
                           double* part, hipStream_t stream) {
   const int64_t launches = norm_launches(count);
+  const double bytes = norm_bytes_read(numels, dtypes, count);
+  const int64_t chunk = norm_chunk_bytes(bytes);
   int64_t total = 0;
-  for (int64_t i = 0; i < count; ++i) total += norm_chunks(grads[i], numels[i], dtype_bytes(dtypes[i]));
+  for (int64_t i = 0; i < count; ++i) total += norm_chunks(grads[i], numels[i], dtype_bytes(dtypes[i]), chunk);
   auto blocks_of = [&](int64_t chunks) -> int {   // this launch's share of the workgroups
     if (total <= kNormBlocks) return (int)std::max<int64_t>(1, chunks);
     return (int)std::max<int64_t>(1, (int64_t)((double)kNormBlocks * (double)chunks / (double)total));
@@ -1291,8 +1318,8 @@ flce_status run_grad_norm(const void* const* grads, void* const* outs, const int
   int parts = 0;
   if (!given) {
     for (int64_t l = 0; l < launches; ++l) {
-      const int blocks = blocks_of(norm_table(t, grads, outs, numels, dtypes, count, l));
-      if (flce::launch_grad_norm(t, inf_norm, part + parts, blocks, stream) != hipSuccess) return FLCE_ERR_HIP;
+      const int blocks = blocks_of(norm_table(t, grads, outs, numels, dtypes, count, l, chunk));
+      if (flce::launch_grad_norm(t, inf_norm, bytes > kNormStreamBytes, part + parts, blocks, stream) != hipSuccess) return FLCE_ERR_HIP;
       parts += blocks;
     }
   }
@@ -1304,7 +1331,7 @@ flce_status run_grad_norm(const void* const* grads, void* const* outs, const int
                ? FLCE_OK : FLCE_ERR_HIP;
   }
   for (int64_t l = 0; l < launches; ++l) {
-    const int blocks = blocks_of(norm_table(t, grads, outs, numels, dtypes, count, l));
+    const int blocks = blocks_of(norm_table(t, grads, outs, numels, dtypes, count, l, chunk));
     if (flce::launch_grad_clip(t, inf_norm, part, parts, given, l == 0 ? norm_out : nullptr, max_norm, blocks, stream) !=
         hipSuccess)
       return FLCE_ERR_HIP;

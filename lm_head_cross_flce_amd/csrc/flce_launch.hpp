@@ -174,7 +174,6 @@ hipError_t launch_layer_backward(const LayerBwd& a, int dtype, hipStream_t st);
 // ---------------------------------------------------------------------------
 
 constexpr int kNormTensors = 96;             // tensors of one launch: their table fits in the kernel arguments
-constexpr int64_t kNormChunkBytes = 32768;   // gradient bytes of one chunk of work
 
 struct NormTable {
   const void* in[kNormTensors];
@@ -183,11 +182,13 @@ struct NormTable {
   int64_t end[kNormTensors];        // chunks of this tensor and the ones before it
   uint8_t dtype[kNormTensors];
   int count;
+  int chunk_bytes;                  // gradient bytes of one chunk: a power of two, 4096 or more
   int in_place;                     // out is in for every tensor
 };
 
-// parts partial sums of squares (or maxima) of the table's tensors, one per workgroup.
-hipError_t launch_grad_norm(const NormTable& t, bool inf_norm, double* part, int parts, hipStream_t st);
+// parts partial sums of squares (or maxima) of the table's tensors, one per
+// workgroup.  stream: read past the memory-side cache.
+hipError_t launch_grad_norm(const NormTable& t, bool inf_norm, bool stream, double* part, int parts, hipStream_t st);
 // The norm of `parts` partials, or *given, to norm_out (if set), and the table's tensors scaled by it.
 hipError_t launch_grad_clip(const NormTable& t, bool inf_norm, const double* part, int parts, const float* given,
                             float* norm_out, float max_norm, int blocks, hipStream_t st);

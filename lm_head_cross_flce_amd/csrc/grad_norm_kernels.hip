@@ -6,8 +6,9 @@
 // HBM bounds both passes.  The tensors' addresses and sizes travel in the
 // kernel arguments (a table of up to kNormTensors), so the library copies
 // nothing to the device and a captured graph holds them.  A launch's tensors
-// are cut into chunks of kChunkBytes; a workgroup takes a run of consecutive
-// chunks, so it looks its first tensor up once and then walks the table.
+// are cut into chunks of 4 KB or more (more in a large call); a workgroup takes
+// a run of consecutive chunks, so it looks its first tensor up once and then
+// walks the table.
 // Sums of squares are kept in fp64: one element's square can pass fp32's
 // range, and the fp64 additions cost less than the loads they hide under.
 // Every workgroup leaves one partial and adds are made in a fixed order, so a
@@ -91,8 +92,8 @@ template <class T> __device__ __forceinline__ void put(T* p, float v) {
 struct Span {
   int64_t head, lo, hi;   // [lo, hi): the chunk's elements; chunk 0 also has [0, head)
 };
-template <class T> __device__ __forceinline__ Span span_of(const T* p, int64_t n, int64_t c) {
-  constexpr int64_t CH = kNormChunkBytes / (int64_t)sizeof(T);
+template <class T> __device__ __forceinline__ Span span_of(const T* p, int64_t n, int64_t c, int chunk_bytes) {
+  const int64_t CH = chunk_bytes / (int)sizeof(T);
   Span s;
   s.head = ((16 - ((uintptr_t)p & 15)) & 15) / sizeof(T);
   s.head = s.head < n ? s.head : n;
@@ -102,20 +103,22 @@ template <class T> __device__ __forceinline__ Span span_of(const T* p, int64_t n
 }
 
 // One chunk into the accumulator: 16 bytes a thread, 4 loads in flight.
-template <class T, bool INF>
-__device__ __forceinline__ void norm_chunk(NormAcc<INF>& a, const T* p, int64_t n, int64_t c) {
-  const Span s = span_of(p, n, c);
+// STREAM: loads that leave nothing in the memory-side cache.
+template <class T, bool INF, bool STREAM>
+__device__ __forceinline__ void norm_chunk(NormAcc<INF>& a, const T* p, int64_t n, int64_t c, int chunk_bytes) {
+  const Span s = span_of(p, n, c, chunk_bytes);
   const int tid = threadIdx.x;
   if (c == 0 && tid < s.head) a.add(one(p + tid));
   constexpr int V = Vec<T>::kN;
   const int64_t len = s.hi > s.lo ? s.hi - s.lo : 0;
   const int nv = (int)(len / V);
   const u32x4* q = (const u32x4*)(p + s.lo);
+  auto fetch = [&](int i) { return STREAM ? __builtin_nontemporal_load(q + i) : q[i]; };
   int i = tid;
   for (; i + 768 < nv; i += 1024) {
     u32x4 w[4];
 #pragma unroll
-    for (int k = 0; k < 4; ++k) w[k] = q[i + 256 * k];
+    for (int k = 0; k < 4; ++k) w[k] = fetch(i + 256 * k);
 #pragma unroll
     for (int k = 0; k < 4; ++k) {
       const Vec<T> v(w[k]);
@@ -124,7 +127,7 @@ __device__ __forceinline__ void norm_chunk(NormAcc<INF>& a, const T* p, int64_t 
     }
   }
   for (; i < nv; i += 256) {
-    const Vec<T> v(q[i]);
+    const Vec<T> v(fetch(i));
 #pragma unroll
     for (int e = 0; e < V; ++e) a.add(v.v[e]);
   }
@@ -133,8 +136,8 @@ __device__ __forceinline__ void norm_chunk(NormAcc<INF>& a, const T* p, int64_t 
 }
 
 template <class T>
-__device__ __forceinline__ void clip_chunk(const T* p, T* d, int64_t n, int64_t c, float coef) {
-  const Span s = span_of(p, n, c);
+__device__ __forceinline__ void clip_chunk(const T* p, T* d, int64_t n, int64_t c, int chunk_bytes, float coef) {
+  const Span s = span_of(p, n, c, chunk_bytes);
   const int tid = threadIdx.x;
   constexpr int V = Vec<T>::kN;
   if (c == 0 && tid < s.head) put(d + tid, one(p + tid) * coef);
@@ -154,20 +157,20 @@ __device__ __forceinline__ void clip_chunk(const T* p, T* d, int64_t n, int64_t 
   for (int64_t t = s.lo + (int64_t)nv * V + tid; t < s.hi; t += 256) put(d + t, one(p + t) * coef);
 }
 
-// First tensor whose chunks end past chunk c.
+// The tensor that holds chunk c: the number of tensors whose chunks end at or
+// before it, counted by all lanes at once (a search through the table would
+// wait for a load from the kernel arguments at each step).
 __device__ __forceinline__ int find_tensor(const NormTable& t, int64_t c) {
-  int lo = 0, hi = t.count - 1;
-  while (lo < hi) {
-    const int mid = (lo + hi) >> 1;
-    if (t.end[mid] > c) hi = mid;
-    else lo = mid + 1;
-  }
-  return lo;
+  static_assert(kNormTensors <= 128, "two entries a lane");
+  const int lane = threadIdx.x & 63;
+  const bool a = lane < t.count && t.end[lane] <= c;
+  const bool b = lane + 64 < t.count && t.end[lane + 64 < kNormTensors ? lane + 64 : 0] <= c;
+  return __popcll(__ballot(a)) + __popcll(__ballot(b));
 }
 
 }  // namespace
 
-template <bool INF> __global__ void __launch_bounds__(256) grad_norm_kernel(NormTable t, double* part) {
+template <bool INF, bool STREAM> __global__ void __launch_bounds__(256) grad_norm_kernel(NormTable t, double* part) {
   const int64_t total = t.count ? t.end[t.count - 1] : 0;
   const int64_t c0 = total * blockIdx.x / gridDim.x, c1 = total * (blockIdx.x + 1) / gridDim.x;
   NormAcc<INF> a{};
@@ -175,9 +178,9 @@ template <bool INF> __global__ void __launch_bounds__(256) grad_norm_kernel(Norm
   for (int64_t c = c0; c < c1; ++c) {
     while (t.end[k] <= c) ++k;
     const int64_t cc = c - (k ? t.end[k - 1] : 0);
-    if (t.dtype[k] == 1) norm_chunk<uint16_t, INF>(a, (const uint16_t*)t.in[k], t.n[k], cc);
-    else if (t.dtype[k] == 2) norm_chunk<_Float16, INF>(a, (const _Float16*)t.in[k], t.n[k], cc);
-    else norm_chunk<float, INF>(a, (const float*)t.in[k], t.n[k], cc);
+    if (t.dtype[k] == 1) norm_chunk<uint16_t, INF, STREAM>(a, (const uint16_t*)t.in[k], t.n[k], cc, t.chunk_bytes);
+    else if (t.dtype[k] == 2) norm_chunk<_Float16, INF, STREAM>(a, (const _Float16*)t.in[k], t.n[k], cc, t.chunk_bytes);
+    else norm_chunk<float, INF, STREAM>(a, (const float*)t.in[k], t.n[k], cc, t.chunk_bytes);
   }
   a = block_reduce(a);
   if (threadIdx.x == 0) part[blockIdx.x] = INF ? (double)a.m : a.s;
@@ -211,21 +214,26 @@ template <bool INF> __global__ void __launch_bounds__(256) grad_clip_kernel(Norm
   const double cd = (double)max_norm / (nd + 1e-6);
   const float coef = cd > 1.0 ? 1.f : (float)cd;   // NaN stays
   if (coef == 1.f && t.in_place) return;           // every gradient keeps its value
+  // The run of chunks that this workgroup of the norm's launch read, last one
+  // first: those are still in the memory-side cache.
   const int64_t total = t.end[t.count - 1];
   const int64_t c0 = total * blockIdx.x / gridDim.x, c1 = total * (blockIdx.x + 1) / gridDim.x;
-  int k = c0 < c1 ? find_tensor(t, c0) : 0;
-  for (int64_t c = c0; c < c1; ++c) {
-    while (t.end[k] <= c) ++k;
+  int k = c0 < c1 ? find_tensor(t, c1 - 1) : 0;
+  for (int64_t c = c1 - 1; c >= c0; --c) {
+    while (k && t.end[k - 1] > c) --k;
     const int64_t cc = c - (k ? t.end[k - 1] : 0);
-    if (t.dtype[k] == 1) clip_chunk((const uint16_t*)t.in[k], (uint16_t*)t.out[k], t.n[k], cc, coef);
-    else if (t.dtype[k] == 2) clip_chunk((const _Float16*)t.in[k], (_Float16*)t.out[k], t.n[k], cc, coef);
-    else clip_chunk((const float*)t.in[k], (float*)t.out[k], t.n[k], cc, coef);
+    if (t.dtype[k] == 1) clip_chunk((const uint16_t*)t.in[k], (uint16_t*)t.out[k], t.n[k], cc, t.chunk_bytes, coef);
+    else if (t.dtype[k] == 2) clip_chunk((const _Float16*)t.in[k], (_Float16*)t.out[k], t.n[k], cc, t.chunk_bytes, coef);
+    else clip_chunk((const float*)t.in[k], (float*)t.out[k], t.n[k], cc, t.chunk_bytes, coef);
   }
 }
 
-hipError_t launch_grad_norm(const NormTable& t, bool inf_norm, double* part, int parts, hipStream_t st) {
-  if (inf_norm) FLCE_LAUNCH((grad_norm_kernel<true>), dim3(parts), dim3(256), 0, st, t, part);
-  else FLCE_LAUNCH((grad_norm_kernel<false>), dim3(parts), dim3(256), 0, st, t, part);
+hipError_t launch_grad_norm(const NormTable& t, bool inf_norm, bool stream, double* part, int parts, hipStream_t st) {
+  const dim3 grid(parts), blk(256);
+  if (inf_norm && stream) FLCE_LAUNCH((grad_norm_kernel<true, true>), grid, blk, 0, st, t, part);
+  else if (inf_norm) FLCE_LAUNCH((grad_norm_kernel<true, false>), grid, blk, 0, st, t, part);
+  else if (stream) FLCE_LAUNCH((grad_norm_kernel<false, true>), grid, blk, 0, st, t, part);
+  else FLCE_LAUNCH((grad_norm_kernel<false, false>), grid, blk, 0, st, t, part);
   return hipGetLastError();
 }
 

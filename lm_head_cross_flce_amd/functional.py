@@ -11,6 +11,7 @@ gradients produced in backward rather than in forward (DeepSpeed PR 8792).
 
 from __future__ import annotations
 
+import operator
 from typing import Optional, Tuple
 
 import torch
@@ -600,6 +601,13 @@ def _is_dense(t: torch.Tensor) -> bool:
     return True
 
 
+# One attribute of every tensor of a list: a training step passes hundreds, and
+# a Python loop over them would take longer than the kernels.
+_contiguous, _address, _numel, _shape = (torch.Tensor.is_contiguous, torch.Tensor.data_ptr, torch.Tensor.numel,
+                                         torch.Tensor.size)
+_dtype, _device, _layout = (operator.attrgetter(a) for a in ("dtype", "device", "layout"))
+
+
 def _prep_grads(grads, out):
     grads = list(grads)
     if not grads:
@@ -607,37 +615,37 @@ def _prep_grads(grads, out):
     dev = grads[0].device
     if not grads[0].is_cuda:
         raise ValueError("tensors must live on a GPU")
-    for g in grads:
-        if g.device != dev:
-            raise ValueError("all gradients must be on one device")
-        _dtype_code(g)
-        if g.layout != torch.strided:
-            raise ValueError("gradients must be dense tensors")
+    if set(map(_device, grads)) != {dev}:
+        raise ValueError("all gradients must be on one device")
+    if set(map(_layout, grads)) != {torch.strided}:
+        raise ValueError("gradients must be dense tensors")
+    dtypes = list(map(_dtype, grads))
+    for t in set(dtypes):
+        if t not in _DTYPES:
+            raise TypeError(f"unsupported dtype {t}; use bfloat16, float16 or float32")
     if out is not None:
         out = list(out)
-        if len(out) != len(grads):
-            raise ValueError("out must have one tensor per gradient")
-        for g, o in zip(grads, out):
-            if o.dtype != g.dtype or o.shape != g.shape or o.device != dev:
-                raise ValueError("each out tensor must have its gradient's shape, dtype and device")
-    return grads, out, dev
+        if (list(map(_shape, grads)) != list(map(_shape, out)) or dtypes != list(map(_dtype, out))
+                or set(map(_device, out)) != {dev}):
+            raise ValueError("out must have one tensor per gradient, of its shape, dtype and device")
+    return grads, out, dev, _lib.dtype_array([_DTYPES[t] for t in dtypes])
 
 
-def _grad_arrays(grads):
-    return (_lib.pointer_array([g.data_ptr() for g in grads]), _lib.size_array([g.numel() for g in grads]),
-            _lib.dtype_array([_DTYPES[g.dtype] for g in grads]), len(grads))
+def _norm_workspace(count, dev):
+    nbytes = _lib.flce_grad_norm_workspace_size(count)
+    return torch.empty(nbytes, dtype=torch.uint8, device=dev), torch.empty(1, dtype=torch.float32, device=dev)
 
 
 def flce_grad_norm(grads, norm_type: float = 2.0) -> torch.Tensor:
     """The norm (2 or inf) over every element of every tensor, float32 [1]."""
-    grads, _, dev = _prep_grads(grads, None)
-    grads = [g if _is_dense(g) else g.contiguous() for g in grads]
-    norm = torch.empty(1, dtype=torch.float32, device=dev)
-    nbytes = _lib.flce_grad_norm_workspace_size(len(grads))
-    workspace = torch.empty(nbytes, dtype=torch.uint8, device=dev)
+    grads, _, dev, dtypes = _prep_grads(grads, None)
+    if not all(map(_contiguous, grads)):
+        grads = [g if _is_dense(g) else g.contiguous() for g in grads]
+    workspace, norm = _norm_workspace(len(grads), dev)
     with torch.cuda.device(dev):
         stream = torch.cuda.current_stream(dev).cuda_stream
-        _lib.flce_grad_norm(*_grad_arrays(grads), float(norm_type), norm.data_ptr(), workspace.data_ptr(), nbytes,
+        _lib.flce_grad_norm(_lib.pointer_array(map(_address, grads)), _lib.size_array(map(_numel, grads)), dtypes,
+                            len(grads), float(norm_type), norm.data_ptr(), workspace.data_ptr(), workspace.numel(),
                             stream)
     return norm
 
@@ -656,37 +664,39 @@ def flce_clip_grads_with_norm(grads, max_norm: float, norm: torch.Tensor, out=No
 
 
 def _clip(grads, max_norm, norm_type, given, out):
-    grads, out, dev = _prep_grads(grads, out)
+    grads, out, dev, dtypes = _prep_grads(grads, out)
     if given is not None and given.device != dev:
         raise ValueError("norm and the gradients must be on one device")
-    # A gradient whose elements do not fill one stretch of memory goes through
-    # a dense copy, as does one whose out tensor orders its elements otherwise.
     dst = grads if out is None else out
-    for d in dst:
-        if any(st == 0 and sz > 1 for st, sz in zip(d.stride(), d.shape)):
-            raise ValueError("a tensor that repeats its elements cannot be scaled")
-    src, tmp = [], []
-    for g, d in zip(grads, dst):
-        plain = _is_dense(g) and _is_dense(d) and (g.stride() == d.stride() or (g.is_contiguous() and d.is_contiguous()))
-        src.append(g if plain else g.contiguous())
-        tmp.append(d if plain else torch.empty(g.shape, dtype=g.dtype, device=dev))
-    arrays = _grad_arrays(src)
-    outs = None if out is None and all(a is b for a, b in zip(tmp, dst)) else _lib.pointer_array(
-        [t.data_ptr() for t in tmp])
+    src, tmp = grads, dst
+    if not (all(map(_contiguous, grads)) and (out is None or all(map(_contiguous, out)))):
+        # A gradient whose elements do not fill one stretch of memory goes through
+        # a dense copy, as does one whose out tensor orders its elements otherwise.
+        src, tmp = [], []
+        for g, d in zip(grads, dst):
+            if any(st == 0 and sz > 1 for st, sz in zip(d.stride(), d.shape)):
+                raise ValueError("a tensor that repeats its elements cannot be scaled")
+            plain = _is_dense(g) and _is_dense(d) and (g.stride() == d.stride()
+                                                       or (g.is_contiguous() and d.is_contiguous()))
+            src.append(g if plain else g.contiguous())
+            tmp.append(d if plain else torch.empty(g.shape, dtype=g.dtype, device=dev))
+    count = len(src)
+    addresses, sizes = _lib.pointer_array(map(_address, src)), _lib.size_array(map(_numel, src))
+    outs = None if tmp is grads else _lib.pointer_array(map(_address, tmp))
+    norm = None
     with torch.cuda.device(dev):
         stream = torch.cuda.current_stream(dev).cuda_stream
         if given is not None:
-            _lib.flce_clip_grads_with_norm(arrays[0], outs, *arrays[1:], float(max_norm), given.data_ptr(), stream)
-            norm = None
+            _lib.flce_clip_grads_with_norm(addresses, outs, sizes, dtypes, count, float(max_norm), given.data_ptr(),
+                                           stream)
         else:
-            norm = torch.empty(1, dtype=torch.float32, device=dev)
-            nbytes = _lib.flce_grad_norm_workspace_size(len(grads))
-            workspace = torch.empty(nbytes, dtype=torch.uint8, device=dev)
-            _lib.flce_clip_grad_norm(arrays[0], outs, *arrays[1:], float(max_norm), float(norm_type),
-                                     norm.data_ptr(), workspace.data_ptr(), nbytes, stream)
-    for t, d in zip(tmp, dst):
-        if t is not d:
-            d.copy_(t)
+            workspace, norm = _norm_workspace(count, dev)
+            _lib.flce_clip_grad_norm(addresses, outs, sizes, dtypes, count, float(max_norm), float(norm_type),
+                                     norm.data_ptr(), workspace.data_ptr(), workspace.numel(), stream)
+    if tmp is not dst:
+        for t, d in zip(tmp, dst):
+            if t is not d:
+                d.copy_(t)
     return norm
 
 
