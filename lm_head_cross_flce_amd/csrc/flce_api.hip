@@ -997,14 +997,14 @@ int64_t part_depth(int64_t K, int64_t parts) { return parts > 1 ? cdiv(cdiv(K, p
 // activation): within a fifth of most, and it picks the fastest or one within
 // 15% of it.  Some of them, us at S = 8 / 4 / 2: 300 x 700 x 500 20.4 / 8.4 / 5.0,
 // 1024 x 4096 x 1024 23.5 / 16.3 / 10.8, 2048 x 4096 x 1024 35.6 / 17.4 / 24.1,
-// 4096 x 4096 x 4096 90 / 120 / 175; fp32 300 x 700 x 500 - / 37 / 12,
-// 4096 x 4096 x 1024 - / 275 / 294.
+// 4096 x 4096 x 4096 90 / 120 / 175; fp32 at S = 4 / 2: 100 x 64 x 64 3.9 / 1.3,
+// 300 x 700 x 500 16.8 / 11.3, 4096 x 4096 x 1024 167 / 218.
 struct TileCost {
   int S;
   double alone, shared, per_tile, fixed;
 };
 constexpr TileCost kCost16[] = {{8, 20.0, 20.0, 7000.0, 0.0}, {4, 10.5, 7.3, 500.0, 1000.0}, {2, 8.0, 2.7, 200.0, 800.0}};
-constexpr TileCost kCost32[] = {{4, 72.0, 67.0, 500.0, 1500.0}, {2, 23.0, 18.0, 200.0, 1000.0}};
+constexpr TileCost kCost32[] = {{4, 55.0, 41.0, 700.0, 2500.0}, {2, 24.0, 15.0, 200.0, 1000.0}};
 constexpr double kJoinNs = 1500.0, kJoinNsPerByte = 0.235e-3;
 
 // FLCE_DEBUG_LAYER_TILE: the tests run every S (2, 4, 8) on every shape with it,

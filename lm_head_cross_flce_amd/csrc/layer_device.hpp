@@ -249,7 +249,8 @@ __device__ __forceinline__ void buf_load_vec(__amdgpu_buffer_rsrc_t r, uint32_t 
 template <class T, int S_> struct Tile {
   static_assert(S_ == 2 || S_ == 4 || (S_ == 8 && sizeof(T) == 2), "tile sizes");
   static constexpr int S = S_, M = 32 * S;
-  static constexpr int kPerCu = S == 8 ? 1 : S == 4 ? 2 : 4;
+  // workgroups a CU should hold; fp32's staged values need a third more registers
+  static constexpr int kPerCu = S == 8 ? 1 : S == 4 ? 2 : sizeof(T) == 4 ? 3 : 4;
 };
 
 // Column order of a tile: in each wave's half (16 NJ rows of the weight
@@ -504,16 +505,47 @@ __device__ __forceinline__ void gemm_small(f32x4 (&acc)[S][S], const CA& ca, int
   }
 }
 
-// fp32: 32-deep stages through registers into padded LDS rows.  MFMA bounds it
-// (v_mfma_f32_16x16x4_f32 takes 32 cycles, against one 16-byte LDS read per S
-// of them): 127 TFLOP/s at 4096 x 4096 x 1024 and S = 4.  The scheduling barrier
-// keeps one half stage's fragments live at a time; with the raised priority it
-// took that product from 280 to 270 us, 4096 x 4096 x 2048 from 580 to 550.
+// fp32 products on the bf16 matrix cores.  A float's 24 significant bits are
+// exactly three bfloat16 parts of 8, x = h + m + l (each the truncation of what
+// the parts before it leave), so of the nine products of parts the six with
+// weight 2^-16 or more, hh + hm + mh + hl + lh + mm, give x y to about 2^-23
+// relative, as near as one fp32 rounding, and they accumulate in fp32 like
+// any product here.  Six 16-cycle instructions do 32 k of a block, where the
+// fp32 instruction takes eight of 32 cycles: 4096 x 4096 x 1024 at S = 4 takes 167 us
+// (205 TFLOP/s), 270 with those.  An infinity among the operands gives NaN (its second part is
+// infinity less infinity).
 constexpr int kF32K = 32;
+constexpr int kPartRow = 208;   // LDS bytes of a row: 3 parts x 32 k, and a pad that spreads 16 rows over the banks
+
+struct Parts {
+  u32x2 p[3];   // four values' h, m, l
+};
+__device__ __forceinline__ Parts split_parts(const u32x4& v) {
+  uint32_t m[4], l[4];
+#pragma unroll
+  for (int e = 0; e < 4; ++e) {
+    const float r = __uint_as_float(v[e]) - __uint_as_float(v[e] & 0xffff0000u);
+    m[e] = __float_as_uint(r);
+    l[e] = __float_as_uint(r - __uint_as_float(m[e] & 0xffff0000u));
+  }
+  auto high = [](uint32_t a, uint32_t b) { return __builtin_amdgcn_perm(b, a, 0x07060302u); };   // both upper halves
+  Parts o;
+  o.p[0] = u32x2{high(v[0], v[1]), high(v[2], v[3])};
+  o.p[1] = u32x2{high(m[0], m[1]), high(m[2], m[3])};
+  o.p[2] = u32x2{high(l[0], l[1]), high(l[2], l[3])};
+  return o;
+}
+// Four consecutive k (k4 their index / 4) of a row to LDS.
+__device__ __forceinline__ void store_parts(lds_t* row, int k4, const u32x4& v) {
+  typedef __attribute__((address_space(3))) u32x2 lds_u32x2;
+  const Parts o = split_parts(v);
+#pragma unroll
+  for (int k = 0; k < 3; ++k) *(lds_u32x2*)(row + 64 * k + 8 * k4) = o.p[k];
+}
 
 template <int S, bool PERM, bool GLU> struct RowCopy<float, S, PERM, GLU> {
-  static constexpr int kBytes = 32 * S * kRowBytes;
-  u32x4 r[S];
+  static constexpr int kBytes = 32 * S * kPartRow;
+  u32x4 r[2][S];
   uint32_t off[S];
   const float* base[2];
   int kc4;
@@ -528,23 +560,23 @@ template <int S, bool PERM, bool GLU> struct RowCopy<float, S, PERM, GLU> {
       off[q] = m0 + row < rows ? (uint32_t)(((int64_t)row * ld + kc4) * 4) : kOOB;
     }
   }
-  __device__ __forceinline__ void load(int k0, int kext) {
+  __device__ __forceinline__ void load(int h, int k0, int kext) {
     const __amdgpu_buffer_rsrc_t r0 = make_rsrc(base[0] + k0), r1 = make_rsrc(base[1] + k0);
     const bool in = k0 + kc4 < kext;
 #pragma unroll
-    for (int q = 0; q < S; ++q) r[q] = buf_load16(GLU && pass_is_up<S>(q) ? r1 : r0, in ? off[q] : kOOB);
+    for (int q = 0; q < S; ++q) r[h][q] = buf_load16(GLU && pass_is_up<S>(q) ? r1 : r0, in ? off[q] : kOOB);
   }
-  __device__ __forceinline__ void store(lds_t* buf, int tid) const {
+  __device__ __forceinline__ void store(int h, lds_t* buf, int tid) const {
 #pragma unroll
-    for (int q = 0; q < S; ++q) lds_store16(buf + ((tid >> 3) + 32 * q) * kRowBytes + (tid & 7) * 16, r[q]);
+    for (int q = 0; q < S; ++q) store_parts(buf + ((tid >> 3) + 32 * q) * kPartRow, tid & 7, r[h][q]);
   }
 };
 
 // M-contiguous operand: 4 x 4 blocks transposed in registers, thread (kc, mc)
 // = (tid % 8, tid / 8); S = 2 needs half the threads.
 template <int S> struct ColCopy<float, S> {
-  static constexpr int kBytes = 32 * S * kRowBytes;
-  u32x4 r[4];
+  static constexpr int kBytes = 32 * S * kPartRow;
+  u32x4 r[2][4];
   uint32_t off[4];
   SegRows s;
   int m0;
@@ -556,69 +588,71 @@ template <int S> struct ColCopy<float, S> {
     for (int e = 0; e < 4; ++e)
       off[e] = m < 32 * S && m0 + m < cols ? (uint32_t)(((int64_t)(k + e) * s.ld + m) * 4) : kOOB;
   }
-  __device__ __forceinline__ void load(int k0, int) {
+  __device__ __forceinline__ void load(int h, int k0, int) {
     const __amdgpu_buffer_rsrc_t rs = s.rsrc<4>(k0, m0);
 #pragma unroll
-    for (int e = 0; e < 4; ++e) r[e] = buf_load16(rs, off[e]);
+    for (int e = 0; e < 4; ++e) r[h][e] = buf_load16(rs, off[e]);
   }
-  __device__ __forceinline__ void store(lds_t* buf, int tid) const {
+  __device__ __forceinline__ void store(int h, lds_t* buf, int tid) const {
     const int m = (tid >> 3) * 4;
     if (m >= 32 * S) return;
 #pragma unroll
     for (int i = 0; i < 4; ++i)
-      lds_store16(buf + (m + i) * kRowBytes + (tid & 7) * 16, u32x4{r[0][i], r[1][i], r[2][i], r[3][i]});
+      store_parts(buf + (m + i) * kPartRow, tid & 7, u32x4{r[h][0][i], r[h][1][i], r[h][2][i], r[h][3][i]});
   }
 };
 
+// One LDS buffer an operand: the next two stages' values are on their way into
+// registers while this one is computed, and the CU's other workgroups run under
+// the two barriers and the splitting.
 template <int S, class CA, class CB>
 __device__ __forceinline__ void gemm_small_f32(f32x4 (&acc)[S][S], CA& ca, int ka, CB& cb, int kb, int K, int tid) {
-  __shared__ __attribute__((aligned(16))) char lds[2][2][CA::kBytes];
-  static_assert(CA::kBytes == CB::kBytes, "square tiles");
+  __shared__ __attribute__((aligned(16))) char lds_a[CA::kBytes];
+  __shared__ __attribute__((aligned(16))) char lds_b[CB::kBytes];
   const int lane = tid & 63, wave = tid >> 6;
 #pragma unroll
   for (int i = 0; i < S; ++i)
 #pragma unroll
     for (int j = 0; j < S; ++j) acc[i][j] = f32x4{0.f, 0.f, 0.f, 0.f};
-  const int frag = (lane & 15) * kRowBytes + (lane >> 4) * 16;
-  const int pa = (wave >> 1) * 16 * S * kRowBytes + frag, pb = (wave & 1) * 16 * S * kRowBytes + frag;
+  const int frag = (lane & 15) * kPartRow + (lane >> 4) * 16;
+  const lds_t* A = (const lds_t*)lds_a + (wave >> 1) * 16 * S * kPartRow + frag;
+  const lds_t* B = (const lds_t*)lds_b + (wave & 1) * 16 * S * kPartRow + frag;
   const int KT = (K + kF32K - 1) / kF32K;
-  ca.load(0, ka);
-  cb.load(0, kb);
-  ca.store((lds_t*)lds[0][0], tid);
-  cb.store((lds_t*)lds[0][1], tid);
-  __syncthreads();
-  for (int kt = 0; kt < KT; ++kt) {
-    const int cur = kt & 1;
-    if (kt + 1 < KT) {
-      ca.load((kt + 1) * kF32K, ka);
-      cb.load((kt + 1) * kF32K, kb);
-    }
-    const lds_t* A = (const lds_t*)lds[cur][0];
-    const lds_t* B = (const lds_t*)lds[cur][1];
+  auto load = [&](int h, int kt) {   // stages past K read zeros
+    ca.load(h, kt * kF32K, ka);
+    cb.load(h, kt * kF32K, kb);
+  };
+  auto stage = [&](int h, int kt) {
+    ca.store(h, (lds_t*)lds_a, tid);
+    cb.store(h, (lds_t*)lds_b, tid);
+    __syncthreads();
+    load(h, kt + 2);
+    u32x4 b[3][S];
 #pragma unroll
-    for (int h = 0; h < 2; ++h) {
-      __builtin_amdgcn_sched_barrier(0);
-      f32x4 a[S], b[S];
+    for (int k = 0; k < 3; ++k)
 #pragma unroll
-      for (int i = 0; i < S; ++i) {
-        a[i] = __builtin_bit_cast(f32x4, lds_load16(A + pa + 16 * i * kRowBytes + 64 * h));
-        b[i] = __builtin_bit_cast(f32x4, lds_load16(B + pb + 16 * i * kRowBytes + 64 * h));
-      }
+      for (int j = 0; j < S; ++j) b[k][j] = lds_load16(B + 16 * j * kPartRow + 64 * k);
+#pragma unroll
+    for (int k = 2; k >= 0; --k) {   // the small products first
+      u32x4 a[S];
+#pragma unroll
+      for (int i = 0; i < S; ++i) a[i] = lds_load16(A + 16 * i * kPartRow + 64 * k);
       __builtin_amdgcn_s_setprio(1);
 #pragma unroll
-      for (int e = 0; e < 4; ++e)
+      for (int l = 2 - k; l >= 0; --l)
 #pragma unroll
         for (int i = 0; i < S; ++i)
 #pragma unroll
-          for (int j = 0; j < S; ++j)
-            acc[i][j] = __builtin_amdgcn_mfma_f32_16x16x4f32(a[i][e], b[j][e], acc[i][j], 0, 0, 0);
+          for (int j = 0; j < S; ++j) mma_frag<uint16_t>(acc[i][j], a[i], b[l][j]);
       __builtin_amdgcn_s_setprio(0);
     }
-    if (kt + 1 < KT) {
-      ca.store((lds_t*)lds[cur ^ 1][0], tid);
-      cb.store((lds_t*)lds[cur ^ 1][1], tid);
-    }
     __syncthreads();
+  };
+  load(0, 0);
+  load(1, 1);
+  for (int kt = 0; kt < KT; kt += 2) {
+    stage(0, kt);
+    if (kt + 1 < KT) stage(1, kt + 1);
   }
 }
 
