@@ -386,9 +386,9 @@ flce_status flce_shard_backward(const void* x, const void* W_shard, const void* 
  * own transform), each with its gradients.  Conventions as above; also:
  *  - x [N, H], weights [F, H], outputs and their gradients [N, F], biases [F];
  *    every [.., ..] tensor 16-byte aligned, biases and their gradients
- *    element-aligned; H a multiple of 8 (FLCE_ERR_UNSUPPORTED otherwise), F
- *    and N any size, N = 0 included (weight gradients are then zero, and the
- *    token tensors may be NULL).
+ *    element-aligned.  Any H, F and N, N = 0 included (weight gradients are then
+ *    zero, and the token tensors may be NULL).  An H that is no multiple of 8
+ *    costs a launch and a padded copy of x and the weights in the workspace.
  *  - Products accumulate in fp32 whatever the dtype; results are rounded once.
  *    float32 operands (more than 16 tokens) are multiplied as three bfloat16
  *    parts each, which hold all 24 bits: a product is right to about 2^-23, as
@@ -422,9 +422,9 @@ typedef FLCE_ENUM(flce_activation) {
  * z is the forward's, ignored with FLCE_ACT_NONE.
  *
  * flce_linear_workspace_size: bytes for the forward (fp32 partial sums when a
- * few output tiles are split along H; 0 otherwise, and the workspace may then
- * be NULL) and the backward (dz unless it is dy itself, fp32 partials of db
- * and of split products); pure host arithmetic, either output may be NULL.
+ * few output tiles are split along H, and padded rows; 0 otherwise, and the
+ * workspace may then be NULL) and the backward (dz unless it is dy itself, fp32
+ * partials of db and of split products, padded rows); pure host arithmetic, either output may be NULL.
  */
 flce_status flce_linear_workspace_size(int64_t N, int64_t H, int64_t F, flce_dtype dtype, flce_activation activation,
                                        size_t* fwd_bytes, size_t* bwd_bytes);

@@ -1044,6 +1044,8 @@ Cut product_cut(int64_t M, int64_t N, int64_t K, int dtype) {
 }
 
 struct LayerGeometry {
+  int64_t Hp;          // H rounded up to 8: the width of the rows that the kernels read
+  size_t pad_bytes;    // padded copies of x and the weights (none when Hp == H), first in both workspaces
   int fwd_tile, TM, TN, fwd_parts;
   int64_t kc, ldp;
   size_t fwd_total;
@@ -1056,9 +1058,12 @@ struct LayerGeometry {
   size_t off_dbp, off_part, bwd_total;
 };
 
-LayerGeometry layer_geometry(int64_t N, int64_t H, int64_t F, int dtype, int act, int nmat) {
+LayerGeometry layer_geometry(int64_t N, int64_t Hout, int64_t F, int dtype, int act, int nmat) {
   LayerGeometry g{};
   const int64_t es = dtype == FLCE_F32 ? 4 : 2;
+  const int64_t H = cdiv(Hout, 8) * 8;
+  g.Hp = H;
+  g.pad_bytes = H == Hout ? 0 : align_up((size_t)(N + nmat * F) * H * es);
   Cut fwd = product_cut(N, nmat * F, H, dtype);
   const int forced = forced_tile();
   if (forced == 1 ? N <= flce::kSkinnyMost : forced == 0 && N <= flce::skinny_tokens(dtype)) fwd = {0, 1};
@@ -1068,7 +1073,7 @@ LayerGeometry layer_geometry(int64_t N, int64_t H, int64_t F, int dtype, int act
   g.fwd_parts = fwd.parts;
   g.kc = part_depth(H, g.fwd_parts);
   g.ldp = nmat * cdiv(F, 8) * 8;
-  g.fwd_total = g.fwd_parts > 1 ? align_up((size_t)g.fwd_parts * N * g.ldp * 4) : 0;
+  g.fwd_total = g.pad_bytes + (g.fwd_parts > 1 ? align_up((size_t)g.fwd_parts * N * g.ldp * 4) : 0);
 
   // dz: rows padded to 16-byte pieces; the gated product's two halves each to
   // a whole 64-deep copy block, so that no block of the dx product straddles
@@ -1076,7 +1081,7 @@ LayerGeometry layer_geometry(int64_t N, int64_t H, int64_t F, int dtype, int act
   g.dz_is_dy = nmat == 1 && act == FLCE_ACT_NONE && F % 8 == 0;
   g.segk = nmat == 2 ? cdiv(F, 64) * 64 : int64_t(1) << 30;
   g.ldz = nmat == 2 ? 2 * g.segk : cdiv(F, 8) * 8;
-  size_t off = g.dz_is_dy ? 0 : align_up((size_t)N * g.ldz * es);
+  size_t off = g.pad_bytes + (g.dz_is_dy ? 0 : align_up((size_t)N * g.ldz * es));
   // Column sums: 64 tokens a block, more when that makes over 64 blocks.
   g.db_rows = (int)(cdiv(cdiv(N, 64), 64) * 64);
   if (g.db_rows < 64) g.db_rows = 64;
@@ -1104,7 +1109,6 @@ flce_status check_layer(int64_t N, int64_t H, int64_t F, int dtype, int act, int
   if (dtype != FLCE_F32 && dtype != FLCE_BF16 && dtype != FLCE_F16) return FLCE_ERR_UNSUPPORTED;
   if (N > (int64_t(1) << 30) || H > (int64_t(1) << 20) || F > (int64_t(1) << (nmat == 2 ? 19 : 20)))
     return FLCE_ERR_UNSUPPORTED;
-  if (H % 8 != 0) return FLCE_ERR_UNSUPPORTED;
   const int64_t wide = H > F ? H : F;   // every plane of output tiles fits in an int
   if (cdiv(N, 64) * cdiv(wide, 32) > (int64_t(1) << 27) || cdiv(F, 32) * cdiv(H, 64) > (int64_t(1) << 27))
     return FLCE_ERR_UNSUPPORTED;
@@ -1112,6 +1116,20 @@ flce_status check_layer(int64_t N, int64_t H, int64_t F, int dtype, int act, int
 }
 
 bool bad_tensor(const void* p, size_t align, bool required) { return p ? !aligned(p, align) : required; }
+
+// x and the weights as the kernels read them: themselves, or padded copies in
+// the workspace.
+bool pad_rows(const LayerGeometry& g, const void* x, const void* const (&W)[2], int64_t N, int64_t H, int64_t F, int dtype,
+              int nmat, char* ws, hipStream_t stream, const void*& xo, const void* (&Wo)[2]) {
+  xo = x;
+  for (int m = 0; m < nmat; ++m) Wo[m] = W[m];
+  if (g.Hp == H) return true;
+  const int64_t row = g.Hp * (dtype == FLCE_F32 ? 4 : 2);
+  const flce::LayerPad p{{x, W[0], W[1]}, {N, F, nmat == 2 ? F : 0}, (int)H, (int)g.Hp, ws};
+  xo = ws;
+  for (int m = 0; m < nmat; ++m) Wo[m] = ws + (N + m * F) * row;
+  return flce::launch_layer_pad(p, dtype, stream) == hipSuccess;
+}
 
 // The entry points' shared parts: nmat = 1 is the linear layer, 2 the gated product.
 flce_status layer_forward(const void* x, const void* const (&W)[2], const void* const (&b)[2], const void* residual,
@@ -1130,22 +1148,22 @@ flce_status layer_forward(const void* x, const void* const (&W)[2], const void* 
   if (workspace_bytes < g.fwd_total) return FLCE_ERR_WORKSPACE_TOO_SMALL;
   if (bad_tensor(workspace, 16, g.fwd_total > 0)) return FLCE_ERR_INVALID_ARGUMENT;
   if (!rows) return FLCE_OK;
+  char* ws = (char*)workspace;
   flce::LayerFwd a{};
-  a.x = x;
+  (void)hipGetLastError();
+  flce::mark_launch(stream, nullptr);
+  if (!pad_rows(g, x, W, N, H, F, dtype, nmat, ws, stream, a.x, a.W)) return FLCE_ERR_HIP;
   for (int m = 0; m < nmat; ++m) {
-    a.W[m] = W[m];
     a.b[m] = b[m];
     a.z[m] = z[m];
   }
   a.residual = residual;
   a.y = y;
-  a.N = (int)N; a.H = (int)H; a.F = (int)F;
+  a.N = (int)N; a.H = (int)g.Hp; a.F = (int)F;
   a.act = act; a.nmat = nmat;
   a.tile = g.fwd_tile; a.TM = g.TM; a.TN = g.TN;
   a.parts = g.fwd_parts; a.kc = (int)g.kc;
-  a.part = (float*)workspace; a.ldp = g.ldp;
-  (void)hipGetLastError();
-  flce::mark_launch(stream, nullptr);
+  a.part = (float*)(ws + g.pad_bytes); a.ldp = g.ldp;
   return flce::launch_layer_forward(a, dtype, stream) == hipSuccess ? FLCE_OK : FLCE_ERR_HIP;
 }
 
@@ -1170,25 +1188,26 @@ flce_status layer_backward(const void* x, const void* const (&W)[2], const float
   if (!dx && !dW[0] && !dW[1] && !want_db) return FLCE_OK;
   char* ws = (char*)workspace;
   flce::LayerBwd a{};
-  a.x = x; a.dy = dy;
+  (void)hipGetLastError();
+  flce::mark_launch(stream, nullptr);
+  if (!pad_rows(g, x, W, N, H, F, dtype, nmat, ws, stream, a.x, a.W)) return FLCE_ERR_HIP;
+  a.dy = dy;
   for (int m = 0; m < nmat; ++m) {
-    a.W[m] = W[m];
     a.z[m] = z[m];
     a.dW[m] = dW[m];
     a.db[m] = db[m];
   }
-  a.N = (int)N; a.H = (int)H; a.F = (int)F;
+  a.N = (int)N; a.H = (int)g.Hp; a.F = (int)F;
+  a.Hout = (int)H;
   a.act = act; a.nmat = nmat;
   a.dz_is_dy = g.dz_is_dy;
-  a.dz = g.dz_is_dy ? const_cast<void*>(dy) : ws;
+  a.dz = g.dz_is_dy ? const_cast<void*>(dy) : ws + g.pad_bytes;
   a.ldz = g.ldz; a.segk = (int)g.segk;
   a.dbp = want_db ? (float*)(ws + g.off_dbp) : nullptr;
   a.ldb = g.ldb; a.db_blocks = g.db_blocks; a.db_rows = g.db_rows;
   a.dx = dx; a.dx_tile = g.dx_tile; a.dx_parts = g.dx_parts; a.dx_kc = (int)g.dx_kc;
   a.dw_tile = g.dw_tile; a.dw_parts = g.dw_parts; a.dw_kc = (int)g.dw_kc;
   a.part = (float*)(ws + g.off_part);
-  (void)hipGetLastError();
-  flce::mark_launch(stream, nullptr);
   return flce::launch_layer_backward(a, dtype, stream) == hipSuccess ? FLCE_OK : FLCE_ERR_HIP;
 }
 

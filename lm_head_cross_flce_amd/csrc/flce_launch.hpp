@@ -136,8 +136,17 @@ enum Activation { kActNone = 0, kActRelu = 1, kActGelu = 2, kActGeluTanh = 3, kA
 constexpr int skinny_tokens(int dtype) { return dtype == 0 ? 16 : 4; }
 constexpr int kSkinnyMost = 16;
 
+// Rows of H elements that are no whole 16-byte pieces (H % 8 != 0): x [rows[0]]
+// and the weights copied to dst, one after the other, as rows of the padded
+// width with zeros.
+struct LayerPad {
+  const void* src[3]; int64_t rows[3];
+  int H, width;
+  void* dst;
+};
+
 struct LayerFwd {
-  const void* x; const void* W[2]; const void* b[2];
+  const void* x; const void* W[2]; const void* b[2];   // rows of H elements (padded: H % 8 == 0)
   const void* residual;   // [N][F] added to the output, or null; may be y itself
   void* y;                // [N][F]
   float* z[2];            // [N][F] pre-activations kept for the backward (linear: z[0]), or null
@@ -153,7 +162,8 @@ struct LayerBwd {
   const void* x; const void* W[2];
   const float* z[2];      // kept pre-activations (linear with kActNone: null)
   const void* dy;         // [N][F]
-  int N, H, F, act, nmat;
+  int N, H, F, act, nmat; // x, W: rows of H elements (padded: H % 8 == 0)
+  int Hout;               // dx, dW: rows of Hout elements
   void* dz;               // [N][ldz]: dz, zero from column F on; gated: dg, then du from column segk
   int64_t ldz;
   int segk;               // K (columns of dz) where weight 1 starts; past every K when nmat == 1
@@ -163,9 +173,10 @@ struct LayerBwd {
   void* db[2];
   void* dx; int dx_tile, dx_parts, dx_kc;
   void* dW[2]; int dw_tile, dw_parts, dw_kc;
-  float* part;            // split products: dx [parts][N][H], then dW [parts][mats written][F][H]
+  float* part;            // split products: dx [parts][N][Hout], then dW [parts][mats written][F][Hout]
 };
 
+hipError_t launch_layer_pad(const LayerPad& a, int dtype, hipStream_t st);
 hipError_t launch_layer_forward(const LayerFwd& a, int dtype, hipStream_t st);
 hipError_t launch_layer_backward(const LayerBwd& a, int dtype, hipStream_t st);
 

@@ -12,6 +12,34 @@
 
 namespace flce {
 
+// Eight elements of a padded row a thread.
+template <class T> __global__ void __launch_bounds__(256) layer_pad_kernel(LayerPad a) {
+  const int pieces = a.width / 8;
+  const int64_t all = (a.rows[0] + a.rows[1] + a.rows[2]) * pieces;
+  for (int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x; i < all; i += (int64_t)gridDim.x * 256) {
+    int64_t row = i / pieces;
+    const int h = (int)(i - row * pieces) * 8;
+    const T* src = (const T*)a.src[0];
+    if (row >= a.rows[0]) {
+      row -= a.rows[0];
+      src = (const T*)a.src[1];
+      if (row >= a.rows[1]) {
+        row -= a.rows[1];
+        src = (const T*)a.src[2];
+      }
+    }
+    float v[8];
+    load_some<T, 8>(src + row * a.H + h, a.H - h, v);
+    store_vec<T, 8>((T*)a.dst + i * 8, v);
+  }
+}
+
+template <class T> static hipError_t layer_pad(const LayerPad& a, hipStream_t st) {
+  const int64_t blocks = ((a.rows[0] + a.rows[1] + a.rows[2]) * (a.width / 8) + 255) / 256;
+  FLCE_LAUNCH((layer_pad_kernel<T>), dim3((unsigned)(blocks < 4096 ? blocks : 4096)), dim3(256), 0, st, a);
+  return hipGetLastError();
+}
+
 // ---------------------------------------------------------------------------
 // Forward, tiles
 // ---------------------------------------------------------------------------
@@ -419,6 +447,32 @@ template <class T> __global__ void __launch_bounds__(256) layer_db_kernel(LayerB
   if (f < a.F && a.db[m] && !a.dW[m]) column_sum<T>(a, m, f);
 }
 
+// A lane's values of C[h][row]: four consecutive h of the rows row0 + 16 j (to
+// rows), at h0 + 16 i, into a [rows][width] matrix of T (SPLIT: of fp32 sums).
+template <class T, int S, bool SPLIT, class A>
+__device__ __forceinline__ void store_rows(const A& acc, void* out, int width, int row0, int rows, int h0) {
+  typedef typename std::conditional<SPLIT, float, T>::type E;
+  auto all = [&](auto whole) {   // whole: width % 4 == 0, as a constant
+    unrolled<S>([&](auto col) {
+      constexpr int j = col.value;
+      const int row = row0 + 16 * j;
+      E* p = (E*)out + (int64_t)row * width;
+      unrolled<S>([&](auto block) {
+        constexpr int i = block.value;
+        const f32x4 z = block_sums<S>(acc[i][j]);
+        const int h = h0 + 16 * i;
+        if (row < rows && h < width) {
+          const float v[4] = {z[0], z[1], z[2], z[3]};
+          if constexpr (whole.value) store_vec<E, 4>(p + h, v);
+          else store_some<E, 4>(p + h, width - h, v);
+        }
+      });
+    });
+  };
+  if (width % 4 == 0) all(std::true_type{});
+  else all(std::false_type{});
+}
+
 // dx[n][h] = sum over the rows f of W (gated: of Wg, then of Wu) of
 // dz[n][f] W[f][h]: C[h][n], so a lane holds four consecutive h of a token.
 // Workgroup b computes tile b % G over part b / G of K.
@@ -433,19 +487,8 @@ __global__ void __launch_bounds__(kThreads, (Tile<T, S>::kPerCu)) layer_dx_kerne
   const int K = max(1, min(a.dx_kc, (int)a.ldz - k0));
   const SegRows rows{{a.W[0], a.W[1]}, a.H, a.F, a.segk, k0};
   auto epilogue = [&](auto& acc) {
-#pragma unroll
-    for (int j = 0; j < S; ++j) {
-      const int n = n0 + wn * 16 * S + 16 * j + (lane & 15);
-#pragma unroll
-      for (int i = 0; i < S; ++i) {
-        const f32x4 z = block_sums<S>(acc[i][j]);
-        const int h = h0 + wm * 16 * S + 16 * i + 4 * (lane >> 4);
-        if (n < a.N && h < a.H) {
-          if constexpr (SPLIT) *(f32x4*)(a.part + ((int64_t)part * a.N + n) * a.H + h) = z;
-          else store4<T>((T*)a.dx + (int64_t)n * a.H + h, z[0], z[1], z[2], z[3]);
-        }
-      }
-    }
+    store_rows<T, S, SPLIT>(acc, SPLIT ? (void*)(a.part + (int64_t)part * a.N * a.Hout) : a.dx, a.Hout,
+                            n0 + wn * 16 * S + (lane & 15), a.N, h0 + wm * 16 * S + 4 * (lane >> 4));
   };
   if constexpr (S == 8) {
     FLCE_LDS(L, T);
@@ -495,19 +538,8 @@ __global__ void __launch_bounds__(kThreads, (Tile<T, S>::kPerCu)) layer_dw_kerne
   const T* dz = (const T*)a.dz + (int64_t)k0 * a.ldz + (int64_t)m * a.segk;
   if (tm == 0 && part == 0 && a.db[m] && tid < M && f0 + tid < a.F) column_sum<T>(a, m, f0 + tid);
   auto epilogue = [&](auto& acc) {
-#pragma unroll
-    for (int j = 0; j < S; ++j) {
-      const int f = f0 + wn * 16 * S + 16 * j + (lane & 15);
-#pragma unroll
-      for (int i = 0; i < S; ++i) {
-        const f32x4 z = block_sums<S>(acc[i][j]);
-        const int h = h0 + wm * 16 * S + 16 * i + 4 * (lane >> 4);
-        if (f < a.F && h < a.H) {
-          if constexpr (SPLIT) *(f32x4*)(a.part + (((int64_t)part * mats + second) * a.F + f) * a.H + h) = z;
-          else store4<T>((T*)a.dW[m] + (int64_t)f * a.H + h, z[0], z[1], z[2], z[3]);
-        }
-      }
-    }
+    store_rows<T, S, SPLIT>(acc, SPLIT ? (void*)(a.part + ((int64_t)part * mats + second) * a.F * a.Hout) : a.dW[m], a.Hout,
+                            f0 + wn * 16 * S + (lane & 15), a.F, h0 + wm * 16 * S + 4 * (lane >> 4));
   };
   if constexpr (S == 8) {
     FLCE_LDS(L, T);
@@ -528,22 +560,30 @@ __global__ void __launch_bounds__(kThreads, (Tile<T, S>::kPerCu)) layer_dw_kerne
   }
 }
 
-// A split product's parts added in part order: n values to d0, and the n
-// after them in each part to d1 if there is one.  Four values a thread.
+// A split product's parts added in part order: n values to d0 (blockIdx.y 0),
+// and the n after them in each part to d1.  Four values a thread.
 template <class T>
 __global__ void __launch_bounds__(256) layer_join_kernel(const float* part, int parts, int64_t n, T* d0, T* d1) {
-  const int64_t all = d1 ? 2 * n : n;
-  for (int64_t i = ((int64_t)blockIdx.x * 256 + threadIdx.x) * 4; i < all; i += (int64_t)gridDim.x * 1024) {
-    f32x4 v = *(const f32x4*)(part + i);
-    for (int p = 1; p < parts; ++p) v += *(const f32x4*)(part + p * all + i);
-    store4<T>(i < n ? d0 + i : d1 + (i - n), v[0], v[1], v[2], v[3]);
+  const int64_t all = n * gridDim.y;
+  const float* s = part + blockIdx.y * n;
+  T* d = blockIdx.y ? d1 : d0;
+  for (int64_t i = ((int64_t)blockIdx.x * 256 + threadIdx.x) * 4; i < n; i += (int64_t)gridDim.x * 1024) {
+    const int left = (int)min((int64_t)4, n - i);
+    float v[4], t[4];
+    load_some<float, 4>(s + i, left, v);
+    for (int p = 1; p < parts; ++p) {
+      load_some<float, 4>(s + p * all + i, left, t);
+#pragma unroll
+      for (int e = 0; e < 4; ++e) v[e] += t[e];
+    }
+    store_some<T, 4>(d + i, left, v);
   }
 }
 
 template <class T> static void launch_join(const float* part, int parts, int64_t n, void* d0, void* d1, hipStream_t st) {
-  const int64_t blocks = ((d1 ? 2 * n : n) / 4 + 255) / 256;
-  FLCE_LAUNCH((layer_join_kernel<T>), dim3((unsigned)(blocks < 4096 ? blocks : 4096)), dim3(256), 0, st, part, parts, n,
-              (T*)d0, (T*)d1);
+  const int64_t blocks = ((n + 3) / 4 + 255) / 256;
+  FLCE_LAUNCH((layer_join_kernel<T>), dim3((unsigned)(blocks < 2048 ? blocks : 2048), d1 ? 2 : 1), dim3(256), 0, st, part,
+              parts, n, (T*)d0, (T*)d1);
 }
 
 template <class T, bool GLU> static void launch_dz(const LayerBwd& a, hipStream_t st) {
@@ -571,7 +611,7 @@ template <class T> static void launch_bwd(const LayerBwd& a, hipStream_t st) {
         FLCE_LAUNCH((layer_dx_kernel<T, S, false>), dim3(TH * TM), blk, 0, st, a, TH, TM);
       }
     });
-    if (a.dx_parts > 1) launch_join<T>(a.part, a.dx_parts, (int64_t)a.N * a.H, a.dx, nullptr, st);
+    if (a.dx_parts > 1) launch_join<T>(a.part, a.dx_parts, (int64_t)a.N * a.Hout, a.dx, nullptr, st);
   }
   if (a.dW[0] || a.dW[1]) {
     const int m0 = a.dW[0] ? 0 : 1, mats = (a.dW[0] && a.dW[1]) ? 2 : 1;
@@ -585,7 +625,7 @@ template <class T> static void launch_bwd(const LayerBwd& a, hipStream_t st) {
       }
     });
     if (a.dw_parts > 1)
-      launch_join<T>(a.part, a.dw_parts, (int64_t)a.F * a.H, a.dW[m0], mats == 2 ? a.dW[1] : nullptr, st);
+      launch_join<T>(a.part, a.dw_parts, (int64_t)a.F * a.Hout, a.dW[m0], mats == 2 ? a.dW[1] : nullptr, st);
   }
 }
 

@@ -429,9 +429,9 @@ def _dense(t: Optional[torch.Tensor]) -> Optional[torch.Tensor]:
 
 
 def _prep_layer(x, weights, rows, bias=(), kept=()):
-    """The operands of a feed-forward call, checked and dense, with H padded to
-    a multiple of 8: x [N, H], weights [F, H], rows [N, F] (or None), bias [F]
-    (or None); kept: float32 pre-activations [N, F] (or None)."""
+    """The operands of a feed-forward call, checked and dense: x [N, H], weights
+    [F, H], rows [N, F] (or None), bias [F] (or None); kept: float32
+    pre-activations [N, F] (or None)."""
     if x.dim() != 2 or any(w.dim() != 2 for w in weights):
         raise ValueError("x must be [N, H] and the weights [F, H]")
     if not x.is_cuda:
@@ -459,7 +459,7 @@ def _prep_layer(x, weights, rows, bias=(), kept=()):
     if H < 1 or F < 1:
         raise ValueError("H and F must be at least 1")
     _dtype_code(x)
-    return ([_pad_hidden(_dense(t)) for t in (x, *weights)], [_dense(t) for t in rows],
+    return ([_dense(t) for t in (x, *weights)], [_dense(t) for t in rows],
             [b.contiguous() if b is not None else None for b in bias], [_dense(t) for t in kept])
 
 
@@ -475,16 +475,6 @@ def _workspace(workspace: Optional[torch.Tensor], nbytes: int, dev) -> Optional[
 
 def _nbytes(t: Optional[torch.Tensor]) -> int:
     return 0 if t is None else t.numel()
-
-
-def _layer_grads(x, H0, H, F, weights, need_dx, need_dW):
-    """(dx, [dW]) to fill, [.., H] wide."""
-    dx = torch.empty(x.shape[0], H, dtype=x.dtype, device=x.device) if need_dx else None
-    return dx, [torch.empty(F, H, dtype=x.dtype, device=x.device) if need else None for need in need_dW]
-
-
-def _narrow(t: Optional[torch.Tensor], H0: int) -> Optional[torch.Tensor]:
-    return t if t is None or t.shape[1] == H0 else t[:, :H0].contiguous()
 
 
 def flce_linear_workspace_size(N: int, H: int, F: int, dtype: torch.dtype,
@@ -526,10 +516,11 @@ def flce_linear_backward(x: torch.Tensor, W: torch.Tensor, dy: torch.Tensor, z: 
         z = None
     elif z is None:
         raise ValueError("z is what flce_linear_forward returned with keep=True")
-    H0, N, F = x.shape[-1], x.shape[0], W.shape[0]
+    N, F = x.shape[0], W.shape[0]
     (x, W), (dy,), _, (z,) = _prep_layer(x, (W,), (dy,), kept=(z,))
     dt, dev, H = _dtype_code(x), x.device, x.shape[1]
-    dx, (dW,) = _layer_grads(x, H0, H, F, (W,), need_dx, (need_dW,))
+    dx = torch.empty_like(x) if need_dx else None
+    dW = torch.empty_like(W) if need_dW else None
     db = torch.empty(F, dtype=x.dtype, device=dev) if need_db else None
     _, bwd_bytes = _lib.flce_linear_workspace_size(N, H, F, dt, act)
     workspace = _workspace(workspace, bwd_bytes, dev)
@@ -537,7 +528,7 @@ def flce_linear_backward(x: torch.Tensor, W: torch.Tensor, dy: torch.Tensor, z: 
         stream = torch.cuda.current_stream(dev).cuda_stream
         _lib.flce_linear_backward(x.data_ptr(), W.data_ptr(), _ptr(z), dy.data_ptr(), N, H, F, dt, act, _ptr(dx),
                                   _ptr(dW), _ptr(db), _ptr(workspace), _nbytes(workspace), stream)
-    return _narrow(dx, H0), _narrow(dW, H0), db
+    return dx, dW, db
 
 
 def flce_glu_workspace_size(N: int, H: int, F: int, dtype: torch.dtype) -> Tuple[int, int]:
@@ -573,10 +564,12 @@ def flce_glu_backward(x: torch.Tensor, Wg: torch.Tensor, Wu: torch.Tensor, g: to
     act = _activation_code(activation)
     if g is None or u is None:
         raise ValueError("g and u are what flce_glu_forward returned with keep=True")
-    H0, N, F = x.shape[-1], x.shape[0], Wg.shape[0]
+    N, F = x.shape[0], Wg.shape[0]
     (x, Wg, Wu), (dh,), _, (g, u) = _prep_layer(x, (Wg, Wu), (dh,), kept=(g, u))
     dt, dev, H = _dtype_code(x), x.device, x.shape[1]
-    dx, (dWg, dWu) = _layer_grads(x, H0, H, F, (Wg, Wu), need_dx, (need_dWg, need_dWu))
+    dx = torch.empty_like(x) if need_dx else None
+    dWg = torch.empty_like(Wg) if need_dWg else None
+    dWu = torch.empty_like(Wu) if need_dWu else None
     dbg, dbu = ((torch.empty(F, dtype=x.dtype, device=dev), torch.empty(F, dtype=x.dtype, device=dev)) if need_db
                 else (None, None))
     _, bwd_bytes = _lib.flce_glu_workspace_size(N, H, F, dt)
@@ -586,7 +579,7 @@ def flce_glu_backward(x: torch.Tensor, Wg: torch.Tensor, Wu: torch.Tensor, g: to
         _lib.flce_glu_backward(x.data_ptr(), Wg.data_ptr(), Wu.data_ptr(), g.data_ptr(), u.data_ptr(), dh.data_ptr(),
                                N, H, F, dt, act, _ptr(dx), _ptr(dWg), _ptr(dWu), _ptr(dbg), _ptr(dbu),
                                _ptr(workspace), _nbytes(workspace), stream)
-    return _narrow(dx, H0), _narrow(dWg, H0), _narrow(dWu, H0), dbg, dbu
+    return dx, dWg, dWu, dbg, dbu
 
 
 def _is_dense(t: torch.Tensor) -> bool:

@@ -281,10 +281,20 @@ def test_no_rows(dtype):
     assert out[0].shape == (0, 24) and not any(bool(t.any()) for t in out[1:])
 
 
-@pytest.mark.parametrize("shape", [(3, 13, 21), (300, 75, 333)], ids=str)
-def test_hidden_sizes_the_library_pads(shape):
-    check_linear(*shape, torch.bfloat16, "gelu", True, True)
-    check_glu(*shape, torch.float16, "silu", True)
+@pytest.mark.parametrize("dtype", ["bf16", "f16", "f32"])
+@pytest.mark.parametrize("shape", [(1, 1, 1), (3, 13, 21), (16, 1001, 8), (300, 75, 333), (130, 2049, 70), (600, 7, 900)],
+                         ids=str)
+def test_hidden_sizes_that_are_no_whole_pieces(shape, dtype):
+    check_linear(*shape, DT[dtype], "gelu", True, True)
+    check_glu(*shape, DT[dtype], "silu", True)
+
+
+@pytest.mark.parametrize("tile", [8, 4, 2])
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+def test_odd_hidden_size_in_every_tile(monkeypatch, dtype, tile):
+    monkeypatch.setenv("FLCE_DEBUG_LAYER_TILE", str(tile))
+    check_linear(270, 301, 275, DT[dtype], "silu", True, True)
+    check_glu(270, 301, 275, DT[dtype], "silu", True)
 
 
 @pytest.mark.parametrize("N", [9, 200, 600])
@@ -328,7 +338,7 @@ def test_residual_in_place(N):
         L.flce_linear_forward(x, W, None, None, out=torch.empty(72, N, dtype=r.dtype, device="cuda").T)
 
 
-@pytest.mark.parametrize("N,H,F", [(7, 64, 33), (70, 1024, 72), (300, 64, 333)])
+@pytest.mark.parametrize("N,H,F", [(7, 64, 33), (70, 1024, 72), (300, 64, 333), (7, 61, 33), (300, 1027, 72)])
 @pytest.mark.parametrize("dtype", ["bf16", "f32"])
 def test_nothing_is_written_outside_the_outputs(N, H, F, dtype):
     # outputs and workspaces inside larger buffers of a known pattern

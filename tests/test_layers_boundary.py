@@ -69,7 +69,6 @@ def test_layer_sizes_and_enums(fn):
     refused(fn, INVALID, N=-1)
     refused(fn, INVALID, H=0)
     refused(fn, INVALID, F=0)
-    refused(fn, UNSUPPORTED, H=4100)          # not a multiple of 8
     refused(fn, UNSUPPORTED, H=1 << 21)
     refused(fn, UNSUPPORTED, F=1 << 21)
     refused(fn, UNSUPPORTED, N=1 << 31)
@@ -119,9 +118,12 @@ def test_layer_workspace_arithmetic():
     assert f == 0 and b <= 128 * 12288 * 4 + 512
     f, b = _lib.flce_glu_workspace_size(8192, 4096, 12288, 1)
     assert f == 0 and 2 * 8192 * 12288 * 2 <= b <= 2 * 8192 * 12288 * 2 + 2 * 128 * 12288 * 4 + 512
+    # rows of no whole 16-byte pieces: padded copies of x and the weights in both
+    a, b = _lib.flce_glu_workspace_size(300, 61, 40, 1), _lib.flce_glu_workspace_size(300, 64, 40, 1)
+    assert all(380 * 64 * 2 <= p - q <= 380 * 64 * 2 + 512 for p, q in zip(a, b))
     # no rows: nothing
     assert _lib.flce_linear_workspace_size(0, 64, 64, 1, 4)[0] == 0
-    for bad in ((-1, 64, 64), (4, 60, 64), (4, 64, 0)):
+    for bad in ((-1, 64, 64), (4, 0, 64), (4, 64, 0)):
         with pytest.raises(_lib.FlceError):
             _lib.flce_linear_workspace_size(*bad, 1, 0)
         with pytest.raises(_lib.FlceError):
