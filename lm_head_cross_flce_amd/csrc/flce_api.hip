@@ -1023,6 +1023,7 @@ Cut product_cut(int64_t M, int64_t N, int64_t K, int dtype) {
     if ((forced == 2 || forced == 4 || (forced == 8 && dtype != FLCE_F32)) && t.S != forced) return;
     const int64_t tiles = cdiv(M, 32 * t.S) * cdiv(N, 32 * t.S);
     for (int64_t parts : {1, 2, 3, 4, 6, 8, 12, 16}) {
+      if (t.S == 2 && tiles * parts >= (int64_t(1) << 23)) return;   // a launch has fewer than 2^32 threads
       const int64_t kc = part_depth(K, parts);
       if (parts > 1 && (kc < 256 || cdiv(K, kc) != parts)) continue;
       const double q = (double)cdiv(tiles * parts, kCUs);

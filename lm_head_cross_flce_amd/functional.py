@@ -11,6 +11,7 @@ gradients produced in backward rather than in forward (DeepSpeed PR 8792).
 
 from __future__ import annotations
 
+import contextlib
 import operator
 from typing import Optional, Tuple
 
@@ -432,35 +433,42 @@ def _prep_layer(x, weights, rows, bias=(), kept=()):
     """The operands of a feed-forward call, checked and dense: x [N, H], weights
     [F, H], rows [N, F] (or None), bias [F] (or None); kept: float32
     pre-activations [N, F] (or None)."""
-    if x.dim() != 2 or any(w.dim() != 2 for w in weights):
+    if x.dim() != 2 or weights[0].dim() != 2:
         raise ValueError("x must be [N, H] and the weights [F, H]")
     if not x.is_cuda:
         raise ValueError("tensors must live on a GPU")
-    N, H = x.shape
+    dtype, dev, (N, H) = x.dtype, x.device, x.shape
     F = weights[0].shape[0]
-    for w in weights:
-        if tuple(w.shape) != (F, H):
-            raise ValueError("x and the weights disagree on their sizes")
-    for t in (*rows, *kept):
-        if t is not None and tuple(t.shape) != (N, F):
-            raise ValueError(f"expected a tensor of shape {(N, F)}, not {tuple(t.shape)}")
-    for b in bias:
-        if b is not None and tuple(b.shape) != (F,):
-            raise ValueError("a bias must be [F]")
-    for t in (*weights, *rows, *bias):
-        if t is not None and t.dtype != x.dtype:
-            raise TypeError("all tensors must share one dtype")
-    for t in kept:
-        if t is not None and t.dtype != torch.float32:
-            raise TypeError("the kept pre-activations are float32")
-    for t in (*weights, *rows, *bias, *kept):
-        if t is not None and t.device != x.device:
-            raise ValueError("all tensors must be on one device")
     if H < 1 or F < 1:
         raise ValueError("H and F must be at least 1")
-    _dtype_code(x)
-    return ([_dense(t) for t in (x, *weights)], [_dense(t) for t in rows],
-            [b.contiguous() if b is not None else None for b in bias], [_dense(t) for t in kept])
+    if dtype not in _DTYPES:
+        raise TypeError(f"unsupported dtype {dtype}; use bfloat16, float16 or float32")
+
+    def dense(t, shape, want):
+        if t is None:
+            return None
+        if t.shape != shape:
+            raise ValueError(f"expected a tensor of shape {tuple(shape)}, not {tuple(t.shape)}")
+        if t.dtype != want:
+            raise TypeError(f"expected a {want} tensor, not {t.dtype}: all tensors share x's dtype, but the kept "
+                            "pre-activations are float32")
+        if t.device != dev:
+            raise ValueError("all tensors must be on one device")
+        return _dense(t)
+
+    nf = (N, F)
+    return ([_dense(x), *[dense(w, (F, H), dtype) for w in weights]], [dense(t, nf, dtype) for t in rows],
+            [dense(b, (F,), dtype) for b in bias], [dense(t, nf, torch.float32) for t in kept])
+
+
+# The current stream of a device, as its address, without a Stream object.
+_raw_stream = torch._C._cuda_getCurrentRawStream
+_HERE = contextlib.nullcontext()
+
+
+def _on(dev):
+    """The device made current, if it is not."""
+    return _HERE if torch.cuda.current_device() == dev.index else torch.cuda.device(dev)
 
 
 def _workspace(workspace: Optional[torch.Tensor], nbytes: int, dev) -> Optional[torch.Tensor]:
@@ -499,8 +507,8 @@ def flce_linear_forward(x: torch.Tensor, W: torch.Tensor, b: Optional[torch.Tens
     z = torch.empty(N, F, dtype=torch.float32, device=dev) if keep and activation != "none" else None
     fwd_bytes, _ = _lib.flce_linear_workspace_size(N, H, F, dt, act)
     workspace = _workspace(workspace, fwd_bytes, dev)
-    with torch.cuda.device(dev):
-        stream = torch.cuda.current_stream(dev).cuda_stream
+    with _on(dev):
+        stream = _raw_stream(dev.index)
         _lib.flce_linear_forward(x.data_ptr(), W.data_ptr(), _ptr(b), _ptr(residual_), N, H, F, dt, act, y.data_ptr(),
                                  _ptr(z), _ptr(workspace), _nbytes(workspace), stream)
     return y, z
@@ -524,8 +532,8 @@ def flce_linear_backward(x: torch.Tensor, W: torch.Tensor, dy: torch.Tensor, z: 
     db = torch.empty(F, dtype=x.dtype, device=dev) if need_db else None
     _, bwd_bytes = _lib.flce_linear_workspace_size(N, H, F, dt, act)
     workspace = _workspace(workspace, bwd_bytes, dev)
-    with torch.cuda.device(dev):
-        stream = torch.cuda.current_stream(dev).cuda_stream
+    with _on(dev):
+        stream = _raw_stream(dev.index)
         _lib.flce_linear_backward(x.data_ptr(), W.data_ptr(), _ptr(z), dy.data_ptr(), N, H, F, dt, act, _ptr(dx),
                                   _ptr(dW), _ptr(db), _ptr(workspace), _nbytes(workspace), stream)
     return dx, dW, db
@@ -549,8 +557,8 @@ def flce_glu_forward(x: torch.Tensor, Wg: torch.Tensor, Wu: torch.Tensor, bg: Op
     g, u = (torch.empty(N, F, dtype=torch.float32, device=dev) for _ in range(2)) if keep else (None, None)
     fwd_bytes, _ = _lib.flce_glu_workspace_size(N, H, F, dt)
     workspace = _workspace(workspace, fwd_bytes, dev)
-    with torch.cuda.device(dev):
-        stream = torch.cuda.current_stream(dev).cuda_stream
+    with _on(dev):
+        stream = _raw_stream(dev.index)
         _lib.flce_glu_forward(x.data_ptr(), Wg.data_ptr(), Wu.data_ptr(), _ptr(bg), _ptr(bu), N, H, F, dt, act,
                               h.data_ptr(), _ptr(g), _ptr(u), _ptr(workspace), _nbytes(workspace), stream)
     return h, g, u
@@ -574,8 +582,8 @@ def flce_glu_backward(x: torch.Tensor, Wg: torch.Tensor, Wu: torch.Tensor, g: to
                 else (None, None))
     _, bwd_bytes = _lib.flce_glu_workspace_size(N, H, F, dt)
     workspace = _workspace(workspace, bwd_bytes, dev)
-    with torch.cuda.device(dev):
-        stream = torch.cuda.current_stream(dev).cuda_stream
+    with _on(dev):
+        stream = _raw_stream(dev.index)
         _lib.flce_glu_backward(x.data_ptr(), Wg.data_ptr(), Wu.data_ptr(), g.data_ptr(), u.data_ptr(), dh.data_ptr(),
                                N, H, F, dt, act, _ptr(dx), _ptr(dWg), _ptr(dWu), _ptr(dbg), _ptr(dbu),
                                _ptr(workspace), _nbytes(workspace), stream)
@@ -635,8 +643,8 @@ def flce_grad_norm(grads, norm_type: float = 2.0) -> torch.Tensor:
     if not all(map(_contiguous, grads)):
         grads = [g if _is_dense(g) else g.contiguous() for g in grads]
     workspace, norm = _norm_workspace(len(grads), dev)
-    with torch.cuda.device(dev):
-        stream = torch.cuda.current_stream(dev).cuda_stream
+    with _on(dev):
+        stream = _raw_stream(dev.index)
         _lib.flce_grad_norm(_lib.pointer_array(map(_address, grads)), _lib.size_array(map(_numel, grads)), dtypes,
                             len(grads), float(norm_type), norm.data_ptr(), workspace.data_ptr(), workspace.numel(),
                             stream)
@@ -677,8 +685,8 @@ def _clip(grads, max_norm, norm_type, given, out):
     addresses, sizes = _lib.pointer_array(map(_address, src)), _lib.size_array(map(_numel, src))
     outs = None if tmp is grads else _lib.pointer_array(map(_address, tmp))
     norm = None
-    with torch.cuda.device(dev):
-        stream = torch.cuda.current_stream(dev).cuda_stream
+    with _on(dev):
+        stream = _raw_stream(dev.index)
         if given is not None:
             _lib.flce_clip_grads_with_norm(addresses, outs, sizes, dtypes, count, float(max_norm), given.data_ptr(),
                                            stream)
