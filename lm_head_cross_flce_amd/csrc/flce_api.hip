@@ -982,6 +982,7 @@ namespace {
 // (S = 8, 16-bit only; 4; 2) and parts of K.
 struct Cut {
   int S, parts;
+  double ns;
 };
 
 // Depth of a part: the 64-deep copy block divides it, so every part starts on
@@ -1014,8 +1015,9 @@ int forced_tile() {
   return env ? std::atoi(env) : 0;
 }
 
-Cut product_cut(int64_t M, int64_t N, int64_t K, int dtype) {
-  Cut best{2, 1};
+// only: the S to use (0: any).
+Cut product_cut(int64_t M, int64_t N, int64_t K, int dtype, int only = 0) {
+  Cut best{only ? only : 2, 1, 1e300};
   if (M < 1 || N < 1) return best;
   const int forced = forced_tile();
   double least = 0.0;
@@ -1032,7 +1034,7 @@ Cut product_cut(int64_t M, int64_t N, int64_t K, int dtype) {
       if (parts > 1) ns += kJoinNs + kJoinNsPerByte * 4.0 * (double)parts * (double)M * (double)N;
       if (least == 0.0 || ns < least) {
         least = ns;
-        best = {t.S, (int)parts};
+        best = {t.S, (int)parts, ns};
       }
     }
   };
@@ -1056,7 +1058,7 @@ struct LayerGeometry {
   int64_t ldb;
   int dx_tile, dx_parts, dw_tile, dw_parts;
   int64_t dx_kc, dw_kc;
-  size_t off_dbp, off_part, bwd_total;
+  size_t off_dbp, off_part, off_dw_part, bwd_total;
 };
 
 LayerGeometry layer_geometry(int64_t N, int64_t Hout, int64_t F, int dtype, int act, int nmat) {
@@ -1067,7 +1069,7 @@ LayerGeometry layer_geometry(int64_t N, int64_t Hout, int64_t F, int dtype, int 
   g.pad_bytes = H == Hout ? 0 : align_up((size_t)(N + nmat * F) * H * es);
   Cut fwd = product_cut(N, nmat * F, H, dtype);
   const int forced = forced_tile();
-  if (forced == 1 ? N <= flce::kSkinnyMost : forced == 0 && N <= flce::skinny_tokens(dtype)) fwd = {0, 1};
+  if (forced == 1 ? N <= flce::kSkinnyMost : forced == 0 && N <= flce::skinny_tokens(dtype)) fwd = {0, 1, 0.0};
   g.fwd_tile = fwd.S;
   g.TM = fwd.S ? (int)cdiv(N, 32 * fwd.S) : 0;
   g.TN = fwd.S ? (int)cdiv(F, 32 * fwd.S / nmat) : 0;
@@ -1090,7 +1092,15 @@ LayerGeometry layer_geometry(int64_t N, int64_t Hout, int64_t F, int dtype, int 
   g.ldb = nmat * F;
   g.off_dbp = off;
   off = align_up(off + (size_t)g.db_blocks * g.ldb * 4);
-  const Cut cx = product_cut(H, N, g.ldz, dtype), cw = product_cut(H, nmat * F, N, dtype);
+  // Two small products share a launch, and with it their tiles' size.
+  Cut cx = product_cut(H, N, g.ldz, dtype), cw = product_cut(H, nmat * F, N, dtype);
+  if (cx.S < 8 && cw.S < 8 && cx.S != cw.S) {
+    const Cut x4 = product_cut(H, N, g.ldz, dtype, 4), w4 = product_cut(H, nmat * F, N, dtype, 4);
+    const Cut x2 = product_cut(H, N, g.ldz, dtype, 2), w2 = product_cut(H, nmat * F, N, dtype, 2);
+    const bool two = x2.ns + w2.ns < x4.ns + w4.ns;
+    cx = two ? x2 : x4;
+    cw = two ? w2 : w4;
+  }
   g.dx_tile = cx.S;
   g.dx_parts = cx.parts;
   g.dw_tile = cw.S;
@@ -1098,9 +1108,9 @@ LayerGeometry layer_geometry(int64_t N, int64_t Hout, int64_t F, int dtype, int 
   g.dx_kc = part_depth(g.ldz, g.dx_parts);
   g.dw_kc = part_depth(N, g.dw_parts);
   g.off_part = off;
-  const size_t dxp = g.dx_parts > 1 ? (size_t)g.dx_parts * N * H * 4 : 0;
-  const size_t dwp = g.dw_parts > 1 ? (size_t)g.dw_parts * nmat * F * H * 4 : 0;
-  g.bwd_total = align_up(off + (dxp > dwp ? dxp : dwp));
+  off = align_up(off + (g.dx_parts > 1 ? (size_t)g.dx_parts * N * Hout * 4 : 0));
+  g.off_dw_part = off;
+  g.bwd_total = align_up(off + (g.dw_parts > 1 ? (size_t)g.dw_parts * nmat * F * Hout * 4 : 0));
   return g;
 }
 
@@ -1208,7 +1218,8 @@ flce_status layer_backward(const void* x, const void* const (&W)[2], const float
   a.ldb = g.ldb; a.db_blocks = g.db_blocks; a.db_rows = g.db_rows;
   a.dx = dx; a.dx_tile = g.dx_tile; a.dx_parts = g.dx_parts; a.dx_kc = (int)g.dx_kc;
   a.dw_tile = g.dw_tile; a.dw_parts = g.dw_parts; a.dw_kc = (int)g.dw_kc;
-  a.part = (float*)(ws + g.off_part);
+  a.dx_part = (float*)(ws + g.off_part);
+  a.dw_part = (float*)(ws + g.off_dw_part);
   return flce::launch_layer_backward(a, dtype, stream) == hipSuccess ? FLCE_OK : FLCE_ERR_HIP;
 }
 

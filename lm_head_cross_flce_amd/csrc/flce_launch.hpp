@@ -171,9 +171,9 @@ struct LayerBwd {
   float* dbp; int64_t ldb;   // [db_blocks][ldb] fp32 partial column sums; null if no db
   int db_blocks, db_rows;    // token rows per block
   void* db[2];
-  void* dx; int dx_tile, dx_parts, dx_kc;
+  void* dx; int dx_tile, dx_parts, dx_kc;   // dx_tile and dw_tile, where neither is 8, are the same
   void* dW[2]; int dw_tile, dw_parts, dw_kc;
-  float* part;            // split products: dx [parts][N][Hout], then dW [parts][mats written][F][Hout]
+  float* dx_part; float* dw_part;   // split products: [parts][N][Hout], [parts][mats written][F][Hout]
 };
 
 hipError_t launch_layer_pad(const LayerPad& a, int dtype, hipStream_t st);

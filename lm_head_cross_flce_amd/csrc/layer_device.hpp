@@ -448,6 +448,23 @@ template <int S> struct ColFrag {
   }
 };
 
+// A small tile's LDS buffers, declared by the kernel (SMALL_LDS): 16-bit, two
+// an operand; fp32, one (in p[0] and p[2]).
+struct SmallLds {
+  lds_t* p[4];
+};
+template <class T, int S> struct SmallLdsSize {
+  static constexpr int kA = 32 * S * (sizeof(T) == 2 ? 128 : 208), kB = sizeof(T) == 2 ? kA : 16;
+};
+#define SMALL_LDS(name, T, S)                                                             \
+  __shared__ __attribute__((aligned(16))) char name##_0[SmallLdsSize<T, S>::kA];           \
+  __shared__ __attribute__((aligned(16))) char name##_1[SmallLdsSize<T, S>::kB];           \
+  __shared__ __attribute__((aligned(16))) char name##_2[SmallLdsSize<T, S>::kA];           \
+  __shared__ __attribute__((aligned(16))) char name##_3[SmallLdsSize<T, S>::kB];           \
+  const SmallLds name {                                                                   \
+    { (lds_t*)name##_0, (lds_t*)name##_1, (lds_t*)name##_2, (lds_t*)name##_3 }            \
+  }
+
 // acc = the tile's sums over K, 16-bit.  Block b + 1 is copied while block b is
 // computed; the barrier at the head of a block publishes it and frees the other
 // buffer.  Each buffer is its own object, so that the compiler need not wait
@@ -456,11 +473,8 @@ template <int S> struct ColFrag {
 // workgroups fill the waits (4096 x 4096 x 1024 bf16 at S = 4: 40.0 -> 37.6 us).
 template <class T, int S, class FA, class FB, class CA, class CB>
 __device__ __forceinline__ void gemm_small(f32x4 (&acc)[S][S], const CA& ca, int ka, const CB& cb, int kb, int K,
-                                           int tid) {
-  __shared__ __attribute__((aligned(16))) char a0[CA::kBytes];
-  __shared__ __attribute__((aligned(16))) char a1[CA::kBytes];
-  __shared__ __attribute__((aligned(16))) char b0[CB::kBytes];
-  __shared__ __attribute__((aligned(16))) char b1[CB::kBytes];
+                                           const SmallLds& L, int tid) {
+  lds_t *const a0 = L.p[0], *const a1 = L.p[1], *const b0 = L.p[2], *const b1 = L.p[3];
   const int lane = tid & 63, wave = tid >> 6;
   FA fa;
   FB fb;
@@ -471,8 +485,8 @@ __device__ __forceinline__ void gemm_small(f32x4 (&acc)[S][S], const CA& ca, int
 #pragma unroll
     for (int j = 0; j < S; ++j) acc[i][j] = f32x4{0.f, 0.f, 0.f, 0.f};
   const int KB = (K + kBlockK - 1) / kBlockK;
-  ca.issue(0, ka, (lds_t*)a0);
-  cb.issue(0, kb, (lds_t*)b0);
+  ca.issue(0, ka, a0);
+  cb.issue(0, kb, b0);
   auto step = [&](int b, const lds_t* A, const lds_t* B, lds_t* nA, lds_t* nB) {
     __builtin_amdgcn_s_waitcnt(waitcnt_vm_lgkm0<0>());
     __builtin_amdgcn_s_barrier();
@@ -500,8 +514,8 @@ __device__ __forceinline__ void gemm_small(f32x4 (&acc)[S][S], const CA& ca, int
     __builtin_amdgcn_s_setprio(0);
   };
   for (int b = 0; b < KB; b += 2) {
-    step(b, (const lds_t*)a0, (const lds_t*)b0, (lds_t*)a1, (lds_t*)b1);
-    if (b + 1 < KB) step(b + 1, (const lds_t*)a1, (const lds_t*)b1, (lds_t*)a0, (lds_t*)b0);
+    step(b, a0, b0, a1, b1);
+    if (b + 1 < KB) step(b + 1, a1, b1, a0, b0);
   }
 }
 
@@ -606,25 +620,26 @@ template <int S> struct ColCopy<float, S> {
 // registers while this one is computed, and the CU's other workgroups run under
 // the two barriers and the splitting.
 template <int S, class CA, class CB>
-__device__ __forceinline__ void gemm_small_f32(f32x4 (&acc)[S][S], CA& ca, int ka, CB& cb, int kb, int K, int tid) {
-  __shared__ __attribute__((aligned(16))) char lds_a[CA::kBytes];
-  __shared__ __attribute__((aligned(16))) char lds_b[CB::kBytes];
+__device__ __forceinline__ void gemm_small_f32(f32x4 (&acc)[S][S], CA& ca, int ka, CB& cb, int kb, int K,
+                                               const SmallLds& L, int tid) {
+  static_assert(CA::kBytes == SmallLdsSize<float, S>::kA && CB::kBytes == CA::kBytes, "the kernel's buffers");
+  lds_t *const lds_a = L.p[0], *const lds_b = L.p[2];
   const int lane = tid & 63, wave = tid >> 6;
 #pragma unroll
   for (int i = 0; i < S; ++i)
 #pragma unroll
     for (int j = 0; j < S; ++j) acc[i][j] = f32x4{0.f, 0.f, 0.f, 0.f};
   const int frag = (lane & 15) * kPartRow + (lane >> 4) * 16;
-  const lds_t* A = (const lds_t*)lds_a + (wave >> 1) * 16 * S * kPartRow + frag;
-  const lds_t* B = (const lds_t*)lds_b + (wave & 1) * 16 * S * kPartRow + frag;
+  const lds_t* A = lds_a + (wave >> 1) * 16 * S * kPartRow + frag;
+  const lds_t* B = lds_b + (wave & 1) * 16 * S * kPartRow + frag;
   const int KT = (K + kF32K - 1) / kF32K;
   auto load = [&](int h, int kt) {   // stages past K read zeros
     ca.load(h, kt * kF32K, ka);
     cb.load(h, kt * kF32K, kb);
   };
   auto stage = [&](int h, int kt) {
-    ca.store(h, (lds_t*)lds_a, tid);
-    cb.store(h, (lds_t*)lds_b, tid);
+    ca.store(h, lds_a, tid);
+    cb.store(h, lds_b, tid);
     __syncthreads();
     load(h, kt + 2);
     u32x4 b[3][S];

@@ -202,8 +202,9 @@ __global__ void __launch_bounds__(kThreads, (Tile<T, S>::kPerCu)) layer_fwd_kern
     RowCopy<T, S, true, GLU> cb;
     ca.init(A.p, nullptr, A.ld, a.N, n0, tid);
     cb.init(B.p, (const T*)a.W[1] + k0, B.ld, a.F, f0, tid);
-    if constexpr (sizeof(T) == 2) gemm_small<T, S, RowFrag<S>, RowFrag<S>>(acc, ca, A.kext, cb, B.kext, A.kext, tid);
-    else gemm_small_f32<S>(acc, ca, A.kext, cb, B.kext, A.kext, tid);
+    SMALL_LDS(L, T, S);
+    if constexpr (sizeof(T) == 2) gemm_small<T, S, RowFrag<S>, RowFrag<S>>(acc, ca, A.kext, cb, B.kext, A.kext, L, tid);
+    else gemm_small_f32<S>(acc, ca, A.kext, cb, B.kext, A.kext, L, tid);
     tile(acc, n0, f0, SPLIT ? t / tiles : 0, b0, b1);
   }
 }
@@ -448,15 +449,14 @@ template <class T> __global__ void __launch_bounds__(256) layer_db_kernel(LayerB
 }
 
 // A lane's values of C[h][row]: four consecutive h of the rows row0 + 16 j (to
-// rows), at h0 + 16 i, into a [rows][width] matrix of T (SPLIT: of fp32 sums).
-template <class T, int S, bool SPLIT, class A>
-__device__ __forceinline__ void store_rows(const A& acc, void* out, int width, int row0, int rows, int h0) {
-  typedef typename std::conditional<SPLIT, float, T>::type E;
+// rows), at h0 + 16 i, into a [rows][width] matrix of E.
+template <class E, int S, class A>
+__device__ __forceinline__ void store_rows(const A& acc, E* out, int width, int row0, int rows, int h0) {
   auto all = [&](auto whole) {   // whole: width % 4 == 0, as a constant
     unrolled<S>([&](auto col) {
       constexpr int j = col.value;
       const int row = row0 + 16 * j;
-      E* p = (E*)out + (int64_t)row * width;
+      E* p = out + (int64_t)row * width;
       unrolled<S>([&](auto block) {
         constexpr int i = block.value;
         const f32x4 z = block_sums<S>(acc[i][j]);
@@ -473,117 +473,144 @@ __device__ __forceinline__ void store_rows(const A& acc, void* out, int width, i
   else all(std::false_type{});
 }
 
-// dx[n][h] = sum over the rows f of W (gated: of Wg, then of Wu) of
-// dz[n][f] W[f][h]: C[h][n], so a lane holds four consecutive h of a token.
-// Workgroup b computes tile b % G over part b / G of K.
-template <class T, int S, bool SPLIT>
-__global__ void __launch_bounds__(kThreads, (Tile<T, S>::kPerCu)) layer_dx_kernel(LayerBwd a, int TH, int TM) {
-  constexpr int M = Tile<T, S>::M;
-  const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6, wm = wave >> 1, wn = wave & 1;
-  const int G = TH * TM, part = SPLIT ? blockIdx.x / G : 0;
+// Where a workgroup stands in one of the two gradient products.
+//   dx[n][h] = sum over the rows f of W (gated: of Wg, then of Wu) of dz[n][f] W[f][h]: C[h][n]
+//   dW[f][h] = sum_n dz[n][f] x[n][h]: C[h][f]
+// so a lane holds four consecutive h of a row.  Workgroup w computes tile w % G
+// over part w / G of K.  dW: column tile tn belongs to weight m0 (tn < TF) or
+// the next.  That is told by a compare: a division put the descriptors'
+// addresses into vector registers, which costs a loop over the lanes at every
+// copy (N=8192, H=4096, 24576 rows took 1463 us so, 1127 now).
+struct GradTile {
+  int h0, c0, k0, part, m, second;   // second: 1 for the next weight (dW)
+};
+template <int S> __device__ __forceinline__ GradTile dx_place(const LayerBwd& a, int w, int TH, int TM) {
+  const int G = TH * TM, part = a.dx_parts > 1 ? w / G : 0;
   int tm, tn;
-  tile_coords(blockIdx.x - part * G, G, TH, TM, tm, tn);
-  const int h0 = tm * M, n0 = tn * M, k0 = part * a.dx_kc;
-  const int K = max(1, min(a.dx_kc, (int)a.ldz - k0));
-  const SegRows rows{{a.W[0], a.W[1]}, a.H, a.F, a.segk, k0};
-  auto epilogue = [&](auto& acc) {
-    store_rows<T, S, SPLIT>(acc, SPLIT ? (void*)(a.part + (int64_t)part * a.N * a.Hout) : a.dx, a.Hout,
-                            n0 + wn * 16 * S + (lane & 15), a.N, h0 + wm * 16 * S + 4 * (lane >> 4));
-  };
-  if constexpr (S == 8) {
-    FLCE_LDS(L, T);
-    const Opnd<T> A{(const T*)a.W[0], a.H, a.H, K};   // K only: rows past F read zeros
-    const Opnd<T> B{(const T*)a.dz + k0, a.ldz, a.N, (int)a.ldz - k0};
-    Acc acc;
-    TileCopy<false, true, DmaSeg, Dma<true>> tc;
-    tc.da.d.init(A, h0, tid);
-    tc.da.s = rows;
-    tc.da.m0 = h0;
-    tc.db.init(B, n0, tid);
-    tc.begin(A, B, L, tid);
-    gemm_tile_bf16_run<false, true>(acc, A, B, K, L, tid, tc);
-    acc_drain();
-    epilogue(acc);
-  } else {
-    f32x4 acc[S][S];
+  tile_coords(w - part * G, G, TH, TM, tm, tn);
+  return {tm * 32 * S, tn * 32 * S, part * a.dx_kc, part, 0, 0};
+}
+template <int S> __device__ __forceinline__ GradTile dw_place(const LayerBwd& a, int w, int TH, int TF, int m0, int mats) {
+  const int G = TH * TF * mats, part = a.dw_parts > 1 ? w / G : 0;
+  int tm, tn;
+  tile_coords(w - part * G, G, TH, TF * mats, tm, tn);
+  const int second = tn >= TF ? 1 : 0;
+  return {tm * 32 * S, (tn - second * TF) * 32 * S, part * a.dw_kc, part, m0 + second, second};
+}
+
+// The tile's sums to the gradient, or to its part's fp32 partial sums.
+template <class T, int S, class A>
+__device__ __forceinline__ void store_dx(const LayerBwd& a, const GradTile& t, const A& acc, int tid) {
+  const int lane = tid & 63, wave = tid >> 6;
+  const int n = t.c0 + (wave & 1) * 16 * S + (lane & 15), h = t.h0 + (wave >> 1) * 16 * S + 4 * (lane >> 4);
+  if (a.dx_parts > 1) store_rows<float, S>(acc, a.dx_part + (int64_t)t.part * a.N * a.Hout, a.Hout, n, a.N, h);
+  else store_rows<T, S>(acc, (T*)a.dx, a.Hout, n, a.N, h);
+}
+template <class T, int S, class A>
+__device__ __forceinline__ void store_dw(const LayerBwd& a, const GradTile& t, int mats, const A& acc, int tid) {
+  const int lane = tid & 63, wave = tid >> 6;
+  const int f = t.c0 + (wave & 1) * 16 * S + (lane & 15), h = t.h0 + (wave >> 1) * 16 * S + 4 * (lane >> 4);
+  if (a.dw_parts > 1)
+    store_rows<float, S>(acc, a.dw_part + ((int64_t)t.part * mats + t.second) * a.F * a.Hout, a.Hout, f, a.F, h);
+  else store_rows<T, S>(acc, (T*)a.dW[t.m], a.Hout, f, a.F, h);
+}
+
+// The first H tile's workgroups of dW also finish db for their columns.
+template <class T, int S> __device__ __forceinline__ void finish_db(const LayerBwd& a, const GradTile& t, int tid) {
+  if (t.h0 == 0 && t.part == 0 && a.db[t.m] && tid < 32 * S && t.c0 + tid < a.F) column_sum<T>(a, t.m, t.c0 + tid);
+}
+
+// S = 8: one launch a product.
+template <class T> __global__ void __launch_bounds__(kThreads, 1) layer_dx_kernel(LayerBwd a, int TH, int TM) {
+  const int tid = threadIdx.x;
+  const GradTile t = dx_place<8>(a, blockIdx.x, TH, TM);
+  const int K = max(1, min(a.dx_kc, (int)a.ldz - t.k0));
+  FLCE_LDS(L, T);
+  const Opnd<T> A{(const T*)a.W[0], a.H, a.H, K};   // K only: rows past F read zeros
+  const Opnd<T> B{(const T*)a.dz + t.k0, a.ldz, a.N, (int)a.ldz - t.k0};
+  Acc acc;
+  TileCopy<false, true, DmaSeg, Dma<true>> tc;
+  tc.da.d.init(A, t.h0, tid);
+  tc.da.s = SegRows{{a.W[0], a.W[1]}, a.H, a.F, a.segk, t.k0};
+  tc.da.m0 = t.h0;
+  tc.db.init(B, t.c0, tid);
+  tc.begin(A, B, L, tid);
+  gemm_tile_bf16_run<false, true>(acc, A, B, K, L, tid, tc);
+  acc_drain();
+  store_dx<T, 8>(a, t, acc, tid);
+}
+template <class T>
+__global__ void __launch_bounds__(kThreads, 1) layer_dw_kernel(LayerBwd a, int TH, int TF, int m0, int mats) {
+  const int tid = threadIdx.x;
+  const GradTile t = dw_place<8>(a, blockIdx.x, TH, TF, m0, mats);
+  const int K = max(0, min(a.dw_kc, a.N - t.k0)), width = a.nmat == 2 ? a.segk : (int)a.ldz;
+  finish_db<T, 8>(a, t, tid);
+  FLCE_LDS(L, T);
+  const Opnd<T> A{(const T*)a.x + (int64_t)t.k0 * a.H, a.H, a.H, K};
+  const Opnd<T> B{(const T*)a.dz + (int64_t)t.k0 * a.ldz + (int64_t)t.m * a.segk, a.ldz, width, K};
+  Acc acc;
+  gemm_tile<T, false, false>(acc, A, t.h0, B, t.c0, max(K, 1), L, tid);   // K >= 1: no token sums zeros
+  acc_drain();
+  store_dw<T, 8>(a, t, mats, acc, tid);
+}
+
+// S = 4, 2: both products in one launch, dx in the first gx workgroups: small
+// products leave CUs idle, which the other's workgroups take (N=1037, H=1000,
+// F=2731 gated fp16: the two launches took 36 us one after the other).
+template <class T, int S>
+__global__ void __launch_bounds__(kThreads, (Tile<T, S>::kPerCu)) layer_grads_kernel(LayerBwd a, int gx, int TH, int TM,
+                                                                                   int TF, int m0, int mats) {
+  const int tid = threadIdx.x;
+  SMALL_LDS(L, T, S);
+  f32x4 acc[S][S];
+  if ((int)blockIdx.x < gx) {
+    const GradTile t = dx_place<S>(a, blockIdx.x, TH, TM);
+    const int K = max(1, min(a.dx_kc, (int)a.ldz - t.k0));
     ColCopy<T, S> ca;
     RowCopy<T, S, false, false> cb;
-    ca.init(rows, a.H, h0, tid);
-    cb.init((const T*)a.dz + k0, nullptr, a.ldz, a.N, n0, tid);
-    if constexpr (sizeof(T) == 2) gemm_small<T, S, ColFrag<S>, RowFrag<S>>(acc, ca, K, cb, (int)a.ldz - k0, K, tid);
-    else gemm_small_f32<S>(acc, ca, K, cb, (int)a.ldz - k0, K, tid);
-    epilogue(acc);
-  }
-}
-
-// dW[f][h] = sum_n dz[n][f] x[n][h]: C[h][f].  Column tile tn belongs to
-// weight m0 (tn < TF) or the next.  SPLIT: part b / G of the tokens.
-// The weight is told by a compare: a division put the descriptors' addresses
-// into vector registers, which costs a loop over the lanes at every copy (the
-// product at N=8192, H=4096, 24576 rows took 1463 us so).  The first H tile's
-// workgroups also finish db for their columns.
-template <class T, int S, bool SPLIT>
-__global__ void __launch_bounds__(kThreads, (Tile<T, S>::kPerCu)) layer_dw_kernel(LayerBwd a, int TH, int TF, int m0,
-                                                                                int mats) {
-  constexpr int M = Tile<T, S>::M;
-  const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6, wm = wave >> 1, wn = wave & 1;
-  const int G = TH * TF * mats, part = SPLIT ? blockIdx.x / G : 0;
-  int tm, tn;
-  tile_coords(blockIdx.x - part * G, G, TH, TF * mats, tm, tn);
-  const int second = tn >= TF ? 1 : 0, m = m0 + second;
-  const int h0 = tm * M, f0 = (tn - second * TF) * M, k0 = part * a.dw_kc;
-  const int K = min(a.dw_kc, a.N - k0);
-  const int width = a.nmat == 2 ? a.segk : (int)a.ldz;
-  const T* x = (const T*)a.x + (int64_t)k0 * a.H;
-  const T* dz = (const T*)a.dz + (int64_t)k0 * a.ldz + (int64_t)m * a.segk;
-  if (tm == 0 && part == 0 && a.db[m] && tid < M && f0 + tid < a.F) column_sum<T>(a, m, f0 + tid);
-  auto epilogue = [&](auto& acc) {
-    store_rows<T, S, SPLIT>(acc, SPLIT ? (void*)(a.part + ((int64_t)part * mats + second) * a.F * a.Hout) : a.dW[m], a.Hout,
-                            f0 + wn * 16 * S + (lane & 15), a.F, h0 + wm * 16 * S + 4 * (lane >> 4));
-  };
-  if constexpr (S == 8) {
-    FLCE_LDS(L, T);
-    const Opnd<T> A{x, a.H, a.H, max(K, 0)};
-    const Opnd<T> B{dz, a.ldz, width, max(K, 0)};
-    Acc acc;
-    gemm_tile<T, false, false>(acc, A, h0, B, f0, max(K, 1), L, tid);   // K >= 1: no token sums zeros
-    acc_drain();
-    epilogue(acc);
+    ca.init(SegRows{{a.W[0], a.W[1]}, a.H, a.F, a.segk, t.k0}, a.H, t.h0, tid);
+    cb.init((const T*)a.dz + t.k0, nullptr, a.ldz, a.N, t.c0, tid);
+    if constexpr (sizeof(T) == 2) gemm_small<T, S, ColFrag<S>, RowFrag<S>>(acc, ca, K, cb, (int)a.ldz - t.k0, K, L, tid);
+    else gemm_small_f32<S>(acc, ca, K, cb, (int)a.ldz - t.k0, K, L, tid);
+    store_dx<T, S>(a, t, acc, tid);
   } else {
-    f32x4 acc[S][S];
+    const GradTile t = dw_place<S>(a, blockIdx.x - gx, TH, TF, m0, mats);
+    const int K = max(0, min(a.dw_kc, a.N - t.k0)), width = a.nmat == 2 ? a.segk : (int)a.ldz;
+    finish_db<T, S>(a, t, tid);
+    const T* x = (const T*)a.x + (int64_t)t.k0 * a.H;
+    const T* dz = (const T*)a.dz + (int64_t)t.k0 * a.ldz + (int64_t)t.m * a.segk;
     ColCopy<T, S> ca, cb;
-    ca.init(SegRows{{x, x}, a.H, max(K, 0), 1 << 30, 0}, a.H, h0, tid);
-    cb.init(SegRows{{dz, dz}, a.ldz, max(K, 0), 1 << 30, 0}, width, f0, tid);
-    if constexpr (sizeof(T) == 2) gemm_small<T, S, ColFrag<S>, ColFrag<S>>(acc, ca, K, cb, K, K, tid);
-    else gemm_small_f32<S>(acc, ca, K, cb, K, K, tid);
-    epilogue(acc);
+    ca.init(SegRows{{x, x}, a.H, K, 1 << 30, 0}, a.H, t.h0, tid);
+    cb.init(SegRows{{dz, dz}, a.ldz, K, 1 << 30, 0}, width, t.c0, tid);
+    if constexpr (sizeof(T) == 2) gemm_small<T, S, ColFrag<S>, ColFrag<S>>(acc, ca, K, cb, K, K, L, tid);
+    else gemm_small_f32<S>(acc, ca, K, cb, K, K, L, tid);
+    store_dw<T, S>(a, t, mats, acc, tid);
   }
 }
 
-// A split product's parts added in part order: n values to d0 (blockIdx.y 0),
-// and the n after them in each part to d1.  Four values a thread.
-template <class T>
-__global__ void __launch_bounds__(256) layer_join_kernel(const float* part, int parts, int64_t n, T* d0, T* d1) {
-  const int64_t all = n * gridDim.y;
-  const float* s = part + blockIdx.y * n;
-  T* d = blockIdx.y ? d1 : d0;
+// Split products' parts added in part order: blockIdx.y is dx, dW of the first
+// weight written, dW of the next.  Four values a thread.
+template <class T> struct Join {
+  const float* part[3];
+  int64_t n[3], stride[3];   // values, and from one part to the next
+  int parts[3];
+  T* out[3];
+};
+template <class T> __global__ void __launch_bounds__(256) layer_join_kernel(Join<T> a) {
+  const int y = blockIdx.y;
+  const float* s = a.part[y];
+  const int64_t n = a.n[y];
   for (int64_t i = ((int64_t)blockIdx.x * 256 + threadIdx.x) * 4; i < n; i += (int64_t)gridDim.x * 1024) {
     const int left = (int)min((int64_t)4, n - i);
     float v[4], t[4];
     load_some<float, 4>(s + i, left, v);
-    for (int p = 1; p < parts; ++p) {
-      load_some<float, 4>(s + p * all + i, left, t);
+    for (int p = 1; p < a.parts[y]; ++p) {
+      load_some<float, 4>(s + p * a.stride[y] + i, left, t);
 #pragma unroll
       for (int e = 0; e < 4; ++e) v[e] += t[e];
     }
-    store_some<T, 4>(d + i, left, v);
+    store_some<T, 4>(a.out[y] + i, left, v);
   }
-}
-
-template <class T> static void launch_join(const float* part, int parts, int64_t n, void* d0, void* d1, hipStream_t st) {
-  const int64_t blocks = ((n + 3) / 4 + 255) / 256;
-  FLCE_LAUNCH((layer_join_kernel<T>), dim3((unsigned)(blocks < 2048 ? blocks : 2048), d1 ? 2 : 1), dim3(256), 0, st, part,
-              parts, n, (T*)d0, (T*)d1);
 }
 
 template <class T, bool GLU> static void launch_dz(const LayerBwd& a, hipStream_t st) {
@@ -601,31 +628,42 @@ template <class T> static void launch_bwd(const LayerBwd& a, hipStream_t st) {
   if ((a.db[0] && !a.dW[0]) || (a.db[1] && !a.dW[1]))
     FLCE_LAUNCH((layer_db_kernel<T>), dim3((a.F + 255) / 256, a.nmat), dim3(256), 0, st, a);
   auto tiles = [](int n, int s) { return (n + 32 * s - 1) / (32 * s); };
-  if (a.dx && a.N > 0) {
-    with_tile<T>(a.dx_tile, [&](auto tile) {
-      constexpr int S = tile.value;
-      const int TH = tiles(a.H, S), TM = tiles(a.N, S);
-      if (a.dx_parts > 1) {
-        FLCE_LAUNCH((layer_dx_kernel<T, S, true>), dim3(TH * TM * a.dx_parts), blk, 0, st, a, TH, TM);
-      } else {
-        FLCE_LAUNCH((layer_dx_kernel<T, S, false>), dim3(TH * TM), blk, 0, st, a, TH, TM);
-      }
-    });
-    if (a.dx_parts > 1) launch_join<T>(a.part, a.dx_parts, (int64_t)a.N * a.Hout, a.dx, nullptr, st);
+  const bool dx = a.dx && a.N > 0, dw = a.dW[0] || a.dW[1];
+  const int m0 = a.dW[0] ? 0 : 1, mats = (a.dW[0] && a.dW[1]) ? 2 : 1;
+  Join<T> join{};
+  int joins = 0;
+  int64_t most = 0;
+  if (dx && a.dx_parts > 1) {
+    const int64_t n = (int64_t)a.N * a.Hout;
+    join.part[0] = a.dx_part; join.n[0] = join.stride[0] = n; join.parts[0] = a.dx_parts; join.out[0] = (T*)a.dx;
+    joins = 1;
+    most = n;
   }
-  if (a.dW[0] || a.dW[1]) {
-    const int m0 = a.dW[0] ? 0 : 1, mats = (a.dW[0] && a.dW[1]) ? 2 : 1;
-    with_tile<T>(a.dw_tile, [&](auto tile) {
-      constexpr int S = tile.value;
-      const int TH = tiles(a.H, S), TF = tiles(a.F, S);
-      if (a.dw_parts > 1) {
-        FLCE_LAUNCH((layer_dw_kernel<T, S, true>), dim3(TH * TF * mats * a.dw_parts), blk, 0, st, a, TH, TF, m0, mats);
-      } else {
-        FLCE_LAUNCH((layer_dw_kernel<T, S, false>), dim3(TH * TF * mats), blk, 0, st, a, TH, TF, m0, mats);
-      }
-    });
-    if (a.dw_parts > 1)
-      launch_join<T>(a.part, a.dw_parts, (int64_t)a.F * a.Hout, a.dW[m0], mats == 2 ? a.dW[1] : nullptr, st);
+  for (int k = 0; dw && a.dw_parts > 1 && k < mats; ++k, ++joins) {
+    const int64_t n = (int64_t)a.F * a.Hout;
+    join.part[joins] = a.dw_part + k * n; join.n[joins] = n; join.stride[joins] = mats * n;
+    join.parts[joins] = a.dw_parts; join.out[joins] = (T*)a.dW[m0 + k];
+    most = most > n ? most : n;
+  }
+  // dx_tile and dw_tile, where neither is 8, are the same.
+  auto small = [&](auto tile, bool with_dx, bool with_dw) {
+    constexpr int S = tile.value;
+    if constexpr (S < 8) {
+      const int TH = tiles(a.H, S), TM = tiles(a.N, S), TF = tiles(a.F, S);
+      const int gx = with_dx ? TH * TM * a.dx_parts : 0, gw = with_dw ? TH * TF * mats * a.dw_parts : 0;
+      FLCE_LAUNCH((layer_grads_kernel<T, S>), dim3(gx + gw), blk, 0, st, a, gx, TH, TM, TF, m0, mats);
+    }
+  };
+  const bool dx8 = a.dx_tile == 8, dw8 = a.dw_tile == 8;
+  if constexpr (sizeof(T) == 2) {
+    if (dx && dx8) FLCE_LAUNCH((layer_dx_kernel<T>), dim3(tiles(a.H, 8) * tiles(a.N, 8) * a.dx_parts), blk, 0, st, a, tiles(a.H, 8), tiles(a.N, 8));
+    if (dw && dw8) FLCE_LAUNCH((layer_dw_kernel<T>), dim3(tiles(a.H, 8) * tiles(a.F, 8) * mats * a.dw_parts), blk, 0, st, a, tiles(a.H, 8), tiles(a.F, 8), m0, mats);
+  }
+  if ((dx && !dx8) || (dw && !dw8))
+    with_tile<T>(dx8 ? a.dw_tile : a.dx_tile, [&](auto tile) { small(tile, dx && !dx8, dw && !dw8); });
+  if (joins) {
+    const int64_t blocks = ((most + 3) / 4 + 255) / 256;
+    FLCE_LAUNCH((layer_join_kernel<T>), dim3((unsigned)(blocks < 2048 ? blocks : 2048), joins), dim3(256), 0, st, join);
   }
 }
 
