@@ -57,8 +57,10 @@ __global__ void __launch_bounds__(kThreads, (Tile<T, S>::kPerCu)) layer_fwd_kern
   constexpr int M = Tile<T, S>::M;
   constexpr int FT = GLU ? M / 2 : M;   // features of a tile
   constexpr int C = GLU ? S / 2 : S;    // consecutive features of a lane
-  const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6, wm = wave >> 1, wn = wave & 1;
-  const int g = lane >> 4, c = lane & 15;
+  // The wave's index as a scalar: the epilogue's descriptors start at its rows,
+  // and one made from a vector register costs a loop over the lanes at each store.
+  const int tid = threadIdx.x, lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6);
+  const int wm = wave >> 1, wn = wave & 1, g = lane >> 4, c = lane & 15;
   const int tiles = a.TM * a.TN, total = tiles * a.parts;
   int n0, f0, k0;
   auto place = [&](int t) {
