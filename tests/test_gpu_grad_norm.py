@@ -229,3 +229,17 @@ def test_graph_replays():
         graph.replay()
         torch.cuda.synchronize()
         assert torch.equal(norm, want) and all(torch.equal(a, b) for a, b in zip(out, ref)), i
+
+
+@pytest.mark.parametrize("dt", [BF, FP], ids=str)
+def test_a_tensor_past_32_bits(dt):
+    n = 2 ** 31 + 12_345
+    g = torch.full((n,), 0.5, dtype=dt, device="cuda")
+    g[n - 7:] = 3.0
+    ref = math.sqrt(0.25 * (n - 7) + 9.0 * 7)
+    norm = L.flce_clip_grad_norm([g, torch.full((3,), 0.5, device="cuda")], ref / 4)
+    assert abs(float(norm) - math.sqrt(ref * ref + 0.75)) <= 2.0 ** -23 * ref
+    c = (ref / 4) / (math.sqrt(ref * ref + 0.75) + 1e-6)
+    for i, v in ((0, 0.5), (2 ** 30, 0.5), (2 ** 31 - 1, 0.5), (2 ** 31, 0.5), (n - 8, 0.5), (n - 7, 3.0), (n - 1, 3.0)):
+        assert abs(float(g[i]) - v * c) <= v * c * (torch.finfo(dt).eps / 2 + 2.0 ** -22), i
+    assert int((g > 0.2).sum()) == 7

@@ -537,3 +537,54 @@ def test_gradients_only_where_needed_in_autograd():
         L.fused_linear(x, w.bfloat16())
     with pytest.raises(ValueError):
         L.fused_linear(x, w[:, :8])
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+def test_offsets_past_32_bits(dtype):
+    # 2.5e9 outputs: elements and bytes past 2^31 and 2^32 in y, z, dy and dz; sampled rows and all of dW
+    dt = DT[dtype]
+    N, H, F = 300_003, 16, 8200
+    x, W = randn(N, H, dt=dt, seed=1), randn(F, H, dt=dt, seed=2, scale=0.25)
+    y, z = L.flce_linear_forward(x, W, None, None, "gelu_tanh", keep=True)
+    rows = torch.tensor([0, 1, 131_072, 261_900, 261_901, 262_143, N - 2, N - 1], device="cuda")
+    z64, ez = z_with_err(x[rows], W, None)
+    y64 = act64("gelu_tanh")(z64)
+    close(y[rows], y64, 1.13 * ez + act_err(dt) * y64.abs() + half(y64, dt), "y")
+    close(z[rows], z64, ez + half(z64, torch.float32), "z")
+    del y
+    dy = torch.zeros(N, F, dtype=dt, device="cuda")   # zero but for the sampled rows: dW is theirs alone
+    dy[rows] = randn(len(rows), F, dt=dt, seed=3)
+    dx, dW, db = L.flce_linear_backward(x, W, dy, z, "gelu_tanh", need_db=True)
+    d64 = dy[rows].double()
+    dz64 = d64 * dact64("gelu_tanh", z64)
+    edz = d64.abs() * (ez + half(z64, torch.float32)) + 4 * act_err(dt) * d64.abs() + half(dz64, dt)
+    x64, W64 = x[rows].double(), W.double()
+    dx64, dW64, db64 = dz64 @ W64, dz64.T @ x64, dz64.sum(0)
+    close(dx[rows], dx64, product_tol(dz64, edz, W64, dx64, dt), "dx")
+    close(dW, dW64, product_tol(dz64.T, edz.T, x64, dW64, dt), "dW")
+    ones = torch.ones(len(rows), 1, dtype=torch.float64, device="cuda")
+    close(db, db64, product_tol(dz64.T, edz.T, ones, db64[:, None], dt)[:, 0], "db")
+    dx[rows] = 0
+    assert not bool(dx.any())
+
+
+def test_two_streams_at_once():
+    # calls in flight together, each with its own workspace
+    args = [(randn(300 + 37 * i, 1024, dt=torch.bfloat16, seed=i), randn(136, 1024, dt=torch.bfloat16, seed=9),
+             randn(300 + 37 * i, 136, dt=torch.bfloat16, seed=20 + i)) for i in range(4)]
+
+    def call(x, W, dy):
+        h, g, u = L.flce_glu_forward(x, W, W, keep=True)
+        return (h, *L.flce_glu_backward(x, W, W, g, u, dy, need_db=True))
+
+    ref = [call(*a) for a in args]
+    streams = [torch.cuda.Stream() for _ in range(4)]
+    torch.cuda.synchronize()
+    for _ in range(3):
+        got = []
+        for s, a in zip(streams, args):
+            with torch.cuda.stream(s):
+                got.append(call(*a))
+        torch.cuda.synchronize()
+        for r, g in zip(ref, got):
+            assert all(torch.equal(p, q) for p, q in zip(r, g))
