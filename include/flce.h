@@ -482,7 +482,7 @@ flce_status flce_glu_backward(const void* x, const void* Wg, const void* Wu, con
  * flce_clip_grads_with_norm scales by a norm the caller has on the device (a
  * norm over several ranks' gradients, say).
  * flce_grad_norm_workspace_size: bytes for a call with `count` tensors (about
- * 16 KB); pure host arithmetic.
+ * 8 KB); pure host arithmetic.
  */
 flce_status flce_grad_norm_workspace_size(int64_t count, size_t* bytes);
 
