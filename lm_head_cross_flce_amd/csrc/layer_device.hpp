@@ -485,6 +485,7 @@ __device__ __forceinline__ void gemm_small(f32x4 (&acc)[S][S], const CA& ca, int
 #pragma unroll
     for (int j = 0; j < S; ++j) acc[i][j] = f32x4{0.f, 0.f, 0.f, 0.f};
   const int KB = (K + kBlockK - 1) / kBlockK;
+  if (KB < 1) return;   // no copy may be under way when the workgroup ends
   ca.issue(0, ka, a0);
   cb.issue(0, kb, b0);
   auto step = [&](int b, const lds_t* A, const lds_t* B, lds_t* nA, lds_t* nB) {
