@@ -100,17 +100,22 @@ def _code_only(text):
     return " ".join(text.split())
 
 
+# The files of the operators around the loss: none of the loss's kernels, nor the
+# host code that launches them, is compiled from these.
+OTHER_OPERATORS = ("layer_", "grad_norm_")
+
+
 def kernel_source_hash(sources=None):
-    """Hash of the HIP sources' code (comments and whitespace ignored); a traffic
-    figure is valid only for this hash.  ``sources``: {file name: text}, default
-    the files under csrc/."""
+    """Hash of the loss's HIP sources' code (comments and whitespace ignored); a
+    recorded figure is valid only for this hash.  ``sources``: {file name: text},
+    default the files under csrc/."""
     if sources is None:
         sources = {}
         for f in glob.glob(os.path.join(ROOT, "lm_head_cross_flce_amd", "csrc", "*")):
             with open(f, encoding="utf-8") as fh:
                 sources[os.path.basename(f)] = fh.read()
     h = hashlib.sha256()
-    for name in sorted(sources):
+    for name in sorted(n for n in sources if not n.startswith(OTHER_OPERATORS)):
         h.update(name.encode() + _code_only(sources[name]).encode())
     return h.hexdigest()[:16]
 
