@@ -41,13 +41,14 @@ int forced_tile() {
   return env ? std::atoi(env) : 0;
 }
 
-// only: the S to use (0: any).
+// only: the S to use (0: any); an S that no launch can have costs 1e300.
 Cut product_cut(int64_t M, int64_t N, int64_t K, int dtype, int only = 0) {
+  if (M < 1 || N < 1) return {only ? only : 2, 1, 0.0};   // nothing to form
   Cut best{only ? only : 2, 1, 1e300};
-  if (M < 1 || N < 1) return best;
   const int forced = forced_tile();
   double least = 0.0;
   auto consider = [&](const TileCost& t) {
+    if (only && t.S != only) return;
     if ((forced == 2 || forced == 4 || (forced == 8 && dtype != FLCE_F32)) && t.S != forced) return;
     const int64_t tiles = cdiv(M, 32 * t.S) * cdiv(N, 32 * t.S);
     for (int64_t parts : {1, 2, 3, 4, 6, 8, 12, 16}) {
@@ -119,7 +120,9 @@ LayerGeometry layer_geometry(int64_t N, int64_t Hout, int64_t F, int dtype, int 
   g.ldb = nmat * F;
   g.off_dbp = off;
   off = align_up(off + (size_t)g.db_blocks * g.ldb * 4);
-  // Two small products share a launch, and with it their tiles' size.
+  // Two small products share a launch, and with it their tiles' size: the one
+  // whose times add up to less.  It holds for a call that asks for one gradient
+  // alone too, which so has the same bits as beside the other.
   Cut cx = product_cut(H, N, g.ldz, dtype), cw = product_cut(H, nmat * F, N, dtype);
   if (cx.S < 8 && cw.S < 8 && cx.S != cw.S) {
     const Cut x4 = product_cut(H, N, g.ldz, dtype, 4), w4 = product_cut(H, nmat * F, N, dtype, 4);
