@@ -121,7 +121,7 @@ LayerGeometry layer_geometry(int64_t N, int64_t Hout, int64_t F, int dtype, int 
   off = align_up(off + (size_t)g.db_blocks * g.ldb * 4);
   // Two small products share a launch, and with it their tiles' size: where their
   // own picks differ, S = 4 with the splits costed for it.  (Of 70 such shapes,
-  // N to 4096, H and F to 8192, all types, S = 4 took 1.2% more than the faster of
+  // N to 4096, H and F to 8192, all types, S = 4 took 1-2% more than the faster of
   // both on average and 16% at worst; the size whose times add up to less, 4% and
   // 57%, as the products fill each other's rounds.)  It holds for a call that asks
   // for one gradient alone too, which so has the same bits as beside the other.

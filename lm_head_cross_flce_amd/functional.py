@@ -765,11 +765,14 @@ class FusedLinearCrossEntropyLoss(torch.nn.Module):
 
 
 class FusedLinearFunction(torch.autograd.Function):
-    """y = act(x weight^T + bias) + residual; keeps the pre-activations if there is an activation."""
+    """y = act(x weight^T + bias) + residual; keeps the pre-activations if there is an activation.
+
+    grad: whether a backward may follow.  needs_input_grad says which inputs require gradients, also under
+    no_grad and inference_mode, and forward itself always runs without gradients."""
 
     @staticmethod
-    def forward(ctx, x, weight, bias=None, residual=None, activation="none"):
-        y, z = flce_linear_forward(x, weight, bias, residual, activation, keep=any(ctx.needs_input_grad[:3]))
+    def forward(ctx, x, weight, bias=None, residual=None, activation="none", grad=True):
+        y, z = flce_linear_forward(x, weight, bias, residual, activation, keep=grad and any(ctx.needs_input_grad[:3]))
         ctx.save_for_backward(x, weight, z)
         ctx.activation = activation
         return y
@@ -782,15 +785,16 @@ class FusedLinearFunction(torch.autograd.Function):
         dx = dW = db = None
         if any(need[:3]):
             dx, dW, db = flce_linear_backward(x, weight, dy, z, ctx.activation, need[0], need[1], need[2])
-        return dx, dW, db, dy if need[3] else None, None
+        return dx, dW, db, dy if need[3] else None, None, None
 
 
 class FusedGLUFunction(torch.autograd.Function):
-    """h = act(x w_gate^T + b_gate) * (x w_up^T + b_up); keeps both projections."""
+    """h = act(x w_gate^T + b_gate) * (x w_up^T + b_up); keeps both projections.  grad: as in FusedLinearFunction."""
 
     @staticmethod
-    def forward(ctx, x, w_gate, w_up, b_gate=None, b_up=None, activation="silu"):
-        h, g, u = flce_glu_forward(x, w_gate, w_up, b_gate, b_up, activation, keep=any(ctx.needs_input_grad[:5]))
+    def forward(ctx, x, w_gate, w_up, b_gate=None, b_up=None, activation="silu", grad=True):
+        h, g, u = flce_glu_forward(x, w_gate, w_up, b_gate, b_up, activation,
+                                   keep=grad and any(ctx.needs_input_grad[:5]))
         ctx.save_for_backward(x, w_gate, w_up, g, u)
         ctx.activation = activation
         return h
@@ -802,7 +806,7 @@ class FusedGLUFunction(torch.autograd.Function):
         need = ctx.needs_input_grad
         dx, dWg, dWu, dbg, dbu = flce_glu_backward(x, w_gate, w_up, g, u, dh, ctx.activation, need[0], need[1], need[2],
                                                    need[3] or need[4])
-        return dx, dWg, dWu, dbg if need[3] else None, dbu if need[4] else None, None
+        return dx, dWg, dWu, dbg if need[3] else None, dbu if need[4] else None, None, None
 
 
 def fused_linear(x, weight, bias=None, residual=None, activation="none"):
@@ -812,13 +816,14 @@ def fused_linear(x, weight, bias=None, residual=None, activation="none"):
         if residual.shape != (*lead, F):
             raise ValueError(f"residual must be {(*lead, F)}")
         residual = residual.reshape(-1, F)
-    return FusedLinearFunction.apply(x.reshape(-1, x.shape[-1]), weight, bias, residual, activation).reshape(*lead, F)
+    return FusedLinearFunction.apply(x.reshape(-1, x.shape[-1]), weight, bias, residual, activation,
+                                     torch.is_grad_enabled()).reshape(*lead, F)
 
 
 def fused_glu(x, w_gate, w_up, b_gate=None, b_up=None, activation="silu"):
     """act(x w_gate^T + b_gate) * (x w_up^T + b_up) for x [..., H]; differentiable."""
-    return FusedGLUFunction.apply(x.reshape(-1, x.shape[-1]), w_gate, w_up, b_gate, b_up,
-                                  activation).reshape(*x.shape[:-1], w_gate.shape[0])
+    return FusedGLUFunction.apply(x.reshape(-1, x.shape[-1]), w_gate, w_up, b_gate, b_up, activation,
+                                  torch.is_grad_enabled()).reshape(*x.shape[:-1], w_gate.shape[0])
 
 
 class GatedFeedForward(torch.nn.Module):
