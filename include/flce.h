@@ -402,6 +402,9 @@ flce_status flce_shard_backward(const void* x, const void* W_shard, const void* 
  *    values under 2^-14 to multiples of 2^-24, as float16 autograd of the
  *    formulas does.
  *  - Results do not depend on what else runs: sums are added in a fixed order.
+ *  - No output, kept pre-activation or workspace may share memory with another
+ *    tensor of the call (FLCE_ERR_INVALID_ARGUMENT); the linear forward's y may be
+ *    its residual.
  */
 typedef FLCE_ENUM(flce_activation) {
   FLCE_ACT_NONE = 0,      /* act(z) = z */
@@ -414,8 +417,7 @@ typedef FLCE_ENUM(flce_activation) {
 
 /*
  * Linear layer:  z = x W^T + b,  y = act(z) + residual.
- * b and residual may be NULL; y may be residual itself (any other overlap of
- * an output with an input is not allowed).  z: if non-NULL, the forward writes
+ * b and residual may be NULL; y may be residual itself.  z: if non-NULL, the forward writes
  * the pre-activations there for the backward (not needed with FLCE_ACT_NONE).
  *
  * Backward, given dy [N, F]:  dz = dy act'(z),  dx = dz W,  dW = dz^T x,

@@ -186,6 +186,12 @@ flce_status layer_forward(const void* x, const void* const (&W)[2], const void* 
   if (workspace_bytes < g.fwd_total) return FLCE_ERR_WORKSPACE_TOO_SMALL;
   if (bad_tensor(workspace, 16, g.fwd_total > 0)) return FLCE_ERR_INVALID_ARGUMENT;
   if (!rows) return FLCE_OK;
+  const size_t nf = (size_t)N * F * es, fh = (size_t)F * H * es;
+  const Memory mem[] = {{x, (size_t)N * H * es, false}, {W[0], fh, false}, {W[1], fh, false},
+                        {b[0], F * es, false}, {b[1], F * es, false}, {residual == y ? nullptr : residual, nf, false},
+                        {y, nf, true}, {z[0], (size_t)N * F * 4, true}, {z[1], (size_t)N * F * 4, true},
+                        {workspace, g.fwd_total, true}};
+  if (clash(mem, 10)) return FLCE_ERR_INVALID_ARGUMENT;
   char* ws = (char*)workspace;
   flce::LayerFwd a{};
   (void)hipGetLastError();
@@ -224,6 +230,11 @@ flce_status layer_backward(const void* x, const void* const (&W)[2], const float
   if (bad_tensor(workspace, 16, g.bwd_total > 0)) return FLCE_ERR_INVALID_ARGUMENT;
   const bool want_db = db[0] || db[1];
   if (!dx && !dW[0] && !dW[1] && !want_db) return FLCE_OK;
+  const size_t nh = (size_t)N * H * es, fh = (size_t)F * H * es, kept = need_z ? (size_t)N * F * 4 : 0;
+  const Memory mem[] = {{x, nh, false}, {W[0], fh, false}, {W[1], fh, false}, {z[0], kept, false}, {z[1], kept, false},
+                        {dy, (size_t)N * F * es, false}, {dx, nh, true}, {dW[0], fh, true}, {dW[1], fh, true},
+                        {db[0], F * es, true}, {db[1], F * es, true}, {workspace, g.bwd_total, true}};
+  if (clash(mem, 12)) return FLCE_ERR_INVALID_ARGUMENT;
   char* ws = (char*)workspace;
   flce::LayerBwd a{};
   (void)hipGetLastError();

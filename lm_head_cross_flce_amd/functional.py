@@ -496,7 +496,8 @@ def flce_linear_forward(x: torch.Tensor, W: torch.Tensor, b: Optional[torch.Tens
                         workspace: Optional[torch.Tensor] = None, out: Optional[torch.Tensor] = None):
     """act(x W^T + b) + residual.  Returns (y, z): z the float32 pre-activations
     that flce_linear_backward takes, with keep and an activation, else None.
-    out: the tensor to write y to (it may be residual)."""
+    out: the tensor to write y to; it may be residual, and may share memory with no
+    other tensor of the call."""
     act = _activation_code(activation)
     N, F = x.shape[0], W.shape[0]
     (x, W), (residual_, out_), (b,), _ = _prep_layer(x, (W,), (residual, out), (b,))
