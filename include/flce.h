@@ -479,7 +479,9 @@ flce_status flce_glu_backward(const void* x, const void* Wg, const void* Wu, con
  * flce_clip_grad_norm: outs NULL scales the gradients in place, else outs[i]
  * receives grads[i] scaled (outs[i] may be grads[i]), and a factor of 1 leaves
  * in-place gradients untouched.  No output may share memory with any other
- * tensor of the call (FLCE_ERR_INVALID_ARGUMENT); max_norm >= 0.
+ * tensor of the call, and neither may norm or the workspace; a given norm may lie
+ * in a gradient that the call leaves alone (FLCE_ERR_INVALID_ARGUMENT otherwise).
+ * max_norm >= 0.
  * norm: float32 [1] on the device.
  * flce_clip_grads_with_norm scales by a norm the caller has on the device (a
  * norm over several ranks' gradients, say).

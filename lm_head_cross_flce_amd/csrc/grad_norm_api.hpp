@@ -85,6 +85,26 @@ flce_status check_disjoint(const void* const* grads, void* const* outs, const in
   return FLCE_OK;
 }
 
+// Nor may the norm (written, or given and read by every workgroup) or the
+// workspace share memory with a tensor, beyond a given norm with what is only read.
+flce_status check_scalars(const void* const* grads, void* const* outs, const int64_t* numels, const flce_dtype* dtypes,
+                          int64_t count, bool clip, const float* given, const float* norm_out, const void* workspace,
+                          size_t workspace_bytes) {
+  Memory m[] = {{given, 4, false}, {norm_out, 4, true}, {workspace, workspace_bytes, true}, {}};
+  if (clash(m, 3)) return FLCE_ERR_INVALID_ARGUMENT;
+  auto meets = [&](const void* p, size_t bytes, bool written) {
+    m[3] = {p, bytes, written};
+    return clash(m, 4);
+  };
+  for (int64_t i = 0; i < count; ++i) {
+    const size_t bytes = (size_t)(numels[i] * dtype_bytes(dtypes[i]));
+    const void* out = outs ? outs[i] : grads[i];
+    if (meets(grads[i], bytes, clip && out == grads[i]) || (clip && out != grads[i] && meets(out, bytes, true)))
+      return FLCE_ERR_INVALID_ARGUMENT;
+  }
+  return FLCE_OK;
+}
+
 // Launch table l of a call: tensors [l * kNormTensors, ...).  Returns its chunks.
 int64_t norm_table(flce::NormTable& t, const void* const* grads, void* const* outs, const int64_t* numels,
                    const flce_dtype* dtypes, int64_t count, int64_t l, int64_t chunk) {
@@ -171,6 +191,9 @@ flce_status grad_norm_call(const void* const* grads, void* const* outs, const in
       return FLCE_ERR_HIP;
     }
   }
+  const flce_status sc = check_scalars(grads, outs, numels, dtypes, count, clip, given, norm_out, given ? nullptr : workspace,
+                                       given ? 0 : norm_bytes(count));
+  if (sc != FLCE_OK) return sc;
   return run_grad_norm(grads, outs, numels, dtypes, count, max_norm, inf_norm, given, clip, norm_out, (double*)workspace,
                        stream);
 }
