@@ -603,6 +603,60 @@ def _is_dense(t: torch.Tensor) -> bool:
     return True
 
 
+def _extent(t: torch.Tensor):
+    """The addresses of t's first byte and of the one past its last (equal when t is empty)."""
+    lo = t.data_ptr()
+    if t.numel() == 0:
+        return lo, lo
+    return lo, lo + t.element_size() * (1 + sum((n - 1) * s for n, s in zip(t.shape, t.stride())))
+
+
+def _share_memory(a: torch.Tensor, b: torch.Tensor) -> bool:
+    """Whether two strided tensors have a byte in common: whether the difference of their addresses is a sum of
+    whole multiples of their strides, each multiple within its dimension's range.  Strides are tried from the
+    largest on, where few multiples come near enough; a search past 10000 steps counts as yes."""
+    if a.numel() == 0 or b.numel() == 0:
+        return False
+    span = {1: [1 - b.element_size(), a.element_size() - 1]}   # a byte's place in either element
+    for t, end in ((a, 1), (b, 0)):
+        for n, s in zip(t.shape, t.stride()):
+            r = span.setdefault(s * t.element_size(), [0, 0])
+            r[end] += (n - 1) if end else (1 - n)
+    span.pop(0, None)
+    steps = sorted(span.items(), reverse=True)
+    below = [(0, 0)]   # what the strides from here on can add up to
+    for s, (lo, hi) in reversed(steps):
+        below.append((below[-1][0] + s * lo, below[-1][1] + s * hi))
+    below.reverse()
+    left = 10000
+
+    def reach(i: int, diff: int) -> bool:
+        nonlocal left
+        if i == len(steps):
+            return diff == 0
+        s, (lo, hi) = steps[i]
+        rest_lo, rest_hi = below[i + 1]
+        for x in range(max(lo, -((rest_hi - diff) // s)), min(hi, (diff - rest_lo) // s) + 1):
+            left -= 1
+            if left < 0 or reach(i + 1, diff - s * x):
+                return True
+        return False
+
+    return reach(0, b.data_ptr() - a.data_ptr())
+
+
+def _check_written(tensors) -> None:
+    """Refuses tensors of which two share memory, whatever their strides."""
+    spans = sorted(((*_extent(t), i) for i, t in enumerate(tensors)))
+    open_ = []   # tensors whose extent reaches past the current one's start
+    for lo, hi, i in spans:
+        open_ = [(h, j) for h, j in open_ if h > lo]
+        for _, j in open_:
+            if _share_memory(tensors[i], tensors[j]):
+                raise ValueError("tensors to be scaled share memory")
+        open_.append((hi, i))
+
+
 # One attribute of every tensor of a list: a training step passes hundreds, and
 # a Python loop over them would take longer than the kernels.
 _contiguous, _address, _numel, _shape = (torch.Tensor.is_contiguous, torch.Tensor.data_ptr, torch.Tensor.numel,
@@ -654,7 +708,8 @@ def flce_grad_norm(grads, norm_type: float = 2.0) -> torch.Tensor:
 
 def flce_clip_grad_norm(grads, max_norm: float, norm_type: float = 2.0, out=None) -> torch.Tensor:
     """Scales the gradients by min(1, max_norm / (norm + 1e-6)), in place or
-    into the out tensors; returns the norm before, float32 [1]."""
+    into the out tensors; returns the norm before, float32 [1].  No two tensors
+    that are written may share memory."""
     return _clip(grads, max_norm, norm_type, None, out)
 
 
@@ -674,6 +729,8 @@ def _clip(grads, max_norm, norm_type, given, out):
     if not (all(map(_contiguous, grads)) and (out is None or all(map(_contiguous, out)))):
         # A gradient whose elements do not fill one stretch of memory goes through
         # a dense copy, as does one whose out tensor orders its elements otherwise.
+        # The library sees the copies' addresses, so overlaps are looked for here.
+        _check_written(dst)
         src, tmp = [], []
         for g, d in zip(grads, dst):
             if any(st == 0 and sz > 1 for st, sz in zip(d.stride(), d.shape)):

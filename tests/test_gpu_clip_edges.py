@@ -29,3 +29,22 @@ def test_a_given_norm_inside_a_gradient():
     with pytest.raises(_lib.FlceError):
         L.flce_clip_grads_with_norm([g], 1.0, out[7:8], out=[out])
     assert torch.equal(g, keep)
+
+
+def test_the_same_strided_memory_twice():
+    # gradients whose elements fill no single stretch go through copies, whose addresses differ
+    buf = rand(20, 600, seed=2)
+    keep = buf.clone()
+    for grads in ([buf[:, ::2], buf[:, ::2]], [buf[:, :301], buf[:, 300:]], [buf, buf[:, ::2]]):
+        with pytest.raises((ValueError, _lib.FlceError)):
+            L.flce_clip_grad_norm(grads, 1.0)
+        assert torch.equal(buf, keep)
+        with pytest.raises((ValueError, _lib.FlceError)):
+            L.flce_clip_grad_norm([g.contiguous() for g in grads], 1.0, out=grads)
+        assert torch.equal(buf, keep)
+    # side by side in one buffer they are scaled as ever
+    n = math.sqrt(float(keep.double().square().sum()))
+    norm = L.flce_clip_grad_norm([buf[:, ::2], buf[:, 1::2]], n / 2)
+    assert abs(float(norm) - n) <= 2.0 ** -23 * n
+    c = (n / 2) / (n + 1e-6)
+    assert bool(((buf.double() - keep.double() * c).abs() <= keep.double().abs() * c * 2.0 ** -22).all())
