@@ -481,6 +481,11 @@ def _workspace(workspace: Optional[torch.Tensor], nbytes: int, dev) -> Optional[
     return workspace
 
 
+# Tells autograd that the library wrote into a caller's tensor (or a list of
+# them), so that a graph that saved it refuses to use it.
+_wrote = torch.autograd.graph.increment_version
+
+
 def _nbytes(t: Optional[torch.Tensor]) -> int:
     return 0 if t is None else t.numel()
 
@@ -512,6 +517,8 @@ def flce_linear_forward(x: torch.Tensor, W: torch.Tensor, b: Optional[torch.Tens
         stream = _raw_stream(dev.index)
         _lib.flce_linear_forward(x.data_ptr(), W.data_ptr(), _ptr(b), _ptr(residual_), N, H, F, dt, act, y.data_ptr(),
                                  _ptr(z), _ptr(workspace), _nbytes(workspace), stream)
+    if out is not None:
+        _wrote(out)
     return y, z
 
 
@@ -756,6 +763,7 @@ def _clip(grads, max_norm, norm_type, given, out):
         for t, d in zip(tmp, dst):
             if t is not d:
                 d.copy_(t)
+    _wrote(dst)
     return norm
 
 
