@@ -461,8 +461,12 @@ def _prep_layer(x, weights, rows, bias=(), kept=()):
             [dense(b, (F,), dtype) for b in bias], [dense(t, nf, torch.float32) for t in kept])
 
 
-# The current stream of a device, as its address, without a Stream object.
-_raw_stream = torch._C._cuda_getCurrentRawStream
+def _current_stream(index: int) -> int:
+    return torch.cuda.current_stream(index).cuda_stream
+
+
+# The current stream of a device, as its address; torch's own call for it makes no Stream object.
+_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", _current_stream)
 _HERE = contextlib.nullcontext()
 
 

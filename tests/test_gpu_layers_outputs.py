@@ -44,3 +44,9 @@ def test_equal_weights_are_no_clash():
     x = randn(8, 64, seed=1)   # x its own weights
     y, _ = L.flce_linear_forward(x, x)
     assert torch.equal(y, L.flce_linear_forward(x, x.clone())[0])
+
+
+def test_both_ways_to_the_current_stream():
+    for s in (torch.cuda.current_stream(), torch.cuda.Stream()):
+        with torch.cuda.stream(s):
+            assert L._raw_stream(0) == L._current_stream(0) == s.cuda_stream

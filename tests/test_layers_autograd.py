@@ -1,5 +1,9 @@
 """What the feed-forward autograd functions ask of the library, and what importing the binding needs (CPU)."""
 
+import os
+import subprocess
+import sys
+
 import pytest
 import torch
 
@@ -48,3 +52,22 @@ def test_projections_are_kept_for_a_backward(kept):
     assert kept == [True, True, True, False, True, True]
     F.fused_glu(x, block.gate_proj.weight.detach(), block.up_proj.weight.detach())
     assert kept[-1] is False
+
+
+def test_the_binding_imports_without_a_gpu_build_of_torch():
+    # what a build of torch without a GPU lacks, taken away before the import
+    code = ("import torch\n"
+            "del torch._C._cuda_getCurrentRawStream\n"
+            "from lm_head_cross_flce_amd import functional as F\n"
+            "for call in (lambda: F.flce_linear_forward(torch.zeros(2, 8), torch.zeros(4, 8)),\n"
+            "             lambda: F.flce_grad_norm([torch.zeros(2)])):\n"
+            "    try:\n"
+            "        call()\n"
+            "    except ValueError as e:\n"
+            "        assert 'GPU' in str(e)\n"
+            "    else:\n"
+            "        raise AssertionError\n"
+            "print('imported')\n")
+    root = os.path.dirname(os.path.dirname(os.path.abspath(__file__)))
+    r = subprocess.run([sys.executable, "-c", code], capture_output=True, text=True, cwd=root, timeout=300)
+    assert r.returncode == 0 and "imported" in r.stdout, r.stderr
