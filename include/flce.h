@@ -405,6 +405,9 @@ flce_status flce_shard_backward(const void* x, const void* W_shard, const void* 
  *  - No output, kept pre-activation or workspace may share memory with another
  *    tensor of the call (FLCE_ERR_INVALID_ARGUMENT); the linear forward's y may be
  *    its residual.
+ *  - The environment variable FLCE_DEBUG_LAYER_TILE (1, 2, 4 or 8; for tests) is read
+ *    at every call and size query and changes the workspaces' sizes: a workspace
+ *    sized under another value may be refused as too small.
  */
 typedef FLCE_ENUM(flce_activation) {
   FLCE_ACT_NONE = 0,      /* act(z) = z */

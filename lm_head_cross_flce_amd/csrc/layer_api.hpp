@@ -34,17 +34,18 @@ constexpr TileCost kCost32[] = {{4, 55.0, 41.0, 700.0, 2500.0}, {2, 24.0, 15.0, 
 constexpr double kJoinNs = 1500.0, kJoinNsPerByte = 0.235e-3;
 
 // FLCE_DEBUG_LAYER_TILE: the tests run every S (2, 4, 8) on every shape with it,
-// and 1 the few-token kernel wherever it fits.
+// and 1 the few-token kernel wherever it fits.  Read once a call; 0 for anything
+// else.
 int forced_tile() {
   const char* env = std::getenv("FLCE_DEBUG_LAYER_TILE");
-  return env ? std::atoi(env) : 0;
+  const int s = env ? std::atoi(env) : 0;
+  return s == 1 || s == 2 || s == 4 || s == 8 ? s : 0;
 }
 
-// only: the S to use (0: any).
-Cut product_cut(int64_t M, int64_t N, int64_t K, int dtype, int only = 0) {
+// forced: from forced_tile.  only: the S to use (0: any).
+Cut product_cut(int64_t M, int64_t N, int64_t K, int dtype, int forced, int only = 0) {
   if (M < 1 || N < 1) return {only ? only : 2, 1};   // nothing to form
   Cut best{only ? only : 2, 1};
-  const int forced = forced_tile();
   double least = 0.0;
   auto consider = [&](const TileCost& t) {
     if (only && t.S != only) return;
@@ -93,8 +94,8 @@ LayerGeometry layer_geometry(int64_t N, int64_t Hout, int64_t F, int dtype, int 
   const int64_t H = cdiv(Hout, 8) * 8;
   g.Hp = H;
   g.pad_bytes = H == Hout ? 0 : align_up((size_t)(N + nmat * F) * H * es);
-  Cut fwd = product_cut(N, nmat * F, H, dtype);
   const int forced = forced_tile();
+  Cut fwd = product_cut(N, nmat * F, H, dtype, forced);
   if (forced == 1 ? N <= flce::kSkinnyMost : forced == 0 && N <= flce::skinny_tokens(dtype)) fwd = {0, 1};
   g.fwd_tile = fwd.S;
   g.TM = fwd.S ? (int)cdiv(N, 32 * fwd.S) : 0;
@@ -125,10 +126,10 @@ LayerGeometry layer_geometry(int64_t N, int64_t Hout, int64_t F, int dtype, int 
   // both on average and 16% at worst; the size whose times add up to less, 4% and
   // 57%, as the products fill each other's rounds.)  It holds for a call that asks
   // for one gradient alone too, which so has the same bits as beside the other.
-  Cut cx = product_cut(H, N, g.ldz, dtype), cw = product_cut(H, nmat * F, N, dtype);
+  Cut cx = product_cut(H, N, g.ldz, dtype, forced), cw = product_cut(H, nmat * F, N, dtype, forced);
   if (cx.S < 8 && cw.S < 8 && cx.S != cw.S) {
-    cx = product_cut(H, N, g.ldz, dtype, 4);
-    cw = product_cut(H, nmat * F, N, dtype, 4);
+    cx = product_cut(H, N, g.ldz, dtype, forced, 4);
+    cw = product_cut(H, nmat * F, N, dtype, forced, 4);
   }
   g.dx_tile = cx.S;
   g.dx_parts = cx.parts;

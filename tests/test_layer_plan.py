@@ -29,3 +29,19 @@ def test_both_gradient_products_take_one_tile(monkeypatch, op):
             monkeypatch.setenv("FLCE_DEBUG_LAYER_TILE", tile)
             want.add(backward_bytes(op, N, H, F, 0))
         assert got in want, (N, H, F, got, want)
+
+
+def test_unknown_forced_tiles_are_ignored(monkeypatch):
+    shapes = [(N, H, F) for N in (1, 5, 70, 517, 1037) for H in (72, 1000) for F in (40, 2731)]
+
+    def sizes():
+        return [f(*s, d, *a) for s in shapes for d in (0, 1, 2)
+                for f, a in ((_lib.flce_linear_workspace_size, (4,)), (_lib.flce_glu_workspace_size, ()))]
+
+    monkeypatch.delenv("FLCE_DEBUG_LAYER_TILE", raising=False)
+    free = sizes()
+    for value in ("", "0", "3", "16", "-4", "tile"):
+        monkeypatch.setenv("FLCE_DEBUG_LAYER_TILE", value)
+        assert sizes() == free, value
+    monkeypatch.setenv("FLCE_DEBUG_LAYER_TILE", "4")
+    assert sizes() != free
