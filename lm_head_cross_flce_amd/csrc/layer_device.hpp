@@ -186,6 +186,10 @@ template <class T, int C> __device__ __forceinline__ void store_vec(T* p, const 
   }
 }
 
+__device__ __forceinline__ float buf_load4(__amdgpu_buffer_rsrc_t r, uint32_t off) {
+  return __uint_as_float(__builtin_amdgcn_raw_buffer_load_b32(r, off, 0, 0));
+}
+
 // The first `left` of them (any left; none when it is not positive), zeros for the rest.
 template <class T, int C> __device__ __forceinline__ void load_some(const T* p, int left, float (&v)[C]) {
   if (left >= C) {
@@ -527,8 +531,7 @@ __device__ __forceinline__ void gemm_small(f32x4 (&acc)[S][S], const CA& ca, int
 // relative, as near as one fp32 rounding, and they accumulate in fp32 like
 // any product here.  Six 16-cycle instructions do 32 k of a block, where the
 // fp32 instruction takes eight of 32 cycles: 4096 x 4096 x 1024 at S = 4 takes 167 us
-// (205 TFLOP/s), 270 with those.  An infinity among the operands gives NaN (its second part is
-// infinity less infinity).
+// (205 TFLOP/s), 270 with those.
 constexpr int kF32K = 32;
 constexpr int kPartRow = 208;   // LDS bytes of a row: 3 parts x 32 k, and a pad that spreads 16 rows over the banks
 
@@ -563,12 +566,16 @@ template <int S, bool PERM, bool GLU> struct RowCopy<float, S, PERM, GLU> {
   u32x4 r[2][S];
   uint32_t off[S];
   const float* base[2];
-  int kc4;
-  __device__ __forceinline__ void init(const float* p0, const float* p1, int64_t ld, int rows, int m0, int tid) {
+  const float* lead;   // the passes' that pass_is_up leaves: S = 2's waves read one weight each
+  int64_t ld;
+  int kc4, left;       // rows of the operand from m0 on
+  __device__ __forceinline__ void init(const float* p0, const float* p1, int64_t ld_, int rows, int m0, int tid) {
+    ld = ld_;
+    left = rows - m0;
     kc4 = (tid & 7) * 4;
     base[0] = p0 + (int64_t)m0 * ld;
     base[1] = GLU ? p1 + (int64_t)m0 * ld : base[0];
-    if (S == 2 && __builtin_amdgcn_readfirstlane(tid >> 7)) base[0] = base[1];
+    lead = S == 2 && __builtin_amdgcn_readfirstlane(tid >> 7) ? base[1] : base[0];
 #pragma unroll
     for (int q = 0; q < S; ++q) {
       const int t = (tid >> 3) + 32 * q, row = PERM ? weight_row<S, GLU>(t) : t;
@@ -576,10 +583,16 @@ template <int S, bool PERM, bool GLU> struct RowCopy<float, S, PERM, GLU> {
     }
   }
   __device__ __forceinline__ void load(int h, int k0, int kext) {
-    const __amdgpu_buffer_rsrc_t r0 = make_rsrc(base[0] + k0), r1 = make_rsrc(base[1] + k0);
+    const __amdgpu_buffer_rsrc_t r0 = make_rsrc(lead + k0), r1 = make_rsrc(base[1] + k0);
     const bool in = k0 + kc4 < kext;
 #pragma unroll
     for (int q = 0; q < S; ++q) r[h][q] = buf_load16(GLU && pass_is_up<S>(q) ? r1 : r0, in ? off[q] : kOOB);
+  }
+  // Row 16 i + lane % 16 of the half's 16 S rows, k = k0 + lane / 16.
+  __device__ __forceinline__ float value(int i, int half, int k0, int kext, int lane) const {
+    const int t = (half * S + i) * 16 + (lane & 15), g = lane >> 4, row = PERM ? weight_row<S, GLU>(t) : t;
+    const bool in = row < left && k0 + g < kext;
+    return buf_load4(make_rsrc(base[GLU && i >= S / 2] + k0), in ? (uint32_t)((row * ld + g) * 4) : kOOB);
   }
   __device__ __forceinline__ void store(int h, lds_t* buf, int tid) const {
 #pragma unroll
@@ -594,10 +607,11 @@ template <int S> struct ColCopy<float, S> {
   u32x4 r[2][4];
   uint32_t off[4];
   SegRows s;
-  int m0;
+  int m0, left;   // columns of the operand from m0 on
   __device__ __forceinline__ void init(const SegRows& rows, int cols, int m0_, int tid) {
     s = rows;
     m0 = m0_;
+    left = cols - m0;
     const int k = (tid & 7) * 4, m = (tid >> 3) * 4;
 #pragma unroll
     for (int e = 0; e < 4; ++e)
@@ -615,7 +629,37 @@ template <int S> struct ColCopy<float, S> {
     for (int i = 0; i < 4; ++i)
       store_parts(buf + (m + i) * kPartRow, tid & 7, u32x4{r[h][0][i], r[h][1][i], r[h][2][i], r[h][3][i]});
   }
+  // As RowCopy's.  k0 is a multiple of 4, so its four k lie in one weight.
+  __device__ __forceinline__ float value(int i, int half, int k0, int, int lane) const {
+    const int t = (half * S + i) * 16 + (lane & 15);
+    return buf_load4(s.rsrc<4>(k0, m0), t < left ? (uint32_t)(((lane >> 4) * s.ld + t) * 4) : kOOB);
+  }
 };
+
+// The same sums with the fp32 matrix instruction, each wave on its own from
+// global memory: what a wave with a NaN among its sums takes instead of them.
+// The parts of an infinity hold a NaN (infinity less infinity), while the
+// formula may give an infinity.
+template <int S, class CA, class CB>
+__device__ __forceinline__ void gemm_wave_f32(f32x4 (&acc)[S][S], const CA& ca, int ka, const CB& cb, int kb, int K, int lane,
+                                              int wave) {
+#pragma unroll
+  for (int i = 0; i < S; ++i)
+#pragma unroll
+    for (int j = 0; j < S; ++j) acc[i][j] = f32x4{0.f, 0.f, 0.f, 0.f};
+#pragma unroll 1
+  for (int k = 0; k < K; k += 4) {
+    float a[S], b[S];
+#pragma unroll
+    for (int i = 0; i < S; ++i) a[i] = ca.value(i, wave >> 1, k, ka, lane);
+#pragma unroll
+    for (int j = 0; j < S; ++j) b[j] = cb.value(j, wave & 1, k, kb, lane);
+#pragma unroll
+    for (int i = 0; i < S; ++i)
+#pragma unroll
+      for (int j = 0; j < S; ++j) acc[i][j] = __builtin_amdgcn_mfma_f32_16x16x4f32(a[i], b[j], acc[i][j], 0, 0, 0);
+  }
+}
 
 // One LDS buffer an operand: the next two stages' values are on their way into
 // registers while this one is computed, and the CU's other workgroups run under
@@ -670,6 +714,14 @@ __device__ __forceinline__ void gemm_small_f32(f32x4 (&acc)[S][S], CA& ca, int k
     stage(0, kt);
     if (kt + 1 < KT) stage(1, kt + 1);
   }
+  bool nan = false;
+#pragma unroll
+  for (int i = 0; i < S; ++i)
+#pragma unroll
+    for (int j = 0; j < S; ++j)
+#pragma unroll
+      for (int r = 0; r < 4; ++r) nan |= acc[i][j][r] != acc[i][j][r];
+  if (__ballot(nan)) gemm_wave_f32<S>(acc, ca, ka, cb, kb, K, lane, wave);
 }
 
 // f(integral_constant<int, 0>) .. f(integral_constant<int, N - 1>): an unrolled
