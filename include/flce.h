@@ -391,9 +391,10 @@ flce_status flce_shard_backward(const void* x, const void* W_shard, const void* 
  *    costs a launch and a padded copy of x and the weights in the workspace.
  *  - Products accumulate in fp32 whatever the dtype; results are rounded once.
  *    float32 operands (except in the forward of at most 16 tokens) are
- *    multiplied as three bfloat16 parts each, which hold all 24 bits: a product
- *    is right to about 2^-23, as one float32 rounding.  Infinities and NaN give
- *    what float32 products give.
+ *    multiplied as three bfloat16 parts each, which hold all 24 bits: a product is
+ *    right to 2^-22 at worst, with errors of either sign, before its float32
+ *    addition.  Operands under 2^-109 in size keep fewer bits (8 at 2^-125).
+ *    Infinities and NaN give what float32 products give.
  *    The kept pre-activations (z; g and u) are float32 [N, F] whatever the
  *    dtype: rounded to 16 bits they would add as much error to the gradients
  *    as the gradients' own rounding does.  The gradients with respect to them

@@ -525,13 +525,16 @@ __device__ __forceinline__ void gemm_small(f32x4 (&acc)[S][S], const CA& ca, int
 }
 
 // fp32 products on the bf16 matrix cores.  A float's 24 significant bits are
-// exactly three bfloat16 parts of 8, x = h + m + l (each the truncation of what
-// the parts before it leave), so of the nine products of parts the six with
-// weight 2^-16 or more, hh + hm + mh + hl + lh + mm, give x y to about 2^-23
-// relative, as near as one fp32 rounding, and they accumulate in fp32 like
-// any product here.  Six 16-cycle instructions do 32 k of a block, where the
-// fp32 instruction takes eight of 32 cycles: 4096 x 4096 x 1024 at S = 4 takes 167 us
-// (205 TFLOP/s), 270 with those.
+// exactly three bfloat16 parts of 8, x = h + m + l: h is x rounded to nearest, m and
+// l cut off what it leaves, |m| <= 2^-8 |x|, |l| < 2^-15 |x|.  Of the nine products of
+// parts the six of weight 2^-16 or more, hh + hm + mh + hl + lh + mm, give x y to 2^-22
+// relative and mostly nearer; what the rest would add has either sign, as h's
+// rounding has, so it does not pile up in a sum.  They accumulate in fp32 like any
+// product here.  (h cut off too, the parts leave up to 2^-21, always of one sign; m
+// rounded too, 2^-23.  4096 x 4096 x 1024: 183, 185 and 188 us.)  Below about 2^-109 the
+// last part is no normal bfloat16, and an operand keeps fewer bits.
+// Six 16-cycle instructions do 32 k of a block, where the fp32 instruction takes
+// eight of 32 cycles: the loop alone took 167 us (205 TFLOP/s), 270 with those.
 constexpr int kF32K = 32;
 constexpr int kPartRow = 208;   // LDS bytes of a row: 3 parts x 32 k, and a pad that spreads 16 rows over the banks
 
@@ -539,18 +542,20 @@ struct Parts {
   u32x2 p[3];   // four values' h, m, l
 };
 __device__ __forceinline__ Parts split_parts(const u32x4& v) {
-  uint32_t m[4], l[4];
-#pragma unroll
-  for (int e = 0; e < 4; ++e) {
-    const float r = __uint_as_float(v[e]) - __uint_as_float(v[e] & 0xffff0000u);
-    m[e] = __float_as_uint(r);
-    l[e] = __float_as_uint(r - __uint_as_float(m[e] & 0xffff0000u));
-  }
-  auto high = [](uint32_t a, uint32_t b) { return __builtin_amdgcn_perm(b, a, 0x07060302u); };   // both upper halves
+  auto high = [](float a, float b) {   // both upper halves
+    return __builtin_amdgcn_perm(__float_as_uint(b), __float_as_uint(a), 0x07060302u);
+  };
+  auto rest = [](float a) { return a - __uint_as_float(__float_as_uint(a) & 0xffff0000u); };
   Parts o;
-  o.p[0] = u32x2{high(v[0], v[1]), high(v[2], v[3])};
-  o.p[1] = u32x2{high(m[0], m[1]), high(m[2], m[3])};
-  o.p[2] = u32x2{high(l[0], l[1]), high(l[2], l[3])};
+#pragma unroll
+  for (int e = 0; e < 4; e += 2) {
+    const uint32_t h = pack_bf16x2(__uint_as_float(v[e]), __uint_as_float(v[e + 1]));
+    const float a = __uint_as_float(v[e]) - __uint_as_float(h << 16);
+    const float b = __uint_as_float(v[e + 1]) - __uint_as_float(h & 0xffff0000u);
+    o.p[0][e / 2] = h;
+    o.p[1][e / 2] = high(a, b);
+    o.p[2][e / 2] = high(rest(a), rest(b));
+  }
   return o;
 }
 // Four consecutive k (k4 their index / 4) of a row to LDS.

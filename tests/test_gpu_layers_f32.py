@@ -1,4 +1,13 @@
-"""float32 products of infinite operands and of the largest floats."""
+"""float32 products: infinite operands, and how near a product comes to the exact one.
+
+Tolerances.  A float32 operand x is multiplied as three bfloat16 parts h + m + l of 8 bits each, h rounded to
+nearest, m and l cut off what it leaves: |m| <= 2^-8 |x| and |l| < 2^-15 |x|.  The products left out,
+ml + lm + ll, are at most (2 * 2^-23 + 2^-30) |x y|.  The six that are added up come to x y in float32 with the
+small ones first: their own additions round at 2^-23 (an adder that cuts off) of values under 2^-7 |x y|, and the last,
+of hh, at 2^-23 |x y|.  So one product is within
+    2^-22 (left out) + 2^-23 (the last addition) + 5 * 2^-23 * 2^-7 (the others) < 3.1 * 2^-23
+of x y.
+"""
 
 import math
 
@@ -88,4 +97,35 @@ def test_the_largest_floats():
     ref = x[:, :1].double() * W[:, 0].double()
     over = ref.abs() > big
     assert bool(torch.isinf(y[over]).all()) and torch.equal(y[over] > 0, ref[over] > 0)
-    assert bool(((y.double() - ref).abs()[~over] <= 2.0 ** -20 * ref.abs()[~over]).all())
+    assert bool(((y.double() - ref).abs()[~over] <= 3.1 * 2.0 ** -23 * ref.abs()[~over]).all())
+
+
+@pytest.mark.parametrize("tile", ["4", "2"])
+def test_one_product(monkeypatch, tile):
+    # rows and weights with one element that is not zero: each output is one product
+    monkeypatch.setenv("FLCE_DEBUG_LAYER_TILE", tile)
+    N, H, F = 400, 40, 300
+    x, W = torch.zeros(N, H, device="cuda"), torch.zeros(F, H, device="cuda")
+    x[:, 7], W[:, 7] = randn(N, seed=1), randn(F, seed=2)
+    x[0, 7] = W[0, 7] = 1 + 2.0 ** -7 - 2.0 ** -23   # a long run of ones behind the first part
+    y, _ = L.flce_linear_forward(x, W)
+    ref = x[:, 7:8].double() * W[:, 7].double()
+    rel = (y.double() - ref) / ref
+    assert float(rel.abs().max()) <= 3.1 * 2.0 ** -23
+    # the parts' errors have either sign: the mean over 400 x 300 products, of at least 300 independent ones, lies
+    # within 6 standard errors of 0
+    assert abs(float(rel.mean())) <= 6 * float(rel.square().mean().sqrt()) / math.sqrt(300)
+
+
+@pytest.mark.parametrize("tile", ["4", "2"])
+def test_long_sums_have_no_bias(monkeypatch, tile):
+    # sums of K products that are all positive: independent errors of at most 3.1 * 2^-23 of each product (root mean
+    # square at most that) grow with sqrt(K); a one-sided error of the parts would grow with K.  The float32
+    # accumulation rounds K / 4 times or more at up to 2^-24 of the sum so far, of either sign: 8 standard deviations.
+    monkeypatch.setenv("FLCE_DEBUG_LAYER_TILE", tile)
+    N, H, F = 130, 4096, 96
+    x, W = randn(N, H, seed=1).abs() + 0.5, randn(F, H, seed=2).abs() + 0.5
+    y, _ = L.flce_linear_forward(x, W)
+    ref = x.double() @ W.double().T
+    tol = 8 * math.sqrt(H) * (3.1 * 2.0 ** -23 / H * 2 + 2.0 ** -24)
+    assert float(((y.double() - ref) / ref).abs().max()) <= tol
