@@ -21,17 +21,35 @@ template <class T> __device__ __forceinline__ float sigmoid(float z) {
   else return __builtin_amdgcn_rcpf(1.f + fast_exp2(-kLog2e * z));
 }
 
+// exp(-z^2 / 2).  The argument of exp2 is up to 126 in size, and its float32
+// rounding would be as large a relative error of the result: 8e-6 at z = -12.  fp32
+// keeps it in two floats (z^2 and its product with log2(e) / 2 with their fma
+// remainders): 2e-7.  z is held to 16, past which the result is 0, so that no
+// remainder is infinity less infinity; the callers' other terms keep a NaN.
+template <class T> __device__ __forceinline__ float gauss(float z) {
+  constexpr float c = -0.5f * kLog2e;
+  if constexpr (sizeof(T) == 4) {
+    constexpr float c_lo = (float)(-0.5 * 1.4426950408889634 - (double)c);
+    const float a = fminf(fabsf(z), 16.f), s = a * a, hi = c * s;
+    const float lo = fmaf(c_lo, s, fmaf(c, fmaf(a, a, -s), fmaf(c, s, -hi)));
+    const float e = fast_exp2(hi);
+    return fmaf(0.69314718f * e, lo, e);
+  } else {
+    return fast_exp2(c * z * z);
+  }
+}
+
 // Phi(z), the normal distribution function, without branches (the tile
 // epilogue holds 256 accumulators, and calls or branches there cost it its
 // registers): erfc(x) = t P(t) exp(-x^2) with t = 1 / (1 + p x) for
 // x = |z| / sqrt(2) >= 0.  P was fitted to erfc(x) exp(x^2) / t on [0, 9.5] by
 // linear programming for the least largest relative error: degree 5 (p = 0.65)
 // has 8.7e-6, a 50th of a half step of bf16 or fp16; degree 8 (p = 0.4)
-// evaluates to within 3.8e-7 in fp32.  The negative tail keeps that relative
-// error, as it takes erfc itself.
+// evaluates to within 3.8e-7 in fp32, and with gauss the tail to 4.6e-7 of itself
+// down to z = -12.9, as it takes erfc itself.
 template <class T> __device__ __forceinline__ float normal_cdf(float z) {
   const float x = 0.70710678f * fabsf(z);
-  const float e = fast_exp2(-0.5f * kLog2e * z * z);
+  const float e = gauss<T>(z);
   float t, q;
   if constexpr (sizeof(T) == 4) {
     t = 1.f / fmaf(0.4f, x, 1.f);
@@ -82,7 +100,7 @@ template <class T, int ACT> __device__ __forceinline__ float act_bwd(float z, fl
   } else if constexpr (ACT == kActGelu) {
     const float p = normal_cdf<T>(z);
     v = z * p;
-    return dy * (p + z * (0.39894228f * fast_exp2(-0.5f * kLog2e * z * z)));
+    return dy * (p + z * (0.39894228f * gauss<T>(z)));
   } else if constexpr (ACT == kActGeluTanh) {
     const float zc = gelu_clamp(z), s = sigmoid<T>(gelu_arg(zc));
     v = z * s;
