@@ -48,3 +48,22 @@ def test_the_same_strided_memory_twice():
     assert abs(float(norm) - n) <= 2.0 ** -23 * n
     c = (n / 2) / (n + 1e-6)
     assert bool(((buf.double() - keep.double() * c).abs() <= keep.double().abs() * c * 2.0 ** -22).all())
+
+
+@pytest.mark.parametrize("dt", [torch.bfloat16, torch.float16, torch.float32], ids=str)
+@pytest.mark.parametrize("place", ["first", "middle", "last"])
+def test_max_norm_of_more_than_the_cache_holds(dt, place):
+    # over 160 MB the loads bypass the memory-side cache: the largest element anywhere, of either sign, and a NaN
+    n = (200 << 20) // dt.itemsize + 77
+    g = rand(n, dt=torch.float32, seed=3).clamp_(-4, 4).to(dt)
+    small = rand(1001, seed=4)
+    i = {"first": 0, "middle": n // 2, "last": n - 1}[place]
+    g[i] = -9.0
+    assert float(L.flce_grad_norm([small, g], math.inf)) == 9.0
+    norm = L.flce_clip_grad_norm([small, g], 4.5, math.inf)
+    assert float(norm) == 9.0
+    # 9 * 4.5 / (9 + 1e-6), its product's and its type's rounding
+    assert abs(float(g[i]) + 4.5) <= 4.5 * (torch.finfo(dt).eps / 2 + 2.0 ** -22) and float(g.abs().max()) == -float(g[i])
+    g[i] = math.nan
+    assert math.isnan(float(L.flce_grad_norm([small, g], math.inf)))
+    assert math.isnan(float(L.flce_grad_norm([small, g])))
