@@ -2,6 +2,8 @@
 // tables, entry points.  Included once, by flce_api.hip.
 #pragma once
 
+#include "layer_api.hpp"   // clash
+
 namespace {
 
 // Workgroups over all launches of one call (each launch has at least one): 4

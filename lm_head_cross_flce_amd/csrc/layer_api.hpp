@@ -4,6 +4,25 @@
 
 namespace {
 
+// A tensor of a call (p null or no bytes: absent).
+struct Memory {
+  const void* p;
+  size_t bytes;
+  bool written;
+};
+
+// Whether a tensor that the call writes shares a byte with another of them:
+// workgroups of both would race.
+bool clash(const Memory* m, int count) {
+  for (int i = 0; i < count; ++i)
+    for (int j = 0; j < i; ++j) {
+      if (!m[i].p || !m[j].p || !m[i].bytes || !m[j].bytes || !(m[i].written || m[j].written)) continue;
+      const uintptr_t a = (uintptr_t)m[i].p, b = (uintptr_t)m[j].p;
+      if (a < b + m[j].bytes && b < a + m[i].bytes) return true;
+    }
+  return false;
+}
+
 // How a product of M x N outputs over K is cut: output tiles of 32 S x 32 S
 // (S = 8, 16-bit only; 4; 2) and parts of K.
 struct Cut {
