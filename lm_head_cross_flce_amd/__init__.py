@@ -17,9 +17,9 @@ def __getattr__(name):
         return importlib.import_module(f"{__name__}.{name}")
     if name in ("flce_forward", "flce_backward", "flce_workspace_size", "fused_linear_cross_entropy_loss",
                 "FusedLinearCrossEntropyLoss", "FusedLinearCrossEntropyFunction", "fused_linear", "fused_glu",
-                "GatedFeedForward", "clip_grad_norm_", "flce_linear_forward", "flce_linear_backward",
-                "flce_glu_forward", "flce_glu_backward", "flce_grad_norm", "flce_clip_grad_norm",
-                "flce_clip_grads_with_norm"):
+                "GatedFeedForward", "clip_grad_norm_", "flce_linear_workspace_size",
+                "flce_linear_forward", "flce_linear_backward", "flce_glu_workspace_size", "flce_glu_forward",
+                "flce_glu_backward", "flce_grad_norm", "flce_clip_grad_norm", "flce_clip_grads_with_norm"):
         from . import functional
         return getattr(functional, name)
     raise AttributeError(name)

@@ -45,3 +45,12 @@ def test_unknown_forced_tiles_are_ignored(monkeypatch):
         assert sizes() == free, value
     monkeypatch.setenv("FLCE_DEBUG_LAYER_TILE", "4")
     assert sizes() != free
+
+
+def test_the_package_names_the_size_queries():
+    import torch
+
+    import lm_head_cross_flce_amd as pkg
+    assert pkg.flce_linear_workspace_size(70, 264, 100, torch.bfloat16, "gelu") == _lib.flce_linear_workspace_size(
+        70, 264, 100, 1, 2)
+    assert pkg.flce_glu_workspace_size(70, 264, 100, torch.float32) == _lib.flce_glu_workspace_size(70, 264, 100, 0)
