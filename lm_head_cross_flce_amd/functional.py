@@ -916,8 +916,9 @@ class GatedFeedForward(torch.nn.Module):
 
 
 def clip_grad_norm_(parameters, max_norm: float, norm_type: float = 2.0) -> torch.Tensor:
-    """Clips the parameters' gradients in place by their global norm, as
-    torch.nn.utils.clip_grad_norm_ does; returns the norm before (a scalar tensor)."""
+    """Clips the parameters' gradients in place by their global norm, by the formula of
+    torch.nn.utils.clip_grad_norm_; returns the norm before (a scalar tensor).  norm_type is 2 or infinity;
+    the gradients are on one device, and no two of them share memory (no parameter comes twice)."""
     if isinstance(parameters, torch.Tensor):
         parameters = [parameters]
     grads = [p.grad for p in parameters if p.grad is not None]
