@@ -467,6 +467,125 @@ flce_status flce_glu_backward(const void* x, const void* Wg, const void* Wu, con
                               void* workspace, size_t workspace_bytes, hipStream_t stream);
 
 /*
+ * Root-mean-square norm, with the residual's addition before it:
+ *
+ *   h = x + residual  (x itself without a residual)
+ *   rstd[n] = (mean over c of h[n, c]^2 + eps)^(-1/2)
+ *   y = h * rstd * weight                              (weight NULL: 1)
+ *
+ * x, residual, h, y [N, H], weight [H], one dtype; any H, N = 0 included (the token
+ * tensors may then be NULL).  Everything is formed in fp32 and rounded once: y comes
+ * from the sum before h is rounded.  [.., ..] tensors 16-byte aligned, weight
+ * element-aligned, rstd float32.
+ * flce_rms_norm_forward writes y, h (only with a residual; may be x or the residual)
+ * and rstd [N]; h and rstd may be NULL.
+ * flce_rms_norm_mx_forward writes the fp32 y as a microscaled tensor (below) instead.
+ * flce_rms_norm_backward, given h (x without a residual) and rstd as the forward wrote
+ * them, dy, and dh, the gradient that reaches h past the norm (NULL: none):
+ *   n = h * rstd,  dn = dy * weight
+ *   dx = dh + rstd * (dn - n * mean over c of dn * n),   dweight = sum over rows of dy * n
+ * dx is the residual's gradient too.  dx, dweight may be NULL; dx may be dh, or, with H up
+ * to 16384 or without dweight, dy.  h is the rounded sum, so 16-bit gradients take its
+ * rounding beside their own.  dweight is summed in fp32 in a fixed order.
+ * No other two tensors of a call of which one is written may share memory
+ * (FLCE_ERR_INVALID_ARGUMENT).  eps is finite and not negative.
+ * flce_rms_norm_workspace_size: bytes for a backward that writes dweight (without it
+ * the workspace may be NULL); pure host arithmetic.
+ */
+typedef FLCE_ENUM(flce_mx_format) {
+  FLCE_MX_E4M3 = 0, /* a byte: 4 bits of exponent, 3 of mantissa, to 448 */
+  FLCE_MX_E2M1 = 1  /* half a byte: 2 and 1, to 6; the even column in the low half */
+} flce_mx_format;
+
+flce_status flce_rms_norm_forward(const void* x, const void* residual, const void* weight, int64_t N, int64_t H,
+                                  flce_dtype dtype, float eps, void* y, void* h, float* rstd, hipStream_t stream);
+
+flce_status flce_rms_norm_mx_forward(const void* x, const void* residual, const void* weight, int64_t N, int64_t H,
+                                     flce_dtype dtype, float eps, flce_mx_format format, uint8_t* codes, uint8_t* scales,
+                                     void* h, float* rstd, hipStream_t stream);
+
+flce_status flce_rms_norm_workspace_size(int64_t N, int64_t H, flce_dtype dtype, size_t* bwd_bytes);
+
+flce_status flce_rms_norm_backward(const void* h, const void* weight, const float* rstd, const void* dy, const void* dh,
+                                   int64_t N, int64_t H, flce_dtype dtype, void* dx, void* dweight, void* workspace,
+                                   size_t workspace_bytes, hipStream_t stream);
+
+/*
+ * Microscaled tensors (the OCP microscaling formats MXFP8 e4m3 and MXFP4): every 32
+ * consecutive columns of a row share a scale 2^(s - 127), s one byte.  A tensor [R, C]
+ * is stored as Cp columns, C rounded up to 128, zeros past C:
+ *   codes   uint8 [R, Cp] (e4m3) or [R, Cp / 2] (e2m1), 16-byte aligned
+ *   scales  uint8 [R, Cp / 32], 4-byte aligned
+ * Any C; R = 0 is allowed and its pointers then ignored.
+ * flce_mx_quantize: s - 127 = floor(log2(largest magnitude)) - 8 (e4m3) or - 2 (e2m1),
+ * not below -127; elements are x 2^(127 - s) rounded to nearest, ties to even, and held to
+ * the format's largest.  A block with a NaN or an infinity gets s = 255, NaN (and
+ * zero codes); a block of zeros s = 0.
+ * flce_mx_dequantize: the values, rounded to the dtype (bfloat16 holds all that are in
+ * its range; a float16 past 65504 is an infinity).
+ */
+flce_status flce_mx_quantize(const void* x, int64_t R, int64_t C, flce_dtype dtype, flce_mx_format format, uint8_t* codes,
+                             uint8_t* scales, hipStream_t stream);
+
+flce_status flce_mx_dequantize(const uint8_t* codes, const uint8_t* scales, int64_t R, int64_t C, flce_mx_format format,
+                               flce_dtype dtype, void* y, hipStream_t stream);
+
+/*
+ * Linear layer over microscaled operands: y = act(x W^T + b) + residual, x [N, K] in
+ * x_format, W [F, K] in e2m1, b [F], residual and y [N, F] of the dtype; b and residual
+ * may be NULL, y may be the residual.  Any N (0 included), K and F.  Element products
+ * are exact.  Their sums are fp32, but for 16-bit results of an e4m3 x: the matrix
+ * instruction adds those in pieces of 128 columns that drop bits under about 2^-13 of
+ * a piece's largest product (on normally distributed operands 5e-6 of the result).
+ * With float32 results an e4m3 x meets W in bfloat16, which holds their values down to
+ * 2^-126; smaller ones may count as 0.
+ * A NaN scale makes the results of its row (of W: its feature) NaN.
+ * flce_mx_linear_workspace_size: bytes for the call (fp32 partial sums of a product
+ * split along K; often 0, and the workspace may then be NULL); pure host arithmetic.
+ */
+flce_status flce_mx_linear_workspace_size(int64_t N, int64_t K, int64_t F, flce_mx_format x_format, flce_dtype dtype,
+                                          size_t* bytes);
+
+flce_status flce_mx_linear(const uint8_t* x, const uint8_t* x_scales, flce_mx_format x_format, const uint8_t* W,
+                           const uint8_t* W_scales, const void* b, const void* residual, int64_t N, int64_t K, int64_t F,
+                           flce_dtype dtype, flce_activation activation, void* y, void* workspace, size_t workspace_bytes,
+                           hipStream_t stream);
+
+/*
+ * Sampling: one token from each row of logits [N, V], by a given u[n] in [0, 1).
+ *
+ *   w[j] = exp((z[j] - max z) / temperature); tokens rank by z from the largest, equal
+ *   ones by index (-0 equals 0)
+ *   top_k (1 to V - 1; others: off) keeps the first k tokens
+ *   top_p (under 1; others, NaN included: off) keeps, of those, each whose predecessors'
+ *   w add up to less than top_p times the sum of those; the first token always
+ *   min_p (over 0; others, NaN included: off) keeps, of those, w[j] >= min(min_p, 1)
+ *   token = the first in the vocabulary's order at which the kept w add up to more
+ *   than u times their sum (u under 0 or NaN counts as 0, from 1 on as the last kept token)
+ *
+ * A temperature that is not above 0 (NaN included) takes the largest logit's first
+ * token.  A masked token's logit is -infinity; it is never taken.  Rows without any
+ * other logit, and rows with a NaN, give -1.  If the largest logit is infinite, the
+ * tokens that have it share the weight.  Each parameter is one number for all rows or,
+ * where its pointer is not NULL, float32 (top_ks int64) [N] on the device.  Weights are
+ * formed in fp64 and added exactly, as whole numbers, so results do not depend on any order.
+ * logits 16-byte aligned, tokens int64 [N].
+ */
+typedef struct flce_sampling {
+  float temperature;
+  int64_t top_k;
+  float top_p;
+  float min_p;
+  const float* temperatures;
+  const int64_t* top_ks;
+  const float* top_ps;
+  const float* min_ps;
+} flce_sampling;
+
+flce_status flce_sample(const void* logits, const float* u, int64_t N, int64_t V, flce_dtype dtype,
+                        const flce_sampling* params, int64_t* tokens, hipStream_t stream);
+
+/*
  * Global gradient norm and clipping, over `count` tensors of any dtypes and
  * sizes (numels[i] elements at grads[i], element-aligned; numels[i] = 0 is
  * allowed and its pointer then ignored).  grads, outs, numels and dtypes are

@@ -19,7 +19,10 @@ def __getattr__(name):
                 "FusedLinearCrossEntropyLoss", "FusedLinearCrossEntropyFunction", "fused_linear", "fused_glu",
                 "GatedFeedForward", "clip_grad_norm_", "flce_linear_workspace_size",
                 "flce_linear_forward", "flce_linear_backward", "flce_glu_workspace_size", "flce_glu_forward",
-                "flce_glu_backward", "flce_grad_norm", "flce_clip_grad_norm", "flce_clip_grads_with_norm"):
+                "flce_glu_backward", "flce_grad_norm", "flce_clip_grad_norm", "flce_clip_grads_with_norm",
+                "flce_rms_norm_workspace_size", "flce_rms_norm_forward", "flce_rms_norm_mx_forward",
+                "flce_rms_norm_backward", "flce_mx_quantize", "flce_mx_dequantize", "flce_mx_linear_workspace_size",
+                "flce_mx_linear", "flce_sample", "MXTensor", "fused_rms_norm", "RMSNorm", "MXLinear"):
         from . import functional
         return getattr(functional, name)
     raise AttributeError(name)

@@ -29,6 +29,8 @@ FLCE_F16 = 2
 
 REDUCTIONS = {"none": 0, "sum": 1, "mean": 2}
 
+MX_FORMATS = {"e4m3": 0, "e2m1": 1}
+
 ACTIVATIONS = {"none": 0, "relu": 1, "gelu": 2, "gelu_tanh": 3, "silu": 4, "sigmoid": 5}
 
 # Every symbol the public header declares.
@@ -41,11 +43,21 @@ EXPORTS = ("flce_workspace_size", "flce_forward", "flce_backward", "flce_forward
            "flce_shard_backward",
            "flce_linear_workspace_size", "flce_linear_forward", "flce_linear_backward",
            "flce_glu_workspace_size", "flce_glu_forward", "flce_glu_backward",
-           "flce_grad_norm_workspace_size", "flce_grad_norm", "flce_clip_grad_norm", "flce_clip_grads_with_norm")
+           "flce_grad_norm_workspace_size", "flce_grad_norm", "flce_clip_grad_norm", "flce_clip_grads_with_norm",
+           "flce_rms_norm_forward", "flce_rms_norm_mx_forward", "flce_rms_norm_workspace_size", "flce_rms_norm_backward",
+           "flce_mx_quantize", "flce_mx_dequantize", "flce_mx_linear_workspace_size", "flce_mx_linear", "flce_sample")
+
 
 class FlceOptions(ctypes.Structure):
     """struct flce_options of flce.h."""
     _fields_ = [("logit_scale", ctypes.c_float), ("accumulate", ctypes.c_int), ("z_loss", ctypes.c_void_p)]
+
+
+class FlceSampling(ctypes.Structure):
+    """struct flce_sampling of flce.h."""
+    _fields_ = [("temperature", ctypes.c_float), ("top_k", ctypes.c_int64), ("top_p", ctypes.c_float),
+                ("min_p", ctypes.c_float), ("temperatures", ctypes.c_void_p), ("top_ks", ctypes.c_void_p),
+                ("top_ps", ctypes.c_void_p), ("min_ps", ctypes.c_void_p)]
 
 
 _lock = threading.Lock()
@@ -151,6 +163,24 @@ def load() -> ctypes.CDLL:
         lib.flce_clip_grad_norm.restype = c_int
         lib.flce_clip_grads_with_norm.argtypes = [vp, vp, vp, vp, i64, f32, vp, vp]
         lib.flce_clip_grads_with_norm.restype = c_int
+        lib.flce_rms_norm_forward.argtypes = [vp, vp, vp, i64, i64, c_int, f32, vp, vp, vp, vp]
+        lib.flce_rms_norm_forward.restype = c_int
+        lib.flce_rms_norm_mx_forward.argtypes = [vp, vp, vp, i64, i64, c_int, f32, c_int, vp, vp, vp, vp, vp]
+        lib.flce_rms_norm_mx_forward.restype = c_int
+        lib.flce_rms_norm_workspace_size.argtypes = [i64, i64, c_int, psz]
+        lib.flce_rms_norm_workspace_size.restype = c_int
+        lib.flce_rms_norm_backward.argtypes = [vp, vp, vp, vp, vp, i64, i64, c_int, vp, vp, vp, sz, vp]
+        lib.flce_rms_norm_backward.restype = c_int
+        lib.flce_mx_quantize.argtypes = [vp, i64, i64, c_int, c_int, vp, vp, vp]
+        lib.flce_mx_quantize.restype = c_int
+        lib.flce_mx_dequantize.argtypes = [vp, vp, i64, i64, c_int, c_int, vp, vp]
+        lib.flce_mx_dequantize.restype = c_int
+        lib.flce_mx_linear_workspace_size.argtypes = [i64, i64, i64, c_int, c_int, psz]
+        lib.flce_mx_linear_workspace_size.restype = c_int
+        lib.flce_mx_linear.argtypes = [vp, vp, c_int, vp, vp, vp, vp, i64, i64, i64, c_int, c_int, vp, vp, sz, vp]
+        lib.flce_mx_linear.restype = c_int
+        lib.flce_sample.argtypes = [vp, vp, i64, i64, c_int, ctypes.POINTER(FlceSampling), vp, vp]
+        lib.flce_sample.restype = c_int
         _lib = lib
         return lib
 
@@ -401,6 +431,74 @@ def flce_clip_grads_with_norm(grads, outs, numels, dtypes, count, max_norm, norm
     _check(load().flce_clip_grads_with_norm(_host(grads), _host(outs), _host(numels), _host(dtypes), count, max_norm, norm,
                                             stream or None),
            "flce_clip_grads_with_norm")
+
+
+def flce_rms_norm_forward(x, residual, weight, N, H, dtype, eps, y, h, rstd, stream) -> None:
+    """Raw call: every tensor argument is an integer device address (or 0/None)."""
+    _check(load().flce_rms_norm_forward(x or None, residual or None, weight or None, N, H, dtype, eps, y or None,
+                                        h or None, rstd or None, stream or None), "flce_rms_norm_forward")
+
+
+def flce_rms_norm_mx_forward(x, residual, weight, N, H, dtype, eps, format, codes, scales, h, rstd, stream) -> None:
+    """Raw call: every tensor argument is an integer device address (or 0/None)."""
+    _check(load().flce_rms_norm_mx_forward(x or None, residual or None, weight or None, N, H, dtype, eps, format,
+                                           codes or None, scales or None, h or None, rstd or None, stream or None),
+           "flce_rms_norm_mx_forward")
+
+
+def flce_rms_norm_workspace_size(N: int, H: int, dtype: int) -> int:
+    b = ctypes.c_size_t(0)
+    _check(load().flce_rms_norm_workspace_size(N, H, dtype, ctypes.byref(b)), "flce_rms_norm_workspace_size")
+    return b.value
+
+
+def flce_rms_norm_backward(h, weight, rstd, dy, dh, N, H, dtype, dx, dweight, workspace, workspace_bytes,
+                           stream) -> None:
+    """Raw call: every tensor argument is an integer device address (or 0/None)."""
+    _check(load().flce_rms_norm_backward(h or None, weight or None, rstd or None, dy or None, dh or None, N, H, dtype,
+                                         dx or None, dweight or None, workspace or None, workspace_bytes,
+                                         stream or None), "flce_rms_norm_backward")
+
+
+def flce_mx_quantize(x, R, C, dtype, format, codes, scales, stream) -> None:
+    """Raw call: every tensor argument is an integer device address (or 0/None)."""
+    _check(load().flce_mx_quantize(x or None, R, C, dtype, format, codes or None, scales or None, stream or None),
+           "flce_mx_quantize")
+
+
+def flce_mx_dequantize(codes, scales, R, C, format, dtype, y, stream) -> None:
+    """Raw call: every tensor argument is an integer device address (or 0/None)."""
+    _check(load().flce_mx_dequantize(codes or None, scales or None, R, C, format, dtype, y or None, stream or None),
+           "flce_mx_dequantize")
+
+
+def flce_mx_linear_workspace_size(N: int, K: int, F: int, x_format: int, dtype: int) -> int:
+    b = ctypes.c_size_t(0)
+    _check(load().flce_mx_linear_workspace_size(N, K, F, x_format, dtype, ctypes.byref(b)),
+           "flce_mx_linear_workspace_size")
+    return b.value
+
+
+def flce_mx_linear(x, x_scales, x_format, W, W_scales, b, residual, N, K, F, dtype, activation, y, workspace,
+                   workspace_bytes, stream) -> None:
+    """Raw call: every tensor argument is an integer device address (or 0/None)."""
+    _check(load().flce_mx_linear(x or None, x_scales or None, x_format, W or None, W_scales or None, b or None,
+                                 residual or None, N, K, F, dtype, activation, y or None, workspace or None,
+                                 workspace_bytes, stream or None), "flce_mx_linear")
+
+
+def sampling(temperature: float = 1.0, top_k: int = 0, top_p: float = 1.0, min_p: float = 0.0, temperatures=None,
+             top_ks=None, top_ps=None, min_ps=None) -> FlceSampling:
+    """An flce_sampling value; the plural arguments are integer device addresses or None."""
+    return FlceSampling(float(temperature), int(top_k), float(top_p), float(min_p), temperatures or None,
+                        top_ks or None, top_ps or None, min_ps or None)
+
+
+def flce_sample(logits, u, N, V, dtype, params, tokens, stream) -> None:
+    """Raw call: every tensor argument is an integer device address (or 0/None); params from sampling()."""
+    _check(load().flce_sample(logits or None, u or None, N, V, dtype,
+                              ctypes.byref(params) if params is not None else None, tokens or None, stream or None),
+           "flce_sample")
 
 
 def flce_timing_start(capacity: int) -> None:

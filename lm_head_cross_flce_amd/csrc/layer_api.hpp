@@ -335,3 +335,7 @@ flce_status flce_glu_backward(const void* x, const void* Wg, const void* Wu, con
 }
 
 }  // extern "C"
+
+#include "layer_norm_api.hpp"
+#include "layer_mx_api.hpp"
+#include "layer_sample_api.hpp"

@@ -1,0 +1,135 @@
+// Host side of the microscaled tensors: argument checks, tile and split choice,
+// workspace layout, entry points.  Included once, at the end of layer_api.hpp.
+#pragma once
+
+#include "layer_norm_api.hpp"
+
+namespace {
+
+flce_status check_mx(int64_t R, int64_t C, int dtype, int format) {
+  if (R < 0 || C < 1 || bad_format(format)) return FLCE_ERR_INVALID_ARGUMENT;
+  if (dtype != FLCE_F32 && dtype != FLCE_BF16 && dtype != FLCE_F16) return FLCE_ERR_UNSUPPORTED;
+  if (R > (int64_t(1) << 30) || C > (int64_t(1) << 20)) return FLCE_ERR_UNSUPPORTED;
+  return FLCE_OK;
+}
+
+flce_status mx_convert(const void* x, void* y, uint8_t* codes, uint8_t* scales, int64_t R, int64_t C, int dtype, int format,
+                       bool quantize, hipStream_t stream) {
+  const flce_status st = check_mx(R, C, dtype, format);
+  if (st != FLCE_OK) return st;
+  const void* plain = quantize ? x : y;
+  if (bad_tensor(plain, 16, R > 0) || bad_tensor(codes, 16, R > 0) || bad_tensor(scales, 4, R > 0)) return FLCE_ERR_INVALID_ARGUMENT;
+  if (R == 0) return FLCE_OK;
+  const Memory mem[] = {{plain, (size_t)R * C * type_bytes(dtype), !quantize}, {codes, R * mx_code_bytes(C, format), quantize},
+                        {scales, R * mx_scale_bytes(C), quantize}};
+  if (clash(mem, 3)) return FLCE_ERR_INVALID_ARGUMENT;
+  flce::MxConvert a{};
+  a.x = x; a.y = y; a.codes = codes; a.scales = scales;
+  a.R = R; a.C = (int)C; a.Cp = (int)mx_cols(C);
+  a.format = format;
+  (void)hipGetLastError();
+  flce::mark_launch(stream, nullptr);
+  return (quantize ? flce::launch_mx_quantize(a, dtype, stream) : flce::launch_mx_dequantize(a, dtype, stream)) == hipSuccess
+             ? FLCE_OK : FLCE_ERR_HIP;
+}
+
+struct MxGeometry {
+  int tile, TM, TN, parts;   // tile 0: the few-token kernel, parts waves to a group of features
+  int64_t kc, ldp;
+  size_t total;
+};
+
+constexpr int64_t kMxFew = 16;   // most tokens of the few-token kernel
+
+MxGeometry mx_geometry(int64_t N, int64_t K, int64_t F) {
+  MxGeometry g{};
+  const int64_t Kp = mx_cols(K);
+  if (N <= kMxFew) {
+    // enough waves for every CU, each with K of its own to walk
+    g.parts = 1;
+    while (g.parts < 8 && cdiv(F, 16) * g.parts < 8 * kCUs && Kp / 128 >= 2 * g.parts) g.parts *= 2;
+    g.kc = Kp;
+    return g;
+  }
+  const int64_t big = cdiv(N, 128) * cdiv(F, 128);
+  g.tile = big >= 2 * kCUs ? 4 : 2;
+  const int64_t M = 32 * g.tile;
+  g.TM = (int)cdiv(N, M);
+  g.TN = (int)cdiv(F, M);
+  g.parts = 1;
+  // parts of 1024 columns at least, while the tiles leave CUs idle
+  while (g.parts < 8 && (int64_t)g.TM * g.TN * g.parts * 2 <= 2 * kCUs && Kp / (2 * g.parts) >= 1024) g.parts *= 2;
+  g.kc = cdiv(cdiv(Kp, g.parts), 256) * 256;
+  g.parts = (int)cdiv(Kp, g.kc);
+  g.ldp = cdiv(F, 8) * 8;
+  g.total = g.parts > 1 ? align_up((size_t)g.parts * N * g.ldp * 4) : 0;
+  return g;
+}
+
+flce_status check_mx_linear(int64_t N, int64_t K, int64_t F, int dtype, int format, int act) {
+  if (N < 0 || K < 1 || F < 1 || bad_format(format)) return FLCE_ERR_INVALID_ARGUMENT;
+  if (act < FLCE_ACT_NONE || act > FLCE_ACT_SIGMOID) return FLCE_ERR_INVALID_ARGUMENT;
+  if (dtype != FLCE_F32 && dtype != FLCE_BF16 && dtype != FLCE_F16) return FLCE_ERR_UNSUPPORTED;
+  if (N > (int64_t(1) << 30) || K > (int64_t(1) << 20) || F > (int64_t(1) << 20)) return FLCE_ERR_UNSUPPORTED;
+  if (cdiv(N, 64) * cdiv(F, 64) > (int64_t(1) << 22)) return FLCE_ERR_UNSUPPORTED;   // a launch has fewer than 2^32 threads
+  return FLCE_OK;
+}
+
+}  // namespace
+
+extern "C" {
+
+flce_status flce_mx_quantize(const void* x, int64_t R, int64_t C, flce_dtype dtype, flce_mx_format format, uint8_t* codes,
+                             uint8_t* scales, hipStream_t stream) {
+  return mx_convert(x, nullptr, codes, scales, R, C, dtype, format, true, stream);
+}
+
+flce_status flce_mx_dequantize(const uint8_t* codes, const uint8_t* scales, int64_t R, int64_t C, flce_mx_format format,
+                               flce_dtype dtype, void* y, hipStream_t stream) {
+  return mx_convert(nullptr, y, const_cast<uint8_t*>(codes), const_cast<uint8_t*>(scales), R, C, dtype, format, false, stream);
+}
+
+flce_status flce_mx_linear_workspace_size(int64_t N, int64_t K, int64_t F, flce_mx_format x_format, flce_dtype dtype,
+                                          size_t* bytes) {
+  const flce_status st = check_mx_linear(N, K, F, dtype, x_format, FLCE_ACT_NONE);
+  if (st != FLCE_OK) return st;
+  if (bytes) *bytes = mx_geometry(N, K, F).total;
+  return FLCE_OK;
+}
+
+flce_status flce_mx_linear(const uint8_t* x, const uint8_t* x_scales, flce_mx_format x_format, const uint8_t* W,
+                           const uint8_t* W_scales, const void* b, const void* residual, int64_t N, int64_t K, int64_t F,
+                           flce_dtype dtype, flce_activation activation, void* y, void* workspace, size_t workspace_bytes,
+                           hipStream_t stream) {
+  const flce_status st = check_mx_linear(N, K, F, dtype, x_format, activation);
+  if (st != FLCE_OK) return st;
+  const size_t es = type_bytes(dtype);
+  const bool rows = N > 0;
+  if (bad_tensor(x, 16, rows) || bad_tensor(x_scales, 4, rows) || bad_tensor(W, 16, true) || bad_tensor(W_scales, 4, true) ||
+      bad_tensor(b, es, false) || bad_tensor(residual, 16, false) || bad_tensor(y, 16, rows))
+    return FLCE_ERR_INVALID_ARGUMENT;
+  const MxGeometry g = mx_geometry(N, K, F);
+  if (workspace_bytes < g.total) return FLCE_ERR_WORKSPACE_TOO_SMALL;
+  if (bad_tensor(workspace, 16, g.total > 0)) return FLCE_ERR_INVALID_ARGUMENT;
+  if (!rows) return FLCE_OK;
+  const size_t nf = (size_t)N * F * es;
+  const Memory mem[] = {{x, N * mx_code_bytes(K, x_format), false}, {x_scales, N * mx_scale_bytes(K), false},
+                        {W, F * mx_code_bytes(K, FLCE_MX_E2M1), false}, {W_scales, F * mx_scale_bytes(K), false},
+                        {b, (size_t)F * es, false}, {residual == y ? nullptr : residual, nf, false}, {y, nf, true},
+                        {workspace, g.total, true}};
+  if (clash(mem, 8)) return FLCE_ERR_INVALID_ARGUMENT;
+  flce::MxLinear a{};
+  a.x = x; a.xs = x_scales; a.W = W; a.Ws = W_scales;
+  a.b = b; a.residual = residual; a.y = y;
+  a.N = (int)N; a.F = (int)F; a.Kp = (int)mx_cols(K);
+  a.format = x_format;
+  a.act = activation;
+  a.tile = g.tile; a.TM = g.TM; a.TN = g.TN;
+  a.parts = g.parts; a.kc = (int)g.kc;
+  a.part = (float*)workspace; a.ldp = g.ldp;
+  (void)hipGetLastError();
+  flce::mark_launch(stream, nullptr);
+  return flce::launch_mx_linear(a, dtype, stream) == hipSuccess ? FLCE_OK : FLCE_ERR_HIP;
+}
+
+}  // extern "C"

@@ -13,7 +13,7 @@ from __future__ import annotations
 
 import contextlib
 import operator
-from typing import Optional, Tuple
+from typing import NamedTuple, Optional, Tuple, Union
 
 import torch
 from torch.autograd.function import once_differentiable
@@ -771,6 +771,242 @@ def _clip(grads, max_norm, norm_type, given, out):
     return norm
 
 
+def _format_code(format: str) -> int:
+    if format not in _lib.MX_FORMATS:
+        raise ValueError(f"format must be one of {tuple(_lib.MX_FORMATS)}")
+    return _lib.MX_FORMATS[format]
+
+
+class MXTensor(NamedTuple):
+    """A microscaled matrix: every 32 columns of a row share a scale 2^(s - 127).
+
+    codes: uint8 [R, C'] (e4m3) or [R, C' / 2] (e2m1, the even column in the low half), C' the columns rounded
+    up to 128 with zeros past them; scales: uint8 [R, C' / 32]; cols: the columns; format: "e4m3" or "e2m1"."""
+    codes: torch.Tensor
+    scales: torch.Tensor
+    cols: int
+    format: str
+
+    @property
+    def shape(self) -> Tuple[int, int]:
+        return self.codes.shape[0], self.cols
+
+
+def _mx_empty(rows: int, cols: int, format: str, dev) -> MXTensor:
+    padded = (cols + 127) // 128 * 128
+    codes = torch.empty(rows, padded // 2 if format == "e2m1" else padded, dtype=torch.uint8, device=dev)
+    return MXTensor(codes, torch.empty(rows, padded // 32, dtype=torch.uint8, device=dev), cols, format)
+
+
+def _prep_mx(q: MXTensor) -> MXTensor:
+    """q checked and dense."""
+    codes, scales, cols, format = q
+    _format_code(format)
+    if codes.dtype != torch.uint8 or scales.dtype != torch.uint8:
+        raise TypeError("codes and scales must be uint8")
+    if cols < 1:
+        raise ValueError("a microscaled matrix has at least one column")
+    padded = (cols + 127) // 128 * 128
+    want = padded // 2 if format == "e2m1" else padded
+    if codes.dim() != 2 or codes.shape[1] != want or scales.shape != (codes.shape[0], padded // 32):
+        raise ValueError(f"{cols} columns in {format} have codes [rows, {want}] and scales [rows, {padded // 32}]")
+    if not codes.is_cuda:
+        raise ValueError("tensors must live on a GPU")
+    if scales.device != codes.device:
+        raise ValueError("all tensors must be on one device")
+    return MXTensor(_dense(codes), _dense(scales), cols, format)
+
+
+def _prep_rows(x: torch.Tensor, rows=(), vectors=(), what: str = "x"):
+    """x [N, H], other tensors of its shape and vectors [H] (or None) of its type, checked and dense."""
+    if x.dim() != 2:
+        raise ValueError(f"{what} must be [N, H]")
+    if not x.is_cuda:
+        raise ValueError("tensors must live on a GPU")
+    if x.shape[1] < 1:
+        raise ValueError("H must be at least 1")
+    _dtype_code(x)
+
+    def dense(t, shape):
+        if t is None:
+            return None
+        if t.shape != shape:
+            raise ValueError(f"expected a tensor of shape {tuple(shape)}, not {tuple(t.shape)}")
+        if t.dtype != x.dtype:
+            raise TypeError(f"all tensors must share {what}'s dtype")
+        if t.device != x.device:
+            raise ValueError("all tensors must be on one device")
+        return _dense(t)
+
+    return _dense(x), [dense(t, x.shape) for t in rows], [dense(t, x.shape[1:]) for t in vectors]
+
+
+def flce_rms_norm_workspace_size(N: int, H: int, dtype: torch.dtype) -> int:
+    """Bytes of flce_rms_norm_backward with dweight."""
+    return _lib.flce_rms_norm_workspace_size(N, H, _DTYPES[dtype])
+
+
+def flce_rms_norm_forward(x: torch.Tensor, weight: Optional[torch.Tensor] = None,
+                          residual: Optional[torch.Tensor] = None, eps: float = 1e-6, keep: bool = False):
+    """y = h * (mean(h^2) + eps)^(-1/2) * weight over the rows of h = x + residual.  Returns (y, h, rstd): h is x
+    without a residual; rstd, float32 [N], what flce_rms_norm_backward takes, with keep, else None."""
+    x, (residual,), (weight,) = _prep_rows(x, (residual,), (weight,))
+    N, H = x.shape
+    dt, dev = _dtype_code(x), x.device
+    y = torch.empty_like(x)
+    h = torch.empty_like(x) if residual is not None else None
+    rstd = torch.empty(N, dtype=torch.float32, device=dev) if keep else None
+    with _on(dev):
+        _lib.flce_rms_norm_forward(x.data_ptr(), _ptr(residual), _ptr(weight), N, H, dt, float(eps), y.data_ptr(),
+                                   _ptr(h), _ptr(rstd), _raw_stream(dev.index))
+    return y, x if h is None else h, rstd
+
+
+def flce_rms_norm_mx_forward(x: torch.Tensor, weight: Optional[torch.Tensor] = None,
+                             residual: Optional[torch.Tensor] = None, eps: float = 1e-6, format: str = "e4m3"):
+    """flce_rms_norm_forward with y microscaled, from its float32 values.  Returns (y, h), y an MXTensor."""
+    code = _format_code(format)
+    x, (residual,), (weight,) = _prep_rows(x, (residual,), (weight,))
+    N, H = x.shape
+    dt, dev = _dtype_code(x), x.device
+    q = _mx_empty(N, H, format, dev)
+    h = torch.empty_like(x) if residual is not None else None
+    with _on(dev):
+        _lib.flce_rms_norm_mx_forward(x.data_ptr(), _ptr(residual), _ptr(weight), N, H, dt, float(eps), code,
+                                      q.codes.data_ptr(), q.scales.data_ptr(), _ptr(h), None, _raw_stream(dev.index))
+    return q, x if h is None else h
+
+
+def flce_rms_norm_backward(h: torch.Tensor, weight: Optional[torch.Tensor], rstd: torch.Tensor, dy: torch.Tensor,
+                           dh: Optional[torch.Tensor] = None, need_dx: bool = True, need_dweight: bool = True,
+                           workspace: Optional[torch.Tensor] = None):
+    """Returns (dx, dweight) in the input dtype (None where not requested); h and rstd as flce_rms_norm_forward
+    returned them, dh the gradient that reaches h past the norm.  dx is the residual's gradient too."""
+    h, (dy, dh), (weight,) = _prep_rows(h, (dy, dh), (weight,), "h")
+    N, H = h.shape
+    dt, dev = _dtype_code(h), h.device
+    if rstd is None or rstd.dtype != torch.float32 or rstd.shape != (N,) or rstd.device != dev:
+        raise ValueError(f"rstd must be a float32 [{N}] tensor on {dev} (as flce_rms_norm_forward returns it)")
+    rstd = rstd.contiguous()
+    dx = torch.empty_like(h) if need_dx else None
+    dweight = torch.empty(H, dtype=h.dtype, device=dev) if need_dweight else None
+    workspace = _workspace(workspace, _lib.flce_rms_norm_workspace_size(N, H, dt) if need_dweight else 0, dev)
+    with _on(dev):
+        _lib.flce_rms_norm_backward(h.data_ptr(), _ptr(weight), rstd.data_ptr(), dy.data_ptr(), _ptr(dh), N, H, dt,
+                                    _ptr(dx), _ptr(dweight), _ptr(workspace), _nbytes(workspace),
+                                    _raw_stream(dev.index))
+    return dx, dweight
+
+
+def flce_mx_quantize(x: torch.Tensor, format: str = "e2m1") -> MXTensor:
+    """x [R, C] microscaled: each 32 columns' scale from their largest magnitude, elements rounded to nearest even."""
+    code = _format_code(format)
+    x, _, _ = _prep_rows(x)
+    R, C = x.shape
+    dev = x.device
+    q = _mx_empty(R, C, format, dev)
+    with _on(dev):
+        _lib.flce_mx_quantize(x.data_ptr(), R, C, _dtype_code(x), code, q.codes.data_ptr(), q.scales.data_ptr(),
+                              _raw_stream(dev.index))
+    return q
+
+
+def flce_mx_dequantize(q: MXTensor, dtype: torch.dtype = torch.bfloat16) -> torch.Tensor:
+    """The values of a microscaled matrix, [R, C]; bfloat16 and float32 hold them exactly within their range."""
+    if dtype not in _DTYPES:
+        raise TypeError(f"unsupported dtype {dtype}; use bfloat16, float16 or float32")
+    q = _prep_mx(q)
+    dev = q.codes.device
+    y = torch.empty(q.shape, dtype=dtype, device=dev)
+    with _on(dev):
+        _lib.flce_mx_dequantize(q.codes.data_ptr(), q.scales.data_ptr(), *q.shape, _format_code(q.format),
+                                _DTYPES[dtype], y.data_ptr(), _raw_stream(dev.index))
+    return y
+
+
+def flce_mx_linear_workspace_size(N: int, K: int, F: int, x_format: str, dtype: torch.dtype) -> int:
+    """Bytes of flce_mx_linear."""
+    return _lib.flce_mx_linear_workspace_size(N, K, F, _format_code(x_format), _DTYPES[dtype])
+
+
+def flce_mx_linear(x: MXTensor, W: MXTensor, b: Optional[torch.Tensor] = None, residual: Optional[torch.Tensor] = None,
+                   activation: str = "none", dtype: torch.dtype = torch.bfloat16,
+                   workspace: Optional[torch.Tensor] = None, out: Optional[torch.Tensor] = None) -> torch.Tensor:
+    """act(x W^T + b) + residual in dtype, for microscaled x [N, K] of either format and W [F, K] in e2m1.
+    out: the tensor to write to; it may be residual, and may share memory with no other tensor of the call."""
+    act = _activation_code(activation)
+    if dtype not in _DTYPES:
+        raise TypeError(f"unsupported dtype {dtype}; use bfloat16, float16 or float32")
+    x, W = _prep_mx(x), _prep_mx(W)
+    if W.format != "e2m1":
+        raise ValueError("W must be in e2m1")
+    (N, K), F, dev = x.shape, W.shape[0], x.codes.device
+    if W.cols != K:
+        raise ValueError("x and W disagree on their columns")
+    if F < 1:
+        raise ValueError("W has no rows")
+    for t, shape in ((W.codes, None), (b, (F,)), (residual, (N, F)), (out, (N, F))):
+        if t is None:
+            continue
+        if t.device != dev:
+            raise ValueError("all tensors must be on one device")
+        if shape is not None and t.shape != shape:
+            raise ValueError(f"expected a tensor of shape {shape}, not {tuple(t.shape)}")
+        if shape is not None and t.dtype != dtype:
+            raise TypeError(f"b, residual and out must be {dtype}, as the result")
+    residual_ = _dense(residual)
+    if out is not None and (_dense(out) is not out or (residual_ is not residual and residual is out)):
+        raise ValueError("out must be contiguous from a 16-byte boundary")
+    b = None if b is None else b.contiguous()
+    y = out if out is not None else torch.empty(N, F, dtype=dtype, device=dev)
+    code, dt = _format_code(x.format), _DTYPES[dtype]
+    workspace = _workspace(workspace, _lib.flce_mx_linear_workspace_size(N, K, F, code, dt), dev)
+    with _on(dev):
+        _lib.flce_mx_linear(x.codes.data_ptr(), x.scales.data_ptr(), code, W.codes.data_ptr(), W.scales.data_ptr(),
+                            _ptr(b), _ptr(residual_), N, K, F, dt, act, y.data_ptr(), _ptr(workspace),
+                            _nbytes(workspace), _raw_stream(dev.index))
+    if out is not None:
+        _wrote(out)
+    return y
+
+
+def flce_sample(logits: torch.Tensor, u: torch.Tensor, temperature: Union[float, torch.Tensor, None] = None,
+                top_k: Union[int, torch.Tensor, None] = None, top_p: Union[float, torch.Tensor, None] = None,
+                min_p: Union[float, torch.Tensor, None] = None) -> torch.Tensor:
+    """A token of each row of logits [N, V] by u [N], float32 in [0, 1): int64 [N], -1 for a row with no token left
+    or with a NaN.  Parameters are one number for all rows, or a tensor of one per row (None: temperature 1, and
+    nothing cut off): the first top_k tokens by logit; of those, each whose predecessors' probabilities add up to
+    less than top_p; of those, the ones at least min_p times as likely as the first.  temperature 0 takes the
+    largest logit.  A masked token's logit is -infinity."""
+    if logits.dim() != 2 or logits.shape[1] < 1:
+        raise ValueError("logits must be [N, V], V at least 1")
+    if not logits.is_cuda:
+        raise ValueError("tensors must live on a GPU")
+    dt, dev, (N, V) = _dtype_code(logits), logits.device, logits.shape
+    logits = _dense(logits)
+    held = []   # the tensors whose addresses go into the call
+
+    def per_row(t, dtype, name):
+        if t.device != dev or t.shape != (N,) or t.dtype != dtype:
+            raise ValueError(f"{name} must be a {dtype} [{N}] tensor on {dev}")
+        held.append(t.contiguous())
+        return held[-1].data_ptr()
+
+    u_ptr = per_row(u, torch.float32, "u")
+    kw = {}
+    for name, value, dtype in (("temperature", temperature, torch.float32), ("top_k", top_k, torch.int64),
+                               ("top_p", top_p, torch.float32), ("min_p", min_p, torch.float32)):
+        if isinstance(value, torch.Tensor):
+            kw[name + "s"] = per_row(value, dtype, name)
+        elif value is not None:
+            kw[name] = value
+    tokens = torch.empty(N, dtype=torch.int64, device=dev)
+    with _on(dev):
+        _lib.flce_sample(logits.data_ptr(), u_ptr, N, V, dt, _lib.sampling(**kw), tokens.data_ptr(),
+                         _raw_stream(dev.index))
+    return tokens
+
+
 class FusedLinearCrossEntropyFunction(torch.autograd.Function):
     """loss = FLCE(x, target, weight, bias); saves only lse and the count."""
 
@@ -879,6 +1115,48 @@ class FusedGLUFunction(torch.autograd.Function):
         return dx, dWg, dWu, dbg if need[3] else None, dbu if need[4] else None, None, None
 
 
+class FusedRMSNormFunction(torch.autograd.Function):
+    """rms_norm(x) weight, or with a residual (rms_norm(h) weight, h = x + residual); keeps h and a float32 a row.
+    grad: as in FusedLinearFunction.
+
+    The tensors come in their own shapes and are flattened here: x and the residual share one gradient, and autograd
+    copies it for one of two leaves when it sees the same tensor twice, but not when views taken outside hide that."""
+
+    @staticmethod
+    def forward(ctx, x, weight=None, residual=None, eps=1e-6, grad=True):
+        H = x.shape[-1]
+        y, h, rstd = flce_rms_norm_forward(x.reshape(-1, H), weight, None if residual is None else residual.reshape(-1, H),
+                                           eps, keep=grad and any(ctx.needs_input_grad[:3]))
+        ctx.set_materialize_grads(False)
+        if residual is None:
+            ctx.save_for_backward(x, weight, rstd)
+            return y.view(x.shape)
+        h = h.view(x.shape)
+        ctx.save_for_backward(h, weight, rstd)
+        return y.view(x.shape), h
+
+    @staticmethod
+    @once_differentiable
+    def backward(ctx, dy, dh=None):
+        h, weight, rstd = ctx.saved_tensors
+        need = ctx.needs_input_grad
+        if dy is None:   # only h went on
+            dx, dw = dh, torch.zeros_like(weight) if need[1] else None
+        else:
+            H = h.shape[-1]
+            dx, dw = flce_rms_norm_backward(h.reshape(-1, H), weight, rstd, dy.reshape(-1, H),
+                                            None if dh is None else dh.reshape(-1, H), need[0] or need[2], need[1])
+            dx = None if dx is None else dx.view(h.shape)
+        return dx if need[0] else None, dw, dx if need[2] else None, None, None
+
+
+def fused_rms_norm(x, weight=None, residual=None, eps=1e-6):
+    """rms_norm(x) weight for x [..., H], or (rms_norm(x + residual) weight, x + residual); differentiable."""
+    if residual is not None and residual.shape != x.shape:
+        raise ValueError(f"residual must be {tuple(x.shape)}")
+    return FusedRMSNormFunction.apply(x, weight, residual, eps, torch.is_grad_enabled())
+
+
 def fused_linear(x, weight, bias=None, residual=None, activation="none"):
     """act(x weight^T + bias) + residual for x [..., H], residual [..., F]; differentiable."""
     lead, F = x.shape[:-1], weight.shape[0]
@@ -913,6 +1191,46 @@ class GatedFeedForward(torch.nn.Module):
         h = fused_glu(x, self.gate_proj.weight, self.up_proj.weight, self.gate_proj.bias, self.up_proj.bias,
                       self.activation)
         return fused_linear(h, self.down_proj.weight, self.down_proj.bias, residual)
+
+
+class RMSNorm(torch.nn.Module):
+    """Root-mean-square norm over the last dimension: norm(x), or norm(x, residual) for (y, x + residual)."""
+
+    def __init__(self, hidden: int, eps: float = 1e-6, device=None, dtype=None):
+        super().__init__()
+        self.eps = eps
+        self.weight = torch.nn.Parameter(torch.ones(hidden, device=device, dtype=dtype))
+
+    def forward(self, x, residual=None):
+        return fused_rms_norm(x, self.weight, residual, self.eps)
+
+
+class MXLinear(torch.nn.Module):
+    """A linear layer for inference with its weight in 4 bits, made from a torch.nn.Linear on a GPU.  x: [..., K],
+    quantised to x_format on the way in, or an MXTensor (as flce_rms_norm_mx_forward returns it)."""
+
+    def __init__(self, linear: torch.nn.Linear, activation: str = "none", x_format: str = "e4m3"):
+        super().__init__()
+        _activation_code(activation)
+        _format_code(x_format)
+        self.activation, self.x_format = activation, x_format
+        self.cols, self.dtype = linear.in_features, linear.weight.dtype
+        q = flce_mx_quantize(linear.weight.detach(), "e2m1")
+        self.register_buffer("codes", q.codes)
+        self.register_buffer("scales", q.scales)
+        self.register_buffer("bias", None if linear.bias is None else linear.bias.detach().clone())
+
+    @torch.no_grad()
+    def forward(self, x, residual=None):
+        lead = x.shape[:1] if isinstance(x, MXTensor) else x.shape[:-1]
+        q = x if isinstance(x, MXTensor) else flce_mx_quantize(x.reshape(-1, x.shape[-1]), self.x_format)
+        W = MXTensor(self.codes, self.scales, self.cols, "e2m1")
+        F = self.codes.shape[0]
+        if residual is not None:
+            if residual.shape != (*lead, F):
+                raise ValueError(f"residual must be {(*lead, F)}")
+            residual = residual.reshape(-1, F)
+        return flce_mx_linear(q, W, self.bias, residual, self.activation, self.dtype).reshape(*lead, F)
 
 
 def clip_grad_norm_(parameters, max_norm: float, norm_type: float = 2.0) -> torch.Tensor:
