@@ -540,6 +540,8 @@ flce_status flce_mx_dequantize(const uint8_t* codes, const uint8_t* scales, int6
  * With float32 results an e4m3 x meets W in bfloat16, which holds their values down to
  * 2^-126; smaller ones may count as 0.
  * A NaN scale makes the results of its row (of W: its feature) NaN.
+ * The environment variable FLCE_DEBUG_MX_TILE (2, 4 or 8; for tests) forces the size of the output tiles, and with it
+ * the workspace's.
  * flce_mx_linear_workspace_size: bytes for the call (fp32 partial sums of a product
  * split along K; often 0, and the workspace may then be NULL); pure host arithmetic.
  */

@@ -41,18 +41,28 @@ struct MxGeometry {
 
 constexpr int64_t kMxFew = 16;   // most tokens of the few-token kernel
 
-MxGeometry mx_geometry(int64_t N, int64_t K, int64_t F) {
+// The tests' override of the tile, or 0.
+int forced_mx_tile() {
+  const char* env = std::getenv("FLCE_DEBUG_MX_TILE");
+  const int s = env ? std::atoi(env) : 0;
+  return s == 2 || s == 4 || s == 8 ? s : 0;
+}
+
+MxGeometry mx_geometry(int64_t N, int64_t K, int64_t F, int format, int dtype) {
   MxGeometry g{};
   const int64_t Kp = mx_cols(K);
-  if (N <= kMxFew) {
+  const int forced = forced_mx_tile();
+  if (N <= kMxFew && !forced) {
     // enough waves for every CU, each with K of its own to walk
     g.parts = 1;
     while (g.parts < 8 && cdiv(F, 16) * g.parts < 8 * kCUs && Kp / 128 >= 2 * g.parts) g.parts *= 2;
     g.kc = Kp;
     return g;
   }
-  const int64_t big = cdiv(N, 128) * cdiv(F, 128);
-  g.tile = big >= 2 * kCUs ? 4 : 2;
+  // The 256-row tile moves scales in runs of 512 columns and has no float32 variant for an e4m3 x.
+  const bool big = Kp >= 512 && (dtype != FLCE_F32 || format == FLCE_MX_E2M1);
+  g.tile = big && cdiv(N, 256) * cdiv(F, 256) >= kCUs ? 8 : cdiv(N, 128) * cdiv(F, 128) >= 2 * kCUs ? 4 : 2;
+  if (forced) g.tile = forced == 8 && !big ? 4 : forced;
   const int64_t M = 32 * g.tile;
   g.TM = (int)cdiv(N, M);
   g.TN = (int)cdiv(F, M);
@@ -93,7 +103,7 @@ flce_status flce_mx_linear_workspace_size(int64_t N, int64_t K, int64_t F, flce_
                                           size_t* bytes) {
   const flce_status st = check_mx_linear(N, K, F, dtype, x_format, FLCE_ACT_NONE);
   if (st != FLCE_OK) return st;
-  if (bytes) *bytes = mx_geometry(N, K, F).total;
+  if (bytes) *bytes = mx_geometry(N, K, F, x_format, dtype).total;
   return FLCE_OK;
 }
 
@@ -108,7 +118,7 @@ flce_status flce_mx_linear(const uint8_t* x, const uint8_t* x_scales, flce_mx_fo
   if (bad_tensor(x, 16, rows) || bad_tensor(x_scales, 4, rows) || bad_tensor(W, 16, true) || bad_tensor(W_scales, 4, true) ||
       bad_tensor(b, es, false) || bad_tensor(residual, 16, false) || bad_tensor(y, 16, rows))
     return FLCE_ERR_INVALID_ARGUMENT;
-  const MxGeometry g = mx_geometry(N, K, F);
+  const MxGeometry g = mx_geometry(N, K, F, x_format, dtype);
   if (workspace_bytes < g.total) return FLCE_ERR_WORKSPACE_TOO_SMALL;
   if (bad_tensor(workspace, 16, g.total > 0)) return FLCE_ERR_INVALID_ARGUMENT;
   if (!rows) return FLCE_OK;

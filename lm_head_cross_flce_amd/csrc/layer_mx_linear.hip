@@ -13,7 +13,7 @@
 // and 2.1e-4); for float32 results an e4m3 x and W are expanded to bfloat16, which
 // holds every element and scale exactly, for the bf16 instruction with its float32
 // sums (EXACT below).
-#include "layer_mx_device.hpp"
+#include "layer_mx_tile.hpp"
 
 namespace flce {
 
@@ -125,7 +125,7 @@ template <int S, int FMT> struct MxLds {
 };
 
 // The epilogue of one lane's run of C features of token n (features f ..), sums z.
-template <class T, int C>
+template <class T, int C, bool ACT = true>
 __device__ __forceinline__ void mx_finish(const MxLinear& a, int64_t n, int f, const float (&bias)[C], float (&z)[C]) {
   const int64_t o = n * a.F + f;
   const int left = a.F - f;
@@ -133,7 +133,8 @@ __device__ __forceinline__ void mx_finish(const MxLinear& a, int64_t n, int f, c
   if (a.residual) load_some<T, C>((const T*)a.residual + o, left, r);
 #pragma unroll
   for (int e = 0; e < C; ++e) {
-    z[e] = act_fwd_rt<T>(a.act, z[e] + bias[e]);
+    z[e] += bias[e];
+    if (ACT) z[e] = act_fwd_rt<T>(a.act, z[e]);
     if (a.residual) z[e] += r[e];
   }
   store_some<T, C>((T*)a.y + o, left, z);
@@ -250,6 +251,118 @@ __global__ void __launch_bounds__(256) mx_linear_kernel(MxLinear a) {
     }
 }
 
+// 256 x 256 tiles, for large products (not for EXACT's types): workgroup w computes tiles w, w + grid, ...  The next
+// tile's first copies start before the epilogue, and its stores drain under the next tile.  VEC: every lane's run of 8
+// features is whole and aligned (F % 8 == 0).
+template <class T, int FMT, bool ACT, bool SPLIT, bool VEC>
+__global__ void __launch_bounds__(256, 1) mx_linear_big_kernel(MxLinear a) {
+  constexpr int XB = FMT == kMxE4M3 ? 2 : 1, ES = sizeof(T);
+  const int tid = threadIdx.x, lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6);
+  const int wm = wave >> 1, wn = wave & 1, g = lane >> 4, c = lane & 15;
+  const int tiles = a.TM * a.TN, total = tiles * a.parts;
+  MX_LDS(L);
+  MxCopies<FMT> cp;
+  int n0, f0, part;
+  auto begin = [&](int t) {
+    part = SPLIT ? t / tiles : 0;
+    int tm, tn;
+    tile_coords(t - part * tiles, tiles, a.TM, a.TN, tm, tn);
+    n0 = tm * 256;
+    f0 = tn * 256;
+    cp.k0 = part * a.kc;
+    cp.kext = min(a.kc, a.Kp - cp.k0);
+    cp.x.init(a.x + (int64_t)cp.k0 * XB / 2, (int64_t)a.Kp * XB / 2, a.N, n0, tid);
+    cp.w.init(a.W + cp.k0 / 2, a.Kp / 2, a.F, f0, tid);
+    cp.s.init(a.xs, a.N, n0, a.Ws, a.F, f0, a.Kp / kMxBlock, tid);
+    cp.begin(L);
+  };
+  int t = blockIdx.x;
+  begin(t);
+  __builtin_amdgcn_s_waitcnt(waitcnt_vm_lgkm0<0>());   // the tile's first wait allows for an epilogue's stores
+  Acc acc;
+  while (true) {
+    mx_tile_run<FMT, 32>(acc, cp, L, tid);
+    const int n0w = n0 + wm * 128, f = f0 + (wn * 16 + c) * 8, ld = SPLIT ? (int)a.ldp : a.F;
+    const int64_t base = ((int64_t)part * a.N + n0w) * ld;
+    float bias[8] = {};
+    if (!SPLIT && a.b) load_some<T, 8>((const T*)a.b + f, a.F - f, bias);
+    __builtin_amdgcn_sched_barrier(0);
+    // copies that ran past the last step's columns, and the bias
+    __builtin_amdgcn_s_waitcnt(waitcnt_vm_lgkm0<0>());
+    t += gridDim.x;
+    const bool more = t < total;
+    if (more) begin(t);
+    acc_drain();
+    if constexpr (VEC) {
+      // Value (i, r) of a lane is token n0w + 4 g + 16 i + r: the lane's byte offset plus the wave's, at most 128 rows.
+      const int lim = f < ld ? a.N - n0w - 4 * g : 0;
+      const uint32_t lane0 = (uint32_t)(4 * g * ld + f);
+      const __amdgpu_buffer_rsrc_t ry = SPLIT ? make_rsrc(a.part + base) : make_rsrc((const T*)a.y + base);
+      const __amdgpu_buffer_rsrc_t rr = make_rsrc((const T*)a.residual + base);
+      const bool res = !SPLIT && a.residual != nullptr;
+      unrolled<8>([&](auto block) {
+        constexpr int i = block.value;
+        constexpr int S = SPLIT ? 4 : ES;
+        float rs[4][8];
+        if (!SPLIT && res) {
+#pragma unroll
+          for (int r = 0; r < 4; ++r) {
+            const uint32_t o = 16 * i + r < lim ? lane0 * S : kOOB;
+            if constexpr (ES == 2) {
+              buf_load_vec<T, 8>(rr, o, (16 * i + r) * ld * S, rs[r]);
+            } else {
+#pragma unroll
+              for (int h = 0; h < 2; ++h) {
+                const f32x4 v = __builtin_bit_cast(
+                    f32x4, __builtin_amdgcn_raw_buffer_load_b128(rr, o + 16 * h, (16 * i + r) * ld * S, 0));
+#pragma unroll
+                for (int e = 0; e < 4; ++e) rs[r][4 * h + e] = v[e];
+              }
+            }
+          }
+        }
+        f32x4 z[8];
+#pragma unroll
+        for (int j = 0; j < 8; ++j) z[j] = acc_read4(acc[i][j]);
+#pragma unroll
+        for (int r = 0; r < 4; ++r) {
+          float v[8];
+#pragma unroll
+          for (int e = 0; e < 8; ++e) {
+            v[e] = z[e][r] + bias[e];
+            if (ACT) v[e] = act_fwd_rt<T>(a.act, v[e]);
+            if (!SPLIT && res) v[e] += rs[r][e];
+          }
+          const uint32_t o = 16 * i + r < lim ? lane0 * S : kOOB;
+          if constexpr (SPLIT) buf_store_vec<float, 8>(ry, o, (16 * i + r) * ld * S, v);
+          else buf_store_vec<T, 8>(ry, o, (16 * i + r) * ld * S, v);
+        }
+        __builtin_amdgcn_sched_barrier(0);
+      });
+    } else {
+      unrolled<8>([&](auto block) {
+        constexpr int i = block.value;
+        f32x4 z[8];
+#pragma unroll
+        for (int j = 0; j < 8; ++j) z[j] = acc_read4(acc[i][j]);
+#pragma unroll
+        for (int r = 0; r < 4; ++r) {
+          const int n = n0w + 16 * i + 4 * g + r;
+          if (n >= a.N) continue;
+          float v[8];
+#pragma unroll
+          for (int j = 0; j < 8; ++j) v[j] = z[j][r];
+          mx_finish<T, 8, ACT>(a, n, f, bias, v);
+        }
+        __builtin_amdgcn_sched_barrier(0);
+      });
+      // lanes past the row stored nothing
+      __builtin_amdgcn_s_waitcnt(waitcnt_vm_lgkm0<0>());
+    }
+    if (!more) break;
+  }
+}
+
 // The epilogue of a split product: thread i takes 8 features of a token.
 template <class T> __global__ void __launch_bounds__(256) mx_join_kernel(MxLinear a) {
   const int F8 = (a.F + 7) / 8;
@@ -362,12 +475,21 @@ template <class T, int FMT> static void mx_launch(const MxLinear& a, hipStream_t
     return;
   }
   const dim3 grid(a.TM * a.TN * a.parts), blk(256);
+  if constexpr (sizeof(T) == 2 || FMT == kMxE2M1) {
+    if (a.tile == 8) {
+      const dim3 persist(grid.x < kPersistGrid ? grid.x : kPersistGrid);
+      if (a.parts > 1) FLCE_LAUNCH((mx_linear_big_kernel<T, FMT, false, true, true>), persist, blk, 0, st, a);
+      else if (a.F % 8 != 0) FLCE_LAUNCH((mx_linear_big_kernel<T, FMT, true, false, false>), persist, blk, 0, st, a);
+      else if (a.act == kActNone) FLCE_LAUNCH((mx_linear_big_kernel<T, FMT, false, false, true>), persist, blk, 0, st, a);
+      else FLCE_LAUNCH((mx_linear_big_kernel<T, FMT, true, false, true>), persist, blk, 0, st, a);
+    }
+  }
   auto tiles = [&](auto s) {
     if (a.parts > 1) FLCE_LAUNCH((mx_linear_kernel<T, FMT, s.value, true>), grid, blk, 0, st, a);
     else FLCE_LAUNCH((mx_linear_kernel<T, FMT, s.value, false>), grid, blk, 0, st, a);
   };
   if (a.tile == 4) tiles(std::integral_constant<int, 4>{});
-  else tiles(std::integral_constant<int, 2>{});
+  else if (a.tile == 2) tiles(std::integral_constant<int, 2>{});
   if (a.parts > 1) {
     const int64_t blocks = ((int64_t)a.N * ((a.F + 7) / 8) + 255) / 256;
     FLCE_LAUNCH((mx_join_kernel<T>), dim3((unsigned)(blocks < 4096 ? blocks : 4096)), dim3(256), 0, st, a);

@@ -238,6 +238,26 @@ def test_linear_large_tiles(dtype, fmt):
     check(2100, 640, 4200, fmt, DT[dtype], "gelu", True, True)
 
 
+@pytest.mark.parametrize("tile", [2, 4, 8])
+@pytest.mark.parametrize("fmt", FORMATS)
+@pytest.mark.parametrize("dtype", list(DT))
+def test_every_tile(monkeypatch, dtype, fmt, tile):
+    # whole and partial tiles, K of every remainder by the tiles' steps and runs, K split or not, whole and ragged features
+    monkeypatch.setenv("FLCE_DEBUG_MX_TILE", str(tile))
+    for N, K, F in ((1, 512, 8), (300, 640, 700), (257, 1152, 264), (60, 1300, 513), (256, 1408, 256), (130, 1700, 96),
+                    (513, 2048, 320), (20, 2300, 40), (270, 4600, 260), (520, 5000, 1000)):
+        check(N, K, F, fmt, DT[dtype])
+        check(N, K, F, fmt, DT[dtype], "gelu", True, True, seed=11)
+
+
+@pytest.mark.parametrize("dtype", list(DT))
+def test_large_tiles_in_several_rounds(monkeypatch, dtype):
+    # more tiles of 256 x 256 than CUs: each workgroup's stores run on under its next tile
+    for fmt in FORMATS:
+        for F in (8200, 8193):
+            check(2300, 1024, F, fmt, DT[dtype], "none", False, F == 8200)
+
+
 @pytest.mark.parametrize("act", tuple(_lib.ACTIVATIONS))
 @pytest.mark.parametrize("N", [5, 40, 400])
 def test_every_activation(act, N):
