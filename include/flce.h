@@ -570,8 +570,11 @@ flce_status flce_mx_linear(const uint8_t* x, const uint8_t* x_scales, flce_mx_fo
  * other logit, and rows with a NaN, give -1.  If the largest logit is infinite, the
  * tokens that have it share the weight.  Each parameter is one number for all rows or,
  * where its pointer is not NULL, float32 (top_ks int64) [N] on the device.  Weights are
- * formed in fp64 and added exactly, as whole numbers, so results do not depend on any order.
+ * formed in fp64 (to 2^-45; under e^-45 of the largest they count as 0) and added in fp64 in a fixed order or, where
+ * tokens are ranked, exactly, as whole numbers: results do not depend on what else runs.
  * logits 16-byte aligned, tokens int64 [N].
+ * flce_sample_workspace_size: bytes for the call (0 up to 8192 tokens a row, and the workspace may then be NULL; else
+ * about 5 V / 8 a row); pure host arithmetic.
  */
 typedef struct flce_sampling {
   float temperature;
@@ -584,8 +587,11 @@ typedef struct flce_sampling {
   const float* min_ps;
 } flce_sampling;
 
+flce_status flce_sample_workspace_size(int64_t N, int64_t V, flce_dtype dtype, size_t* bytes);
+
 flce_status flce_sample(const void* logits, const float* u, int64_t N, int64_t V, flce_dtype dtype,
-                        const flce_sampling* params, int64_t* tokens, hipStream_t stream);
+                        const flce_sampling* params, int64_t* tokens, void* workspace, size_t workspace_bytes,
+                        hipStream_t stream);
 
 /*
  * Global gradient norm and clipping, over `count` tensors of any dtypes and

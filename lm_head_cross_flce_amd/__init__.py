@@ -22,7 +22,7 @@ def __getattr__(name):
                 "flce_glu_backward", "flce_grad_norm", "flce_clip_grad_norm", "flce_clip_grads_with_norm",
                 "flce_rms_norm_workspace_size", "flce_rms_norm_forward", "flce_rms_norm_mx_forward",
                 "flce_rms_norm_backward", "flce_mx_quantize", "flce_mx_dequantize", "flce_mx_linear_workspace_size",
-                "flce_mx_linear", "flce_sample", "MXTensor", "fused_rms_norm", "RMSNorm", "MXLinear"):
+                "flce_mx_linear", "flce_sample_workspace_size", "flce_sample", "MXTensor", "fused_rms_norm", "RMSNorm", "MXLinear"):
         from . import functional
         return getattr(functional, name)
     raise AttributeError(name)

@@ -45,7 +45,8 @@ EXPORTS = ("flce_workspace_size", "flce_forward", "flce_backward", "flce_forward
            "flce_glu_workspace_size", "flce_glu_forward", "flce_glu_backward",
            "flce_grad_norm_workspace_size", "flce_grad_norm", "flce_clip_grad_norm", "flce_clip_grads_with_norm",
            "flce_rms_norm_forward", "flce_rms_norm_mx_forward", "flce_rms_norm_workspace_size", "flce_rms_norm_backward",
-           "flce_mx_quantize", "flce_mx_dequantize", "flce_mx_linear_workspace_size", "flce_mx_linear", "flce_sample")
+           "flce_mx_quantize", "flce_mx_dequantize", "flce_mx_linear_workspace_size", "flce_mx_linear", "flce_sample_workspace_size",
+           "flce_sample")
 
 
 class FlceOptions(ctypes.Structure):
@@ -179,7 +180,9 @@ def load() -> ctypes.CDLL:
         lib.flce_mx_linear_workspace_size.restype = c_int
         lib.flce_mx_linear.argtypes = [vp, vp, c_int, vp, vp, vp, vp, i64, i64, i64, c_int, c_int, vp, vp, sz, vp]
         lib.flce_mx_linear.restype = c_int
-        lib.flce_sample.argtypes = [vp, vp, i64, i64, c_int, ctypes.POINTER(FlceSampling), vp, vp]
+        lib.flce_sample_workspace_size.argtypes = [i64, i64, c_int, psz]
+        lib.flce_sample_workspace_size.restype = c_int
+        lib.flce_sample.argtypes = [vp, vp, i64, i64, c_int, ctypes.POINTER(FlceSampling), vp, vp, sz, vp]
         lib.flce_sample.restype = c_int
         _lib = lib
         return lib
@@ -494,11 +497,17 @@ def sampling(temperature: float = 1.0, top_k: int = 0, top_p: float = 1.0, min_p
                         top_ks or None, top_ps or None, min_ps or None)
 
 
-def flce_sample(logits, u, N, V, dtype, params, tokens, stream) -> None:
+def flce_sample_workspace_size(N: int, V: int, dtype: int) -> int:
+    b = ctypes.c_size_t(0)
+    _check(load().flce_sample_workspace_size(N, V, dtype, ctypes.byref(b)), "flce_sample_workspace_size")
+    return b.value
+
+
+def flce_sample(logits, u, N, V, dtype, params, tokens, workspace, workspace_bytes, stream) -> None:
     """Raw call: every tensor argument is an integer device address (or 0/None); params from sampling()."""
     _check(load().flce_sample(logits or None, u or None, N, V, dtype,
-                              ctypes.byref(params) if params is not None else None, tokens or None, stream or None),
-           "flce_sample")
+                              ctypes.byref(params) if params is not None else None, tokens or None, workspace or None,
+                              workspace_bytes, stream or None), "flce_sample")
 
 
 def flce_timing_start(capacity: int) -> None:

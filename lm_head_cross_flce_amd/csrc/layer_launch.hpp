@@ -95,7 +95,17 @@ struct Sample {
   int64_t* tokens;         // [N]
   int64_t N;
   int V;
+  // Rows of more than kOneLaunchTokens: what a first launch finds of each row's slices and groups.
+  int slices, groups;      // slices 0: one launch does it all
+  uint32_t* group_top;     // [N][groups]: the largest of each kGroupTokens tokens, as value_key
+  uint32_t* slice_top;     // [N][slices], of each kSliceTokens
+  double* slice_sum;       // [N][slices]: sum of exp((z - largest) / T), for rows that need it
+  // Rows with top-p and without top-k: each slice's histogram of exp(z / T), kHistBins bins from slice_bin on.
+  int* slice_bin;          // [N][slices]
+  unsigned long long* hist;   // [N][slices][kHistBins]
+  int hist_shift;          // in whole numbers of 2^-hist_shift
 };
+constexpr int kGroupTokens = 32, kSliceTokens = 8192, kOneLaunchTokens = 8192, kHistBins = 512;
 
 FLCE_WEAK hipError_t launch_sample(const Sample& a, int dtype, hipStream_t st);
 

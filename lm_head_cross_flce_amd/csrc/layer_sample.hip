@@ -7,11 +7,23 @@
 //   token = the first in the vocabulary's order at which the kept w add up to more than u
 //   times their sum
 //
-// Weights are formed in double and added as whole numbers of 2^-s, s as large as
-// keeps a row's sum under 2^63 (46 at 128256 tokens): a whole sum does not depend on
-// its order, so atomics may form it, and every comparison with it is exact.  The
-// rounding, 2^-47 of the largest weight a token, is far under what a float32 u can
-// tell apart.
+// The logits are read once, by as many workgroups as they fill: each takes 8192 tokens
+// and leaves their largest, the largest of every 32, and, for rows that need it, the sum
+// of their w and, for top-p, its histogram.  Then one workgroup a row finds the tokens
+// that can be kept from the largest of each 32 alone: the k-th of those is not above the
+// k-th token, and if the tokens from some value on have p of the sum, no other is kept.
+// It reads these tokens' groups only, and ranks and draws among at most 4096 tokens in
+// LDS.  A nucleus of more tokens is found from the histograms (sample_nucleus); what
+// else keeps more goes through sample_whole, which reads the row several times.  Rows of
+// up to 8192 tokens take one launch: their workgroup finds the groups' largest itself.
+//
+// Weights are formed in double.  Where tokens are ranked, they are added as whole
+// numbers of 2^-s, s as large as keeps a row's sum under 2^62 (45 at 128256 tokens): such a
+// sum does not depend on its order, so atomics may form it, and every comparison with it
+// is exact.  Its rounding, 2^-46 of the largest weight a token, is far under what a float32
+// u can tell apart.
+#include <climits>
+
 #include "layer_device.hpp"
 #include "layer_launch.hpp"
 
@@ -19,21 +31,43 @@ namespace flce {
 
 typedef unsigned long long u64;
 
-// Order of the values as whole numbers; -0 is 0.  Every NaN is above +infinity or below -infinity.
+// Order of the values as whole numbers; -0 is 0.
 __device__ __forceinline__ uint32_t value_key(float v) {
   const uint32_t b = __float_as_uint(v + 0.f);
   return b ^ ((b >> 31) ? 0xffffffffu : 0x80000000u);
 }
 __device__ __forceinline__ float key_value(uint32_t k) { return __uint_as_float(k ^ ((k >> 31) ? 0x80000000u : 0xffffffffu)); }
-constexpr uint32_t kKeyInf = 0xff800000u, kKeyMinusInf = 0x007fffffu;
+constexpr uint32_t kKeyInf = 0xff800000u, kKeyMinusInf = 0x007fffffu, kKeyNan = 0xffffffffu;
 
-// A row's weights as whole numbers.
+// exp(y) for y <= 0, to 2^-45: Taylor's series of degree 11 in what is left of y by the
+// nearest multiple of log 2 (0.347^12 / 12! = 2^-47).  Under e^-45 it is 0: 2^30 tokens of
+// such a weight would not add 2^-34 of the largest.
+__device__ __forceinline__ double exp_negative(double y) {
+  const double n = rint(y * 1.4426950408889634), t = fma(n, -0.69314718055994531, y);
+  double p = 1.0 / 39916800;
+  p = fma(p, t, 1.0 / 3628800);
+  p = fma(p, t, 1.0 / 362880);
+  p = fma(p, t, 1.0 / 40320);
+  p = fma(p, t, 1.0 / 5040);
+  p = fma(p, t, 1.0 / 720);
+  p = fma(p, t, 1.0 / 120);
+  p = fma(p, t, 1.0 / 24);
+  p = fma(p, t, 1.0 / 6);
+  p = fma(p, t, 0.5);
+  p = fma(p, t, 1.0);
+  p = fma(p, t, 1.0);
+  return y < -45.0 ? 0.0 : __builtin_ldexp(p, (int)n);
+}
+
+__device__ __forceinline__ double exp_bin(int bins) { return exp_negative(0.125 * bins); }   // e^(bins / 8), bins <= 0
+
+// Weights relative to a value that is not below any.  unit: 2^s.
 struct Weigh {
   float top;
-  double inv_t, unit, min_w;   // unit: 2^s
+  double inv_t, unit, min_w;
   __device__ __forceinline__ double real(float z) const {
     // equal to the largest: 1, also where that is infinite; masked: 0, whatever T
-    return z == top ? 1.0 : z == -INFINITY || top == INFINITY ? 0.0 : exp(((double)z - (double)top) * inv_t);
+    return z == top ? 1.0 : z == -INFINITY || top == INFINITY ? 0.0 : exp_negative(((double)z - (double)top) * inv_t);
   }
   __device__ __forceinline__ u64 operator()(float z) const { return (u64)rint(real(z) * unit); }
   __device__ __forceinline__ u64 kept(float z) const {
@@ -42,42 +76,206 @@ struct Weigh {
   }
 };
 
-constexpr int kRowThreads = 1024, kRowWaves = kRowThreads / 64;
-constexpr int kBins = 2048, kUnits = 2048;   // the units of a row: runs of 512 tokens, or of more in long rows
+// A row's parameters.
+struct RowParams {
+  float T, p, min_p, u;
+  int64_t k;   // 0: off
+  __device__ __forceinline__ void load(const Sample& a, int64_t row) {
+    T = a.temperature ? a.temperature[row] : a.temperature0;
+    p = a.top_p ? a.top_p[row] : a.top_p0;
+    min_p = a.min_p ? a.min_p[row] : a.min_p0;
+    k = a.top_k ? a.top_k[row] : a.top_k0;
+    if (k <= 0 || k >= a.V) k = 0;
+    u = a.u[row];
+  }
+  __device__ __forceinline__ bool greedy() const { return !(T > 0.f); }
+  __device__ __forceinline__ bool needs_sum() const { return !greedy() && k == 0; }
+  // top-p over the whole row; a p that is not above 0 keeps the first token alone
+  __device__ __forceinline__ bool needs_histogram() const { return needs_sum() && p < 1.f && p > 0.f; }
+};
 
-__device__ __forceinline__ u64 wave_scan(u64 v, int lane) {
+// Histograms of w: bins of an eighth in z / T, so that all slices' bins fall together; a
+// slice keeps the kHistBins below its largest.  A bin holds whole numbers of 2^-s of
+// exp(z / T) over its value at the bin's lower edge.
+struct Bins {
+  double scale;   // bins of a unit of z
+  // Whether z / T is small enough for a largest logit z (to 2^-41).  Slices' own may be twice as far from 0, so one that
+  // has no histogram lies 4096 below any row's largest that has.
+  static __device__ __forceinline__ bool fits(float top, float T, double most) { return fabs((double)top / (double)T) < most; }
+  __device__ __forceinline__ double place(float z) const { return (double)z * scale; }
+  __device__ __forceinline__ int bin(float z) const { return z > -INFINITY ? (int)fmax(floor(place(z)), -1e9) : -1000000000; }
+  // the weight over that at its bin's lower edge, from 1 to e^(1/8)
+  __device__ __forceinline__ double over(float z) const {
+    const double x = place(z);
+    return exp_near((x - floor(x)) * 0.125);
+  }
+  // exp(t), 0 <= t < 1/8: Taylor's series of degree 9 (0.125^10 / 10! = 2^-51)
+  static __device__ __forceinline__ double exp_near(double t) {
+    double p = 1.0 / 362880;
+    p = fma(p, t, 1.0 / 40320);
+    p = fma(p, t, 1.0 / 5040);
+    p = fma(p, t, 1.0 / 720);
+    p = fma(p, t, 1.0 / 120);
+    p = fma(p, t, 1.0 / 24);
+    p = fma(p, t, 1.0 / 6);
+    p = fma(p, t, 0.5);
+    p = fma(p, t, 1.0);
+    return fma(p, t, 1.0);
+  }
+};
+
+template <class V, class F> __device__ __forceinline__ V wave_reduce(V v, F&& f) {
+#pragma unroll
+  for (int d = 1; d < 64; d *= 2) v = f(v, (V)__shfl_xor(v, d));
+  return v;
+}
+
+// ---------------------------------------------------------------------------
+// The pass over the logits
+// ---------------------------------------------------------------------------
+
+// Slice j of a row: 8192 tokens, 32 a thread in four runs of 8; four lanes hold a
+// group of 32 consecutive ones.
+template <class T> __global__ void __launch_bounds__(256) sample_slice_kernel(Sample a) {
+  __shared__ uint32_t red[4];
+  __shared__ double sums[4];
+  __shared__ u64 hist[kHistBins];
+  const int tid = threadIdx.x;
+  const int64_t row = blockIdx.x / a.slices;
+  const int j = (int)(blockIdx.x - row * a.slices), base = j * kSliceTokens;
+  const T* z = (const T*)a.logits + row * a.V + base;
+  RowParams r;
+  r.load(a, row);
+  const int left = a.V - base;
+  float v[4][8];
+  uint32_t top = 0;
+#pragma unroll
+  for (int c = 0; c < 4; ++c) {
+    const int at = c * 2048 + tid * 8;
+    load_some<T, 8>(z + at, left - at, v[c]);
+    uint32_t g = 0;
+#pragma unroll
+    for (int e = 0; e < 8; ++e)
+      if (at + e < left) g = max(g, v[c][e] != v[c][e] ? kKeyNan : value_key(v[c][e]));
+      else v[c][e] = -INFINITY;
+    g = max(g, (uint32_t)__shfl_xor((int)g, 1));
+    g = max(g, (uint32_t)__shfl_xor((int)g, 2));
+    if ((tid & 3) == 0 && at < left) a.group_top[row * a.groups + (base + at) / kGroupTokens] = g;
+    top = max(top, g);
+  }
+  top = wave_reduce(top, [](uint32_t x, uint32_t y) { return max(x, y); });
+  if ((tid & 63) == 0) red[tid >> 6] = top;
+  __syncthreads();
+  top = max(max(red[0], red[1]), max(red[2], red[3]));
+  if (tid == 0) a.slice_top[row * a.slices + j] = top;
+  if (!r.needs_sum()) return;
+  double s = 0.0;
+  const bool some = top <= kKeyInf && top > kKeyMinusInf;
+  if (r.needs_histogram()) {   // its bins' sum stands for the sum
+    int64_t at = row * a.slices + j;
+    const float zt = some ? key_value(top) : 0.f;
+    const bool fits = some && Bins::fits(zt, r.T, 8192.0);
+    const Bins b{8.0 / (double)r.T};
+    const int base_bin = fits ? b.bin(zt) - (kHistBins - 1) : INT_MIN;
+    if (tid == 0) a.slice_bin[at] = base_bin;
+    if (!fits) return;
+    for (int i = tid; i < kHistBins; i += 256) hist[i] = 0;
+    __syncthreads();
+    const double unit = (double)(1ull << a.hist_shift);
+#pragma unroll
+    for (int c = 0; c < 4; ++c)
+#pragma unroll
+      for (int e = 0; e < 8; ++e) {
+        const int i = b.bin(v[c][e]) - base_bin;
+        if (i >= 0) atomicAdd(&hist[i], (u64)rint(b.over(v[c][e]) * unit));
+      }
+    __syncthreads();
+    for (int i = tid; i < kHistBins; i += 256) a.hist[at * kHistBins + i] = hist[i];
+    return;
+  }
+  if (some) {
+    const Weigh w{key_value(top), 1.0 / (double)r.T, 1.0, 0.0};
+#pragma unroll
+    for (int c = 0; c < 4; ++c)
+#pragma unroll
+      for (int e = 0; e < 8; ++e) s += w.real(v[c][e]);
+  }
+  s = wave_reduce(s, [](double x, double y) { return x + y; });
+  if ((tid & 63) == 0) sums[tid >> 6] = s;
+  __syncthreads();
+  if (tid == 0) a.slice_sum[row * a.slices + j] = (sums[0] + sums[1]) + (sums[2] + sums[3]);
+}
+
+// ---------------------------------------------------------------------------
+// One workgroup a row
+// ---------------------------------------------------------------------------
+
+constexpr int kRowThreads = 1024, kRowWaves = kRowThreads / 64;
+constexpr int kBins = 2048, kMost = 4096, kGroups = 8192;
+constexpr int kNucleusMost = 8192, kMaxSlices = 1024;
+constexpr int kUnits = 2048;   // sample_whole: runs of 512 tokens, or of more in long rows
+
+template <class V> __device__ __forceinline__ V wave_scan(V v, int lane) {
 #pragma unroll
   for (int d = 1; d < 64; d *= 2) {
-    const u64 t = __shfl_up(v, d);
+    const V t = __shfl_up(v, d);
     if (lane >= d) v += t;
   }
   return v;
 }
 
 struct RowLds {
-  u64 hist[kBins];
   u64 wave[kRowWaves];
-  u64 mass[kUnits];
-  uint32_t same[kUnits];
-  u64 found_above;
+  u64 found_above, carried;
   uint32_t found, key[kRowWaves];
+  int count;
+  u64 hist[kBins];
+  union {
+    struct {
+      uint32_t group[kGroups];      // largest key of each group; then the groups that pass, in order
+      uint32_t key[kMost], index[kMost];
+      u64 weight[kMost];
+    } list;
+    struct {
+      uint32_t key[kNucleusMost], index[kNucleusMost];
+      double slice[kMaxSlices];
+      u64 extra[kMaxSlices];
+      uint32_t equal[kMaxSlices];
+      int base[kMaxSlices];
+    } nucleus;
+    struct {
+      u64 mass[kUnits];
+      uint32_t same[kUnits];
+    } whole;
+  };
 };
 
-// Sum of v over threads before this one, and over all of them.
-__device__ __forceinline__ u64 block_scan(u64 v, u64& all, RowLds& L) {
+// Sum of v (8 bytes) over threads before this one, and over all of them.
+template <class V> __device__ __forceinline__ V block_scan(V v, V& all, RowLds& L) {
   const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
-  const u64 in = wave_scan(v, lane);
+  const V in = wave_scan(v, lane);
   __syncthreads();
-  if (lane == 63) L.wave[wave] = in;
+  if (lane == 63) L.wave[wave] = __builtin_bit_cast(u64, in);
   __syncthreads();
-  u64 before = in - v;
+  V before = 0;
   all = 0;
 #pragma unroll
   for (int w = 0; w < kRowWaves; ++w) {
-    if (w < wave) before += L.wave[w];
-    all += L.wave[w];
+    const V x = __builtin_bit_cast(V, L.wave[w]);
+    if (w < wave) before += x;
+    all += x;
   }
-  return before;
+  return before + (in - v);
+}
+// The largest of v over all threads.
+__device__ __forceinline__ uint32_t block_max(uint32_t v, RowLds& L) {
+  v = wave_reduce(v, [](uint32_t x, uint32_t y) { return max(x, y); });
+  __syncthreads();
+  if ((threadIdx.x & 63) == 0) L.key[threadIdx.x >> 6] = v;
+  __syncthreads();
+#pragma unroll
+  for (int w = 0; w < kRowWaves; ++w) v = max(v, L.key[w]);
+  return v;
 }
 
 // The bin, from the last one down, in which the sum of the bins passes `want` (from 1
@@ -97,7 +295,49 @@ __device__ __forceinline__ uint32_t find_bin(u64 want, u64& above, RowLds& L) {
   return L.found;
 }
 
-// f(value, index) over the row's tokens from first to last, 8 a lane at a time, by all threads.
+// The key at which, from the largest down, the sum of the weights reaches want (from 1 to
+// their whole sum), and the sum above that key.  each(f) calls f(key, weight) for every
+// element, among all threads; keys lie in [lo, hi].  Each level splits the keys' range
+// into 2048 bins.
+template <class F> __device__ __forceinline__ uint32_t find_key(uint32_t lo, uint32_t hi, u64 want, u64& above, F&& each, RowLds& L) {
+  above = 0;
+#pragma unroll 1
+  while (true) {
+    const int bits = hi > lo ? 32 - __clz((int)(hi - lo)) : 0, shift = bits > 11 ? bits - 11 : 0;
+    __syncthreads();
+    for (int i = threadIdx.x; i < kBins; i += kRowThreads) L.hist[i] = 0;
+    __syncthreads();
+    each([&](uint32_t k, u64 w) {
+      if (k >= lo && k <= hi && w) atomicAdd(&L.hist[(k - lo) >> shift], w);
+    });
+    __syncthreads();
+    u64 a;
+    const uint32_t bin = find_bin(want - above, a, L);
+    above += a;
+    lo += bin << shift;
+    if (shift == 0) return lo;
+    hi = min(hi, lo + ((1u << shift) - 1));
+  }
+}
+
+// What of `ties` equal tokens of weight `each` top-p keeps: the sum before them is above,
+// and those whose predecessors' sum is under want stay (at least one does).
+__device__ __forceinline__ u64 ties_needed(u64 want, u64 above, u64 each) { return (want - above + each - 1) / each; }
+
+// top-p's sum that predecessors have to stay under, a whole number: at least 1, or 0 if only the
+// first token is kept.
+__device__ __forceinline__ u64 nucleus(float p, double all) {
+  const double want = p > 0.f ? ceil((double)p * all) : 0.0;
+  return want < 1.0 ? 0 : (u64)want;
+}
+
+// Which of the kept weights' sum the draw has to pass: u times it, under it.
+__device__ __forceinline__ u64 spot(float u, u64 all) {
+  const double s = u > 0.f ? floor((double)u * (double)all) : 0.0;
+  return s < (double)all ? min((u64)s, all - 1) : all - 1;
+}
+
+// f(value, index) over the row's tokens, 8 a lane at a time, by all threads.
 template <class T, class F> __device__ __forceinline__ void each_token(const T* z, int V, F&& f) {
   for (int j = threadIdx.x * 8; j < V; j += kRowThreads * 8) {
     float v[8];
@@ -108,95 +348,44 @@ template <class T, class F> __device__ __forceinline__ void each_token(const T* 
   }
 }
 
-// The key at which, from the largest down, the sum of `count(value)` reaches want, and the
-// sum above that key.  skip: values whose key is below it count nothing; at it, `at_skip` in all.
-template <class T, class F>
-__device__ __forceinline__ uint32_t find_key(const T* z, int V, u64 want, u64& above, uint32_t skip, u64 at_skip, F&& count,
-                                             RowLds& L) {
-  constexpr int kLevels = sizeof(T) == 2 ? 2 : 3;   // 16-bit values' keys have their lowest 16 bits alike
-  uint32_t prefix = 0;
-  above = 0;
-#pragma unroll 1
-  for (int level = 0; level < kLevels; ++level) {
-    const int shift = level == 0 ? 21 : level == 1 ? 10 : 0, bits = level == 2 ? 10 : 11;
-    __syncthreads();
-    for (int i = threadIdx.x; i < kBins; i += kRowThreads) L.hist[i] = 0;
-    __syncthreads();
-    each_token(z, V, [&](float v, int) {
-      const uint32_t k = value_key(v);
-      if (k <= skip || (level > 0 && (k >> (shift + bits)) != prefix)) return;
-      atomicAdd(&L.hist[(k >> shift) & ((1u << bits) - 1)], count(v));
-    });
-    if (threadIdx.x == 0 && at_skip && (level == 0 || (skip >> (shift + bits)) == prefix))
-      atomicAdd(&L.hist[(skip >> shift) & ((1u << bits) - 1)], at_skip);
-    __syncthreads();
-    u64 a;
-    const uint32_t bin = find_bin(want - above, a, L);
-    above += a;
-    prefix = (prefix << bits) | bin;
-  }
-  // a 16-bit value's key ends in 10 bits of 0 or 1, as its sign bit has it
-  return sizeof(T) == 2 ? (prefix << 10) | ((prefix >> 21) ? 0u : 0x3ffu) : prefix;
-}
-
-// One row a workgroup, read from memory in every pass.
-template <class T> __global__ void __launch_bounds__(kRowThreads) sample_kernel(Sample a) {
-  __shared__ RowLds L;
-  const int64_t row = blockIdx.x;
+// A row with any number of tokens to keep, read from memory in every pass.
+template <class T>
+__device__ __forceinline__ void sample_whole(const Sample& a, int64_t row, const RowParams& r, const Weigh& w, uint32_t top, RowLds& L) {
   const T* z = (const T*)a.logits + row * a.V;
   const int V = a.V, tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
-  // the largest key; a NaN of either sign stands above all
-  uint32_t top = 0;
-  each_token(z, V, [&](float v, int) { top = max(top, v != v ? 0xffffffffu : value_key(v)); });
-#pragma unroll
-  for (int d = 1; d < 64; d *= 2) top = max(top, (uint32_t)__shfl_xor((int)top, d));
-  if (lane == 0) L.key[wave] = top;
-  __syncthreads();
-  for (int w = 0; w < kRowWaves; ++w) top = max(top, L.key[w]);
-  if (top > kKeyInf || top <= kKeyMinusInf) {   // a NaN, or no token left
-    if (tid == 0) a.tokens[row] = -1;
-    return;
-  }
-  const float T0 = a.temperature ? a.temperature[row] : a.temperature0;
-  const int64_t k = a.top_k ? a.top_k[row] : a.top_k0;
-  const float p = a.top_p ? a.top_p[row] : a.top_p0, mp = a.min_p ? a.min_p[row] : a.min_p0, u = a.u[row];
-  const bool greedy = !(T0 > 0.f);
-  const int s = 62 - (V > 2 ? 32 - __clz(V - 1) : 1);   // V 2^s <= 2^62
-  const Weigh w{key_value(top), greedy ? 0.0 : 1.0 / (double)T0, (double)(1ull << s), mp > 0.f ? (double)fminf(mp, 1.f) : 0.0};
-
   // Tokens above key `cut` are kept and the first `ties` at it.
   uint32_t cut = 0;
   u64 ties = 0;
-  if (greedy) {
-    cut = top;
-    ties = 1;
-  } else {
-    if (k > 0 && k < V) {
+  if (r.k) {
+    u64 above;
+    cut = find_key(kKeyMinusInf, top, (u64)r.k, above, [&](auto&& f) { each_token(z, V, [&](float v, int) { f(value_key(v), 1ull); }); }, L);
+    ties = (u64)r.k - above;
+  }
+  if (r.p < 1.f) {
+    u64 sum = 0, all;
+    each_token(z, V, [&](float v, int) { sum += value_key(v) > cut ? w(v) : 0; });
+    block_scan(sum, all, L);
+    const u64 at_cut = cut ? ties * w(key_value(cut)) : 0;
+    all += at_cut;
+    const u64 want = min(nucleus(r.p, (double)all), all);
+    if (want == 0) {
+      cut = top;
+      ties = 1;
+    } else {
       u64 above;
-      cut = find_key(z, V, (u64)k, above, 0u, 0ull, [](float) { return 1ull; }, L);
-      ties = (u64)k - above;
-    }
-    if (p < 1.f) {
-      u64 sum = 0, all;
-      each_token(z, V, [&](float v, int) { sum += value_key(v) > cut ? w(v) : 0; });
-      block_scan(sum, all, L);
-      const u64 at_cut = cut ? ties * w(key_value(cut)) : 0;
-      all += at_cut;
-      const double want = p > 0.f ? ceil((double)p * (double)all) : 0.0;
-      if (want < 1.0) {
-        cut = top;
-        ties = 1;
-      } else {
-        u64 above;
-        const u64 target = min((u64)want, all);
-        const uint32_t c = find_key(z, V, target, above, cut, at_cut, w, L);
-        const u64 each = w(key_value(c));
-        const u64 need = (target - above + each - 1) / each;
-        ties = c == cut ? min(ties, need) : need;
-        cut = c;
-      }
+      const uint32_t was = cut;
+      cut = find_key(max(cut, kKeyMinusInf), top, want, above, [&](auto&& f) {
+        each_token(z, V, [&](float v, int) {
+          const uint32_t k = value_key(v);
+          if (k > was) f(k, w(v));
+        });
+        if (tid == 0 && at_cut) f(was, at_cut);
+      }, L);
+      const u64 need = ties_needed(want, above, w(key_value(cut)));
+      ties = cut == was ? min(ties, need) : need;
     }
   }
+  __syncthreads();
 
   // Kept weight and tokens at the cut of each unit.
   const int unit = 512 * ((V + 512 * kUnits - 1) / (512 * kUnits)), units = (V + unit - 1) / unit;
@@ -214,41 +403,36 @@ template <class T> __global__ void __launch_bounds__(kRowThreads) sample_kernel(
         same += key == cut;
       }
     }
-#pragma unroll
-    for (int d = 1; d < 64; d *= 2) {
-      m += __shfl_xor(m, d);
-      same += __shfl_xor(same, d);
-    }
+    m = wave_reduce(m, [](u64 x, u64 y) { return x + y; });
+    same = wave_reduce(same, [](uint32_t x, uint32_t y) { return x + y; });
     if (lane == 0) {
-      L.mass[i] = m;
-      L.same[i] = same;
+      L.whole.mass[i] = m;
+      L.whole.same[i] = same;
     }
   }
   __syncthreads();
-  const u64 each = cut ? (greedy ? 1 : w.kept(key_value(cut))) : 0;
+  const u64 each = cut ? w.kept(key_value(cut)) : 0;
   // Each thread two units: their kept weight with the ties that the units before leave them.
   u64 m[2] = {0, 0}, n[2] = {0, 0}, all;
 #pragma unroll
   for (int h = 0; h < 2; ++h)
-    if (2 * tid + h < units) n[h] = L.same[2 * tid + h];
+    if (2 * tid + h < units) n[h] = L.whole.same[2 * tid + h];
   u64 before = block_scan(n[0] + n[1], all, L);
   u64 used[2];
 #pragma unroll
   for (int h = 0; h < 2; ++h) {
     used[h] = min(before, ties);
-    const u64 take = min(n[h], ties - used[h]);
-    if (2 * tid + h < units) m[h] = L.mass[2 * tid + h] + take * each;
+    if (2 * tid + h < units) m[h] = L.whole.mass[2 * tid + h] + min(n[h], ties - used[h]) * each;
     before += n[h];
   }
   before = block_scan(m[0] + m[1], all, L);
-  const double spot = u > 0.f ? floor((double)u * (double)all) : 0.0;
-  const u64 want = spot < (double)all ? min((u64)spot, all - 1) : all - 1;
+  const u64 want = spot(r.u, all);
 #pragma unroll
   for (int h = 0; h < 2; ++h) {
     if (before <= want && want < before + m[h]) {
       L.found = 2 * tid + h;
       L.found_above = before;
-      L.mass[0] = used[h];
+      L.carried = used[h];
     }
     before += m[h];
   }
@@ -256,7 +440,7 @@ template <class T> __global__ void __launch_bounds__(kRowThreads) sample_kernel(
   // The first wave walks the unit, 512 tokens at a time.
   if (wave > 0) return;
   const int i = L.found;
-  u64 done = L.found_above, taken = L.mass[0];
+  u64 done = L.found_above, taken = L.carried;
   for (int j0 = i * unit; j0 < min(V, (i + 1) * unit); j0 += 512) {
     const int j = j0 + lane * 8;
     float v[8];
@@ -290,12 +474,542 @@ template <class T> __global__ void __launch_bounds__(kRowThreads) sample_kernel(
   }
 }
 
-hipError_t launch_sample(const Sample& a, int dtype, hipStream_t st) {
-  const dim3 grid((unsigned)a.N), blk(kRowThreads);
-  if (dtype == 1) FLCE_LAUNCH((sample_kernel<uint16_t>), grid, blk, 0, st, a);
-  else if (dtype == 2) FLCE_LAUNCH((sample_kernel<_Float16>), grid, blk, 0, st, a);
-  else FLCE_LAUNCH((sample_kernel<float>), grid, blk, 0, st, a);
+// A row that nothing is cut off from: the slice in which u times the whole sum lies, then the token in it.  The
+// sums are doubles in a fixed order; where their rounding leaves the spot past a slice's last token, that is taken.
+template <class T>
+__device__ __forceinline__ void sample_slices(const Sample& a, int64_t row, const RowParams& r, const Weigh& w, RowLds& L) {
+  const T* z = (const T*)a.logits + row * a.V;
+  const int tid = threadIdx.x;
+  // thread t takes slices per t .. per (t + 1) - 1
+  const int per = (a.slices + kRowThreads - 1) / kRowThreads;
+  auto mass = [&](int j) {
+    const uint32_t top = a.slice_top[row * a.slices + j];
+    return top <= kKeyMinusInf ? 0.0 : a.slice_sum[row * a.slices + j] * w.real(key_value(top));
+  };
+  double own = 0.0, all;
+  for (int j = tid * per; j < min(a.slices, (tid + 1) * per); ++j) own += mass(j);
+  double before = block_scan(own, all, L);
+  const double u = r.u > 0.f ? (double)r.u : 0.0, want = u * all;
+  // the last slice with any weight, should the spot lie past all
+  uint32_t last = 0;
+  double b = before;
+  for (int j = tid * per; j < min(a.slices, (tid + 1) * per); ++j) {
+    const double m = mass(j);
+    if (m > 0.0) last = j + 1;
+    b += m;
+  }
+  last = block_max(last, L);
+  if (tid == 0) L.found = 0;
+  __syncthreads();
+  // the first slice at whose end the sum is past the spot
+  b = before;
+  for (int j = tid * per; j < min(a.slices, (tid + 1) * per); ++j) {
+    const double m = mass(j);
+    if (m > 0.0 && b + m > want) {
+      atomicMax(&L.found, 0x80000000u - (uint32_t)j);
+      break;
+    }
+    b += m;
+  }
+  __syncthreads();
+  const bool past = L.found == 0;
+  const int j = past ? (int)last - 1 : (int)(0x80000000u - L.found);
+  // what the slices before it add up to, as its thread had it
+  __syncthreads();
+  if (tid == j / per) {
+    double s = before;
+    for (int i = tid * per; i < j; ++i) s += mass(i);
+    L.found_above = __builtin_bit_cast(u64, s);
+  }
+  __syncthreads();
+  const double rest = past ? INFINITY : want - __builtin_bit_cast(double, L.found_above);
+  // 8 tokens a thread
+  const int at = j * kSliceTokens + tid * 8;
+  float v[8];
+  load_some<T, 8>(z + at, a.V - at, v);
+  double q[8], sum = 0.0;
+#pragma unroll
+  for (int e = 0; e < 8; ++e) {
+    q[e] = at + e < a.V ? w.real(v[e]) : 0.0;
+    sum += q[e];
+  }
+  double whole;
+  double cum = block_scan(sum, whole, L);
+  uint32_t first = 0, end = 0;   // as 2^31 less the index, and the index + 1
+#pragma unroll
+  for (int e = 0; e < 8; ++e) {
+    cum += q[e];
+    if (q[e] > 0.0) {
+      end = at + e + 1;
+      if (cum > rest && first == 0) first = 0x80000000u - (uint32_t)(at + e);
+    }
+  }
+  first = block_max(first, L);
+  end = block_max(end, L);
+  if (tid == 0) a.tokens[row] = first ? (int64_t)(0x80000000u - first) : (int64_t)end - 1;
+}
+
+// The row's sum of w over that of its largest token, from its slices' histograms; false if z / T is too large for them.
+__device__ __forceinline__ bool sum_of_histograms(const Sample& a, int64_t row, const RowParams& r, uint32_t top, double& sum, RowLds& L) {
+  const float zt = key_value(top);
+  if (!Bins::fits(zt, r.T, 4096.0)) return false;
+  const Bins b{8.0 / (double)r.T};
+  const int top_bin = b.bin(zt);
+  double own = 0.0;
+  for (int64_t i = threadIdx.x; i < (int64_t)a.slices * kHistBins; i += kRowThreads) {
+    const int base = a.slice_bin[row * a.slices + i / kHistBins];
+    if (base == INT_MIN) continue;   // nothing there, or only what is far under the top
+    own += (double)a.hist[row * a.slices * kHistBins + i] * exp_bin(base + (int)(i % kHistBins) - top_bin);
+  }
+  block_scan(own, sum, L);
+  sum /= b.over(zt) * (double)(1ull << a.hist_shift);
+  return true;
+}
+
+// top-p (and min-p) over a row whose nucleus has more tokens than the list holds.  The histograms give the bin in which
+// the nucleus ends; its tokens are listed and ranked; and the slice that the draw falls into is read once more.  False:
+// the bin has too many tokens for the list, or the row too many slices.
+template <class T>
+__device__ __forceinline__ bool sample_nucleus(const Sample& a, int64_t row, const RowParams& r, const Weigh& w, RowLds& L) {
+  const T* z = (const T*)a.logits + row * a.V;
+  const int V = a.V, tid = threadIdx.x, lane = tid & 63, wave = tid >> 6, J = a.slices;
+  if (J > kMaxSlices) return false;
+  const Bins b{8.0 / (double)r.T};
+  const int top_bin = b.bin(w.top);
+  const double unit = (double)(1ull << a.hist_shift);
+  const u64* H = a.hist + row * J * kHistBins;
+  // Bin top_bin - i of all slices, in doubles (whole numbers of at most 2^62), weighted relative to top_bin's lower edge: bins
+  // of thread t < kHistBins are its own.
+  __syncthreads();
+  if (tid < J) L.nucleus.base[tid] = a.slice_bin[row * J + tid];
+  __syncthreads();
+  u64 count = 0;
+  if (tid < kHistBins)
+    for (int j = 0; j < J; ++j) {
+      const int i = top_bin - tid - L.nucleus.base[j];
+      if (L.nucleus.base[j] != INT_MIN && i >= 0 && i < kHistBins) count += H[(int64_t)j * kHistBins + i];
+    }
+  const double mass = (double)count * exp_bin(-tid);
+  double all;
+  const double before = block_scan(mass, all, L);
+  const double need = (double)r.p * all;
+  if (tid == 0) L.found = kHistBins;
+  __syncthreads();
+  if (count && before < need && before + mass >= need) {
+    L.found = tid;
+    L.found_above = __builtin_bit_cast(u64, before);
+  }
+  __syncthreads();
+  int last = L.found;
+  if (last == kHistBins) return false;   // the sums' rounding
+  double rest = need - __builtin_bit_cast(double, L.found_above);   // of the bin, by its lower edge relative to top_bin's
+  // min-p may end higher up: then it alone cuts the bin in which it does
+  bool ranked = true;
+  if (w.min_w > 0.0) {
+    const double x = b.place(w.top) + 8.0 * log(w.min_w), f = floor(x);
+    if (x - f < 1e-6 || x - f > 1.0 - 1e-6) return false;   // an edge that rounding could move
+    if (top_bin - (int)f < last) {
+      last = top_bin - (int)f;
+      ranked = false;
+    }
+  }
+  const int edge = top_bin - last;   // the bin itself
+
+  // Its tokens, in order: each wave a stretch of the row, counted first and then written.
+  const int share = (V + 64 * kRowWaves - 1) / (64 * kRowWaves) * 64, j0 = wave * share, j1 = min(V, j0 + share);
+  const float lo = (float)(((double)edge - 0.01) / b.scale), hi = (float)(((double)edge + 1.01) / b.scale);   // around it
+  auto tokens = [&](auto&& f) {
+    for (int j = j0; j < j1; j += 64) {
+      const float v = j + lane < j1 ? load1<T>(z + j + lane) : -INFINITY;
+      const bool in = v >= lo && v <= hi && b.bin(v) == edge;
+      f(__ballot(in), in, v, j + lane);
+    }
+  };
+  u64 n = 0, total;
+  tokens([&](u64 hit, bool, float, int) { n += __popcll(hit); });
+  u64 first = block_scan(lane == 0 ? n : 0ull, total, L);
+  uint32_t start = (uint32_t)__shfl(first, 0);
+  if (total > kNucleusMost) return false;
+  tokens([&](u64 hit, bool in, float v, int j) {
+    if (in) {
+      const uint32_t i = start + (uint32_t)__popcll(hit & ((1ull << lane) - 1));
+      L.nucleus.key[i] = value_key(v);
+      L.nucleus.index[i] = j;
+    }
+    start += (uint32_t)__popcll(hit);
+  });
+  __syncthreads();
+  const int listed = (int)total;
+  auto weight = [&](uint32_t key) { return (u64)rint(b.over(key_value(key)) * unit); };
+  uint32_t cut = 0;
+  u64 ties = 0;
+  if (ranked && listed > 0) {
+    u64 own = 0, sum;
+    uint32_t most = 0, least = 0;
+    for (int i = tid; i < listed; i += kRowThreads) {
+      own += weight(L.nucleus.key[i]);
+      most = max(most, L.nucleus.key[i]);
+      least = max(least, ~L.nucleus.key[i]);
+    }
+    block_scan(own, sum, L);
+    most = block_max(most, L);
+    least = ~block_max(least, L);
+    const double want_real = ceil(rest / exp_bin(-last));
+    const u64 want = min(want_real < 1.0 ? 1ull : (u64)want_real, sum);
+    u64 above;
+    cut = find_key(least, most, want, above, [&](auto&& f) {
+      for (int i = tid; i < listed; i += kRowThreads) f(L.nucleus.key[i], weight(L.nucleus.key[i]));
+    }, L);
+    ties = ties_needed(want, above, weight(cut));
+  }
+  auto passes = [&](uint32_t key) { return w.min_w == 0.0 || w.real(key_value(key)) >= w.min_w; };
+
+  // Kept mass of each slice: its bins above, and the listed tokens that stay.
+  __syncthreads();
+  if (tid < J) {
+    L.nucleus.extra[tid] = 0;
+    L.nucleus.equal[tid] = 0;
+  }
+  __syncthreads();
+  {
+    // ties in order: thread t has tokens per t .. per (t + 1) - 1 of the list
+    const int per = (listed + kRowThreads - 1) / kRowThreads;
+    u64 same = 0, none;
+    for (int i = tid * per; i < min(listed, (tid + 1) * per); ++i) same += L.nucleus.key[i] == cut;
+    u64 tie = block_scan(same, none, L);
+    for (int i = tid * per; i < min(listed, (tid + 1) * per); ++i) {
+      const uint32_t k = L.nucleus.key[i];
+      const int j = L.nucleus.index[i] / kSliceTokens;
+      bool keep = k > cut;
+      if (k == cut) {
+        atomicAdd(&L.nucleus.equal[j], 1u);
+        keep = tie++ < ties;
+      }
+      if (keep && passes(k)) atomicAdd(&L.nucleus.extra[j], weight(k));
+    }
+  }
+  __syncthreads();
+  // a wave a slice
+  for (int j = wave; j < J; j += kRowWaves) {
+    const int base = L.nucleus.base[j];
+    double m = 0.0;
+    if (base != INT_MIN)
+      for (int i = lane; i < kHistBins; i += 64)
+        if (base + i > edge) m += (double)H[(int64_t)j * kHistBins + i] * exp_bin(base + i - top_bin);
+    m = wave_reduce(m, [](double x, double y) { return x + y; });
+    if (lane == 0) L.nucleus.slice[j] = m + (double)L.nucleus.extra[j] * exp_bin(-last);
+  }
+  __syncthreads();
+  double own = tid < J ? L.nucleus.slice[tid] : 0.0, kept;
+  const u64 equal = tid < J ? L.nucleus.equal[tid] : 0;
+  const double sum_before = block_scan(own, kept, L);
+  u64 equals;
+  const u64 equal_before = block_scan(equal, equals, L);
+  const double spot = (r.u > 0.f ? (double)r.u : 0.0) * kept;
+  uint32_t at = block_max(own > 0.0 && sum_before + own > spot ? kMaxSlices - tid : 0, L);
+  const uint32_t end = block_max(own > 0.0 ? tid + 1 : 0, L);
+  const bool past = at == 0;
+  const int slice = past ? (int)end - 1 : kMaxSlices - (int)at;
+  __syncthreads();
+  if (tid == slice) {
+    L.found_above = __builtin_bit_cast(u64, sum_before);
+    L.carried = equal_before;
+  }
+  __syncthreads();
+  const double left = past ? INFINITY : spot - __builtin_bit_cast(double, L.found_above);
+  u64 tie = L.carried;
+  // 8 tokens a thread
+  const int t0 = slice * kSliceTokens + tid * 8;
+  float v[8];
+  load_some<T, 8>(z + t0, V - t0, v);
+  u64 same = 0, none;
+#pragma unroll
+  for (int e = 0; e < 8; ++e) same += t0 + e < V && value_key(v[e]) == cut;
+  tie += block_scan(same, none, L);
+  double q[8], sum = 0.0;
+#pragma unroll
+  for (int e = 0; e < 8; ++e) {
+    q[e] = 0.0;
+    if (t0 + e >= V) continue;
+    const int bin = b.bin(v[e]);
+    const uint32_t k = value_key(v[e]);
+    bool keep = bin > edge;
+    if (bin == edge) {
+      keep = k > cut || (k == cut && tie < ties);
+      keep = keep && passes(k);
+    }
+    tie += k == cut;
+    if (keep) q[e] = rint(b.over(v[e]) * unit) * exp_bin(bin - top_bin);
+    sum += q[e];
+  }
+  double cum = block_scan(sum, all, L);
+  uint32_t token = 0, tail = 0;   // as 2^31 less the index, and the index + 1
+#pragma unroll
+  for (int e = 0; e < 8; ++e) {
+    cum += q[e];
+    if (q[e] > 0.0) {
+      tail = t0 + e + 1;
+      if (cum > left && token == 0) token = 0x80000000u - (uint32_t)(t0 + e);
+    }
+  }
+  token = block_max(token, L);
+  tail = block_max(tail, L);
+  if (tid == 0) a.tokens[row] = token ? (int64_t)(0x80000000u - token) : (int64_t)tail - 1;
+  return true;
+}
+
+// GROUPS: the groups' largest come from sample_slice_kernel; else the workgroup finds them.
+template <class T, bool GROUPS> __global__ void __launch_bounds__(kRowThreads) sample_row_kernel(Sample a) {
+  __shared__ RowLds L;
+  const int64_t row = blockIdx.x;
+  const T* z = (const T*)a.logits + row * a.V;
+  const int V = a.V, tid = threadIdx.x, lane = tid & 63;
+  RowParams r;
+  r.load(a, row);
+  // Groups of `size` tokens, so many that their largest fit in LDS.
+  int size = kGroupTokens;
+  while ((V + size - 1) / size > kGroups) size *= 2;
+  const int groups = (V + size - 1) / size, merge = size / kGroupTokens;
+  uint32_t top = 0;
+  if constexpr (GROUPS) {
+    for (int i = tid; i < groups; i += kRowThreads) {
+      uint32_t g = 0;
+      for (int m = i * merge; m < min(a.groups, (i + 1) * merge); ++m) g = max(g, a.group_top[row * a.groups + m]);
+      L.list.group[i] = g;
+      top = max(top, g);
+    }
+  } else {
+    for (int j0 = 0; j0 < V; j0 += kRowThreads * 8) {
+      const int j = j0 + tid * 8;
+      float v[8];
+      load_some<T, 8>(z + j, V - j, v);
+      uint32_t g = 0;
+#pragma unroll
+      for (int e = 0; e < 8; ++e)
+        if (j + e < V) g = max(g, v[e] != v[e] ? kKeyNan : value_key(v[e]));
+      g = max(g, (uint32_t)__shfl_xor((int)g, 1));
+      g = max(g, (uint32_t)__shfl_xor((int)g, 2));
+      if ((tid & 3) == 0 && j < V) L.list.group[j / kGroupTokens] = g;
+      top = max(top, g);
+    }
+  }
+  top = block_max(top, L);
+  if (top > kKeyInf || top <= kKeyMinusInf) {   // a NaN, or no token left
+    if (tid == 0) a.tokens[row] = -1;
+    return;
+  }
+  const int s = 62 - (V > 2 ? 32 - __clz(V - 1) : 1);   // V 2^s <= 2^62
+  const Weigh w{key_value(top), 1.0 / (double)r.T, (double)(1ull << s),
+                r.min_p > 0.f ? (double)fminf(r.min_p, 1.f) : 0.0};
+
+  if (r.greedy() || r.p <= 0.f) {   // the first token of the first group that has the largest
+    uint32_t g = 0;
+    for (int i = tid; i < groups; i += kRowThreads)
+      if (L.list.group[i] == top) g = max(g, (uint32_t)(kGroups - i));
+    g = kGroups - block_max(g, L);
+    if (tid >= 64) return;
+    for (int j0 = (int)g * size;; j0 += 64) {
+      const int j = j0 + lane;
+      const u64 hit = __ballot(j < V && value_key(load1<T>(z + min(j, V - 1))) == top);
+      if (hit) {
+        if (lane == 0) a.tokens[row] = j0 + __ffsll((long long)hit) - 1;
+        return;
+      }
+    }
+  }
+
+  // Every token that can be kept has a key of at least `low`.
+  uint32_t low = 0;
+  double whole = 0.0;   // the row's sum of w, for top-p without top-k
+  bool sure = true;     // else only if the tokens from low on have p of the sum
+  // the key of the i-th of the groups' largest
+  auto ith_group = [&](int64_t i) {
+    uint32_t least = 0;   // of those that a mask left, from above
+    u64 n = 0, all;
+    for (int g = tid; g < groups; g += kRowThreads) {
+      const uint32_t k = L.list.group[g];
+      if (k > kKeyMinusInf) {
+        least = max(least, ~k);
+        ++n;
+      }
+    }
+    block_scan(n, all, L);
+    least = ~block_max(least, L);
+    if ((u64)i > all) return 0u;
+    u64 above;
+    return find_key(least, top, (u64)i, above, [&](auto&& f) {
+      for (int g = tid; g < groups; g += kRowThreads) f(L.list.group[g], 1ull);
+    }, L);
+  };
+  if (r.k) {
+    if (r.k <= groups) low = ith_group(r.k);
+  } else {
+    if (GROUPS && !(r.p < 1.f) && w.min_w == 0.0) return sample_slices<T>(a, row, r, w, L);
+    if (w.top == INFINITY) {
+      low = kKeyInf;
+      if (r.p < 1.f) {   // the sum is a number of tokens
+        u64 own = 0, all;
+        for (int j = tid * 8; j < V; j += kRowThreads * 8) {
+          float v[8];
+          load_some<T, 8>(z + j, V - j, v);
+#pragma unroll
+          for (int e = 0; e < 8; ++e) own += j + e < V && v[e] == INFINITY;
+        }
+        block_scan(own, all, L);
+        whole = (double)all;
+      }
+    } else {
+      double least = w.min_w;   // w under which none is kept
+      if (r.p < 1.f) {
+        if constexpr (GROUPS) {
+          if (!sum_of_histograms(a, row, r, top, whole, L)) return sample_whole<T>(a, row, r, w, top, L);
+        } else {
+          double own = 0.0;
+          each_token(z, V, [&](float v, int) { own += w.real(v); });
+          block_scan(own, whole, L);
+        }
+        least = fmax(least, (1.0 - (double)r.p) * whole / V);
+      }
+      if (least > 0.0) {
+        // with a margin for the rounding of all this
+        const double cut = (double)w.top + (double)r.T * (log(fmin(least, 1.0)) - 1e-9);
+        if (cut > -3e38) low = value_key(fminf((float)cut - fabsf((float)cut) * 1e-6f, w.top));
+      }
+      if (GROUPS && r.p < 1.f) {   // a value that some thousand tokens at most should reach
+        const uint32_t some = ith_group(min(2048, groups / 2));
+        if (some > low) {
+          low = some;
+          sure = false;
+        }
+      }
+    }
+  }
+  low = max(low, kKeyMinusInf + 1);   // masked tokens have no weight
+
+  // The groups that have such tokens, in order, in place: thread t looks at `per` consecutive ones.
+  const int per = (groups + kRowThreads - 1) / kRowThreads;
+  uint32_t pass = 0;   // bits: at most 8 groups a thread
+  __syncthreads();
+  for (int i = 0; i < per; ++i)
+    if (tid * per + i < groups && L.list.group[tid * per + i] >= low) pass |= 1u << i;
+  u64 found;
+  u64 at = block_scan((u64)__popc(pass), found, L);
+  __syncthreads();
+  for (int i = 0; i < per; ++i)
+    if (pass >> i & 1) L.list.group[at++] = tid * per + i;
+  __syncthreads();
+  // Their tokens, in order: each wave a stretch of the found groups, counted first and then written.
+  const int wave = tid >> 6, share = ((int)found + kRowWaves - 1) / kRowWaves;
+  const int g0 = min((int)found, wave * share), g1 = min((int)found, g0 + share);
+  u64 n = 0;
+  auto tokens = [&](auto&& f) {
+    // 64 tokens at a time: two groups of 32, or a part of a larger group
+    const int step = size > 64 ? 64 : size, chunks = size / step, at_once = 64 / step;
+    for (int g = g0; g < g1; g += at_once)
+      for (int c = 0; c < chunks; ++c) {
+        const int mine = g + lane / step;
+        const int j = mine < g1 ? (int)L.list.group[mine] * size + c * step + lane % step : V;
+        const float v = j < V ? load1<T>(z + j) : -INFINITY;
+        f(value_key(v), v, j);
+      }
+  };
+  tokens([&](uint32_t k, float, int) { n += __popcll(__ballot(k >= low)); });
+  u64 total;
+  u64 first = block_scan(lane == 0 ? n : 0ull, total, L);
+  uint32_t start = (uint32_t)__shfl(first, 0);
+  if (total > kMost) {
+    if (GROUPS && !r.k && r.p < 1.f && w.top < INFINITY && sample_nucleus<T>(a, row, r, w, L)) return;
+    return sample_whole<T>(a, row, r, w, top, L);
+  }
+  tokens([&](uint32_t k, float v, int j) {
+    const u64 hit = __ballot(k >= low);
+    if (k >= low) {
+      const uint32_t i = start + (uint32_t)__popcll(hit & ((1ull << lane) - 1));
+      L.list.key[i] = k;
+      L.list.index[i] = j;
+      L.list.weight[i] = w(v);
+    }
+    start += (uint32_t)__popcll(hit);
+  });
+  __syncthreads();
+
+  // Tokens above key `cut` are kept and the first `ties` at it.
+  const int count = (int)total;
+  uint32_t cut = 0;
+  u64 ties = 0;
+  if (r.k && r.k < count) {
+    u64 above;
+    cut = find_key(low, top, (u64)r.k, above, [&](auto&& f) {
+      for (int i = tid; i < count; i += kRowThreads) f(L.list.key[i], 1ull);
+    }, L);
+    ties = (u64)r.k - above;
+  }
+  if (r.p < 1.f) {
+    u64 sum = 0, all;
+    for (int i = tid; i < count; i += kRowThreads)
+      if (L.list.key[i] > cut) sum += L.list.weight[i];
+    block_scan(sum, all, L);
+    const u64 at_cut = cut ? ties * w(key_value(cut)) : 0;
+    all += at_cut;
+    const u64 need_all = nucleus(r.p, r.k ? (double)all : whole * w.unit);
+    if (!sure && need_all > all) {   // more tokens are kept than these
+      if (sample_nucleus<T>(a, row, r, w, L)) return;
+      return sample_whole<T>(a, row, r, w, top, L);
+    }
+    const u64 want = min(need_all, all);
+    if (want == 0) {
+      cut = top;
+      ties = 1;
+    } else {
+      u64 above;
+      const uint32_t was = cut;
+      cut = find_key(low, top, want, above, [&](auto&& f) {
+        for (int i = tid; i < count; i += kRowThreads)
+          if (L.list.key[i] > was) f(L.list.key[i], L.list.weight[i]);
+        if (tid == 0 && at_cut) f(was, at_cut);
+      }, L);
+      const u64 need = ties_needed(want, above, w(key_value(cut)));
+      ties = cut == was ? min(ties, need) : need;
+    }
+  }
+  // The draw: thread t has tokens 4 t .. 4 t + 3 of the list.
+  u64 same = 0, none;
+#pragma unroll
+  for (int e = 0; e < 4; ++e) same += 4 * tid + e < count && L.list.key[4 * tid + e] == cut;
+  u64 tie = block_scan(same, none, L);
+  u64 weight[4], sum = 0;
+#pragma unroll
+  for (int e = 0; e < 4; ++e) {
+    const int i = 4 * tid + e;
+    weight[e] = 0;
+    if (i >= count) continue;
+    const uint32_t k = L.list.key[i];
+    if (k > cut || (k == cut && tie++ < ties))
+      weight[e] = w.min_w == 0.0 || w.real(key_value(k)) >= w.min_w ? L.list.weight[i] : 0;
+    sum += weight[e];
+  }
+  u64 all;
+  u64 before = block_scan(sum, all, L);
+  const u64 want = spot(r.u, all);
+#pragma unroll
+  for (int e = 0; e < 4; ++e) {
+    if (before <= want && want < before + weight[e]) a.tokens[row] = L.list.index[4 * tid + e];
+    before += weight[e];
+  }
+}
+
+template <class T> static hipError_t sample_launch(const Sample& a, hipStream_t st) {
+  if (a.slices) {
+    FLCE_LAUNCH((sample_slice_kernel<T>), dim3((unsigned)(a.N * a.slices)), dim3(256), 0, st, a);
+    FLCE_LAUNCH((sample_row_kernel<T, true>), dim3((unsigned)a.N), dim3(kRowThreads), 0, st, a);
+  } else {
+    FLCE_LAUNCH((sample_row_kernel<T, false>), dim3((unsigned)a.N), dim3(kRowThreads), 0, st, a);
+  }
   return hipGetLastError();
+}
+
+hipError_t launch_sample(const Sample& a, int dtype, hipStream_t st) {
+  return dtype == 1 ? sample_launch<uint16_t>(a, st) : dtype == 2 ? sample_launch<_Float16>(a, st) : sample_launch<float>(a, st);
 }
 
 }  // namespace flce

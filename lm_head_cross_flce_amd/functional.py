@@ -970,9 +970,15 @@ def flce_mx_linear(x: MXTensor, W: MXTensor, b: Optional[torch.Tensor] = None, r
     return y
 
 
+def flce_sample_workspace_size(N: int, V: int, dtype: torch.dtype) -> int:
+    """Bytes of flce_sample."""
+    return _lib.flce_sample_workspace_size(N, V, _DTYPES[dtype])
+
+
 def flce_sample(logits: torch.Tensor, u: torch.Tensor, temperature: Union[float, torch.Tensor, None] = None,
                 top_k: Union[int, torch.Tensor, None] = None, top_p: Union[float, torch.Tensor, None] = None,
-                min_p: Union[float, torch.Tensor, None] = None) -> torch.Tensor:
+                min_p: Union[float, torch.Tensor, None] = None,
+                workspace: Optional[torch.Tensor] = None) -> torch.Tensor:
     """A token of each row of logits [N, V] by u [N], float32 in [0, 1): int64 [N], -1 for a row with no token left
     or with a NaN.  Parameters are one number for all rows, or a tensor of one per row (None: temperature 1, and
     nothing cut off): the first top_k tokens by logit; of those, each whose predecessors' probabilities add up to
@@ -1001,9 +1007,10 @@ def flce_sample(logits: torch.Tensor, u: torch.Tensor, temperature: Union[float,
         elif value is not None:
             kw[name] = value
     tokens = torch.empty(N, dtype=torch.int64, device=dev)
+    workspace = _workspace(workspace, _lib.flce_sample_workspace_size(N, V, dt), dev)
     with _on(dev):
-        _lib.flce_sample(logits.data_ptr(), u_ptr, N, V, dt, _lib.sampling(**kw), tokens.data_ptr(),
-                         _raw_stream(dev.index))
+        _lib.flce_sample(logits.data_ptr(), u_ptr, N, V, dt, _lib.sampling(**kw), tokens.data_ptr(), _ptr(workspace),
+                         _nbytes(workspace), _raw_stream(dev.index))
     return tokens
 
 

@@ -102,6 +102,25 @@ def test_large_vocabularies(dtype):
 
 
 @pytest.mark.parametrize("dtype", list(DT))
+@pytest.mark.parametrize("V", [9000, 50_001])
+def test_wide_nuclei(V, dtype):
+    # nuclei of thousands of tokens: ends inside a bin, among ties, cut off by min-p, in a row partly masked
+    N = 6
+    z, u = draw(N, V, DT[dtype], seed=V + 1, scale=1.5)
+    z[1, ::3] = -math.inf
+    z[2] = (z[2] * 2).round() / 2
+    z[3, V // 3:] = -math.inf
+    u[4], u[5] = 0.0, 1 - 2.0 ** -24
+    for kw in (dict(top_p=0.5, temperature=3.0), dict(top_p=0.9, temperature=1.5), dict(top_p=0.99, temperature=1e3),
+               dict(top_p=0.999), dict(top_p=0.95, temperature=2.0, min_p=0.05), dict(top_p=0.3, temperature=2.0, min_p=1e-4),
+               dict(min_p=0.01, temperature=4.0), dict(top_p=0.9, temperature=1e-3), dict(top_p=0.9, temperature=2e-4),
+               dict(top_p=1 - 2.0 ** -24), dict(top_p=2.0 ** -20, temperature=5.0), dict(top_p=0.7, top_k=V // 2, temperature=2.0)):
+        check(z, u, **kw)
+    check(z - 500, u, top_p=0.9, temperature=0.2)      # z / T far from 0
+    check(z.float() * 1e-3 - 41, u, top_p=0.9, temperature=0.01)
+
+
+@pytest.mark.parametrize("dtype", list(DT))
 def test_parameters_of_each_row(dtype):
     N, V = 60, 3000
     z, u = draw(N, V, DT[dtype], seed=5)

@@ -74,7 +74,8 @@ def linear(**o):
 
 
 def sample(params=None, **o):
-    a = dict(logits=X, u=S, N=4, V=1000, dtype=1, params=_lib.sampling(**(params or {})), tokens=Y, stream=None)
+    a = dict(logits=X, u=S, N=4, V=1000, dtype=1, params=_lib.sampling(**(params or {})), tokens=Y, workspace=WS,
+             workspace_bytes=BIG, stream=None)
     a.update(o)
     _lib.flce_sample(**a)
 
@@ -198,10 +199,11 @@ def test_sample_arguments():
     refused(sample, INVALID, N=-1)
     refused(sample, INVALID, V=0)
     refused(sample, UNSUPPORTED, V=(1 << 30) + 1)
-    refused(sample, UNSUPPORTED, N=(1 << 22) + 1)
+    refused(sample, UNSUPPORTED, N=1 << 22)
+    refused(sample, UNSUPPORTED, N=1 << 12, V=1 << 26)
     refused(sample, UNSUPPORTED, dtype=3)
     with pytest.raises(_lib.FlceError):
-        _lib.flce_sample(X, S, 4, 1000, 1, None, Y, None)
+        _lib.flce_sample(X, S, 4, 1000, 1, None, Y, WS, BIG, None)
     for name, value, off in (("logits", X, 8), ("u", S, 2), ("tokens", Y, 4)):
         refused(sample, INVALID, **{name: None})
         refused(sample, INVALID, **{name: value + off})
@@ -212,13 +214,20 @@ def test_sample_arguments():
     refused(sample, INVALID, tokens=X)
     refused(sample, INVALID, tokens=S - 16)
     refused(sample, INVALID, params=dict(top_ks=Y))
+    need = _lib.flce_sample_workspace_size(4, 128256, 1)
+    assert need >= 4 * 128256 // 32 * 4
+    refused(sample, TOO_SMALL, V=128256, workspace_bytes=need - 1)
+    refused(sample, INVALID, V=128256, workspace=None)
+    refused(sample, INVALID, V=128256, workspace=WS + 8)
+    refused(sample, INVALID, V=128256, workspace=X)
+    assert _lib.flce_sample_workspace_size(4, 1000, 1) == 0 and _lib.flce_sample_workspace_size(0, 128256, 1) == 0
 
 
 def test_calls_without_rows_need_no_tensors():
     _lib.flce_rms_norm_forward(None, None, None, 0, 8, 1, 1e-6, None, None, None, None)
     _lib.flce_mx_quantize(None, 0, 8, 1, 1, None, None, None)
     _lib.flce_mx_linear(None, None, 0, Wt, D, None, None, 0, 64, 64, 1, 0, None, None, 0, None)
-    _lib.flce_sample(None, None, 0, 8, 1, _lib.sampling(), None, None)
+    _lib.flce_sample(None, None, 0, 8, 1, _lib.sampling(), None, None, 0, None)
 
 
 def test_binding_refusals():
@@ -250,5 +259,5 @@ def test_package_names():
     import lm_head_cross_flce_amd as pkg
     for name in ("flce_rms_norm_workspace_size", "flce_rms_norm_forward", "flce_rms_norm_mx_forward",
                  "flce_rms_norm_backward", "flce_mx_quantize", "flce_mx_dequantize", "flce_mx_linear_workspace_size",
-                 "flce_mx_linear", "flce_sample", "MXTensor", "fused_rms_norm", "RMSNorm", "MXLinear"):
+                 "flce_mx_linear", "flce_sample_workspace_size", "flce_sample", "MXTensor", "fused_rms_norm", "RMSNorm", "MXLinear"):
         assert getattr(pkg, name) is getattr(F, name)
