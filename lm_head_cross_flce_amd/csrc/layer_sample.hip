@@ -17,7 +17,7 @@
 // else keeps more goes through sample_whole, which reads the row several times.  Rows of
 // up to 8192 tokens take one launch: their workgroup finds the groups' largest itself.
 //
-// Weights are formed in double.  Where tokens are ranked, they are added as whole
+// Weights are formed in double, to 2^-45.  Where tokens are ranked, they are added as whole
 // numbers of 2^-s, s as large as keeps a row's sum under 2^62 (45 at 128256 tokens): such a
 // sum does not depend on its order, so atomics may form it, and every comparison with it
 // is exact.  Its rounding, 2^-46 of the largest weight a token, is far under what a float32
@@ -39,35 +39,36 @@ __device__ __forceinline__ uint32_t value_key(float v) {
 __device__ __forceinline__ float key_value(uint32_t k) { return __uint_as_float(k ^ ((k >> 31) ? 0x80000000u : 0xffffffffu)); }
 constexpr uint32_t kKeyInf = 0xff800000u, kKeyMinusInf = 0x007fffffu, kKeyNan = 0xffffffffu;
 
-// exp(y) for y <= 0, to 2^-45: Taylor's series of degree 11 in what is left of y by the
-// nearest multiple of log 2 (0.347^12 / 12! = 2^-47).  Under e^-45 it is 0: 2^30 tokens of
-// such a weight would not add 2^-34 of the largest.
-__device__ __forceinline__ double exp_negative(double y) {
-  const double n = rint(y * 1.4426950408889634), t = fma(n, -0.69314718055994531, y);
-  double p = 1.0 / 39916800;
-  p = fma(p, t, 1.0 / 3628800);
-  p = fma(p, t, 1.0 / 362880);
-  p = fma(p, t, 1.0 / 40320);
-  p = fma(p, t, 1.0 / 5040);
-  p = fma(p, t, 1.0 / 720);
-  p = fma(p, t, 1.0 / 120);
-  p = fma(p, t, 1.0 / 24);
-  p = fma(p, t, 1.0 / 6);
-  p = fma(p, t, 0.5);
-  p = fma(p, t, 1.0);
-  p = fma(p, t, 1.0);
-  return y < -45.0 ? 0.0 : __builtin_ldexp(p, (int)n);
+// 2^f, |f| <= 1/2, to 2^-45.6: the polynomial of degree 9 through it at the ten Chebyshev
+// points (computed in 50 digits).
+__device__ __forceinline__ double pow2_near(double f) {
+  double p = 1.0205905413765595e-07;
+  p = fma(p, f, 1.325964524488711e-06);
+  p = fma(p, f, 1.5252672924850737e-05);
+  p = fma(p, f, 0.0001540343375125101);
+  p = fma(p, f, 0.0013333558200794592);
+  p = fma(p, f, 0.009618129193934313);
+  p = fma(p, f, 0.05550410866465167);
+  p = fma(p, f, 0.2402265069564034);
+  p = fma(p, f, 0.6931471805599462);
+  return fma(p, f, 1.0000000000000135);
 }
-
-__device__ __forceinline__ double exp_bin(int bins) { return exp_negative(0.125 * bins); }   // e^(bins / 8), bins <= 0
+// 2^x for x <= 0.  Under 2^-65 it is 0: 2^30 tokens of such a weight would not add 2^-34 of
+// the largest.
+__device__ __forceinline__ double pow2_negative(double x) {
+  const double n = rint(x);
+  return x < -65.0 ? 0.0 : __builtin_ldexp(pow2_near(x - n), (int)n);
+}
+constexpr double kLog2eDouble = 1.4426950408889634;
+__device__ __forceinline__ double exp_bin(int bins) { return pow2_negative(0.125 * kLog2eDouble * bins); }   // e^(bins / 8), bins <= 0
 
 // Weights relative to a value that is not below any.  unit: 2^s.
 struct Weigh {
   float top;
-  double inv_t, unit, min_w;
+  double scale, unit, min_w;   // scale: log2(e) / T
   __device__ __forceinline__ double real(float z) const {
     // equal to the largest: 1, also where that is infinite; masked: 0, whatever T
-    return z == top ? 1.0 : z == -INFINITY || top == INFINITY ? 0.0 : exp_negative(((double)z - (double)top) * inv_t);
+    return z == top ? 1.0 : z == -INFINITY || top == INFINITY ? 0.0 : pow2_negative(((double)z - (double)top) * scale);
   }
   __device__ __forceinline__ u64 operator()(float z) const { return (u64)rint(real(z) * unit); }
   __device__ __forceinline__ u64 kept(float z) const {
@@ -107,28 +108,52 @@ struct Bins {
   // the weight over that at its bin's lower edge, from 1 to e^(1/8)
   __device__ __forceinline__ double over(float z) const {
     const double x = place(z);
-    return exp_near((x - floor(x)) * 0.125);
-  }
-  // exp(t), 0 <= t < 1/8: Taylor's series of degree 9 (0.125^10 / 10! = 2^-51)
-  static __device__ __forceinline__ double exp_near(double t) {
-    double p = 1.0 / 362880;
-    p = fma(p, t, 1.0 / 40320);
-    p = fma(p, t, 1.0 / 5040);
-    p = fma(p, t, 1.0 / 720);
-    p = fma(p, t, 1.0 / 120);
-    p = fma(p, t, 1.0 / 24);
-    p = fma(p, t, 1.0 / 6);
-    p = fma(p, t, 0.5);
-    p = fma(p, t, 1.0);
-    return fma(p, t, 1.0);
+    return pow2_near((x - floor(x)) * (0.125 * kLog2eDouble));
   }
 };
 
-template <class V, class F> __device__ __forceinline__ V wave_reduce(V v, F&& f) {
-#pragma unroll
-  for (int d = 1; d < 64; d *= 2) v = f(v, (V)__shfl_xor(v, d));
-  return v;
+// v moved over the wave's lanes by a DPP control, 0 where none comes in.
+template <int CTRL, int ROWS, class V> __device__ __forceinline__ V moved(V v) {
+  if constexpr (sizeof(V) == 8) {
+    typedef uint32_t u32x2_t __attribute__((ext_vector_type(2)));
+    u32x2_t t = __builtin_bit_cast(u32x2_t, v);
+    t[0] = (uint32_t)__builtin_amdgcn_update_dpp(0, (int)t[0], CTRL, ROWS, 0xF, false);
+    t[1] = (uint32_t)__builtin_amdgcn_update_dpp(0, (int)t[1], CTRL, ROWS, 0xF, false);
+    return __builtin_bit_cast(V, t);
+  } else {
+    return (V)__builtin_amdgcn_update_dpp(0, (int)v, CTRL, ROWS, 0xF, false);
+  }
 }
+// Inclusive scans over the 16 lanes of a row and over the wave; f's identity is 0.
+template <class V, class F> __device__ __forceinline__ V row_scan(V v, F&& f) {
+  v = f(v, moved<0x111, 0xF>(v));   // from 1, 2, 4 and 8 lanes below
+  v = f(v, moved<0x112, 0xF>(v));
+  v = f(v, moved<0x114, 0xF>(v));
+  return f(v, moved<0x118, 0xF>(v));
+}
+template <class V, class F> __device__ __forceinline__ V wave_scan(V v, F&& f) {
+  v = row_scan(v, f);
+  v = f(v, moved<0x142, 0xA>(v));   // a row's last lane to rows 1 and 3, lane 31 to rows 2 and 3
+  return f(v, moved<0x143, 0xC>(v));
+}
+template <class V> __device__ __forceinline__ V lane_of(V v, int lane) {
+  if constexpr (sizeof(V) == 8) {
+    typedef uint32_t u32x2_t __attribute__((ext_vector_type(2)));
+    u32x2_t t = __builtin_bit_cast(u32x2_t, v);
+    t[0] = (uint32_t)__builtin_amdgcn_readlane((int)t[0], lane);
+    t[1] = (uint32_t)__builtin_amdgcn_readlane((int)t[1], lane);
+    return __builtin_bit_cast(V, t);
+  } else {
+    return (V)__builtin_amdgcn_readlane((int)v, lane);
+  }
+}
+struct Add {
+  template <class V> __device__ __forceinline__ V operator()(V x, V y) const { return x + y; }
+};
+struct Max {
+  __device__ __forceinline__ uint32_t operator()(uint32_t x, uint32_t y) const { return max(x, y); }
+};
+template <class V, class F> __device__ __forceinline__ V wave_all(V v, F&& f) { return lane_of(wave_scan(v, f), 63); }
 
 // ---------------------------------------------------------------------------
 // The pass over the logits
@@ -163,7 +188,7 @@ template <class T> __global__ void __launch_bounds__(256) sample_slice_kernel(Sa
     if ((tid & 3) == 0 && at < left) a.group_top[row * a.groups + (base + at) / kGroupTokens] = g;
     top = max(top, g);
   }
-  top = wave_reduce(top, [](uint32_t x, uint32_t y) { return max(x, y); });
+  top = wave_all(top, Max());
   if ((tid & 63) == 0) red[tid >> 6] = top;
   __syncthreads();
   top = max(max(red[0], red[1]), max(red[2], red[3]));
@@ -194,13 +219,13 @@ template <class T> __global__ void __launch_bounds__(256) sample_slice_kernel(Sa
     return;
   }
   if (some) {
-    const Weigh w{key_value(top), 1.0 / (double)r.T, 1.0, 0.0};
+    const Weigh w{key_value(top), kLog2eDouble / (double)r.T, 1.0, 0.0};
 #pragma unroll
     for (int c = 0; c < 4; ++c)
 #pragma unroll
       for (int e = 0; e < 8; ++e) s += w.real(v[c][e]);
   }
-  s = wave_reduce(s, [](double x, double y) { return x + y; });
+  s = wave_all(s, Add());
   if ((tid & 63) == 0) sums[tid >> 6] = s;
   __syncthreads();
   if (tid == 0) a.slice_sum[row * a.slices + j] = (sums[0] + sums[1]) + (sums[2] + sums[3]);
@@ -215,21 +240,11 @@ constexpr int kBins = 2048, kMost = 4096, kGroups = 8192;
 constexpr int kNucleusMost = 8192, kMaxSlices = 1024;
 constexpr int kUnits = 2048;   // sample_whole: runs of 512 tokens, or of more in long rows
 
-template <class V> __device__ __forceinline__ V wave_scan(V v, int lane) {
-#pragma unroll
-  for (int d = 1; d < 64; d *= 2) {
-    const V t = __shfl_up(v, d);
-    if (lane >= d) v += t;
-  }
-  return v;
-}
-
 struct RowLds {
-  u64 wave[kRowWaves];
+  u64 wave[2][kRowWaves];
   u64 found_above, carried;
-  uint32_t found, key[kRowWaves];
-  int count;
-  u64 hist[kBins];
+  uint32_t found;
+  u64 hist[kBins];   // zero between find_key's uses
   union {
     struct {
       uint32_t group[kGroups];      // largest key of each group; then the groups that pass, in order
@@ -250,72 +265,74 @@ struct RowLds {
   };
 };
 
-// Sum of v (8 bytes) over threads before this one, and over all of them.
-template <class V> __device__ __forceinline__ V block_scan(V v, V& all, RowLds& L) {
-  const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
-  const V in = wave_scan(v, lane);
+// A row's workgroup.  The waves' results lie in LDS by turns in two places, so one
+// barrier is enough for each sum.
+struct Row {
+  RowLds& m;
+  int turn;
+};
+
+// f over v (8 bytes) of the threads before this one, and of all of them.
+template <class V> __device__ __forceinline__ V block_scan(V v, V& all, Row& L) {
+  const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  const V in = wave_scan(v, Add());
+  u64* place = L.m.wave[L.turn ^= 1];
+  if (lane == 63) place[wave] = __builtin_bit_cast(u64, in);
   __syncthreads();
-  if (lane == 63) L.wave[wave] = __builtin_bit_cast(u64, in);
-  __syncthreads();
-  V before = 0;
-  all = 0;
-#pragma unroll
-  for (int w = 0; w < kRowWaves; ++w) {
-    const V x = __builtin_bit_cast(V, L.wave[w]);
-    if (w < wave) before += x;
-    all += x;
-  }
-  return before + (in - v);
+  const V waves = row_scan(__builtin_bit_cast(V, place[lane & 15]), Add());
+  all = lane_of(waves, 15);
+  const V before = wave ? lane_of(waves, wave - 1) : V(0);
+  return before + moved<0x138, 0xF>(in);   // the lane below's
 }
-// The largest of v over all threads.
-__device__ __forceinline__ uint32_t block_max(uint32_t v, RowLds& L) {
-  v = wave_reduce(v, [](uint32_t x, uint32_t y) { return max(x, y); });
+// The largest of a and of b over all threads.
+__device__ __forceinline__ void block_max(uint32_t& a, uint32_t& b, Row& L) {
+  const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
+  a = wave_scan(a, Max());
+  b = wave_scan(b, Max());
+  u64* place = L.m.wave[L.turn ^= 1];
+  if (lane == 63) place[wave] = (u64)a << 32 | b;
   __syncthreads();
-  if ((threadIdx.x & 63) == 0) L.key[threadIdx.x >> 6] = v;
-  __syncthreads();
-#pragma unroll
-  for (int w = 0; w < kRowWaves; ++w) v = max(v, L.key[w]);
+  const u64 w = place[lane & 15];
+  a = lane_of(row_scan((uint32_t)(w >> 32), Max()), 15);
+  b = lane_of(row_scan((uint32_t)w, Max()), 15);
+}
+__device__ __forceinline__ uint32_t block_max(uint32_t v, Row& L) {
+  uint32_t none = 0;
+  block_max(v, none, L);
   return v;
 }
 
-// The bin, from the last one down, in which the sum of the bins passes `want` (from 1
-// to their whole sum), and the sum of the bins above it.
-__device__ __forceinline__ uint32_t find_bin(u64 want, u64& above, RowLds& L) {
-  const int t = threadIdx.x, hi = kBins - 1 - 2 * t;
-  const u64 a = L.hist[hi], b = L.hist[hi - 1];
-  u64 all;
-  const u64 before = block_scan(a + b, all, L);
-  if (before < want && before + a + b >= want) {
-    const bool first = before + a >= want;
-    L.found = first ? hi : hi - 1;
-    L.found_above = first ? before : before + a;
-  }
-  __syncthreads();
-  above = L.found_above;
-  return L.found;
-}
-
-// The key at which, from the largest down, the sum of the weights reaches want (from 1 to
-// their whole sum), and the sum above that key.  each(f) calls f(key, weight) for every
-// element, among all threads; keys lie in [lo, hi].  Each level splits the keys' range
-// into 2048 bins.
-template <class F> __device__ __forceinline__ uint32_t find_key(uint32_t lo, uint32_t hi, u64 want, u64& above, F&& each, RowLds& L) {
+// The key at which, from the largest down, the sum of the weights reaches want, and the sum
+// above that key; 0 if want is more than their whole sum.  each(f) calls f(key, weight)
+// for every element, among all threads; keys lie in [lo, hi].  Each level splits the
+// keys' range into 2048 bins; coarse: the first level's bin's lowest key.
+template <class F>
+__device__ __forceinline__ uint32_t find_key(uint32_t lo, uint32_t hi, u64 want, u64& above, F&& each, Row& L, bool coarse = false) {
   above = 0;
 #pragma unroll 1
   while (true) {
     const int bits = hi > lo ? 32 - __clz((int)(hi - lo)) : 0, shift = bits > 11 ? bits - 11 : 0;
-    __syncthreads();
-    for (int i = threadIdx.x; i < kBins; i += kRowThreads) L.hist[i] = 0;
-    __syncthreads();
     each([&](uint32_t k, u64 w) {
-      if (k >= lo && k <= hi && w) atomicAdd(&L.hist[(k - lo) >> shift], w);
+      if (k >= lo && k <= hi && w) atomicAdd(&L.m.hist[(k - lo) >> shift], w);
     });
     __syncthreads();
-    u64 a;
-    const uint32_t bin = find_bin(want - above, a, L);
-    above += a;
-    lo += bin << shift;
-    if (shift == 0) return lo;
+    // thread t has bins 2047 - 2 t and the one below it, and leaves them empty
+    const int top = kBins - 1 - 2 * (int)threadIdx.x;
+    const u64 a = L.m.hist[top], b = L.m.hist[top - 1];
+    L.m.hist[top] = 0;
+    L.m.hist[top - 1] = 0;
+    u64 all;
+    const u64 before = above + block_scan(a + b, all, L);
+    if (above + all < want) return 0;
+    if (before < want && before + a + b >= want) {
+      const bool first = before + a >= want;
+      L.m.found = first ? top : top - 1;
+      L.m.found_above = first ? before : before + a;
+    }
+    __syncthreads();
+    above = L.m.found_above;
+    lo += L.m.found << shift;
+    if (shift == 0 || coarse) return lo;
     hi = min(hi, lo + ((1u << shift) - 1));
   }
 }
@@ -348,9 +365,56 @@ template <class T, class F> __device__ __forceinline__ void each_token(const T* 
   }
 }
 
+// Tokens of the row that stay, in order, to put(place, value, index): of runs of 8 tokens, run c from at(c) on (in
+// order), those that keep(value, index) says.  Each wave takes a stretch of the runs, counts and then writes; more than
+// `most` in all are only counted.  Returns their number.
+template <class T, class At, class Keep, class Put>
+__device__ __forceinline__ uint32_t collect(const T* z, int V, int runs, uint32_t most, At&& at, Keep&& keep, Put&& put, Row& L) {
+  constexpr int U = 2;   // runs a lane has under way
+  const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
+  const int share = (runs + 64 * U * kRowWaves - 1) / (64 * U * kRowWaves) * (64 * U);
+  const int c0 = min(runs, wave * share), c1 = min(runs, c0 + share);
+  auto walk = [&](auto&& f) {
+#pragma unroll 1
+    for (int c = c0; c < c1; c += 64 * U) {
+      float v[U][8];
+      int j[U];
+#pragma unroll
+      for (int q = 0; q < U; ++q) {
+        const int run = c + 64 * q + lane;
+        j[q] = run < c1 ? at(run) : V;
+        load_some<T, 8>(z + min(j[q], V), V - j[q], v[q]);
+      }
+#pragma unroll
+      for (int q = 0; q < U; ++q) {
+        uint32_t hits = 0;
+#pragma unroll
+        for (int e = 0; e < 8; ++e) hits |= (uint32_t)(j[q] + e < V && keep(v[q][e], j[q] + e)) << e;
+        f(hits, v[q], j[q]);
+      }
+    }
+  };
+  u64 n = 0, total;
+  walk([&](uint32_t hits, const float (&)[8], int) { n += __popc(hits); });
+  uint32_t start = (uint32_t)block_scan(n, total, L);
+  if (total > most) return (uint32_t)min(total, (u64)0xffffffffu);
+  start = lane_of(start, 0);
+  walk([&](uint32_t hits, const float (&v)[8], int j) {
+    if (!__ballot(hits != 0)) return;
+    const uint32_t own = (uint32_t)__popc(hits), in = wave_scan(own, Add());
+    uint32_t i = start + in - own;
+#pragma unroll
+    for (int e = 0; e < 8; ++e)
+      if (hits >> e & 1) put(i++, v[e], j + e);
+    start += lane_of(in, 63);
+  });
+  __syncthreads();
+  return (uint32_t)total;
+}
+
 // A row with any number of tokens to keep, read from memory in every pass.
 template <class T>
-__device__ __forceinline__ void sample_whole(const Sample& a, int64_t row, const RowParams& r, const Weigh& w, uint32_t top, RowLds& L) {
+__device__ __forceinline__ void sample_whole(const Sample& a, int64_t row, const RowParams& r, const Weigh& w, uint32_t top, Row& L) {
   const T* z = (const T*)a.logits + row * a.V;
   const int V = a.V, tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
   // Tokens above key `cut` are kept and the first `ties` at it.
@@ -403,11 +467,11 @@ __device__ __forceinline__ void sample_whole(const Sample& a, int64_t row, const
         same += key == cut;
       }
     }
-    m = wave_reduce(m, [](u64 x, u64 y) { return x + y; });
-    same = wave_reduce(same, [](uint32_t x, uint32_t y) { return x + y; });
+    m = wave_all(m, Add());
+    same = wave_all(same, Add());
     if (lane == 0) {
-      L.whole.mass[i] = m;
-      L.whole.same[i] = same;
+      L.m.whole.mass[i] = m;
+      L.m.whole.same[i] = same;
     }
   }
   __syncthreads();
@@ -416,13 +480,13 @@ __device__ __forceinline__ void sample_whole(const Sample& a, int64_t row, const
   u64 m[2] = {0, 0}, n[2] = {0, 0}, all;
 #pragma unroll
   for (int h = 0; h < 2; ++h)
-    if (2 * tid + h < units) n[h] = L.whole.same[2 * tid + h];
+    if (2 * tid + h < units) n[h] = L.m.whole.same[2 * tid + h];
   u64 before = block_scan(n[0] + n[1], all, L);
   u64 used[2];
 #pragma unroll
   for (int h = 0; h < 2; ++h) {
     used[h] = min(before, ties);
-    if (2 * tid + h < units) m[h] = L.whole.mass[2 * tid + h] + min(n[h], ties - used[h]) * each;
+    if (2 * tid + h < units) m[h] = L.m.whole.mass[2 * tid + h] + min(n[h], ties - used[h]) * each;
     before += n[h];
   }
   before = block_scan(m[0] + m[1], all, L);
@@ -430,17 +494,17 @@ __device__ __forceinline__ void sample_whole(const Sample& a, int64_t row, const
 #pragma unroll
   for (int h = 0; h < 2; ++h) {
     if (before <= want && want < before + m[h]) {
-      L.found = 2 * tid + h;
-      L.found_above = before;
-      L.carried = used[h];
+      L.m.found = 2 * tid + h;
+      L.m.found_above = before;
+      L.m.carried = used[h];
     }
     before += m[h];
   }
   __syncthreads();
   // The first wave walks the unit, 512 tokens at a time.
   if (wave > 0) return;
-  const int i = L.found;
-  u64 done = L.found_above, taken = L.carried;
+  const int i = L.m.found;
+  u64 done = L.m.found_above, taken = L.m.carried;
   for (int j0 = i * unit; j0 < min(V, (i + 1) * unit); j0 += 512) {
     const int j = j0 + lane * 8;
     float v[8];
@@ -448,7 +512,7 @@ __device__ __forceinline__ void sample_whole(const Sample& a, int64_t row, const
     u64 same = 0;
 #pragma unroll
     for (int e = 0; e < 8; ++e) same += j + e < V && value_key(v[e]) == cut;
-    const u64 scan = wave_scan(same, lane);
+    const u64 scan = wave_scan(same, Add());
     u64 tie = taken + scan - same, weight[8], sum = 0;
 #pragma unroll
     for (int e = 0; e < 8; ++e) {
@@ -459,7 +523,7 @@ __device__ __forceinline__ void sample_whole(const Sample& a, int64_t row, const
       else if (key == cut && tie++ < ties) weight[e] = each;
       sum += weight[e];
     }
-    const u64 in = wave_scan(sum, lane);
+    const u64 in = wave_scan(sum, Add());
     u64 at = done + in - sum;
     if (at <= want && want < at + sum) {
 #pragma unroll
@@ -468,8 +532,8 @@ __device__ __forceinline__ void sample_whole(const Sample& a, int64_t row, const
         at += weight[e];
       }
     }
-    done += __shfl(in, 63);
-    taken += __shfl(scan, 63);
+    done += lane_of(in, 63);
+    taken += lane_of(scan, 63);
     if (done > want) break;
   }
 }
@@ -477,7 +541,7 @@ __device__ __forceinline__ void sample_whole(const Sample& a, int64_t row, const
 // A row that nothing is cut off from: the slice in which u times the whole sum lies, then the token in it.  The
 // sums are doubles in a fixed order; where their rounding leaves the spot past a slice's last token, that is taken.
 template <class T>
-__device__ __forceinline__ void sample_slices(const Sample& a, int64_t row, const RowParams& r, const Weigh& w, RowLds& L) {
+__device__ __forceinline__ void sample_slices(const Sample& a, int64_t row, const RowParams& r, const Weigh& w, Row& L) {
   const T* z = (const T*)a.logits + row * a.V;
   const int tid = threadIdx.x;
   // thread t takes slices per t .. per (t + 1) - 1
@@ -499,30 +563,30 @@ __device__ __forceinline__ void sample_slices(const Sample& a, int64_t row, cons
     b += m;
   }
   last = block_max(last, L);
-  if (tid == 0) L.found = 0;
+  if (tid == 0) L.m.found = 0;
   __syncthreads();
   // the first slice at whose end the sum is past the spot
   b = before;
   for (int j = tid * per; j < min(a.slices, (tid + 1) * per); ++j) {
     const double m = mass(j);
     if (m > 0.0 && b + m > want) {
-      atomicMax(&L.found, 0x80000000u - (uint32_t)j);
+      atomicMax(&L.m.found, 0x80000000u - (uint32_t)j);
       break;
     }
     b += m;
   }
   __syncthreads();
-  const bool past = L.found == 0;
-  const int j = past ? (int)last - 1 : (int)(0x80000000u - L.found);
+  const bool past = L.m.found == 0;
+  const int j = past ? (int)last - 1 : (int)(0x80000000u - L.m.found);
   // what the slices before it add up to, as its thread had it
   __syncthreads();
   if (tid == j / per) {
     double s = before;
     for (int i = tid * per; i < j; ++i) s += mass(i);
-    L.found_above = __builtin_bit_cast(u64, s);
+    L.m.found_above = __builtin_bit_cast(u64, s);
   }
   __syncthreads();
-  const double rest = past ? INFINITY : want - __builtin_bit_cast(double, L.found_above);
+  const double rest = past ? INFINITY : want - __builtin_bit_cast(double, L.m.found_above);
   // 8 tokens a thread
   const int at = j * kSliceTokens + tid * 8;
   float v[8];
@@ -550,7 +614,7 @@ __device__ __forceinline__ void sample_slices(const Sample& a, int64_t row, cons
 }
 
 // The row's sum of w over that of its largest token, from its slices' histograms; false if z / T is too large for them.
-__device__ __forceinline__ bool sum_of_histograms(const Sample& a, int64_t row, const RowParams& r, uint32_t top, double& sum, RowLds& L) {
+__device__ __forceinline__ bool sum_of_histograms(const Sample& a, int64_t row, const RowParams& r, uint32_t top, double& sum, Row& L) {
   const float zt = key_value(top);
   if (!Bins::fits(zt, r.T, 4096.0)) return false;
   const Bins b{8.0 / (double)r.T};
@@ -570,7 +634,7 @@ __device__ __forceinline__ bool sum_of_histograms(const Sample& a, int64_t row, 
 // the nucleus ends; its tokens are listed and ranked; and the slice that the draw falls into is read once more.  False:
 // the bin has too many tokens for the list, or the row too many slices.
 template <class T>
-__device__ __forceinline__ bool sample_nucleus(const Sample& a, int64_t row, const RowParams& r, const Weigh& w, RowLds& L) {
+__device__ __forceinline__ bool sample_nucleus(const Sample& a, int64_t row, const RowParams& r, const Weigh& w, Row& L) {
   const T* z = (const T*)a.logits + row * a.V;
   const int V = a.V, tid = threadIdx.x, lane = tid & 63, wave = tid >> 6, J = a.slices;
   if (J > kMaxSlices) return false;
@@ -581,28 +645,28 @@ __device__ __forceinline__ bool sample_nucleus(const Sample& a, int64_t row, con
   // Bin top_bin - i of all slices, in doubles (whole numbers of at most 2^62), weighted relative to top_bin's lower edge: bins
   // of thread t < kHistBins are its own.
   __syncthreads();
-  if (tid < J) L.nucleus.base[tid] = a.slice_bin[row * J + tid];
+  if (tid < J) L.m.nucleus.base[tid] = a.slice_bin[row * J + tid];
   __syncthreads();
   u64 count = 0;
   if (tid < kHistBins)
     for (int j = 0; j < J; ++j) {
-      const int i = top_bin - tid - L.nucleus.base[j];
-      if (L.nucleus.base[j] != INT_MIN && i >= 0 && i < kHistBins) count += H[(int64_t)j * kHistBins + i];
+      const int i = top_bin - tid - L.m.nucleus.base[j];
+      if (L.m.nucleus.base[j] != INT_MIN && i >= 0 && i < kHistBins) count += H[(int64_t)j * kHistBins + i];
     }
   const double mass = (double)count * exp_bin(-tid);
   double all;
   const double before = block_scan(mass, all, L);
   const double need = (double)r.p * all;
-  if (tid == 0) L.found = kHistBins;
+  if (tid == 0) L.m.found = kHistBins;
   __syncthreads();
   if (count && before < need && before + mass >= need) {
-    L.found = tid;
-    L.found_above = __builtin_bit_cast(u64, before);
+    L.m.found = tid;
+    L.m.found_above = __builtin_bit_cast(u64, before);
   }
   __syncthreads();
-  int last = L.found;
+  int last = L.m.found;
   if (last == kHistBins) return false;   // the sums' rounding
-  double rest = need - __builtin_bit_cast(double, L.found_above);   // of the bin, by its lower edge relative to top_bin's
+  double rest = need - __builtin_bit_cast(double, L.m.found_above);   // of the bin, by its lower edge relative to top_bin's
   // min-p may end higher up: then it alone cuts the bin in which it does
   bool ranked = true;
   if (w.min_w > 0.0) {
@@ -615,31 +679,18 @@ __device__ __forceinline__ bool sample_nucleus(const Sample& a, int64_t row, con
   }
   const int edge = top_bin - last;   // the bin itself
 
-  // Its tokens, in order: each wave a stretch of the row, counted first and then written.
-  const int share = (V + 64 * kRowWaves - 1) / (64 * kRowWaves) * 64, j0 = wave * share, j1 = min(V, j0 + share);
+  // Its tokens, in order.
   const float lo = (float)(((double)edge - 0.01) / b.scale), hi = (float)(((double)edge + 1.01) / b.scale);   // around it
-  auto tokens = [&](auto&& f) {
-    for (int j = j0; j < j1; j += 64) {
-      const float v = j + lane < j1 ? load1<T>(z + j + lane) : -INFINITY;
-      const bool in = v >= lo && v <= hi && b.bin(v) == edge;
-      f(__ballot(in), in, v, j + lane);
-    }
-  };
-  u64 n = 0, total;
-  tokens([&](u64 hit, bool, float, int) { n += __popcll(hit); });
-  u64 first = block_scan(lane == 0 ? n : 0ull, total, L);
-  uint32_t start = (uint32_t)__shfl(first, 0);
-  if (total > kNucleusMost) return false;
-  tokens([&](u64 hit, bool in, float v, int j) {
-    if (in) {
-      const uint32_t i = start + (uint32_t)__popcll(hit & ((1ull << lane) - 1));
-      L.nucleus.key[i] = value_key(v);
-      L.nucleus.index[i] = j;
-    }
-    start += (uint32_t)__popcll(hit);
-  });
-  __syncthreads();
-  const int listed = (int)total;
+  const int listed = (int)min(collect(z, V, (V + 7) / 8, kNucleusMost, [](int c) { return 8 * c; },
+                                      [&](float v, int) {
+                                        const bool near = v >= lo && v <= hi;
+                                        return __ballot(near) ? near && b.bin(v) == edge : false;
+                                      },
+                                      [&](uint32_t i, float v, int j) {
+                                        L.m.nucleus.key[i] = value_key(v);
+                                        L.m.nucleus.index[i] = j;
+                                      }, L), (uint32_t)INT_MAX);
+  if (listed > kNucleusMost) return false;
   auto weight = [&](uint32_t key) { return (u64)rint(b.over(key_value(key)) * unit); };
   uint32_t cut = 0;
   u64 ties = 0;
@@ -647,9 +698,9 @@ __device__ __forceinline__ bool sample_nucleus(const Sample& a, int64_t row, con
     u64 own = 0, sum;
     uint32_t most = 0, least = 0;
     for (int i = tid; i < listed; i += kRowThreads) {
-      own += weight(L.nucleus.key[i]);
-      most = max(most, L.nucleus.key[i]);
-      least = max(least, ~L.nucleus.key[i]);
+      own += weight(L.m.nucleus.key[i]);
+      most = max(most, L.m.nucleus.key[i]);
+      least = max(least, ~L.m.nucleus.key[i]);
     }
     block_scan(own, sum, L);
     most = block_max(most, L);
@@ -658,7 +709,7 @@ __device__ __forceinline__ bool sample_nucleus(const Sample& a, int64_t row, con
     const u64 want = min(want_real < 1.0 ? 1ull : (u64)want_real, sum);
     u64 above;
     cut = find_key(least, most, want, above, [&](auto&& f) {
-      for (int i = tid; i < listed; i += kRowThreads) f(L.nucleus.key[i], weight(L.nucleus.key[i]));
+      for (int i = tid; i < listed; i += kRowThreads) f(L.m.nucleus.key[i], weight(L.m.nucleus.key[i]));
     }, L);
     ties = ties_needed(want, above, weight(cut));
   }
@@ -667,41 +718,41 @@ __device__ __forceinline__ bool sample_nucleus(const Sample& a, int64_t row, con
   // Kept mass of each slice: its bins above, and the listed tokens that stay.
   __syncthreads();
   if (tid < J) {
-    L.nucleus.extra[tid] = 0;
-    L.nucleus.equal[tid] = 0;
+    L.m.nucleus.extra[tid] = 0;
+    L.m.nucleus.equal[tid] = 0;
   }
   __syncthreads();
   {
     // ties in order: thread t has tokens per t .. per (t + 1) - 1 of the list
     const int per = (listed + kRowThreads - 1) / kRowThreads;
     u64 same = 0, none;
-    for (int i = tid * per; i < min(listed, (tid + 1) * per); ++i) same += L.nucleus.key[i] == cut;
+    for (int i = tid * per; i < min(listed, (tid + 1) * per); ++i) same += L.m.nucleus.key[i] == cut;
     u64 tie = block_scan(same, none, L);
     for (int i = tid * per; i < min(listed, (tid + 1) * per); ++i) {
-      const uint32_t k = L.nucleus.key[i];
-      const int j = L.nucleus.index[i] / kSliceTokens;
+      const uint32_t k = L.m.nucleus.key[i];
+      const int j = L.m.nucleus.index[i] / kSliceTokens;
       bool keep = k > cut;
       if (k == cut) {
-        atomicAdd(&L.nucleus.equal[j], 1u);
+        atomicAdd(&L.m.nucleus.equal[j], 1u);
         keep = tie++ < ties;
       }
-      if (keep && passes(k)) atomicAdd(&L.nucleus.extra[j], weight(k));
+      if (keep && passes(k)) atomicAdd(&L.m.nucleus.extra[j], weight(k));
     }
   }
   __syncthreads();
   // a wave a slice
   for (int j = wave; j < J; j += kRowWaves) {
-    const int base = L.nucleus.base[j];
+    const int base = L.m.nucleus.base[j];
     double m = 0.0;
     if (base != INT_MIN)
       for (int i = lane; i < kHistBins; i += 64)
         if (base + i > edge) m += (double)H[(int64_t)j * kHistBins + i] * exp_bin(base + i - top_bin);
-    m = wave_reduce(m, [](double x, double y) { return x + y; });
-    if (lane == 0) L.nucleus.slice[j] = m + (double)L.nucleus.extra[j] * exp_bin(-last);
+    m = wave_all(m, Add());
+    if (lane == 0) L.m.nucleus.slice[j] = m + (double)L.m.nucleus.extra[j] * exp_bin(-last);
   }
   __syncthreads();
-  double own = tid < J ? L.nucleus.slice[tid] : 0.0, kept;
-  const u64 equal = tid < J ? L.nucleus.equal[tid] : 0;
+  double own = tid < J ? L.m.nucleus.slice[tid] : 0.0, kept;
+  const u64 equal = tid < J ? L.m.nucleus.equal[tid] : 0;
   const double sum_before = block_scan(own, kept, L);
   u64 equals;
   const u64 equal_before = block_scan(equal, equals, L);
@@ -712,12 +763,12 @@ __device__ __forceinline__ bool sample_nucleus(const Sample& a, int64_t row, con
   const int slice = past ? (int)end - 1 : kMaxSlices - (int)at;
   __syncthreads();
   if (tid == slice) {
-    L.found_above = __builtin_bit_cast(u64, sum_before);
-    L.carried = equal_before;
+    L.m.found_above = __builtin_bit_cast(u64, sum_before);
+    L.m.carried = equal_before;
   }
   __syncthreads();
-  const double left = past ? INFINITY : spot - __builtin_bit_cast(double, L.found_above);
-  u64 tie = L.carried;
+  const double left = past ? INFINITY : spot - __builtin_bit_cast(double, L.m.found_above);
+  u64 tie = L.m.carried;
   // 8 tokens a thread
   const int t0 = slice * kSliceTokens + tid * 8;
   float v[8];
@@ -760,23 +811,27 @@ __device__ __forceinline__ bool sample_nucleus(const Sample& a, int64_t row, con
 
 // GROUPS: the groups' largest come from sample_slice_kernel; else the workgroup finds them.
 template <class T, bool GROUPS> __global__ void __launch_bounds__(kRowThreads) sample_row_kernel(Sample a) {
-  __shared__ RowLds L;
+  __shared__ RowLds lds;
+  Row L{lds, 0};
   const int64_t row = blockIdx.x;
   const T* z = (const T*)a.logits + row * a.V;
   const int V = a.V, tid = threadIdx.x, lane = tid & 63;
   RowParams r;
   r.load(a, row);
+  L.m.hist[tid] = 0;
+  L.m.hist[tid + kRowThreads] = 0;
   // Groups of `size` tokens, so many that their largest fit in LDS.
   int size = kGroupTokens;
   while ((V + size - 1) / size > kGroups) size *= 2;
   const int groups = (V + size - 1) / size, merge = size / kGroupTokens;
-  uint32_t top = 0;
+  uint32_t top = 0, under = 0;   // under: the complement of the least group that a mask left
   if constexpr (GROUPS) {
     for (int i = tid; i < groups; i += kRowThreads) {
       uint32_t g = 0;
       for (int m = i * merge; m < min(a.groups, (i + 1) * merge); ++m) g = max(g, a.group_top[row * a.groups + m]);
-      L.list.group[i] = g;
+      L.m.list.group[i] = g;
       top = max(top, g);
+      under = max(under, g > kKeyMinusInf ? ~g : 0u);
     }
   } else {
     for (int j0 = 0; j0 < V; j0 += kRowThreads * 8) {
@@ -789,23 +844,24 @@ template <class T, bool GROUPS> __global__ void __launch_bounds__(kRowThreads) s
         if (j + e < V) g = max(g, v[e] != v[e] ? kKeyNan : value_key(v[e]));
       g = max(g, (uint32_t)__shfl_xor((int)g, 1));
       g = max(g, (uint32_t)__shfl_xor((int)g, 2));
-      if ((tid & 3) == 0 && j < V) L.list.group[j / kGroupTokens] = g;
+      if ((tid & 3) == 0 && j < V) L.m.list.group[j / kGroupTokens] = g;
       top = max(top, g);
+      under = max(under, g > kKeyMinusInf && j < V ? ~g : 0u);
     }
   }
-  top = block_max(top, L);
+  block_max(top, under, L);
   if (top > kKeyInf || top <= kKeyMinusInf) {   // a NaN, or no token left
     if (tid == 0) a.tokens[row] = -1;
     return;
   }
   const int s = 62 - (V > 2 ? 32 - __clz(V - 1) : 1);   // V 2^s <= 2^62
-  const Weigh w{key_value(top), 1.0 / (double)r.T, (double)(1ull << s),
+  const Weigh w{key_value(top), kLog2eDouble / (double)r.T, (double)(1ull << s),
                 r.min_p > 0.f ? (double)fminf(r.min_p, 1.f) : 0.0};
 
   if (r.greedy() || r.p <= 0.f) {   // the first token of the first group that has the largest
     uint32_t g = 0;
     for (int i = tid; i < groups; i += kRowThreads)
-      if (L.list.group[i] == top) g = max(g, (uint32_t)(kGroups - i));
+      if (L.m.list.group[i] == top) g = max(g, (uint32_t)(kGroups - i));
     g = kGroups - block_max(g, L);
     if (tid >= 64) return;
     for (int j0 = (int)g * size;; j0 += 64) {
@@ -822,24 +878,12 @@ template <class T, bool GROUPS> __global__ void __launch_bounds__(kRowThreads) s
   uint32_t low = 0;
   double whole = 0.0;   // the row's sum of w, for top-p without top-k
   bool sure = true;     // else only if the tokens from low on have p of the sum
-  // the key of the i-th of the groups' largest
+  // a key that i of the groups' largest reach, and few more
   auto ith_group = [&](int64_t i) {
-    uint32_t least = 0;   // of those that a mask left, from above
-    u64 n = 0, all;
-    for (int g = tid; g < groups; g += kRowThreads) {
-      const uint32_t k = L.list.group[g];
-      if (k > kKeyMinusInf) {
-        least = max(least, ~k);
-        ++n;
-      }
-    }
-    block_scan(n, all, L);
-    least = ~block_max(least, L);
-    if ((u64)i > all) return 0u;
     u64 above;
-    return find_key(least, top, (u64)i, above, [&](auto&& f) {
-      for (int g = tid; g < groups; g += kRowThreads) f(L.list.group[g], 1ull);
-    }, L);
+    return find_key(~under, top, (u64)i, above, [&](auto&& f) {
+      for (int g = tid; g < groups; g += kRowThreads) f(L.m.list.group[g], 1ull);
+    }, L, true);
   };
   if (r.k) {
     if (r.k <= groups) low = ith_group(r.k);
@@ -891,47 +935,27 @@ template <class T, bool GROUPS> __global__ void __launch_bounds__(kRowThreads) s
   uint32_t pass = 0;   // bits: at most 8 groups a thread
   __syncthreads();
   for (int i = 0; i < per; ++i)
-    if (tid * per + i < groups && L.list.group[tid * per + i] >= low) pass |= 1u << i;
+    if (tid * per + i < groups && L.m.list.group[tid * per + i] >= low) pass |= 1u << i;
   u64 found;
   u64 at = block_scan((u64)__popc(pass), found, L);
   __syncthreads();
   for (int i = 0; i < per; ++i)
-    if (pass >> i & 1) L.list.group[at++] = tid * per + i;
+    if (pass >> i & 1) L.m.list.group[at++] = tid * per + i;
   __syncthreads();
-  // Their tokens, in order: each wave a stretch of the found groups, counted first and then written.
-  const int wave = tid >> 6, share = ((int)found + kRowWaves - 1) / kRowWaves;
-  const int g0 = min((int)found, wave * share), g1 = min((int)found, g0 + share);
-  u64 n = 0;
-  auto tokens = [&](auto&& f) {
-    // 64 tokens at a time: two groups of 32, or a part of a larger group
-    const int step = size > 64 ? 64 : size, chunks = size / step, at_once = 64 / step;
-    for (int g = g0; g < g1; g += at_once)
-      for (int c = 0; c < chunks; ++c) {
-        const int mine = g + lane / step;
-        const int j = mine < g1 ? (int)L.list.group[mine] * size + c * step + lane % step : V;
-        const float v = j < V ? load1<T>(z + j) : -INFINITY;
-        f(value_key(v), v, j);
-      }
-  };
-  tokens([&](uint32_t k, float, int) { n += __popcll(__ballot(k >= low)); });
-  u64 total;
-  u64 first = block_scan(lane == 0 ? n : 0ull, total, L);
-  uint32_t start = (uint32_t)__shfl(first, 0);
+  // Their tokens, in order.
+  const int runs = size / 8, shift = 31 - __clz(runs);
+  const uint32_t total = collect(z, V, (int)found << shift, kMost,
+                                 [&](int c) { return (int)L.m.list.group[c >> shift] * size + (c & (runs - 1)) * 8; },
+                                 [&](float v, int) { return value_key(v) >= low; },
+                                 [&](uint32_t i, float v, int j) {
+                                   L.m.list.key[i] = value_key(v);
+                                   L.m.list.index[i] = j;
+                                   L.m.list.weight[i] = w(v);
+                                 }, L);
   if (total > kMost) {
     if (GROUPS && !r.k && r.p < 1.f && w.top < INFINITY && sample_nucleus<T>(a, row, r, w, L)) return;
     return sample_whole<T>(a, row, r, w, top, L);
   }
-  tokens([&](uint32_t k, float v, int j) {
-    const u64 hit = __ballot(k >= low);
-    if (k >= low) {
-      const uint32_t i = start + (uint32_t)__popcll(hit & ((1ull << lane) - 1));
-      L.list.key[i] = k;
-      L.list.index[i] = j;
-      L.list.weight[i] = w(v);
-    }
-    start += (uint32_t)__popcll(hit);
-  });
-  __syncthreads();
 
   // Tokens above key `cut` are kept and the first `ties` at it.
   const int count = (int)total;
@@ -940,14 +964,14 @@ template <class T, bool GROUPS> __global__ void __launch_bounds__(kRowThreads) s
   if (r.k && r.k < count) {
     u64 above;
     cut = find_key(low, top, (u64)r.k, above, [&](auto&& f) {
-      for (int i = tid; i < count; i += kRowThreads) f(L.list.key[i], 1ull);
+      for (int i = tid; i < count; i += kRowThreads) f(L.m.list.key[i], 1ull);
     }, L);
     ties = (u64)r.k - above;
   }
   if (r.p < 1.f) {
     u64 sum = 0, all;
     for (int i = tid; i < count; i += kRowThreads)
-      if (L.list.key[i] > cut) sum += L.list.weight[i];
+      if (L.m.list.key[i] > cut) sum += L.m.list.weight[i];
     block_scan(sum, all, L);
     const u64 at_cut = cut ? ties * w(key_value(cut)) : 0;
     all += at_cut;
@@ -965,7 +989,7 @@ template <class T, bool GROUPS> __global__ void __launch_bounds__(kRowThreads) s
       const uint32_t was = cut;
       cut = find_key(low, top, want, above, [&](auto&& f) {
         for (int i = tid; i < count; i += kRowThreads)
-          if (L.list.key[i] > was) f(L.list.key[i], L.list.weight[i]);
+          if (L.m.list.key[i] > was) f(L.m.list.key[i], L.m.list.weight[i]);
         if (tid == 0 && at_cut) f(was, at_cut);
       }, L);
       const u64 need = ties_needed(want, above, w(key_value(cut)));
@@ -975,7 +999,7 @@ template <class T, bool GROUPS> __global__ void __launch_bounds__(kRowThreads) s
   // The draw: thread t has tokens 4 t .. 4 t + 3 of the list.
   u64 same = 0, none;
 #pragma unroll
-  for (int e = 0; e < 4; ++e) same += 4 * tid + e < count && L.list.key[4 * tid + e] == cut;
+  for (int e = 0; e < 4; ++e) same += 4 * tid + e < count && L.m.list.key[4 * tid + e] == cut;
   u64 tie = block_scan(same, none, L);
   u64 weight[4], sum = 0;
 #pragma unroll
@@ -983,9 +1007,9 @@ template <class T, bool GROUPS> __global__ void __launch_bounds__(kRowThreads) s
     const int i = 4 * tid + e;
     weight[e] = 0;
     if (i >= count) continue;
-    const uint32_t k = L.list.key[i];
+    const uint32_t k = L.m.list.key[i];
     if (k > cut || (k == cut && tie++ < ties))
-      weight[e] = w.min_w == 0.0 || w.real(key_value(k)) >= w.min_w ? L.list.weight[i] : 0;
+      weight[e] = w.min_w == 0.0 || w.real(key_value(k)) >= w.min_w ? L.m.list.weight[i] : 0;
     sum += weight[e];
   }
   u64 all;
@@ -993,7 +1017,7 @@ template <class T, bool GROUPS> __global__ void __launch_bounds__(kRowThreads) s
   const u64 want = spot(r.u, all);
 #pragma unroll
   for (int e = 0; e < 4; ++e) {
-    if (before <= want && want < before + weight[e]) a.tokens[row] = L.list.index[4 * tid + e];
+    if (before <= want && want < before + weight[e]) a.tokens[row] = L.m.list.index[4 * tid + e];
     before += weight[e];
   }
 }
