@@ -10,10 +10,10 @@
 // The logits are read once, by as many workgroups as they fill: each takes 8192 tokens
 // and leaves their largest, the largest of every 32, and, for rows that need it, the sum
 // of their w and, for top-p, its histogram.  Then one workgroup a row finds the tokens
-// that can be kept from the largest of each 32 alone: the k-th of those is not above the
-// k-th token, and if the tokens from some value on have p of the sum, no other is kept.
+// that can be kept from these alone: the k-th of the groups' largest is not above the
+// k-th token, and a histogram says in which bin top-p's nucleus ends.
 // It reads these tokens' groups only, and ranks and draws among at most 4096 tokens in
-// LDS.  A nucleus of more tokens is found from the histograms (sample_nucleus); what
+// LDS.  A nucleus of more tokens is drawn from by the histograms (sample_nucleus); what
 // else keeps more goes through sample_whole, which reads the row several times.  Rows of
 // up to 8192 tokens take one launch: their workgroup finds the groups' largest itself.
 //
@@ -245,6 +245,7 @@ struct RowLds {
   u64 found_above, carried;
   uint32_t found;
   u64 hist[kBins];   // zero between find_key's uses
+  int base[kMaxSlices];   // the slices' first bins
   union {
     struct {
       uint32_t group[kGroups];      // largest key of each group; then the groups that pass, in order
@@ -256,7 +257,6 @@ struct RowLds {
       double slice[kMaxSlices];
       u64 extra[kMaxSlices];
       uint32_t equal[kMaxSlices];
-      int base[kMaxSlices];
     } nucleus;
     struct {
       u64 mass[kUnits];
@@ -613,60 +613,58 @@ __device__ __forceinline__ void sample_slices(const Sample& a, int64_t row, cons
   if (tid == 0) a.tokens[row] = first ? (int64_t)(0x80000000u - first) : (int64_t)end - 1;
 }
 
-// The row's sum of w over that of its largest token, from its slices' histograms; false if z / T is too large for them.
-__device__ __forceinline__ bool sum_of_histograms(const Sample& a, int64_t row, const RowParams& r, uint32_t top, double& sum, Row& L) {
-  const float zt = key_value(top);
-  if (!Bins::fits(zt, r.T, 4096.0)) return false;
+// Where top-p's nucleus ends, from the histograms of the row's slices.
+struct Nucleus {
+  int top_bin, last;   // it ends in bin top_bin - last
+  double sum;          // of w, relative to the largest token's
+  double rest;         // what that bin has to give, relative to top_bin's lower edge, in 2^-hist_shift
+};
+// False: z / T is too large for histograms, or the row has too many slices (or a sum's rounding fell between two bins).
+__device__ __forceinline__ bool find_nucleus(const Sample& a, int64_t row, const RowParams& r, float top, Nucleus& n, Row& L) {
+  if (a.slices > kMaxSlices || !Bins::fits(top, r.T, 4096.0)) return false;
+  const int tid = threadIdx.x, J = a.slices;
   const Bins b{8.0 / (double)r.T};
-  const int top_bin = b.bin(zt);
-  double own = 0.0;
-  for (int64_t i = threadIdx.x; i < (int64_t)a.slices * kHistBins; i += kRowThreads) {
-    const int base = a.slice_bin[row * a.slices + i / kHistBins];
-    if (base == INT_MIN) continue;   // nothing there, or only what is far under the top
-    own += (double)a.hist[row * a.slices * kHistBins + i] * exp_bin(base + (int)(i % kHistBins) - top_bin);
-  }
-  block_scan(own, sum, L);
-  sum /= b.over(zt) * (double)(1ull << a.hist_shift);
-  return true;
-}
-
-// top-p (and min-p) over a row whose nucleus has more tokens than the list holds.  The histograms give the bin in which
-// the nucleus ends; its tokens are listed and ranked; and the slice that the draw falls into is read once more.  False:
-// the bin has too many tokens for the list, or the row too many slices.
-template <class T>
-__device__ __forceinline__ bool sample_nucleus(const Sample& a, int64_t row, const RowParams& r, const Weigh& w, Row& L) {
-  const T* z = (const T*)a.logits + row * a.V;
-  const int V = a.V, tid = threadIdx.x, lane = tid & 63, wave = tid >> 6, J = a.slices;
-  if (J > kMaxSlices) return false;
-  const Bins b{8.0 / (double)r.T};
-  const int top_bin = b.bin(w.top);
-  const double unit = (double)(1ull << a.hist_shift);
+  n.top_bin = b.bin(top);
   const u64* H = a.hist + row * J * kHistBins;
-  // Bin top_bin - i of all slices, in doubles (whole numbers of at most 2^62), weighted relative to top_bin's lower edge: bins
-  // of thread t < kHistBins are its own.
+  if (tid < J) L.m.base[tid] = a.slice_bin[row * J + tid];
+  if (tid == 0) L.m.found = kHistBins;
   __syncthreads();
-  if (tid < J) L.m.nucleus.base[tid] = a.slice_bin[row * J + tid];
-  __syncthreads();
+  // Thread t sums bin top_bin - t over the slices: a whole number of at most 2^62.  Bins are weighted relative to
+  // top_bin's lower edge.
   u64 count = 0;
   if (tid < kHistBins)
+#pragma unroll 4
     for (int j = 0; j < J; ++j) {
-      const int i = top_bin - tid - L.m.nucleus.base[j];
-      if (L.m.nucleus.base[j] != INT_MIN && i >= 0 && i < kHistBins) count += H[(int64_t)j * kHistBins + i];
+      const int base = L.m.base[j], i = n.top_bin - tid - base;
+      if (base != INT_MIN && i >= 0 && i < kHistBins) count += H[(int64_t)j * kHistBins + i];
     }
   const double mass = (double)count * exp_bin(-tid);
   double all;
-  const double before = block_scan(mass, all, L);
-  const double need = (double)r.p * all;
-  if (tid == 0) L.m.found = kHistBins;
-  __syncthreads();
+  const double before = block_scan(mass, all, L), need = (double)r.p * all;
   if (count && before < need && before + mass >= need) {
     L.m.found = tid;
     L.m.found_above = __builtin_bit_cast(u64, before);
   }
   __syncthreads();
-  int last = L.m.found;
-  if (last == kHistBins) return false;   // the sums' rounding
-  double rest = need - __builtin_bit_cast(double, L.m.found_above);   // of the bin, by its lower edge relative to top_bin's
+  n.last = L.m.found;
+  n.rest = need - __builtin_bit_cast(double, L.m.found_above);
+  n.sum = all / (b.over(top) * (double)(1ull << a.hist_shift));
+  return n.last < kHistBins;
+}
+
+// top-p (and min-p) over a row whose nucleus has more tokens than the list holds: the tokens of the bin in which it ends
+// are listed and ranked, and the slice that the draw falls into is read once more.  False: the bin has too many tokens.
+template <class T>
+__device__ __forceinline__ bool sample_nucleus(const Sample& a, int64_t row, const RowParams& r, const Weigh& w, const Nucleus& nuc, Row& L) {
+  const T* z = (const T*)a.logits + row * a.V;
+  const int V = a.V, tid = threadIdx.x, lane = tid & 63, wave = tid >> 6, J = a.slices;
+  const Bins b{8.0 / (double)r.T};
+  const int top_bin = nuc.top_bin;
+  const double unit = (double)(1ull << a.hist_shift);
+  const u64* H = a.hist + row * J * kHistBins;
+  int last = nuc.last;
+  double all;
+  __syncthreads();
   // min-p may end higher up: then it alone cuts the bin in which it does
   bool ranked = true;
   if (w.min_w > 0.0) {
@@ -705,7 +703,7 @@ __device__ __forceinline__ bool sample_nucleus(const Sample& a, int64_t row, con
     block_scan(own, sum, L);
     most = block_max(most, L);
     least = ~block_max(least, L);
-    const double want_real = ceil(rest / exp_bin(-last));
+    const double want_real = ceil(nuc.rest / exp_bin(-last));
     const u64 want = min(want_real < 1.0 ? 1ull : (u64)want_real, sum);
     u64 above;
     cut = find_key(least, most, want, above, [&](auto&& f) {
@@ -742,7 +740,7 @@ __device__ __forceinline__ bool sample_nucleus(const Sample& a, int64_t row, con
   __syncthreads();
   // a wave a slice
   for (int j = wave; j < J; j += kRowWaves) {
-    const int base = L.m.nucleus.base[j];
+    const int base = L.m.base[j];
     double m = 0.0;
     if (base != INT_MIN)
       for (int i = lane; i < kHistBins; i += 64)
@@ -877,55 +875,44 @@ template <class T, bool GROUPS> __global__ void __launch_bounds__(kRowThreads) s
   // Every token that can be kept has a key of at least `low`.
   uint32_t low = 0;
   double whole = 0.0;   // the row's sum of w, for top-p without top-k
-  bool sure = true;     // else only if the tokens from low on have p of the sum
-  // a key that i of the groups' largest reach, and few more
-  auto ith_group = [&](int64_t i) {
-    u64 above;
-    return find_key(~under, top, (u64)i, above, [&](auto&& f) {
-      for (int g = tid; g < groups; g += kRowThreads) f(L.m.list.group[g], 1ull);
-    }, L, true);
-  };
+  Nucleus nuc;
+  bool binned = false;  // top-p's end is known from histograms
   if (r.k) {
-    if (r.k <= groups) low = ith_group(r.k);
+    // a key that k of the groups' largest reach, and few more
+    if (r.k <= groups) {
+      u64 above;
+      low = find_key(~under, top, (u64)r.k, above, [&](auto&& f) {
+        for (int g = tid; g < groups; g += kRowThreads) f(L.m.list.group[g], 1ull);
+      }, L, true);
+    }
   } else {
     if (GROUPS && !(r.p < 1.f) && w.min_w == 0.0) return sample_slices<T>(a, row, r, w, L);
     if (w.top == INFINITY) {
       low = kKeyInf;
       if (r.p < 1.f) {   // the sum is a number of tokens
         u64 own = 0, all;
-        for (int j = tid * 8; j < V; j += kRowThreads * 8) {
-          float v[8];
-          load_some<T, 8>(z + j, V - j, v);
-#pragma unroll
-          for (int e = 0; e < 8; ++e) own += j + e < V && v[e] == INFINITY;
-        }
+        each_token(z, V, [&](float v, int) { own += v == INFINITY; });
         block_scan(own, all, L);
         whole = (double)all;
       }
     } else {
-      double least = w.min_w;   // w under which none is kept
+      double cut = w.min_w > 0.0 ? (double)w.top + (double)r.T * log(w.min_w) : -INFINITY;   // no token under it is kept
       if (r.p < 1.f) {
         if constexpr (GROUPS) {
-          if (!sum_of_histograms(a, row, r, top, whole, L)) return sample_whole<T>(a, row, r, w, top, L);
+          if (!find_nucleus(a, row, r, w.top, nuc, L)) return sample_whole<T>(a, row, r, w, top, L);
+          binned = true;
+          whole = nuc.sum;
+          cut = fmax(cut, (double)(nuc.top_bin - nuc.last) * ((double)r.T * 0.125));
         } else {
           double own = 0.0;
           each_token(z, V, [&](float v, int) { own += w.real(v); });
           block_scan(own, whole, L);
-        }
-        least = fmax(least, (1.0 - (double)r.p) * whole / V);
-      }
-      if (least > 0.0) {
-        // with a margin for the rounding of all this
-        const double cut = (double)w.top + (double)r.T * (log(fmin(least, 1.0)) - 1e-9);
-        if (cut > -3e38) low = value_key(fminf((float)cut - fabsf((float)cut) * 1e-6f, w.top));
-      }
-      if (GROUPS && r.p < 1.f) {   // a value that some thousand tokens at most should reach
-        const uint32_t some = ith_group(min(2048, groups / 2));
-        if (some > low) {
-          low = some;
-          sure = false;
+          cut = fmax(cut, (double)w.top + (double)r.T * log(fmin((1.0 - (double)r.p) * whole / V, 1.0)));
         }
       }
+      // with a margin for the rounding of all this
+      cut -= 1e-6 * (fabs(cut) + fabs((double)w.top)) + 1e-9 * (double)r.T;
+      if (cut > -3e38) low = value_key(fminf((float)cut, w.top));
     }
   }
   low = max(low, kKeyMinusInf + 1);   // masked tokens have no weight
@@ -942,6 +929,8 @@ template <class T, bool GROUPS> __global__ void __launch_bounds__(kRowThreads) s
   for (int i = 0; i < per; ++i)
     if (pass >> i & 1) L.m.list.group[at++] = tid * per + i;
   __syncthreads();
+  // Of so many groups' tokens the list would hardly hold those that stay (independent ones: 3% of the row's).
+  if (binned && found * 20 > (u64)groups * 13 && sample_nucleus<T>(a, row, r, w, nuc, L)) return;
   // Their tokens, in order.
   const int runs = size / 8, shift = 31 - __clz(runs);
   const uint32_t total = collect(z, V, (int)found << shift, kMost,
@@ -950,12 +939,13 @@ template <class T, bool GROUPS> __global__ void __launch_bounds__(kRowThreads) s
                                  [&](uint32_t i, float v, int j) {
                                    L.m.list.key[i] = value_key(v);
                                    L.m.list.index[i] = j;
-                                   L.m.list.weight[i] = w(v);
                                  }, L);
   if (total > kMost) {
-    if (GROUPS && !r.k && r.p < 1.f && w.top < INFINITY && sample_nucleus<T>(a, row, r, w, L)) return;
+    if (binned && sample_nucleus<T>(a, row, r, w, nuc, L)) return;
     return sample_whole<T>(a, row, r, w, top, L);
   }
+  for (int i = tid; i < (int)total; i += kRowThreads) L.m.list.weight[i] = w(key_value(L.m.list.key[i]));
+  __syncthreads();
 
   // Tokens above key `cut` are kept and the first `ties` at it.
   const int count = (int)total;
@@ -975,12 +965,7 @@ template <class T, bool GROUPS> __global__ void __launch_bounds__(kRowThreads) s
     block_scan(sum, all, L);
     const u64 at_cut = cut ? ties * w(key_value(cut)) : 0;
     all += at_cut;
-    const u64 need_all = nucleus(r.p, r.k ? (double)all : whole * w.unit);
-    if (!sure && need_all > all) {   // more tokens are kept than these
-      if (sample_nucleus<T>(a, row, r, w, L)) return;
-      return sample_whole<T>(a, row, r, w, top, L);
-    }
-    const u64 want = min(need_all, all);
+    const u64 want = min(nucleus(r.p, r.k ? (double)all : whole * w.unit), all);
     if (want == 0) {
       cut = top;
       ties = 1;
