@@ -36,7 +36,7 @@ struct NormBwd {
   float* part;               // [parts][H] fp32 sums for dweight
   int64_t N;
   int H;
-  int parts;                 // groups of lanes that walk rows: group p takes rows p, p + parts, ...
+  int parts;                 // workgroups: p takes groups of rows p, p + parts, ...
 };
 
 // Columns that a row's lanes hold in registers; longer rows are walked twice.

@@ -21,12 +21,14 @@ size_t mx_code_bytes(int64_t C, int format) { return (size_t)mx_cols(C) / (forma
 size_t mx_scale_bytes(int64_t C) { return (size_t)mx_cols(C) / flce::kMxBlock; }
 bool bad_format(int format) { return format != FLCE_MX_E4M3 && format != FLCE_MX_E2M1; }
 
-// Groups of lanes that walk the rows in the backward, each with sums of its own for
-// dweight: a whole number of workgroups.
+// Workgroups of the backward, each with sums of its own for dweight: 4 a CU of 256 threads, or
+// one of 1024.  (8192 x 4096 bf16: 1024 workgroups 59 us and 6 for adding their sums, 512 87 and
+// 4.5, 2048 62 and 10; 2000 x 16000: 256 58 and 5, 1024 68 and 12.)  Up to 1024 columns
+// a workgroup has four rows or more at once, and 512 are enough (16384 x 512 fp32).
 int64_t norm_parts(int64_t N, int64_t H) {
   if (H > flce::kNormMost) return std::min<int64_t>(N, 64);
-  const int64_t rows = flce::norm_rows(flce::norm_lanes((int)H, false));
-  return std::min<int64_t>(cdiv(N, rows), 512) * rows;
+  const int lanes = flce::norm_lanes((int)H, false);
+  return std::min<int64_t>(cdiv(N, flce::norm_rows(lanes)), lanes == 1024 ? 256 : lanes == 256 ? 1024 : 512);
 }
 size_t norm_bwd_bytes(int64_t N, int64_t H) { return align_up((size_t)norm_parts(N, H) * H * 4); }
 
@@ -63,8 +65,8 @@ flce_status norm_forward(const void* x, const void* residual, const void* weight
   a.N = N; a.H = (int)H; a.Hp = (int)mx_cols(H);
   a.format = format;
   a.eps = eps;
-  const int64_t groups = cdiv(N, flce::norm_rows(flce::norm_lanes(mx ? a.Hp : a.H, mx)));
-  a.blocks = (int)std::min<int64_t>(groups, 4096);
+  const int lanes = flce::norm_lanes(mx ? a.Hp : a.H, mx);
+  a.blocks = (int)std::min<int64_t>(cdiv(N, flce::norm_rows(lanes)), lanes == 1024 ? 512 : 2048);
   (void)hipGetLastError();
   flce::mark_launch(stream, nullptr);
   return flce::launch_rms_norm_forward(a, dtype, stream) == hipSuccess ? FLCE_OK : FLCE_ERR_HIP;

@@ -159,8 +159,9 @@ template <class T, int OUT> __global__ void __launch_bounds__(1024) norm_fwd_lon
   }
 }
 
-// Group p of lanes takes rows p, p + parts, ... and keeps its sums of dy n for
-// dweight in registers; norm_dw_kernel adds the groups' in their order.
+// A group of lanes keeps its rows' sums of dy n for dweight in registers; the groups of a
+// workgroup add theirs in LDS, and norm_dw_kernel the workgroups', all in a fixed order.
+// (A sum for each group: 4096 rows of 1024 columns had 2048 of them, 8 us to add up.)
 template <class T, int LANES, int C, bool VEC>
 __global__ void __launch_bounds__(norm_threads(LANES)) norm_bwd_kernel(NormBwd a) {
   constexpr int RB = norm_threads(LANES) / LANES;
@@ -169,7 +170,7 @@ __global__ void __launch_bounds__(norm_threads(LANES)) norm_bwd_kernel(NormBwd a
   const int lane = threadIdx.x % LANES, sub = threadIdx.x / LANES;
   float dw[C][8] = {};
   const float inv = 1.f / (float)a.H;
-  for (int64_t r0 = (int64_t)blockIdx.x * RB; r0 < a.N; r0 += a.parts) {
+  for (int64_t r0 = (int64_t)blockIdx.x * RB; r0 < a.N; r0 += (int64_t)a.parts * RB) {
     const int64_t row = r0 + sub, base = row * a.H;
     const bool live = row < a.N;
     const float rstd = live ? a.rstd[row] : 0.f;
@@ -206,7 +207,22 @@ __global__ void __launch_bounds__(norm_threads(LANES)) norm_bwd_kernel(NormBwd a
     }
   }
   if (a.dweight) {
-    float* p = a.part + ((int64_t)blockIdx.x * RB + sub) * a.H;
+    if constexpr (RB > 1) {
+      __shared__ float group[RB - 1][C][LANES][9];   // 9: lanes start on different banks
+#pragma unroll
+      for (int c = 0; c < C; ++c)
+#pragma unroll
+        for (int e = 0; e < 8; ++e)
+          if (sub > 0) group[sub - 1][c][lane][e] = dw[c][e];
+      __syncthreads();
+      if (sub > 0) return;
+#pragma unroll
+      for (int c = 0; c < C; ++c)
+        for (int g = 0; g < RB - 1; ++g)
+#pragma unroll
+          for (int e = 0; e < 8; ++e) dw[c][e] += group[g][c][lane][e];
+    }
+    float* p = a.part + (int64_t)blockIdx.x * a.H;
 #pragma unroll
     for (int c = 0; c < C; ++c) {
       const int col = (c * LANES + lane) * 8;
@@ -337,8 +353,7 @@ template <class T> static hipError_t norm_backward_t(const NormBwd& a, hipStream
     if (a.dweight) FLCE_LAUNCH((norm_dw_long_kernel<T>), dim3((a.H + 2047) / 2048, a.parts), dim3(256), 0, st, a);
   } else if (a.N > 0) {
     with_row<false>(a.H, [&](auto lanes, auto runs) {
-      constexpr int RB = norm_threads(lanes.value) / lanes.value;
-      const dim3 grid(a.parts / RB), blk(norm_threads(lanes.value));
+      const dim3 grid(a.parts), blk(norm_threads(lanes.value));
       if (a.H % 8 == 0) FLCE_LAUNCH((norm_bwd_kernel<T, lanes.value, runs.value, true>), grid, blk, 0, st, a);
       else FLCE_LAUNCH((norm_bwd_kernel<T, lanes.value, runs.value, false>), grid, blk, 0, st, a);
     });

@@ -7,8 +7,9 @@ Tolerances, element by element, with h the float32 step 2^-24:
    halves that, and the mean, eps, root and quotient add 4: under 96 h of rstd, and n = h rstd and y under 100 h;
  - mean(dn n): its sum's additions and its factors' errors, under 300 h of mean |dn n|; so dx is off by at most
    512 h (|dh| + rstd (|dn| + |n| mean |dn n|));
- - dweight: a group adds its rows one by one, then at most 64 groups' sums in a column's thread and 16 of those: under
-   (rows of a group + 256) h of sum |dy n|.
+ - dweight: a group of lanes adds its rows one by one (at most N / 256 of them, in rows past 16384 columns N / 64), a
+   workgroup up to 32 groups' sums, a column's thread up to 64 workgroups' and then 16 threads': under
+   (N / 256 + 256) h of sum |dy n|.
 """
 
 import math
@@ -68,7 +69,7 @@ def check(N, H, dt, residual=True, weight=True, dh=True, eps=1e-6, scale=1.0, se
     mag = rr * (dn.abs() + n.abs() * (dn * n).abs().mean(1, keepdim=True)) + (g.double().abs() if dh else 0)
     close(dx, dx64, half(dx64, dt) + 512 * STEP * mag, "dx")
     dw64 = (dy.double() * n).sum(0)
-    rows = math.ceil(N / 64) if H > 16384 else math.ceil(N / 512)
+    rows = math.ceil(N / 64) if H > 16384 else math.ceil(N / 256)
     close(dw, dw64, half(dw64, dt) + (rows + 256) * STEP * (dy.double() * n).abs().sum(0), "dweight")
     return x, res, w, y, h, rstd, dy, g, dx, dw
 
