@@ -74,7 +74,7 @@ struct MxLinear {
   int N, F, Kp;
   int format;                            // of x
   int act;
-  int tile;                // S of the 32 S x 32 S output tiles; 0: the few-token kernel
+  int tile;                // S of the 32 S x 32 S output tiles; 0: the few-token kernel; 1: its wide form
   int TM, TN;
   int parts, kc;           // K split: parts of kc columns each
   float* part;             // parts > 1: [parts][N][ldp] fp32 sums

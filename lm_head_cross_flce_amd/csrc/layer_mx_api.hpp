@@ -34,12 +34,14 @@ flce_status mx_convert(const void* x, void* y, uint8_t* codes, uint8_t* scales, 
 }
 
 struct MxGeometry {
-  int tile, TM, TN, parts;   // tile 0: the few-token kernel, parts waves to a group of features
+  int tile, TM, TN, parts;   // tile 0: the few-token kernel, parts waves to a group of features; 1: its wide form
   int64_t kc, ldp;
   size_t total;
 };
 
-constexpr int64_t kMxFew = 16;   // most tokens of the few-token kernel
+// Most tokens of the few-token kernels: 4 (16 tokens, 4096 -> 12288: 22 us, 15 in tiles), or 16 where a wave of 64
+// features fills the card three times (16 tokens or one, 4096 -> 128256: 66 and 63 us).
+constexpr int64_t kMxFew = 4, kMxWideFew = 16;
 
 // The tests' override of the tile, or 0.
 int forced_mx_tile() {
@@ -48,29 +50,58 @@ int forced_mx_tile() {
   return s == 2 || s == 4 || s == 8 ? s : 0;
 }
 
+// The cut with the least estimated time, in us, of the busiest CU's q tiles, as product_cut has it:
+//   q * per_tile + steps * max(alone, q * shared) + 4, a step 128 columns of K,
+// by runs of 200 x 8192 x 8192, 517 x 4000 x 10241, 1024 x 4096 x 4096, 2048 and 8192 x 4096 x 12288 and
+// 4096 x 8192 x 8192 at each tile: within a seventh of them.  Some, us at S = 8 / 4 / 2: 8192 x 4096 x 12288 e2m1 200 / 314 / 479,
+// e4m3 279 / 485 / 777; 517 x 4000 x 10241 e4m3 57 / 40 / 56; 1024 x 4096 x 4096 e2m1 37 / 27 / 23.
+struct MxCost {
+  int S;
+  double per_tile, alone, shared;
+};
+constexpr MxCost kMxCost[2][3] = {{{8, 6.7, 1.24, 1.24}, {4, 2.9, 0.87, 0.54}, {2, 0.2, 0.30, 0.27}},    // e4m3
+                                  {{8, 6.8, 0.83, 0.83}, {4, 2.4, 0.66, 0.335}, {2, 0.3, 0.25, 0.147}}};   // e2m1
+constexpr double kMxOddRows = 14.0;   // a 256-row tile's epilogue where F % 8 != 0
+
 MxGeometry mx_geometry(int64_t N, int64_t K, int64_t F, int format, int dtype) {
   MxGeometry g{};
-  const int64_t Kp = mx_cols(K);
+  const int64_t Kp = mx_cols(K), steps = Kp / 128;
   const int forced = forced_mx_tile();
-  if (N <= kMxFew && !forced) {
+  const bool exact = dtype == FLCE_F32 && format == FLCE_MX_E4M3;
+  // The wide few-token kernel and the 256-row tile move scales in runs of 512 columns; neither expands operands.
+  const bool runs = Kp >= 512 && !exact;
+  const bool wide = runs && F >= 64 * 3 * kCUs;
+  if (N <= (wide ? kMxWideFew : kMxFew) && !forced) {
+    g.tile = wide ? 1 : 0;
     // enough waves for every CU, each with K of its own to walk
     g.parts = 1;
-    while (g.parts < 8 && cdiv(F, 16) * g.parts < 8 * kCUs && Kp / 128 >= 2 * g.parts) g.parts *= 2;
+    while (g.parts < 8 && cdiv(F, 16) * g.parts < 8 * kCUs && steps >= 2 * g.parts) g.parts *= 2;
     g.kc = Kp;
     return g;
   }
-  // The 256-row tile moves scales in runs of 512 columns and has no float32 variant for an e4m3 x.
-  const bool big = Kp >= 512 && (dtype != FLCE_F32 || format == FLCE_MX_E2M1);
-  g.tile = big && cdiv(N, 256) * cdiv(F, 256) >= kCUs ? 8 : cdiv(N, 128) * cdiv(F, 128) >= 2 * kCUs ? 4 : 2;
-  if (forced) g.tile = forced == 8 && !big ? 4 : forced;
-  const int64_t M = 32 * g.tile;
-  g.TM = (int)cdiv(N, M);
-  g.TN = (int)cdiv(F, M);
-  g.parts = 1;
-  // parts of 1024 columns at least, while the tiles leave CUs idle
-  while (g.parts < 8 && (int64_t)g.TM * g.TN * g.parts * 2 <= 2 * kCUs && Kp / (2 * g.parts) >= 1024) g.parts *= 2;
-  g.kc = cdiv(cdiv(Kp, g.parts), 256) * 256;
-  g.parts = (int)cdiv(Kp, g.kc);
+  double least = 0.0;
+  for (const MxCost& c : kMxCost[format == FLCE_MX_E2M1]) {
+    if (c.S == 8 && !runs) continue;
+    if (forced && c.S != (forced == 8 && !runs ? 4 : forced)) continue;
+    const int64_t TM = cdiv(N, 32 * c.S), TN = cdiv(F, 32 * c.S);
+    for (int64_t parts : {1, 2, 4, 8}) {
+      const int64_t kc = cdiv(cdiv(Kp, parts), 256) * 256;
+      if (parts > 1 && (kc < 512 || cdiv(Kp, kc) != parts)) continue;
+      const double q = (double)cdiv(TM * TN * parts, kCUs), depth = (double)(parts > 1 ? kc : Kp) / 128.0;
+      const double slow = exact ? 1.7 : 1.0;
+      double us = q * (c.per_tile + (c.S == 8 && parts == 1 && F % 8 != 0 ? kMxOddRows : 0.0)) +
+                  slow * depth * std::max(c.alone, q * c.shared) + 4.0;
+      if (parts > 1) us += 3.0 + 8.0 * (double)parts * (double)N * (double)F / 4e6;   // the sums' way out and back
+      if (least == 0.0 || us < least) {
+        least = us;
+        g.tile = c.S;
+        g.TM = (int)TM;
+        g.TN = (int)TN;
+        g.parts = (int)parts;
+        g.kc = parts > 1 ? kc : Kp;
+      }
+    }
+  }
   g.ldp = cdiv(F, 8) * 8;
   g.total = g.parts > 1 ? align_up((size_t)g.parts * N * g.ldp * 4) : 0;
   return g;

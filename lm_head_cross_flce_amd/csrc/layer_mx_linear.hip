@@ -145,7 +145,7 @@ __device__ __forceinline__ void mx_finish(const MxLinear& a, int64_t n, int f, c
 // consecutive features of a token.  Block b + 1 is copied while block b is computed.
 // SPLIT: the sums go to a.part and mx_join_kernel does the rest.
 template <class T, int FMT, int S, bool SPLIT>
-__global__ void __launch_bounds__(256) mx_linear_kernel(MxLinear a) {
+__global__ void __launch_bounds__(256, (S == 4 ? 2 : 4)) mx_linear_kernel(MxLinear a) {
   constexpr bool EXACT = sizeof(T) == 4 && FMT == kMxE4M3;
   typedef MxBlock<FMT> B;
   typedef MxLds<S, FMT> Z;
@@ -464,11 +464,106 @@ __global__ void __launch_bounds__(64 * kMxWaves) mx_linear_skinny_kernel(MxLinea
   }
 }
 
+// The same for many features: a wave has 64 of them, four blocks that share the token fragments, and all of K.  Four steps
+// of weights are under way while four are computed, and their scales come 16 bytes a row at a time.  K >= 512.
+// (One token, 4096 -> 128256: 81 us with one block of features a wave, whose loads of x and of scales outnumber those of
+// weights four to one.)
+template <class T, int FMT>
+__global__ void __launch_bounds__(256) mx_linear_wide_kernel(MxLinear a) {
+  constexpr int XB = FMT == kMxE4M3 ? 2 : 1, G = 4, U = 4;
+  const int tid = threadIdx.x, lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6);
+  const int g = lane >> 4, rl = lane & 15, f0 = (blockIdx.x * 4 + wave) * 16 * G;
+  if (f0 >= a.F) return;
+  const int tok = min(rl, a.N - 1), ldw = a.Kp / 2, ldx = a.Kp * XB / 2, lds = a.Kp / kMxBlock, steps = a.Kp / 128;
+  const uint32_t offx = (uint32_t)(tok * ldx + 16 * g), offxs = (uint32_t)(tok * lds);
+  uint32_t offw[G], offs[G];
+#pragma unroll
+  for (int q = 0; q < G; ++q) {   // rows past F repeat the last one: their sums are not stored
+    const int row = min(16 * q + rl, a.F - 1 - f0);
+    offw[q] = (uint32_t)(row * ldw + 16 * g);
+    offs[q] = (uint32_t)(row * lds);
+  }
+  const __amdgpu_buffer_rsrc_t rw = make_rsrc(a.W + (int64_t)f0 * ldw), rx = make_rsrc(a.x);
+  const __amdgpu_buffer_rsrc_t rws = make_rsrc(a.Ws + (int64_t)f0 * lds), rxs = make_rsrc(a.xs);
+  f32x4 acc[G] = {};
+  struct Run {
+    u32x4 w[U][G], x[U][XB], ws[G], xs;
+  } P, Q;
+  auto load16 = [](__amdgpu_buffer_rsrc_t r, uint32_t off, int so) {
+    return __builtin_bit_cast(u32x4, __builtin_amdgcn_raw_buffer_load_b128(r, off, so, 0));
+  };
+  auto load = [&](Run& r, int t) {
+    const int run = min(4 * t, lds - 16);   // the last run of a row ends with it
+    // the steps of a row one after the other: two share a line
+#pragma unroll
+    for (int q = 0; q < G; ++q)
+#pragma unroll
+      for (int u = 0; u < U; ++u) r.w[u][q] = load16(rw, t + u < steps ? offw[q] : kOOB, 64 * (t + u));
+#pragma unroll
+    for (int u = 0; u < U; ++u)
+#pragma unroll
+      for (int h = 0; h < XB; ++h) r.x[u][h] = load16(rx, t + u < steps ? offx + 64 * h : kOOB, 64 * XB * (t + u));
+#pragma unroll
+    for (int q = 0; q < G; ++q) r.ws[q] = load16(rws, t < steps ? offs[q] : kOOB, run);
+    r.xs = load16(rxs, t < steps ? offxs : kOOB, run);
+  };
+  auto mma = [&](Run& r, int t) {
+    // dword u + d of a run is step t + u's; steps past K have zeros and a scale of 0
+    const int d = t - min(4 * t, lds - 16) / 4;
+    auto scale = [&](const u32x4& v, int u) {
+      const int i = u + d;
+      const uint32_t s = i == 0 ? v[0] : i == 1 ? v[1] : i == 2 ? v[2] : v[3];
+      return __builtin_amdgcn_ubfe(s, 8 * g, t + u < steps ? 8 : 0);
+    };
+#pragma unroll
+    for (int u = 0; u < U; ++u) {
+      const uint32_t xs = scale(r.xs, u);
+      const u32x4 p = r.x[u][0], p2 = r.x[u][XB - 1];
+      const i32x8 xb = {(int)p[0], (int)p[1], (int)p[2], (int)p[3], (int)p2[0], (int)p2[1], (int)p2[2], (int)p2[3]};
+#pragma unroll
+      for (int q = 0; q < G; ++q) {
+        const u32x4 v = r.w[u][q];
+        const i32x8 wa = {(int)v[0], (int)v[1], (int)v[2], (int)v[3], 0, 0, 0, 0};
+        acc[q] = __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(wa, xb, acc[q], 4, kMxCode<FMT>, 0, (int)scale(r.ws[q], u), 0,
+                                                                  (int)xs);
+      }
+    }
+  };
+  // Waves start at different runs of K, and so at different channels of the memory.
+  const int runs = (steps + U - 1) / U, first = (blockIdx.x * 4 + wave) % runs;
+  auto place = [&](int i) { return U * (i + first < runs ? i + first : i < runs ? i + first - runs : runs); };
+  load(P, place(0));
+  for (int i = 0; i < runs; i += 2) {
+    load(Q, place(i + 1));
+    mma(P, place(i));
+    load(P, place(i + 2));
+    if (i + 1 < runs) mma(Q, place(i + 1));
+  }
+  // Element (feature 4 g + r, token rl) of a block.
+  if (rl >= a.N) return;
+#pragma unroll
+  for (int q = 0; q < G; ++q) {
+    const int f = f0 + 16 * q + 4 * g;
+    if (f >= a.F) continue;
+    float z[4], bias[4] = {};
+#pragma unroll
+    for (int e = 0; e < 4; ++e) z[e] = acc[q][e];
+    if (a.b) load_some<T, 4>((const T*)a.b + f, a.F - f, bias);
+    mx_finish<T, 4>(a, rl, f, bias, z);
+  }
+}
+
 // ---------------------------------------------------------------------------
 // Launches
 // ---------------------------------------------------------------------------
 
 template <class T, int FMT> static void mx_launch(const MxLinear& a, hipStream_t st) {
+  if constexpr (sizeof(T) == 2 || FMT == kMxE2M1) {
+    if (a.tile == 1) {
+      FLCE_LAUNCH((mx_linear_wide_kernel<T, FMT>), dim3((a.F + 255) / 256), dim3(256), 0, st, a);
+      return;
+    }
+  }
   if (a.tile == 0) {
     const int per = 16 * (kMxWaves / a.parts);
     FLCE_LAUNCH((mx_linear_skinny_kernel<T, FMT>), dim3((a.F + per - 1) / per), dim3(64 * kMxWaves), 0, st, a);

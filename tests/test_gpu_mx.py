@@ -250,6 +250,14 @@ def test_every_tile(monkeypatch, dtype, fmt, tile):
         check(N, K, F, fmt, DT[dtype], "gelu", True, True, seed=11)
 
 
+@pytest.mark.parametrize("fmt", FORMATS)
+@pytest.mark.parametrize("dtype", list(DT))
+def test_few_tokens_many_features(dtype, fmt):
+    for N, K, F in ((1, 512, 49_152), (16, 700, 49_170), (3, 1100, 50_001), (7, 130, 49_200)):
+        check(N, K, F, fmt, DT[dtype])
+        check(N, K, F, fmt, DT[dtype], "silu", True, True, seed=5)
+
+
 @pytest.mark.parametrize("dtype", list(DT))
 def test_large_tiles_in_several_rounds(monkeypatch, dtype):
     # more tiles of 256 x 256 than CUs: each workgroup's stores run on under its next tile
@@ -293,11 +301,10 @@ def test_scales_far_apart(fmt, N, dtype):
     assert bool(((y.double() - ref).abs() <= tol + TINY[DT[dtype]]).all())
 
 
-@pytest.mark.parametrize("N", [3, 40, 600])
+@pytest.mark.parametrize("N,K,F", [(3, 300, 90), (40, 300, 90), (600, 300, 90), (2, 600, 49_200), (300, 1664, 8200)])
 @pytest.mark.parametrize("fmt", FORMATS)
 @pytest.mark.parametrize("dtype", list(DT))
-def test_nan_scales_stay_in_their_rows(N, fmt, dtype):
-    K, F = 300, 90
+def test_nan_scales_stay_in_their_rows(N, K, F, fmt, dtype):
     x, W = operands(N, K, F, fmt)
     xs, ws = x.scales.clone(), W.scales.clone()
     xs[1, 3] = 255

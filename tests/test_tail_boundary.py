@@ -189,6 +189,7 @@ def test_linear_workspace():
     refused(linear, INVALID, K=8192, workspace=WS + 8)
     refused(linear, INVALID, K=8192, workspace=Y)
     assert _lib.flce_mx_linear_workspace_size(8192, 4096, 12288, 0, 1) == 0
+    assert _lib.flce_mx_linear_workspace_size(1, 4096, 128256, 0, 1) == 0
     assert _lib.flce_mx_linear_workspace_size(0, 4096, 64, 0, 1) == 0
     for bad in ((-1, 64, 64), (4, 0, 64), (4, 64, 0)):
         with pytest.raises(_lib.FlceError):
