@@ -12,6 +12,7 @@ gradients produced in backward rather than in forward (DeepSpeed PR 8792).
 from __future__ import annotations
 
 import contextlib
+import functools
 import operator
 from typing import NamedTuple, Optional, Tuple, Union
 
@@ -793,66 +794,74 @@ class MXTensor(NamedTuple):
 
 
 def _mx_empty(rows: int, cols: int, format: str, dev) -> MXTensor:
-    padded = (cols + 127) // 128 * 128
-    codes = torch.empty(rows, padded // 2 if format == "e2m1" else padded, dtype=torch.uint8, device=dev)
-    return MXTensor(codes, torch.empty(rows, padded // 32, dtype=torch.uint8, device=dev), cols, format)
+    padded = (cols + 127) & -128
+    return MXTensor(torch.empty((rows, padded // 2 if format == "e2m1" else padded), dtype=torch.uint8, device=dev),
+                    torch.empty((rows, padded // 32), dtype=torch.uint8, device=dev), cols, format)
 
 
-def _prep_mx(q: MXTensor) -> MXTensor:
-    """q checked and dense."""
+def _prep_mx(q: MXTensor):
+    """q's codes and scales, checked and dense, its rows and its format's code."""
     codes, scales, cols, format = q
-    _format_code(format)
-    if codes.dtype != torch.uint8 or scales.dtype != torch.uint8:
+    code = _format_code(format)
+    if codes.dtype is not torch.uint8 or scales.dtype is not torch.uint8:
         raise TypeError("codes and scales must be uint8")
     if cols < 1:
         raise ValueError("a microscaled matrix has at least one column")
-    padded = (cols + 127) // 128 * 128
-    want = padded // 2 if format == "e2m1" else padded
+    padded = (cols + 127) & -128
+    want = padded // 2 if code else padded
     if codes.dim() != 2 or codes.shape[1] != want or scales.shape != (codes.shape[0], padded // 32):
         raise ValueError(f"{cols} columns in {format} have codes [rows, {want}] and scales [rows, {padded // 32}]")
     if not codes.is_cuda:
         raise ValueError("tensors must live on a GPU")
     if scales.device != codes.device:
         raise ValueError("all tensors must be on one device")
-    return MXTensor(_dense(codes), _dense(scales), cols, format)
+    return _dense(codes), _dense(scales), codes.shape[0], code
 
 
-def _prep_rows(x: torch.Tensor, rows=(), vectors=(), what: str = "x"):
-    """x [N, H], other tensors of its shape and vectors [H] (or None) of its type, checked and dense."""
+def _prep_rows(x: torch.Tensor, rows=(), vector: Optional[torch.Tensor] = None, what: str = "x"):
+    """x [N, H], other tensors of its shape and a vector [H] (or None) of its type, checked and dense; and x's device,
+    N, H and type code."""
     if x.dim() != 2:
         raise ValueError(f"{what} must be [N, H]")
     if not x.is_cuda:
         raise ValueError("tensors must live on a GPU")
-    if x.shape[1] < 1:
+    shape, dtype, dev = x.shape, x.dtype, x.device
+    N, H = shape
+    if H < 1:
         raise ValueError("H must be at least 1")
-    _dtype_code(x)
+    code = _dtype_code(x)
+    for t in rows:
+        if t is not None and (t.shape != shape or t.dtype is not dtype or t.device != dev):
+            _refuse_row(t, x, shape, what)
+    if vector is not None and (vector.shape != (H,) or vector.dtype is not dtype or vector.device != dev):
+        _refuse_row(vector, x, shape[1:], what)
+    # (the library reads a vector from any element)
+    return (_dense(x), [_dense(t) for t in rows], None if vector is None else vector.contiguous(), dev, N, H, code)
 
-    def dense(t, shape):
-        if t is None:
-            return None
-        if t.shape != shape:
-            raise ValueError(f"expected a tensor of shape {tuple(shape)}, not {tuple(t.shape)}")
-        if t.dtype != x.dtype:
-            raise TypeError(f"all tensors must share {what}'s dtype")
-        if t.device != x.device:
-            raise ValueError("all tensors must be on one device")
-        return _dense(t)
 
-    return _dense(x), [dense(t, x.shape) for t in rows], [dense(t, x.shape[1:]) for t in vectors]
+def _refuse_row(t: torch.Tensor, x: torch.Tensor, shape, what: str) -> None:
+    if t.shape != shape:
+        raise ValueError(f"expected a tensor of shape {tuple(shape)}, not {tuple(t.shape)}")
+    if t.dtype != x.dtype:
+        raise TypeError(f"all tensors must share {what}'s dtype")
+    raise ValueError("all tensors must be on one device")
+
+
+# Sizes that depend on nothing but these numbers: asked for at every call, and the library's answer takes a microsecond.
+_norm_bytes = functools.lru_cache(maxsize=1024)(_lib.flce_rms_norm_workspace_size)
+_sample_bytes = functools.lru_cache(maxsize=1024)(_lib.flce_sample_workspace_size)
 
 
 def flce_rms_norm_workspace_size(N: int, H: int, dtype: torch.dtype) -> int:
     """Bytes of flce_rms_norm_backward with dweight."""
-    return _lib.flce_rms_norm_workspace_size(N, H, _DTYPES[dtype])
+    return _norm_bytes(N, H, _DTYPES[dtype])
 
 
 def flce_rms_norm_forward(x: torch.Tensor, weight: Optional[torch.Tensor] = None,
                           residual: Optional[torch.Tensor] = None, eps: float = 1e-6, keep: bool = False):
     """y = h * (mean(h^2) + eps)^(-1/2) * weight over the rows of h = x + residual.  Returns (y, h, rstd): h is x
     without a residual; rstd, float32 [N], what flce_rms_norm_backward takes, with keep, else None."""
-    x, (residual,), (weight,) = _prep_rows(x, (residual,), (weight,))
-    N, H = x.shape
-    dt, dev = _dtype_code(x), x.device
+    x, (residual,), weight, dev, N, H, dt = _prep_rows(x, (residual,), weight)
     y = torch.empty_like(x)
     h = torch.empty_like(x) if residual is not None else None
     rstd = torch.empty(N, dtype=torch.float32, device=dev) if keep else None
@@ -866,9 +875,7 @@ def flce_rms_norm_mx_forward(x: torch.Tensor, weight: Optional[torch.Tensor] = N
                              residual: Optional[torch.Tensor] = None, eps: float = 1e-6, format: str = "e4m3"):
     """flce_rms_norm_forward with y microscaled, from its float32 values.  Returns (y, h), y an MXTensor."""
     code = _format_code(format)
-    x, (residual,), (weight,) = _prep_rows(x, (residual,), (weight,))
-    N, H = x.shape
-    dt, dev = _dtype_code(x), x.device
+    x, (residual,), weight, dev, N, H, dt = _prep_rows(x, (residual,), weight)
     q = _mx_empty(N, H, format, dev)
     h = torch.empty_like(x) if residual is not None else None
     with _on(dev):
@@ -882,15 +889,13 @@ def flce_rms_norm_backward(h: torch.Tensor, weight: Optional[torch.Tensor], rstd
                            workspace: Optional[torch.Tensor] = None):
     """Returns (dx, dweight) in the input dtype (None where not requested); h and rstd as flce_rms_norm_forward
     returned them, dh the gradient that reaches h past the norm.  dx is the residual's gradient too."""
-    h, (dy, dh), (weight,) = _prep_rows(h, (dy, dh), (weight,), "h")
-    N, H = h.shape
-    dt, dev = _dtype_code(h), h.device
+    h, (dy, dh), weight, dev, N, H, dt = _prep_rows(h, (dy, dh), weight, "h")
     if rstd is None or rstd.dtype != torch.float32 or rstd.shape != (N,) or rstd.device != dev:
         raise ValueError(f"rstd must be a float32 [{N}] tensor on {dev} (as flce_rms_norm_forward returns it)")
     rstd = rstd.contiguous()
     dx = torch.empty_like(h) if need_dx else None
     dweight = torch.empty(H, dtype=h.dtype, device=dev) if need_dweight else None
-    workspace = _workspace(workspace, _lib.flce_rms_norm_workspace_size(N, H, dt) if need_dweight else 0, dev)
+    workspace = _workspace(workspace, _norm_bytes(N, H, dt) if need_dweight else 0, dev)
     with _on(dev):
         _lib.flce_rms_norm_backward(h.data_ptr(), _ptr(weight), rstd.data_ptr(), dy.data_ptr(), _ptr(dh), N, H, dt,
                                     _ptr(dx), _ptr(dweight), _ptr(workspace), _nbytes(workspace),
@@ -901,12 +906,10 @@ def flce_rms_norm_backward(h: torch.Tensor, weight: Optional[torch.Tensor], rstd
 def flce_mx_quantize(x: torch.Tensor, format: str = "e2m1") -> MXTensor:
     """x [R, C] microscaled: each 32 columns' scale from their largest magnitude, elements rounded to nearest even."""
     code = _format_code(format)
-    x, _, _ = _prep_rows(x)
-    R, C = x.shape
-    dev = x.device
+    x, _, _, dev, R, C, dt = _prep_rows(x)
     q = _mx_empty(R, C, format, dev)
     with _on(dev):
-        _lib.flce_mx_quantize(x.data_ptr(), R, C, _dtype_code(x), code, q.codes.data_ptr(), q.scales.data_ptr(),
+        _lib.flce_mx_quantize(x.data_ptr(), R, C, dt, code, q.codes.data_ptr(), q.scales.data_ptr(),
                               _raw_stream(dev.index))
     return q
 
@@ -915,12 +918,12 @@ def flce_mx_dequantize(q: MXTensor, dtype: torch.dtype = torch.bfloat16) -> torc
     """The values of a microscaled matrix, [R, C]; bfloat16 and float32 hold them exactly within their range."""
     if dtype not in _DTYPES:
         raise TypeError(f"unsupported dtype {dtype}; use bfloat16, float16 or float32")
-    q = _prep_mx(q)
-    dev = q.codes.device
-    y = torch.empty(q.shape, dtype=dtype, device=dev)
+    codes, scales, rows, code = _prep_mx(q)
+    dev, cols = codes.device, q.cols
+    y = torch.empty((rows, cols), dtype=dtype, device=dev)
     with _on(dev):
-        _lib.flce_mx_dequantize(q.codes.data_ptr(), q.scales.data_ptr(), *q.shape, _format_code(q.format),
-                                _DTYPES[dtype], y.data_ptr(), _raw_stream(dev.index))
+        _lib.flce_mx_dequantize(codes.data_ptr(), scales.data_ptr(), rows, cols, code, _DTYPES[dtype], y.data_ptr(),
+                                _raw_stream(dev.index))
     return y
 
 
@@ -937,34 +940,38 @@ def flce_mx_linear(x: MXTensor, W: MXTensor, b: Optional[torch.Tensor] = None, r
     act = _activation_code(activation)
     if dtype not in _DTYPES:
         raise TypeError(f"unsupported dtype {dtype}; use bfloat16, float16 or float32")
-    x, W = _prep_mx(x), _prep_mx(W)
+    K = x.cols
     if W.format != "e2m1":
         raise ValueError("W must be in e2m1")
-    (N, K), F, dev = x.shape, W.shape[0], x.codes.device
     if W.cols != K:
         raise ValueError("x and W disagree on their columns")
+    codes, scales, N, code = _prep_mx(x)
+    W_codes, W_scales, F, _ = _prep_mx(W)
+    dev = codes.device
     if F < 1:
         raise ValueError("W has no rows")
-    for t, shape in ((W.codes, None), (b, (F,)), (residual, (N, F)), (out, (N, F))):
+    if W_codes.device != dev:
+        raise ValueError("all tensors must be on one device")
+    for t, shape in ((b, (F,)), (residual, (N, F)), (out, (N, F))):
         if t is None:
             continue
         if t.device != dev:
             raise ValueError("all tensors must be on one device")
-        if shape is not None and t.shape != shape:
+        if t.shape != shape:
             raise ValueError(f"expected a tensor of shape {shape}, not {tuple(t.shape)}")
-        if shape is not None and t.dtype != dtype:
+        if t.dtype is not dtype:
             raise TypeError(f"b, residual and out must be {dtype}, as the result")
     residual_ = _dense(residual)
     if out is not None and (_dense(out) is not out or (residual_ is not residual and residual is out)):
         raise ValueError("out must be contiguous from a 16-byte boundary")
     b = None if b is None else b.contiguous()
-    y = out if out is not None else torch.empty(N, F, dtype=dtype, device=dev)
-    code, dt = _format_code(x.format), _DTYPES[dtype]
+    y = out if out is not None else torch.empty((N, F), dtype=dtype, device=dev)
+    dt = _DTYPES[dtype]
     workspace = _workspace(workspace, _lib.flce_mx_linear_workspace_size(N, K, F, code, dt), dev)
     with _on(dev):
-        _lib.flce_mx_linear(x.codes.data_ptr(), x.scales.data_ptr(), code, W.codes.data_ptr(), W.scales.data_ptr(),
-                            _ptr(b), _ptr(residual_), N, K, F, dt, act, y.data_ptr(), _ptr(workspace),
-                            _nbytes(workspace), _raw_stream(dev.index))
+        _lib.flce_mx_linear(codes.data_ptr(), scales.data_ptr(), code, W_codes.data_ptr(), W_scales.data_ptr(), _ptr(b),
+                            _ptr(residual_), N, K, F, dt, act, y.data_ptr(), _ptr(workspace), _nbytes(workspace),
+                            _raw_stream(dev.index))
     if out is not None:
         _wrote(out)
     return y
@@ -972,7 +979,7 @@ def flce_mx_linear(x: MXTensor, W: MXTensor, b: Optional[torch.Tensor] = None, r
 
 def flce_sample_workspace_size(N: int, V: int, dtype: torch.dtype) -> int:
     """Bytes of flce_sample."""
-    return _lib.flce_sample_workspace_size(N, V, _DTYPES[dtype])
+    return _sample_bytes(N, V, _DTYPES[dtype])
 
 
 def flce_sample(logits: torch.Tensor, u: torch.Tensor, temperature: Union[float, torch.Tensor, None] = None,
@@ -1007,7 +1014,7 @@ def flce_sample(logits: torch.Tensor, u: torch.Tensor, temperature: Union[float,
         elif value is not None:
             kw[name] = value
     tokens = torch.empty(N, dtype=torch.int64, device=dev)
-    workspace = _workspace(workspace, _lib.flce_sample_workspace_size(N, V, dt), dev)
+    workspace = _workspace(workspace, _sample_bytes(N, V, dt), dev)
     with _on(dev):
         _lib.flce_sample(logits.data_ptr(), u_ptr, N, V, dt, _lib.sampling(**kw), tokens.data_ptr(), _ptr(workspace),
                          _nbytes(workspace), _raw_stream(dev.index))
