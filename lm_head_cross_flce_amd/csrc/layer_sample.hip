@@ -249,11 +249,11 @@ struct RowLds {
   union {
     struct {
       uint32_t group[kGroups];      // largest key of each group; then the groups that pass, in order
-      uint32_t key[kMost], index[kMost];
+      u64 token[kMost];             // key << 32 | index
       u64 weight[kMost];
     } list;
     struct {
-      uint32_t key[kNucleusMost], index[kNucleusMost];
+      u64 token[kNucleusMost];   // key << 32 | index
       double slice[kMaxSlices];
       u64 extra[kMaxSlices];
       uint32_t equal[kMaxSlices];
@@ -365,16 +365,21 @@ template <class T, class F> __device__ __forceinline__ void each_token(const T* 
   }
 }
 
-// Tokens of the row that stay, in order, to put(place, value, index): of runs of 8 tokens, run c from at(c) on (in
-// order), those that keep(value, index) says.  Each wave takes a stretch of the runs, counts and then writes; more than
-// `most` in all are only counted.  Returns their number.
-template <class T, class At, class Keep, class Put>
-__device__ __forceinline__ uint32_t collect(const T* z, int V, int runs, uint32_t most, At&& at, Keep&& keep, Put&& put, Row& L) {
+// Tokens of the row that stay, in order, as (key << 32 | index) in list: of runs of 8 tokens, run c from at(c) on (in
+// order), those that keep(value, index) says.  Returns their number; of more than MOST only that.
+//
+// Each wave takes a stretch of the runs and writes what it finds to a 16th of the list; the parts are then moved
+// together.  If a wave finds more than its part holds, all walk a second time and write to the final places.
+template <class T, int MOST, class At, class Keep>
+__device__ __forceinline__ uint32_t collect(const T* z, int V, int runs, u64* list, At&& at, Keep&& keep, Row& L) {
   constexpr int U = 2;   // runs a lane has under way
-  const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
+  constexpr uint32_t kPart = MOST / kRowWaves;
+  const int tid = threadIdx.x, lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6);
   const int share = (runs + 64 * U * kRowWaves - 1) / (64 * U * kRowWaves) * (64 * U);
   const int c0 = min(runs, wave * share), c1 = min(runs, c0 + share);
-  auto walk = [&](auto&& f) {
+  // to list[first + i] for i under `room`; returns how many there are
+  auto walk = [&](uint32_t first, uint32_t room) {
+    uint32_t n = 0;
 #pragma unroll 1
     for (int c = c0; c < c1; c += 64 * U) {
       float v[U][8];
@@ -390,24 +395,39 @@ __device__ __forceinline__ uint32_t collect(const T* z, int V, int runs, uint32_
         uint32_t hits = 0;
 #pragma unroll
         for (int e = 0; e < 8; ++e) hits |= (uint32_t)(j[q] + e < V && keep(v[q][e], j[q] + e)) << e;
-        f(hits, v[q], j[q]);
+        if (!__ballot(hits != 0)) continue;
+        const uint32_t own = (uint32_t)__popc(hits), in = wave_scan(own, Add());
+        uint32_t i = n + in - own;
+#pragma unroll
+        for (int e = 0; e < 8; ++e)
+          if (hits >> e & 1) {
+            if (i < room) list[first + i] = (u64)value_key(v[q][e]) << 32 | (uint32_t)(j[q] + e);
+            ++i;
+          }
+        n += lane_of(in, 63);
       }
     }
+    return n;
   };
-  u64 n = 0, total;
-  walk([&](uint32_t hits, const float (&)[8], int) { n += __popc(hits); });
-  uint32_t start = (uint32_t)block_scan(n, total, L);
-  if (total > most) return (uint32_t)min(total, (u64)0xffffffffu);
-  start = lane_of(start, 0);
-  walk([&](uint32_t hits, const float (&v)[8], int j) {
-    if (!__ballot(hits != 0)) return;
-    const uint32_t own = (uint32_t)__popc(hits), in = wave_scan(own, Add());
-    uint32_t i = start + in - own;
+  __syncthreads();
+  const uint32_t n = walk(wave * kPart, kPart);
+  // the waves' numbers, and what the ones before have
+  u64 total;
+  const uint32_t start = (uint32_t)lane_of(block_scan((u64)(lane == 0 ? n : 0u), total, L), 0);
+  if (total > MOST) return (uint32_t)min(total, (u64)0xffffffffu);
+  const bool over = block_max(n, L) > kPart;
+  if (over) {
+    walk(start, MOST);
+    __syncthreads();
+    return (uint32_t)total;
+  }
+  u64 own[kPart / 64];
 #pragma unroll
-    for (int e = 0; e < 8; ++e)
-      if (hits >> e & 1) put(i++, v[e], j + e);
-    start += lane_of(in, 63);
-  });
+  for (uint32_t k = 0; k < kPart / 64; ++k) own[k] = list[wave * kPart + 64 * k + lane];
+  __syncthreads();
+#pragma unroll
+  for (uint32_t k = 0; k < kPart / 64; ++k)
+    if (64 * k + lane < n) list[start + 64 * k + lane] = own[k];
   __syncthreads();
   return (uint32_t)total;
 }
@@ -679,16 +699,14 @@ __device__ __forceinline__ bool sample_nucleus(const Sample& a, int64_t row, con
 
   // Its tokens, in order.
   const float lo = (float)(((double)edge - 0.01) / b.scale), hi = (float)(((double)edge + 1.01) / b.scale);   // around it
-  const int listed = (int)min(collect(z, V, (V + 7) / 8, kNucleusMost, [](int c) { return 8 * c; },
-                                      [&](float v, int) {
-                                        const bool near = v >= lo && v <= hi;
-                                        return __ballot(near) ? near && b.bin(v) == edge : false;
-                                      },
-                                      [&](uint32_t i, float v, int j) {
-                                        L.m.nucleus.key[i] = value_key(v);
-                                        L.m.nucleus.index[i] = j;
-                                      }, L), (uint32_t)INT_MAX);
-  if (listed > kNucleusMost) return false;
+  const uint32_t found = collect<T, kNucleusMost>(z, V, (V + 7) / 8, L.m.nucleus.token, [](int c) { return 8 * c; },
+                                                  [&](float v, int) {
+                                                    const bool near = v >= lo && v <= hi;
+                                                    return __ballot(near) ? near && b.bin(v) == edge : false;
+                                                  }, L);
+  if (found > kNucleusMost) return false;
+  const int listed = (int)found;
+  auto key_of = [&](int i) { return (uint32_t)(L.m.nucleus.token[i] >> 32); };
   auto weight = [&](uint32_t key) { return (u64)rint(b.over(key_value(key)) * unit); };
   uint32_t cut = 0;
   u64 ties = 0;
@@ -696,9 +714,9 @@ __device__ __forceinline__ bool sample_nucleus(const Sample& a, int64_t row, con
     u64 own = 0, sum;
     uint32_t most = 0, least = 0;
     for (int i = tid; i < listed; i += kRowThreads) {
-      own += weight(L.m.nucleus.key[i]);
-      most = max(most, L.m.nucleus.key[i]);
-      least = max(least, ~L.m.nucleus.key[i]);
+      own += weight(key_of(i));
+      most = max(most, key_of(i));
+      least = max(least, ~key_of(i));
     }
     block_scan(own, sum, L);
     most = block_max(most, L);
@@ -707,7 +725,7 @@ __device__ __forceinline__ bool sample_nucleus(const Sample& a, int64_t row, con
     const u64 want = min(want_real < 1.0 ? 1ull : (u64)want_real, sum);
     u64 above;
     cut = find_key(least, most, want, above, [&](auto&& f) {
-      for (int i = tid; i < listed; i += kRowThreads) f(L.m.nucleus.key[i], weight(L.m.nucleus.key[i]));
+      for (int i = tid; i < listed; i += kRowThreads) f(key_of(i), weight(key_of(i)));
     }, L);
     ties = ties_needed(want, above, weight(cut));
   }
@@ -724,11 +742,11 @@ __device__ __forceinline__ bool sample_nucleus(const Sample& a, int64_t row, con
     // ties in order: thread t has tokens per t .. per (t + 1) - 1 of the list
     const int per = (listed + kRowThreads - 1) / kRowThreads;
     u64 same = 0, none;
-    for (int i = tid * per; i < min(listed, (tid + 1) * per); ++i) same += L.m.nucleus.key[i] == cut;
+    for (int i = tid * per; i < min(listed, (tid + 1) * per); ++i) same += key_of(i) == cut;
     u64 tie = block_scan(same, none, L);
     for (int i = tid * per; i < min(listed, (tid + 1) * per); ++i) {
-      const uint32_t k = L.m.nucleus.key[i];
-      const int j = L.m.nucleus.index[i] / kSliceTokens;
+      const uint32_t k = key_of(i);
+      const int j = (int)((uint32_t)L.m.nucleus.token[i] / kSliceTokens);
       bool keep = k > cut;
       if (k == cut) {
         atomicAdd(&L.m.nucleus.equal[j], 1u);
@@ -757,6 +775,7 @@ __device__ __forceinline__ bool sample_nucleus(const Sample& a, int64_t row, con
   const double spot = (r.u > 0.f ? (double)r.u : 0.0) * kept;
   uint32_t at = block_max(own > 0.0 && sum_before + own > spot ? kMaxSlices - tid : 0, L);
   const uint32_t end = block_max(own > 0.0 ? tid + 1 : 0, L);
+  if (end == 0) return false;   // not reached: the largest token is kept
   const bool past = at == 0;
   const int slice = past ? (int)end - 1 : kMaxSlices - (int)at;
   __syncthreads();
@@ -930,38 +949,38 @@ template <class T, bool GROUPS> __global__ void __launch_bounds__(kRowThreads) s
     if (pass >> i & 1) L.m.list.group[at++] = tid * per + i;
   __syncthreads();
   // Of so many groups' tokens the list would hardly hold those that stay (independent ones: 3% of the row's).
-  if (binned && found * 20 > (u64)groups * 13 && sample_nucleus<T>(a, row, r, w, nuc, L)) return;
+  if (binned && found * 20 > (u64)groups * 13) {
+    if (!sample_nucleus<T>(a, row, r, w, nuc, L)) sample_whole<T>(a, row, r, w, top, L);   // (its list lies where the groups did)
+    return;
+  }
   // Their tokens, in order.
   const int runs = size / 8, shift = 31 - __clz(runs);
-  const uint32_t total = collect(z, V, (int)found << shift, kMost,
-                                 [&](int c) { return (int)L.m.list.group[c >> shift] * size + (c & (runs - 1)) * 8; },
-                                 [&](float v, int) { return value_key(v) >= low; },
-                                 [&](uint32_t i, float v, int j) {
-                                   L.m.list.key[i] = value_key(v);
-                                   L.m.list.index[i] = j;
-                                 }, L);
+  const uint32_t total = collect<T, kMost>(z, V, (int)found << shift, L.m.list.token,
+                                           [&](int c) { return (int)L.m.list.group[c >> shift] * size + (c & (runs - 1)) * 8; },
+                                           [&](float v, int) { return value_key(v) >= low; }, L);
   if (total > kMost) {
     if (binned && sample_nucleus<T>(a, row, r, w, nuc, L)) return;
     return sample_whole<T>(a, row, r, w, top, L);
   }
-  for (int i = tid; i < (int)total; i += kRowThreads) L.m.list.weight[i] = w(key_value(L.m.list.key[i]));
+  for (int i = tid; i < (int)total; i += kRowThreads) L.m.list.weight[i] = w(key_value((uint32_t)(L.m.list.token[i] >> 32)));
   __syncthreads();
 
   // Tokens above key `cut` are kept and the first `ties` at it.
   const int count = (int)total;
+  auto key_at = [&](int i) { return (uint32_t)(L.m.list.token[i] >> 32); };
   uint32_t cut = 0;
   u64 ties = 0;
   if (r.k && r.k < count) {
     u64 above;
     cut = find_key(low, top, (u64)r.k, above, [&](auto&& f) {
-      for (int i = tid; i < count; i += kRowThreads) f(L.m.list.key[i], 1ull);
+      for (int i = tid; i < count; i += kRowThreads) f(key_at(i), 1ull);
     }, L);
     ties = (u64)r.k - above;
   }
   if (r.p < 1.f) {
     u64 sum = 0, all;
     for (int i = tid; i < count; i += kRowThreads)
-      if (L.m.list.key[i] > cut) sum += L.m.list.weight[i];
+      if (key_at(i) > cut) sum += L.m.list.weight[i];
     block_scan(sum, all, L);
     const u64 at_cut = cut ? ties * w(key_value(cut)) : 0;
     all += at_cut;
@@ -974,7 +993,7 @@ template <class T, bool GROUPS> __global__ void __launch_bounds__(kRowThreads) s
       const uint32_t was = cut;
       cut = find_key(low, top, want, above, [&](auto&& f) {
         for (int i = tid; i < count; i += kRowThreads)
-          if (L.m.list.key[i] > was) f(L.m.list.key[i], L.m.list.weight[i]);
+          if (key_at(i) > was) f(key_at(i), L.m.list.weight[i]);
         if (tid == 0 && at_cut) f(was, at_cut);
       }, L);
       const u64 need = ties_needed(want, above, w(key_value(cut)));
@@ -984,7 +1003,7 @@ template <class T, bool GROUPS> __global__ void __launch_bounds__(kRowThreads) s
   // The draw: thread t has tokens 4 t .. 4 t + 3 of the list.
   u64 same = 0, none;
 #pragma unroll
-  for (int e = 0; e < 4; ++e) same += 4 * tid + e < count && L.m.list.key[4 * tid + e] == cut;
+  for (int e = 0; e < 4; ++e) same += 4 * tid + e < count && key_at(4 * tid + e) == cut;
   u64 tie = block_scan(same, none, L);
   u64 weight[4], sum = 0;
 #pragma unroll
@@ -992,7 +1011,7 @@ template <class T, bool GROUPS> __global__ void __launch_bounds__(kRowThreads) s
     const int i = 4 * tid + e;
     weight[e] = 0;
     if (i >= count) continue;
-    const uint32_t k = L.m.list.key[i];
+    const uint32_t k = key_at(i);
     if (k > cut || (k == cut && tie++ < ties))
       weight[e] = w.min_w == 0.0 || w.real(key_value(k)) >= w.min_w ? L.m.list.weight[i] : 0;
     sum += weight[e];
@@ -1002,7 +1021,7 @@ template <class T, bool GROUPS> __global__ void __launch_bounds__(kRowThreads) s
   const u64 want = spot(r.u, all);
 #pragma unroll
   for (int e = 0; e < 4; ++e) {
-    if (before <= want && want < before + weight[e]) a.tokens[row] = L.m.list.index[4 * tid + e];
+    if (before <= want && want < before + weight[e]) a.tokens[row] = (uint32_t)L.m.list.token[4 * tid + e];
     before += weight[e];
   }
 }
