@@ -350,7 +350,7 @@ template <class T> static hipError_t norm_backward_t(const NormBwd& a, hipStream
       const int blocks = (int)(a.N < 1024 ? a.N : 1024);
       FLCE_LAUNCH((norm_bwd_long_kernel<T>), dim3(blocks), dim3(1024), 0, st, a);
     }
-    if (a.dweight) FLCE_LAUNCH((norm_dw_long_kernel<T>), dim3((a.H + 2047) / 2048, a.parts), dim3(256), 0, st, a);
+    if (a.dweight && a.N > 0) FLCE_LAUNCH((norm_dw_long_kernel<T>), dim3((a.H + 2047) / 2048, a.parts), dim3(256), 0, st, a);
   } else if (a.N > 0) {
     with_row<false>(a.H, [&](auto lanes, auto runs) {
       const dim3 grid(a.parts), blk(norm_threads(lanes.value));

@@ -22,8 +22,6 @@
 // sum does not depend on its order, so atomics may form it, and every comparison with it
 // is exact.  Its rounding, 2^-46 of the largest weight a token, is far under what a float32
 // u can tell apart.
-#include <climits>
-
 #include "layer_device.hpp"
 #include "layer_launch.hpp"
 
@@ -59,6 +57,7 @@ __device__ __forceinline__ double pow2_negative(double x) {
   const double n = rint(x);
   return x < -65.0 ? 0.0 : __builtin_ldexp(pow2_near(x - n), (int)n);
 }
+constexpr int kNoBins = -2000000000;   // the first bin of a slice that has no histogram: past every other's bins
 constexpr double kLog2eDouble = 1.4426950408889634;
 __device__ __forceinline__ double exp_bin(int bins) { return pow2_negative(0.125 * kLog2eDouble * bins); }   // e^(bins / 8), bins <= 0
 
@@ -201,7 +200,7 @@ template <class T> __global__ void __launch_bounds__(256) sample_slice_kernel(Sa
     const float zt = some ? key_value(top) : 0.f;
     const bool fits = some && Bins::fits(zt, r.T, 8192.0);
     const Bins b{8.0 / (double)r.T};
-    const int base_bin = fits ? b.bin(zt) - (kHistBins - 1) : INT_MIN;
+    const int base_bin = fits ? b.bin(zt) - (kHistBins - 1) : kNoBins;
     if (tid == 0) a.slice_bin[at] = base_bin;
     if (!fits) return;
     for (int i = tid; i < kHistBins; i += 256) hist[i] = 0;
@@ -656,7 +655,7 @@ __device__ __forceinline__ bool find_nucleus(const Sample& a, int64_t row, const
 #pragma unroll 4
     for (int j = 0; j < J; ++j) {
       const int base = L.m.base[j], i = n.top_bin - tid - base;
-      if (base != INT_MIN && i >= 0 && i < kHistBins) count += H[(int64_t)j * kHistBins + i];
+      if (i >= 0 && i < kHistBins) count += H[(int64_t)j * kHistBins + i];
     }
   const double mass = (double)count * exp_bin(-tid);
   double all;
@@ -760,7 +759,7 @@ __device__ __forceinline__ bool sample_nucleus(const Sample& a, int64_t row, con
   for (int j = wave; j < J; j += kRowWaves) {
     const int base = L.m.base[j];
     double m = 0.0;
-    if (base != INT_MIN)
+    if (base != kNoBins)
       for (int i = lane; i < kHistBins; i += 64)
         if (base + i > edge) m += (double)H[(int64_t)j * kHistBins + i] * exp_bin(base + i - top_bin);
     m = wave_all(m, Add());
@@ -881,7 +880,7 @@ template <class T, bool GROUPS> __global__ void __launch_bounds__(kRowThreads) s
       if (L.m.list.group[i] == top) g = max(g, (uint32_t)(kGroups - i));
     g = kGroups - block_max(g, L);
     if (tid >= 64) return;
-    for (int j0 = (int)g * size;; j0 += 64) {
+    for (int j0 = (int)g * size; j0 < V; j0 += 64) {
       const int j = j0 + lane;
       const u64 hit = __ballot(j < V && value_key(load1<T>(z + min(j, V - 1))) == top);
       if (hit) {
@@ -889,6 +888,7 @@ template <class T, bool GROUPS> __global__ void __launch_bounds__(kRowThreads) s
         return;
       }
     }
+    return;
   }
 
   // Every token that can be kept has a key of at least `low`.

@@ -124,6 +124,12 @@ def test_no_rows(dtype):
     assert q.codes.shape == (0, 128)
 
 
+def test_no_long_rows_have_a_weight_gradient_of_zero():
+    x = torch.empty(0, 20000, device="cuda")
+    dx, dw = L.flce_rms_norm_backward(x, None, torch.empty(0, device="cuda"), x)
+    assert dx.shape == (0, 20000) and dw.shape == (20000,) and not bool(dw.any())
+
+
 def test_strided_and_unaligned_inputs():
     dt, N, H = torch.bfloat16, 37, 200
     base = randn(N, 3 * H + 1, dt=dt, seed=1)
