@@ -24,11 +24,14 @@ bool bad_format(int format) { return format != FLCE_MX_E4M3 && format != FLCE_MX
 // Workgroups of the backward, each with sums of its own for dweight: 4 a CU of 256 threads, or
 // one of 1024.  (8192 x 4096 bf16: 1024 workgroups 59 us and 6 for adding their sums, 512 87 and
 // 4.5, 2048 62 and 10; 2000 x 16000: 256 58 and 5, 1024 68 and 12.)  Up to 1024 columns
-// a workgroup has four rows or more at once, and 512 are enough (16384 x 512 fp32).
+// a workgroup has four rows or more at once, and 512 are enough (16384 x 512 fp32).  Of these as many
+// as have equally many rows (1037 x 4096 bf16: 519 workgroups 12.5 us and 4.5, 1024, thirteen of them with
+// two rows, 14.7 and 6.1).
 int64_t norm_parts(int64_t N, int64_t H) {
   if (H > flce::kNormMost) return std::min<int64_t>(N, 64);
   const int lanes = flce::norm_lanes((int)H, false);
-  return std::min<int64_t>(cdiv(N, flce::norm_rows(lanes)), lanes == 1024 ? 256 : lanes == 256 ? 1024 : 512);
+  const int64_t groups = cdiv(N, flce::norm_rows(lanes)), most = lanes == 1024 ? 256 : lanes == 256 ? 1024 : 512;
+  return groups ? cdiv(groups, cdiv(groups, most)) : 0;
 }
 size_t norm_bwd_bytes(int64_t N, int64_t H) { return align_up((size_t)norm_parts(N, H) * H * 4); }
 
