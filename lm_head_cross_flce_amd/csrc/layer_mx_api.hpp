@@ -39,8 +39,8 @@ struct MxGeometry {
   size_t total;
 };
 
-// Most tokens of the few-token kernels: 4 (16 tokens, 4096 -> 12288: 22 us, 15 in tiles), or 16 where a wave of 64
-// features fills the card three times (16 tokens or one, 4096 -> 128256: 66 and 63 us).
+// Most tokens of the few-token kernels: 4 (16 tokens, 4096 -> 12288: 22 us, 17 in tiles), or 16 where a wave of 64
+// features fills the card three times (e4m3, 4096 -> 128256: 64 us for one token, 72 for 16; tiles 88 for 17).
 constexpr int64_t kMxFew = 4, kMxWideFew = 16;
 
 // The tests' override of the tile, or 0.

@@ -5,7 +5,11 @@
 // A step is the instruction's 128 columns, 1024 cycles of it with e2m1 operands (four times the rate of bfloat16) and
 // 2048 with an e4m3 x.  What feeds it has to come in whole 128-byte lines: 128 bytes of a row at a time, 256 columns of
 // e2m1 or 128 of e4m3, and scales for four steps, 16 bytes of a row.  (64 bytes of an e2m1 row and a dword of its scales
-// a step through four buffers, copies three steps ahead: 281 us for 8192 x 4096 x 12288.)
+// a step through four buffers, copies three steps ahead: 281 us for 8192 x 4096 x 12288, which takes 203 so.)
+//
+// 8192 x 4096 x 12288: e2m1 203 us (4.1 PFLOP/s), e4m3 279 (3.0); 4096 x 8192 x 8192: 119 and 172.  The matrix
+// instructions take 47% of the cycles with e2m1 operands, at the 2.0 GHz that the power limit leaves; LDS reads, copies
+// and the scales' extraction have the others.
 #pragma once
 
 #include "layer_mx_device.hpp"
@@ -16,7 +20,7 @@ namespace flce {
 // mfma16, and acc_drain() must precede any read of it.  The matrix instruction needs two wait states after a vector
 // instruction that wrote one of its operands, which the compiler does not see to for inline assembly.  Here only the
 // scales are such, and mx_stage sets them at least six slots before their first use.  (Waits in the assembly itself
-// would cost a quarter of the e2m1 tile's issue cycles: 238 us for 8192 x 4096 x 12288.)
+// would cost a quarter of the e2m1 tile's issue cycles: 238 us for 8192 x 4096 x 12288, for 203.)
 template <int FMT, bool ZERO, class A>
 __device__ __forceinline__ void mx_mfma(f32x4& c, const A& a, uint32_t sa, const u32x4& b, uint32_t sb) {
 #ifdef __HIP_DEVICE_COMPILE__   // the host's pass has no registers of 32 bytes
