@@ -11,7 +11,7 @@
 //
 // The backward reads h as it was written: the residual stream in the tensors' type.
 // In bf16 that rounding takes the gradients' error from 1.8e-3 (their own rounding
-// included) to 2.5e-3; an fp32 copy of h, 8 bytes an element more between forward and
+// included) to 2.4e-3; an fp32 copy of h, 8 bytes an element more between forward and
 // backward, would take half as long again.  Without a residual h is x and nothing is lost.
 //
 // A row lies in 8, 64, 256 or 1024 lanes, so that a lane has one to four runs of 8

@@ -328,6 +328,18 @@ def test_no_rows_and_strided_operands():
     assert torch.equal(a, y)
 
 
+@pytest.mark.parametrize("K,F", [(512, 66_000), (512, 66_001), (128, 66_000)])   # 256-row tiles, their ragged rows, small tiles
+def test_linear_past_32_bits(K, F):
+    N = 33_000
+    x, W = operands(N, K, F, "e2m1")
+    y = L.flce_mx_linear(x, W)
+    rows = torch.tensor([0, 32_500, 32_511, 32_512, 32_767, 32_768, N - 1], device="cuda")
+    x64, W64 = values(L.MXTensor(x.codes[rows], x.scales[rows], K, "e2m1")), values(W)
+    ref = x64 @ W64.T
+    tol = tolerance(x64, W64, ref, "e2m1", torch.bfloat16) + ref.abs() * 2.0 ** -8 + TINY[torch.bfloat16]
+    assert bool(((y[rows].double() - ref).abs() <= tol).all())
+
+
 @pytest.mark.parametrize("N", [4, 100, 700])
 def test_residual_in_place(N):
     x, W = operands(N, 512, 256, "e4m3")

@@ -206,6 +206,28 @@ def test_parameters_out_of_their_range():
     assert L.flce_sample(z, torch.full_like(u, 1.0)).tolist() == [399] * 6
 
 
+@pytest.mark.parametrize("V", [500, 9000])
+def test_an_infinite_temperature_makes_tokens_equally_likely(V):
+    z, u = draw(6, V, seed=2)
+    z[1, ::3] = -math.inf
+    for kw in ({}, dict(top_k=40), dict(top_p=0.3), dict(top_p=0.95), dict(min_p=0.5), dict(min_p=1.0, top_p=0.9)):
+        check(z, u, temperature=math.inf, **kw)
+
+
+def test_more_slices_than_a_histogram_walk_takes():
+    V = 1024 * 8192 + 77
+    z, u = draw(2, V, torch.float16, seed=3)
+    for p, T in ((1.0, 1.0), (0.9, 1.0), (0.02, 0.5)):
+        got = L.flce_sample(z, u, temperature=T, top_p=p)
+        for i in range(2):
+            v, order = torch.sort(z[i].double(), descending=True, stable=True)
+            w = torch.exp((v - v[0]) / T)
+            cum = w.cumsum(0)
+            keep = (cum - w < f32(p) * cum[-1]) if p < 1 else torch.ones_like(w, dtype=torch.bool)
+            kept = torch.zeros(V, dtype=torch.float64, device="cuda").index_put_((order[keep],), w[keep]).cumsum(0)
+            assert int(got[i]) == int(torch.searchsorted(kept, float(u[i]) * kept[-1], right=True)), (p, T, i)
+
+
 def test_frequencies():
     # 200000 draws of one row of 6 tokens: each frequency within 6 standard deviations
     z = torch.log(torch.tensor([0.05, 0.3, 0.1, 0.25, 0.2, 0.1], device="cuda")).repeat(200_000, 1)
