@@ -83,6 +83,16 @@ struct MxLinear {
 
 FLCE_WEAK hipError_t launch_mx_linear(const MxLinear& a, int dtype, hipStream_t st);
 
+// The 256-row tile's scales come 16 bytes of a row at a time, for four steps of 128 columns.  The first byte of the run
+// for the four steps from column `first` on, of a row of `bytes` (16 or more) scales: a row's last run ends with it.
+constexpr int mx_scale_run(int first, int bytes) { return first / kMxBlock < bytes - 16 ? first / kMxBlock : bytes - 16; }
+// Where in that run the four bytes of the step at column k lie.  A step past the row (the second of a pair, with an odd
+// number of steps) has none: it is given the last four, so that it reads inside the run too.
+constexpr int mx_scale_place(int k, int first, int bytes) {
+  const int at = k / kMxBlock - mx_scale_run(first, bytes);
+  return at < 12 ? at : 12;
+}
+
 // ---------------------------------------------------------------------------
 // Sampling
 // ---------------------------------------------------------------------------

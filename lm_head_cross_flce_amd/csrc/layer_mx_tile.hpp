@@ -66,23 +66,22 @@ template <bool PERM> struct MxDma {
 };
 
 // Copies of both operands' scales, 16 bytes a row (four steps): x's 256 rows, then W's.  A row's last run starts so that
-// it ends with the row; run() gives where a run starts.
+// it ends with the row (mx_scale_run).
 struct MxScaleDma {
   uint32_t off[2];
   const uint8_t* base[2];
-  int wave, last;
+  int wave, bytes;   // of a row
   __device__ __forceinline__ void init(const uint8_t* xs, int N, int n0, const uint8_t* ws, int F, int f0, int64_t ld, int tid) {
     wave = __builtin_amdgcn_readfirstlane(tid >> 6);
     base[0] = xs + (int64_t)n0 * ld;
     base[1] = ws + (int64_t)f0 * ld;
-    last = (int)ld - 16;
+    bytes = (int)ld;
     const int row = weight_row<8, false>(tid);
     off[0] = n0 + tid < N ? (uint32_t)(tid * ld) : kOOB;
     off[1] = f0 + row < F ? (uint32_t)(row * ld) : kOOB;
   }
-  __device__ __forceinline__ int run(int k) const { return min(k / kMxBlock, last); }   // k: a column of the whole row
-  __device__ __forceinline__ void issue(int k, lds_t* buf, int q) const {
-    dma16(make_rsrc(base[q] + run(k)), buf + 4096 * q + 1024 * wave, off[q]);
+  __device__ __forceinline__ void issue(int k, lds_t* buf, int q) const {   // k: a column of the whole row
+    dma16(make_rsrc(base[q] + mx_scale_run(k, bytes)), buf + 4096 * q + 1024 * wave, off[q]);
   }
 };
 
@@ -186,7 +185,7 @@ __device__ __forceinline__ void mx_stage(Acc& acc, MxRegs<FMT>& P, MxRegs<FMT>& 
     if (kCopyS && i >= 0 && i < 2) cp.copy_s(k - 128 + 512, L.s[si ^ 1], i);
   };
   // where this step's dword lies in its run, and whether the part has the step at all (its scales are 0 if not)
-  const int c4 = cp.k0 + k - 128 * (Q % 4), at = 4 * (Q % 4) + c4 / kMxBlock - cp.s.run(c4);
+  const int at = mx_scale_place(cp.k0 + k, cp.k0 + k - 128 * (Q % 4), cp.s.bytes);
   const uint32_t width = !TAIL || k < cp.kext ? 8 : 0;
   const lds_t *ps = bs + f.s[0] + at, *pw = bs + f.s[1] + at;
   uint32_t raw[16];
