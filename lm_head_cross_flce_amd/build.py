@@ -4,7 +4,8 @@
 
 Each translation unit is compiled by hipcc in parallel, then linked into one
 shared library next to this file.  Packed fp32 instructions are disabled for
-all device code (-packed-fp32-ops).
+all device code (-packed-fp32-ops).  A build fails whose matrix instructions
+come too soon after a write of an operand (matrix_waits).
 """
 
 from __future__ import annotations
@@ -14,6 +15,8 @@ import subprocess
 import sys
 import tempfile
 from concurrent.futures import ThreadPoolExecutor
+
+from . import matrix_waits
 
 PKG = os.path.dirname(os.path.abspath(__file__))
 ROOT = os.path.dirname(PKG)
@@ -42,6 +45,7 @@ def common_flags() -> list:
 
 def build(verbose: bool = False, resource_usage: bool = False) -> str:
     """Compile every source and link libflce.so; returns the library path."""
+    checked = []   # matrix instructions of each object
     with tempfile.TemporaryDirectory(prefix="flce_build_") as tmp:
         def compile_one(src: str) -> str:
             obj = os.path.join(tmp, src + ".o")
@@ -55,10 +59,16 @@ def build(verbose: bool = False, resource_usage: bool = False) -> str:
                 raise RuntimeError(f"hipcc failed on {src}:\n{out}")
             if verbose and out.strip():
                 print(out)
+            try:
+                checked.append(matrix_waits.check(obj))
+            except RuntimeError as e:
+                raise RuntimeError(f"{src}: {e}") from None
             return obj
 
         with ThreadPoolExecutor(len(SOURCES)) as ex:
             objs = list(ex.map(compile_one, SOURCES))
+        if not sum(checked):
+            raise RuntimeError("no matrix instruction was found in the compiled code, so none was checked")
         tmp_lib = os.path.join(tmp, LIB_NAME)
         cmd = [hipcc(), f"--offload-arch={ARCH}", "-shared", "-fPIC", "-o", tmp_lib] + objs
         res = subprocess.run(cmd, capture_output=True, text=True)

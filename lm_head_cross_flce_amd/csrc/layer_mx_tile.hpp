@@ -19,7 +19,8 @@ namespace flce {
 // x's and W's elements for the instruction (0: e4m3, 4: e2m1); the accumulator is tied to the destination as in
 // mfma16, and acc_drain() must precede any read of it.  The matrix instruction needs two wait states after a vector
 // instruction that wrote one of its operands, which the compiler does not see to for inline assembly.  Here only the
-// scales are such, and mx_stage sets them at least six slots before their first use.  (Waits in the assembly itself
+// scales are such, and mx_stage sets them at least six slots before their first use; should a compiler put a copy of
+// another operand in between, the build fails (matrix_waits.py reads the code that it made).  (Waits in the assembly itself
 // would cost a quarter of the e2m1 tile's issue cycles: 238 us for 8192 x 4096 x 12288, for 203.)
 template <int FMT, bool ZERO, class A>
 __device__ __forceinline__ void mx_mfma(f32x4& c, const A& a, uint32_t sa, const u32x4& b, uint32_t sb) {
