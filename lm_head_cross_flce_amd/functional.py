@@ -1221,7 +1221,8 @@ class RMSNorm(torch.nn.Module):
 
 class MXLinear(torch.nn.Module):
     """A linear layer for inference with its weight in 4 bits, made from a torch.nn.Linear on a GPU.  x: [..., K],
-    quantised to x_format on the way in, or an MXTensor (as flce_rms_norm_mx_forward returns it)."""
+    quantised to x_format on the way in, or an MXTensor (as flce_rms_norm_mx_forward returns it).  Its results have the
+    linear layer's type, and follow .half(), .to(dtype) and the like."""
 
     def __init__(self, linear: torch.nn.Linear, activation: str = "none", x_format: str = "e4m3"):
         super().__init__()
@@ -1233,6 +1234,12 @@ class MXLinear(torch.nn.Module):
         self.register_buffer("codes", q.codes)
         self.register_buffer("scales", q.scales)
         self.register_buffer("bias", None if linear.bias is None else linear.bias.detach().clone())
+
+    def _apply(self, fn, *args, **kwargs):
+        # the weight is whole numbers, which a change of type leaves alone: an empty tensor says what becomes of the type
+        super()._apply(fn, *args, **kwargs)
+        self.dtype = fn(torch.empty(0, dtype=self.dtype, device=self.codes.device)).dtype
+        return self
 
     @torch.no_grad()
     def forward(self, x, residual=None):

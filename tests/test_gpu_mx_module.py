@@ -1,0 +1,42 @@
+"""MXLinear under changes of type, and its state."""
+
+import pytest
+import torch
+
+from lm_head_cross_flce_amd import functional as L
+
+pytestmark = pytest.mark.gpu
+
+
+def made(K, F, dtype, bias=True):
+    torch.manual_seed(K + F)
+    return torch.nn.Linear(K, F, bias=bias, device="cuda", dtype=dtype)
+
+
+@pytest.mark.parametrize("bias", [True, False])
+@pytest.mark.parametrize("to", [torch.float16, torch.float32, torch.bfloat16], ids=str)
+@pytest.mark.parametrize("start", [torch.bfloat16, torch.float32], ids=str)
+def test_a_change_of_type_reaches_the_output(start, to, bias):
+    lin = made(300, 70, start, bias)
+    mx = L.MXLinear(lin, activation="silu")
+    W = L.MXTensor(mx.codes.clone(), mx.scales.clone(), 300, "e2m1")
+    x = torch.randn(2, 5, 300, device="cuda").to(to)
+    r = torch.randn(2, 5, 70, device="cuda").to(to)
+    q = L.flce_mx_quantize(x.view(10, 300), "e4m3")
+    b = lin.bias.detach().to(to) if bias else None
+    for changed in (mx.to(to), torch.nn.Sequential(mx).to("cuda", to)[0]):
+        y = changed(x, r)
+        assert y.dtype == to and changed.dtype == to
+        assert torch.equal(y.view(10, 70), L.flce_mx_linear(q, W, b, r.view(10, 70), "silu", to))
+    assert torch.equal(mx.codes, W.codes) and torch.equal(mx.scales, W.scales)
+
+
+def test_half_float_and_bfloat16():
+    mx = L.MXLinear(made(256, 40, torch.bfloat16))
+    x = torch.randn(3, 256, device="cuda")
+    for change, dt in ((mx.half, torch.float16), (mx.float, torch.float32), (mx.bfloat16, torch.bfloat16)):
+        assert change()(x).dtype == dt
+    assert mx.cuda()(x).dtype == torch.bfloat16 and mx.to("cuda:0")(x).dtype == torch.bfloat16
+    with pytest.raises(TypeError):   # no kernel for it: refused, not computed in another type
+        mx.double()(x)
+    assert mx.float()(x).dtype == torch.float32
