@@ -570,8 +570,9 @@ flce_status flce_mx_linear(const uint8_t* x, const uint8_t* x_scales, flce_mx_fo
  * other logit, and rows with a NaN, give -1.  If the largest logit is infinite, the
  * tokens that have it share the weight.  Each parameter is one number for all rows or,
  * where its pointer is not NULL, float32 (top_ks int64) [N] on the device.  Weights are
- * formed in fp64 (to 2^-45; under e^-45 of the largest they count as 0) and added in fp64 in a fixed order or, where
- * tokens are ranked, exactly, as whole numbers: results do not depend on what else runs.
+ * formed in fp64 (to 2^-45; under e^-45 of the largest they may count as 0) and added in fp64 in a fixed order or, where
+ * tokens are ranked, exactly, as whole numbers of a small fraction of the largest or of the row's sum (all roundings of a
+ * row together: at most 2^-27 of what is kept, at any V): results do not depend on what else runs.
  * logits 16-byte aligned, tokens int64 [N].
  * flce_sample_workspace_size: bytes for the call (0 up to 8192 tokens a row, and the workspace may then be NULL; else
  * about 5 V / 8 a row); pure host arithmetic.

@@ -24,10 +24,16 @@
 // 16000) and 64 (62000), and up to 71 with all CUs at work.
 //
 // Weights are formed in double, to 2^-45.  Where tokens are ranked, they are added as whole
-// numbers of 2^-s, s as large as keeps a row's sum under 2^62 (45 at 128256 tokens): such a
+// numbers of 2^-s of the largest, s as large as keeps a row's sum under 2^62: such a
 // sum does not depend on its order, so atomics may form it, and every comparison with it
-// is exact.  Its rounding, 2^-46 of the largest weight a token, is far under what a float32
-// u can tell apart.
+// is exact.  A float32 u tells 2^-24 of the sum apart; all roundings together stay under it:
+//   - up to V = 2^18 tokens s = 62 - ceil(log2 V) (45 at 128256): V 2^-(s + 1) <= 2^-27;
+//   - in longer rows a list of at most 4096 tokens has s = 44: 2^12 2^-45 = 2^-33;
+//   - a longer row that sample_whole walks is summed in double first, to a value in
+//     [2^(e - 1), 2^e), and has s = 62 - e: each rounding is 2^-62 of the sum, and n tokens
+//     kept from the largest down have n / V of it at least, so V 2^-62 of what is kept;
+//   - a histogram's bin holds whole numbers of 2^-40 (2^-38 at 8 million tokens) of the
+//     weight at its lower edge, so each weight to 2^-39 of itself.
 #include "layer_device.hpp"
 #include "layer_launch.hpp"
 
@@ -67,7 +73,7 @@ constexpr int kNoBins = -2000000000;   // the first bin of a slice that has no h
 constexpr double kLog2eDouble = 1.4426950408889634;
 __device__ __forceinline__ double exp_bin(int bins) { return pow2_negative(0.125 * kLog2eDouble * bins); }   // e^(bins / 8), bins <= 0
 
-// Weights relative to a value that is not below any.  unit: 2^s.
+// Weights relative to a value that is not below any.  unit: 2^s (see above).
 struct Weigh {
   float top;
   double scale, unit, min_w;   // scale: log2(e) / T
@@ -243,6 +249,7 @@ template <class T> __global__ void __launch_bounds__(256) sample_slice_kernel(Sa
 constexpr int kRowThreads = 1024, kRowWaves = kRowThreads / 64;
 constexpr int kBins = 2048, kMost = 4096, kGroups = 8192;
 constexpr int kNucleusMost = 8192, kMaxSlices = 1024;
+constexpr int kUnitTokens = 1 << 18;   // of more tokens the unit of weights does not depend on their number
 constexpr int kUnits = 2048;   // sample_whole: runs of 512 tokens, or of more in long rows
 
 struct RowLds {
@@ -439,9 +446,15 @@ __device__ __forceinline__ uint32_t collect(const T* z, int V, int runs, u64* li
 
 // A row with any number of tokens to keep, read from memory in every pass.
 template <class T>
-__device__ __forceinline__ void sample_whole(const Sample& a, int64_t row, const RowParams& r, const Weigh& w, uint32_t top, Row& L) {
+__device__ __forceinline__ void sample_whole(const Sample& a, int64_t row, const RowParams& r, Weigh w, uint32_t top, Row& L) {
   const T* z = (const T*)a.logits + row * a.V;
   const int V = a.V, tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
+  if (V > kUnitTokens) {   // the unit by the row's sum: at least 1, under 2^30
+    double own = 0.0, sum;
+    each_token(z, V, [&](float v, int) { own += w.real(v); });
+    block_scan(own, sum, L);
+    w.unit = __builtin_ldexp(1.0, 61 - ilogb(sum));
+  }
   // Tokens above key `cut` are kept and the first `ties` at it.
   uint32_t cut = 0;
   u64 ties = 0;
@@ -876,7 +889,7 @@ template <class T, bool GROUPS> __global__ void __launch_bounds__(kRowThreads) s
     if (tid == 0) a.tokens[row] = -1;
     return;
   }
-  const int s = 62 - (V > 2 ? 32 - __clz(V - 1) : 1);   // V 2^s <= 2^62
+  const int most = min(V, kUnitTokens), s = 62 - (most > 2 ? 32 - __clz(most - 1) : 1);   // most 2^s <= 2^62
   const Weigh w{key_value(top), kLog2eDouble / (double)r.T, (double)(1ull << s),
                 r.min_p > 0.f ? (double)fminf(r.min_p, 1.f) : 0.0};
 
