@@ -1222,7 +1222,8 @@ class RMSNorm(torch.nn.Module):
 class MXLinear(torch.nn.Module):
     """A linear layer for inference with its weight in 4 bits, made from a torch.nn.Linear on a GPU.  x: [..., K],
     quantised to x_format on the way in, or an MXTensor (as flce_rms_norm_mx_forward returns it).  Its results have the
-    linear layer's type, and follow .half(), .to(dtype) and the like."""
+    linear layer's type, and follow .half(), .to(dtype) and the like.  Its state holds the number of columns, so that
+    the state of another width is refused, also where the padded codes are of one size."""
 
     def __init__(self, linear: torch.nn.Linear, activation: str = "none", x_format: str = "e4m3"):
         super().__init__()
@@ -1240,6 +1241,21 @@ class MXLinear(torch.nn.Module):
         super()._apply(fn, *args, **kwargs)
         self.dtype = fn(torch.empty(0, dtype=self.dtype, device=self.codes.device)).dtype
         return self
+
+    def get_extra_state(self):
+        return torch.tensor(self.cols)
+
+    def set_extra_state(self, state):
+        pass   # compared before anything is loaded
+
+    def _load_from_state_dict(self, state_dict, prefix, local_metadata, strict, missing_keys, unexpected_keys, error_msgs):
+        key = prefix + "_extra_state"
+        held = int(state_dict.get(key, self.cols))
+        if held != self.cols:
+            error_msgs.append(f"{prefix}codes has {held} columns in the state, not {self.cols}")
+            return
+        super()._load_from_state_dict({**state_dict, key: self.get_extra_state()}, prefix, local_metadata, strict,
+                                      missing_keys, unexpected_keys, error_msgs)   # states without columns load too
 
     @torch.no_grad()
     def forward(self, x, residual=None):

@@ -40,3 +40,39 @@ def test_half_float_and_bfloat16():
     with pytest.raises(TypeError):   # no kernel for it: refused, not computed in another type
         mx.double()(x)
     assert mx.float()(x).dtype == torch.float32
+
+
+def test_a_state_of_another_width_is_refused():
+    # 300 and 310 columns are padded to the same 384
+    a, b = L.MXLinear(made(300, 70, torch.bfloat16)), L.MXLinear(made(310, 70, torch.bfloat16))
+    assert a.codes.shape == b.codes.shape and a.scales.shape == b.scales.shape
+    codes, bias = b.codes.clone(), b.bias.clone()
+    for strict in (True, False):
+        with pytest.raises(RuntimeError, match="columns"):
+            b.load_state_dict(a.state_dict(), strict=strict)
+        with pytest.raises(RuntimeError, match="columns"):
+            torch.nn.ModuleDict({"head": b}).load_state_dict(torch.nn.ModuleDict({"head": a}).state_dict(), strict=strict)
+    assert torch.equal(b.codes, codes) and torch.equal(b.bias, bias)
+
+
+def test_states_load_from_files_and_without_columns(tmp_path):
+    a, b = L.MXLinear(made(300, 70, torch.bfloat16)), L.MXLinear(made(300, 70, torch.bfloat16, False))
+    x = torch.randn(4, 300, device="cuda", dtype=torch.bfloat16)
+    net = torch.nn.ModuleDict({"a": a, "b": b})
+    torch.save(net.state_dict(), tmp_path / "net.pt")
+    state = torch.load(tmp_path / "net.pt", weights_only=True)
+    assert all(isinstance(v, torch.Tensor) for v in state.values())
+    other = torch.nn.ModuleDict({"a": L.MXLinear(made(300, 70, torch.float32)), "b": L.MXLinear(made(300, 70, torch.float32, False))})
+    for m in other.values():
+        m.codes.zero_()
+    other.load_state_dict(state)
+    assert other["a"].dtype == torch.float32   # the module's, as a torch.nn.Linear keeps its own
+    other.bfloat16()
+    assert all(torch.equal(other[k](x), net[k](x)) for k in net)
+    # a state from before it held the columns
+    old = {k: v for k, v in state.items() if not k.endswith("_extra_state")}
+    assert len(old) == len(state) - 2
+    for m in other.values():
+        m.codes.zero_()
+    other.load_state_dict(old)
+    assert all(torch.equal(other[k](x), net[k](x)) for k in net)
