@@ -16,8 +16,8 @@
 // to float32's rounding).  16-bit results take that: their own rounding is 1.7e-3 and
 // 2.1e-4 of them, and each e4m3 element stands for a value that it is up to 2^-4 off from.  For
 // float32 results an e4m3 x and W are expanded to bfloat16, which holds every element and
-// scale exactly, for the bf16 instruction with its float32 sums (EXACT below), at a
-// quarter of the rate.
+// scale exactly, for the bf16 instruction with its float32 sums (EXACT below), at half
+// the rate and with the expansion: 1024 x 4096 x 4096 76 us for 34 at S = 4.
 #include "layer_mx_tile.hpp"
 
 namespace flce {

@@ -5,8 +5,8 @@ numbers; past 8.4 million (1024 slices) a nucleus has no histograms.
 
 The library adds weights as whole numbers of 2^-s of the largest.  Up to V = 2^18 tokens s = 62 - ceil(log2 V); each is
 then off by 2^-(s + 1) at most, all by V 2^-(s + 1), 2^-27 of the row's sum at most.  In longer rows a list of up to 4096
-tokens has s = 44 (2^-33 in all), and a row that is walked whole s = 62 - e, where its sum lies in [2^(e - 1), 2^e): a
-token's rounding is 2^-62 of the sum, n kept tokens have n / V of it at least, so all roundings V 2^-62 of what is kept.
+tokens has s = 44 (2^-33 in all), and a row that is walked whole s by a bound on its sum: a token's rounding is 2^-57 of the
+sum, n kept tokens have n / V of it at least, so all roundings V 2^-57 of what is kept (2^-34 at 8.4 million tokens).
 Histograms hold each weight to 2^-39 of itself.  float64 sums of these rows are within 2^-38.  Tokens have to be equal:
 a random draw lies that near to one of n borders with chance under n 2^-32, 1e-5 for all rows here where n is under 4096,
 and for wider rows, whose roundings are as often up as down and hardly add up, less than that too.

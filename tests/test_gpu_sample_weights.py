@@ -1,8 +1,9 @@
 """Sampling where most of a long row's tokens have weights that are small beside the largest.
 
-Rows of more than 2^18 tokens that are walked whole hold weights as whole numbers of 2^-s, s = 62 - e for a sum in
-[2^(e - 1), 2^e), here e = 1.  Where all tokens but one have the same weight, their roundings add up, by at most V 2^-62:
-the tests say how many tokens that is.
+Rows of more than 2^18 tokens that are walked whole hold weights as whole numbers of 2^-s, s = 62 - e for a bound in
+[2^(e - 1), 2^e) on the sum, 32 times the weights of the largest of each 32 tokens: here 32 and a little, so e = 6.  Where
+all tokens but one have the same weight, their roundings of 2^-57 add up, to V 2^-57 at most: the tests say how many tokens
+that is.
 """
 
 import math
@@ -31,8 +32,8 @@ def test_a_long_tail_of_small_weights(V, how):
     else:
         tail = V // 3
         got = L.flce_sample(z, u, top_k=tail + 1).tolist()
-    # each weight is off by 2^-62 of a sum under 2: by so many tokens after V of them, in the cut and in the draw
-    slack = 2 * V * 2.0 ** -61 / w + 2
+    # each weight is off by 2^-57 at most: by so many tokens after V of them, in the cut and in the draw
+    slack = 2 * V * 2.0 ** -57 / w + 2
     for t, v in zip(got, u.tolist()):
         spot = v * (1 + tail * w)
         want = 0 if spot < 1 else 1 + int((spot - 1) / w)
