@@ -493,7 +493,8 @@ def flce_mx_linear(x, x_scales, x_format, W, W_scales, b, residual, N, K, F, dty
 def sampling(temperature: float = 1.0, top_k: int = 0, top_p: float = 1.0, min_p: float = 0.0, temperatures=None,
              top_ks=None, top_ps=None, min_ps=None) -> FlceSampling:
     """An flce_sampling value; the plural arguments are integer device addresses or None."""
-    return FlceSampling(float(temperature), int(top_k), float(top_p), float(min_p), temperatures or None,
+    top_k = max(-1, min(int(top_k), 2 ** 62))   # (the structure's integer would drop what is past 64 bits)
+    return FlceSampling(float(temperature), top_k, float(top_p), float(min_p), temperatures or None,
                         top_ks or None, top_ps or None, min_ps or None)
 
 
