@@ -536,12 +536,13 @@ flce_status flce_mx_dequantize(const uint8_t* codes, const uint8_t* scales, int6
  * may be NULL, y may be the residual.  Any N (0 included), K and F.  Element products
  * are exact.  Their sums are fp32, but for 16-bit results of an e4m3 x: there the matrix
  * instruction cuts each product of eight consecutive columns toward zero before it adds
- * them, at 2^(e - 13) (under the blocks' scales), e the largest sum of two elements' exponents among the
- * eight.  A product loses less than 2^-12 of the largest of its eight, and nothing if it
- * is 2^-6 of that or more: on normally distributed operands 5e-6 of the results' 2-norm,
- * 2e-5 where x's columns differ in size by e^(+-1).  A caller who needs those bits asks
- * for float32 results, where an e4m3 x meets W in bfloat16 and the sums are fp32; bfloat16
- * holds their values down to 2^-126, and smaller ones may count as 0.
+ * them, at 2^(e - 13) (under the blocks' scales), e the largest sum of two elements'
+ * exponents among the eight products that are not 0.  A product loses less than 2^-12 of
+ * the largest of its eight, and nothing if it is 2^-6 of that or more: on normally
+ * distributed operands 5e-6 of the results' 2-norm, 2e-5 where x's columns differ in size
+ * by e^(+-1).  A caller who needs those bits asks for float32 results, where an e4m3 x
+ * meets W in bfloat16 and the sums are fp32; bfloat16 holds their values from 2^-126 to
+ * 2^128, smaller ones may count as 0, larger ones as infinite.
  * A NaN scale makes the results of its row (of W: its feature) NaN.
  * The environment variable FLCE_DEBUG_MX_TILE (2, 4 or 8; for tests) forces the size of the output tiles, and with it
  * the workspace's.

@@ -39,8 +39,8 @@ struct MxGeometry {
   size_t total;
 };
 
-// Most tokens of the few-token kernels: 4 (16 tokens, 4096 -> 12288: 22 us, 17 in tiles), or 16 where a wave of 64
-// features fills the card three times (e4m3, 4096 -> 128256: 64 us for one token, 72 for 16; tiles 88 for 17).
+// Most tokens of the few-token kernels: 4 (16 tokens, 4096 -> 12288: 22 us, 18 in tiles), or 16 where a wave of 64
+// features fills the card three times (e4m3, 4096 -> 128256: 62 us for one token, 72 for 16; tiles 88 for 17).
 constexpr int64_t kMxFew = 4, kMxWideFew = 16;
 
 // The tests' override of the tile, or 0.
@@ -53,8 +53,9 @@ int forced_mx_tile() {
 // The cut with the least estimated time, in us, of the busiest CU's q tiles, as product_cut has it:
 //   q * per_tile + steps * max(alone, q * shared) + 4, a step 128 columns of K,
 // by runs of 200 x 8192 x 8192, 517 x 4000 x 10241, 1024 x 4096 x 4096, 2048 and 8192 x 4096 x 12288 and
-// 4096 x 8192 x 8192 at each tile: within a seventh of them.  Some, us at S = 8 / 4 / 2: 8192 x 4096 x 12288 e2m1 200 / 314 / 479,
-// e4m3 279 / 485 / 777; 517 x 4000 x 10241 e4m3 57 / 40 / 56; 1024 x 4096 x 4096 e2m1 37 / 27 / 23.
+// 4096 x 8192 x 8192 at each tile, within a seventh of them then.  The kernels' times, us at S = 8 / 4 / 2:
+// 8192 x 4096 x 12288 e2m1 206 / 334 / 448, e4m3 293 / 514 / 725; 517 x 4000 x 10241 e4m3 46 (with its join) / 43 / 59;
+// 1024 x 4096 x 4096 e2m1 28 / 22 / 25.
 struct MxCost {
   int S;
   double per_tile, alone, shared;
@@ -88,7 +89,7 @@ MxGeometry mx_geometry(int64_t N, int64_t K, int64_t F, int format, int dtype) {
       const int64_t kc = cdiv(cdiv(Kp, parts), 256) * 256;
       if (parts > 1 && (kc < 512 || cdiv(Kp, kc) != parts)) continue;
       const double q = (double)cdiv(TM * TN * parts, kCUs), depth = (double)(parts > 1 ? kc : Kp) / 128.0;
-      const double slow = exact ? 1.7 : 1.0;
+      const double slow = exact ? 1.7 : 1.0;   // (1024 x 4096 x 4096: 2.2 and 2.4 times at S = 4 and 2)
       double us = q * (c.per_tile + (c.S == 8 && parts == 1 && F % 8 != 0 ? kMxOddRows : 0.0)) +
                   slow * depth * std::max(c.alone, q * c.shared) + 4.0;
       if (parts > 1) us += 3.0 + 8.0 * (double)parts * (double)N * (double)F / 4e6;   // the sums' way out and back

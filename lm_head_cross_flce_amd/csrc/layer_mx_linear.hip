@@ -149,7 +149,7 @@ __device__ __forceinline__ void mx_finish(const MxLinear& a, int64_t n, int f, c
 // the instruction's rows, features its columns in weight_row's order, so a lane holds S
 // consecutive features of a token.  Block b + 1 is copied while block b is computed.
 // Two (S = 4) or four workgroups a CU hide one another's waits; LDS traffic bounds full launches (8192 x 4096 x 12288
-// e2m1: 314 and 479 us), and the copies' latency a launch of few tiles (48 x 2048 x 8192: 7 us).
+// e2m1: 334 and 448 us), and the copies' latency a launch of few tiles (48 x 2048 x 8192: 8 us).
 // SPLIT: the sums go to a.part and mx_join_kernel does the rest.
 template <class T, int FMT, int S, bool SPLIT>
 __global__ void __launch_bounds__(256, (S == 4 ? 2 : 4)) mx_linear_kernel(MxLinear a) {
@@ -395,7 +395,7 @@ template <class T> __global__ void __launch_bounds__(256) mx_join_kernel(MxLinea
 // Features 16 q .. + 15 of at most 16 tokens a group of waves, which split K among
 // them (a.parts waves a group, 8 waves a workgroup); weights go straight to
 // registers, two groups of kU loads in flight.  HBM bounds it where K is long (one token,
-// 12288 -> 4096, 27 MB: 11 us), its loads' latency where it is not.
+// 12288 -> 4096, 27 MB: 10 us), its loads' latency where it is not.
 constexpr int kMxWaves = 8;
 template <class T, int FMT>
 __global__ void __launch_bounds__(64 * kMxWaves) mx_linear_skinny_kernel(MxLinear a) {
@@ -474,7 +474,7 @@ __global__ void __launch_bounds__(64 * kMxWaves) mx_linear_skinny_kernel(MxLinea
 
 // The same for many features: a wave has 64 of them, four blocks that share the token fragments, and all of K.  Four steps
 // of weights are under way while four are computed, and their scales come 16 bytes a row at a time.  K >= 512.
-// One token, 4096 -> 128256: 61 us (4.6 TB/s of codes and scales); 81 with one block of features a wave, whose loads of x
+// One token, 4096 -> 128256: 62 us (4.5 TB/s of codes and scales); 81 with one block of features a wave, whose loads of x
 // and of scales outnumber those of weights four to one.
 template <class T, int FMT>
 __global__ void __launch_bounds__(256) mx_linear_wide_kernel(MxLinear a) {

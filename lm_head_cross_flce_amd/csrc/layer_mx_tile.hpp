@@ -5,11 +5,12 @@
 // A step is the instruction's 128 columns, 1024 cycles of it with e2m1 operands (four times the rate of bfloat16) and
 // 2048 with an e4m3 x.  What feeds it has to come in whole 128-byte lines: 128 bytes of a row at a time, 256 columns of
 // e2m1 or 128 of e4m3, and scales for four steps, 16 bytes of a row.  (64 bytes of an e2m1 row and a dword of its scales
-// a step through four buffers, copies three steps ahead: 281 us for 8192 x 4096 x 12288, which takes 203 so.)
+// a step through four buffers, copies three steps ahead: 281 us for 8192 x 4096 x 12288, 203 so, on one box.)
 //
-// 8192 x 4096 x 12288: e2m1 203 us (4.1 PFLOP/s), e4m3 279 (3.0); 4096 x 8192 x 8192: 119 and 172.  The matrix
-// instructions take 47% of the cycles with e2m1 operands, at the 2.0 GHz that the power limit leaves; LDS reads, copies
-// and the scales' extraction have the others.
+// 8192 x 4096 x 12288: e2m1 206 us (4.0 PFLOP/s), e4m3 293 (2.8); 4096 x 8192 x 8192: 124 and 178; boxes differ by 3%.
+// The matrix instructions are busy for 50% of the active cycles with e2m1 operands and for 67% with an e4m3 x, at the
+// 1.9 to 2.0 GHz that the power limit leaves.  The waves' cycles are 18% and 11% at waits and 24% and 49% for an
+// instruction to issue; LDS serves reads in 25% and 21% of the cycles, a quarter and a fifth of that bank conflicts.
 #pragma once
 
 #include "layer_mx_device.hpp"
@@ -21,7 +22,7 @@ namespace flce {
 // instruction that wrote one of its operands, which the compiler does not see to for inline assembly.  Here only the
 // scales are such, and mx_stage sets them at least six slots before their first use; should a compiler put a copy of
 // another operand in between, the build fails (matrix_waits.py reads the code that it made).  (Waits in the assembly itself
-// would cost a quarter of the e2m1 tile's issue cycles: 238 us for 8192 x 4096 x 12288, for 203.)
+// would cost a quarter of the e2m1 tile's issue cycles: 238 us for 8192 x 4096 x 12288, for 203 on one box.)
 template <int FMT, bool ZERO, class A>
 __device__ __forceinline__ void mx_mfma(f32x4& c, const A& a, uint32_t sa, const u32x4& b, uint32_t sb) {
 #ifdef __HIP_DEVICE_COMPILE__   // the host's pass has no registers of 32 bytes

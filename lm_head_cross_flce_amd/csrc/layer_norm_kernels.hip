@@ -10,13 +10,13 @@
 // takes one rounding (an output in 8 or 4 bits comes from the fp32 y).
 //
 // The backward reads h as it was written: the residual stream in the tensors' type.
-// In bf16 that rounding takes the gradients' error from 1.8e-3 (their own rounding
+// In bf16 that rounding takes the gradients' error from 1.6e-3 (their own rounding
 // included) to 2.4e-3; an fp32 copy of h, 8 bytes an element more between forward and
 // backward, would take half as long again.  Without a residual h is x and nothing is lost.
 //
 // A row lies in 8, 64, 256 or 1024 lanes, so that a lane has one to four runs of 8
 // columns; longer rows (over 16384 columns) are read twice.  8192 x 4096 bf16: forward
-// 45 us (6.0 TB/s of reads and writes), backward 60 (4.4) and 6 for dweight's sums.
+// 47 us (5.7 TB/s of reads and writes), backward 61 (4.4) and 6 for dweight's sums.
 #include "layer_mx_device.hpp"
 
 namespace flce {

@@ -17,11 +17,12 @@
 // else keeps more goes through sample_whole, which reads the row several times.  Rows of
 // up to 8192 tokens take one launch: their workgroup finds the groups' largest itself.
 //
-// HBM bounds the first launch (256 rows of 128256 fp32 logits, 131 MB: 23 us where no
-// sums are asked for, 51 with them, 56 with histograms, whose LDS atomics bound it); the
+// HBM bounds the first launch (256 rows of 128256 fp32 logits, 131 MB: 28 us where no
+// sums are asked for, 55 with them, 56 to 63 with histograms, whose LDS atomics bound it); the
 // second is a chain of barriers and scans in one workgroup a row, 5 us (largest logit), 11
 // (top-k 50), 16 (with top-p and min-p), 20 (a nucleus of under 4096 tokens) to 56 (one of
-// 16000) and 64 (62000), and up to 71 with all CUs at work.
+// 20000) and 64 (62000), and up to 71 with all CUs at work.  Rows that go through
+// sample_whole take 126 (top-k 5000) and 129 (z / T past the histograms' reach).
 //
 // Weights are formed in double, to 2^-45.  Where tokens are ranked, they are added as whole
 // numbers of 2^-s of the largest, s as large as keeps a row's sum under 2^62: such a

@@ -936,6 +936,7 @@ def flce_mx_linear(x: MXTensor, W: MXTensor, b: Optional[torch.Tensor] = None, r
                    activation: str = "none", dtype: torch.dtype = torch.bfloat16,
                    workspace: Optional[torch.Tensor] = None, out: Optional[torch.Tensor] = None) -> torch.Tensor:
     """act(x W^T + b) + residual in dtype, for microscaled x [N, K] of either format and W [F, K] in e2m1.
+    float32 results have float32 sums; 16-bit results of an e4m3 x have the matrix instruction's, which lose 5e-6 to 2e-5.
     out: the tensor to write to; it may be residual, and may share memory with no other tensor of the call."""
     act = _activation_code(activation)
     if dtype not in _DTYPES:
@@ -1208,7 +1209,8 @@ class GatedFeedForward(torch.nn.Module):
 
 
 class RMSNorm(torch.nn.Module):
-    """Root-mean-square norm over the last dimension: norm(x), or norm(x, residual) for (y, x + residual)."""
+    """Root-mean-square norm over the last dimension: norm(x), or norm(x, residual) for (y, x + residual).  The weight
+    has x's type."""
 
     def __init__(self, hidden: int, eps: float = 1e-6, device=None, dtype=None):
         super().__init__()
