@@ -1239,8 +1239,10 @@ class MXLinear(torch.nn.Module):
         self.register_buffer("bias", None if linear.bias is None else linear.bias.detach().clone())
 
     def _apply(self, fn, *args, **kwargs):
-        # the weight is whole numbers, which a change of type leaves alone: an empty tensor says what becomes of the type
+        # the weight is whole numbers, which a change of type leaves alone (.type() does not, but any type holds them): an
+        # empty tensor says what becomes of the results' type
         super()._apply(fn, *args, **kwargs)
+        self.codes, self.scales = self.codes.to(torch.uint8), self.scales.to(torch.uint8)
         self.dtype = fn(torch.empty(0, dtype=self.dtype, device=self.codes.device)).dtype
         return self
 

@@ -42,6 +42,18 @@ def test_half_float_and_bfloat16():
     assert mx.float()(x).dtype == torch.float32
 
 
+@pytest.mark.parametrize("to", [torch.float16, torch.bfloat16, torch.float32, torch.float64], ids=str)
+def test_type_leaves_the_weight_whole_numbers(to):
+    # .type() converts every buffer, also those of whole numbers; 0 to 255 are exact in each of these
+    mx = L.MXLinear(made(256, 400, torch.bfloat16))
+    codes, scales = mx.codes.clone(), mx.scales.clone()
+    x = torch.randn(3, 256, device="cuda")
+    mx.type(to)
+    assert torch.equal(mx.codes, codes) and torch.equal(mx.scales, scales) and mx.dtype == to
+    if to != torch.float64:
+        assert mx(x).dtype == to
+
+
 def test_a_state_of_another_width_is_refused():
     # 300 and 310 columns are padded to the same 384
     a, b = L.MXLinear(made(300, 70, torch.bfloat16)), L.MXLinear(made(310, 70, torch.bfloat16))
